@@ -209,8 +209,7 @@ def prepare(case, seed):
     s["q"], s["k"], s["v"] = s["qkv"][:, :qh], s["qkv"][:, qh:qh + h], s["qkv"][:, qh + h:]
     if own:
         from fp8_ring_kv_gb300.paged import PagedKV
-        kv = PagedKV(h, qh, d, pages, p, _axis_dims(case), (0,) * case["axes"], _pos_count(case), ROPE_BASE, dtype=dt,
-                     max_seqs=b)
+        kv = PagedKV(h, qh, d, pages, p, _axis_dims(case), (0,) * case["axes"], _pos_count(case), ROPE_BASE, dtype=dt)
         for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
             getattr(kv, name)[0].copy_(s[name])
             s[name] = getattr(kv, name)[0]
