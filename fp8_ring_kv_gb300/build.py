@@ -1,6 +1,6 @@
 """Build libkvring.so in-tree with nvcc for sm_103a.
 
-The three translation units are compiled in parallel, then linked into one
+The translation units are compiled in parallel, then linked into one
 shared library next to this file (the CUDA runtime is linked statically, the
 driver's tensor-map encoder is looked up at run time).
 """
@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvring.so")
-SOURCES = ["ring_kernels.cu", "attend.cu", "kvring_api.cu"]
+SOURCES = ["ring_kernels.cu", "attend.cu", "kvring_api.cu", "paged_append.cu", "paged_rows.cu", "paged_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/kvring.h"
+#include "host.h"
 #include "launch.h"
 
 using namespace kvring_dev;
@@ -34,18 +35,31 @@ struct kvring {
   bool calibrated;
 };
 
-namespace {
+static thread_local int g_last_cuda_error = 0;
 
-thread_local int g_last_cuda_error = 0;
+namespace kvring_dev {
 
 int cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int)e;
   return KVRING_ERR_CUDA;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
 
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+}  // namespace kvring_dev
+
+namespace {
 
 struct Layout {
   size_t state, rope[3], k_codes, v_codes, k_scale, v_scale, stat, q_codes, q_scale, head_stat, total;
@@ -57,15 +71,7 @@ bool check_config(const kvring_config* c) {
   if (c->head_dim != 64 && c->head_dim != 128) return false;
   if (c->heads < 1 || 2 * c->heads * (c->head_dim / 16) > 1024) return false;
   if (c->n_slots < 1 || c->n_slots > (1 << 20)) return false;
-  if (c->n_axes < 1 || c->n_axes > 3) return false;
-  int sum = 0;
-  for (int a = 0; a < c->n_axes; ++a) {
-    if (c->axis_dims[a] < 2 || c->axis_dims[a] % 2) return false;
-    if (c->pos_count[a] < 1 || c->pos_count[a] > (1 << 24)) return false;
-    sum += c->axis_dims[a];
-  }
-  if (sum != c->head_dim) return false;
-  if (!(c->rope_base > 1.0) || !std::isfinite(c->rope_base)) return false;
+  if (!rope_axes_ok(c->n_axes, c->axis_dims, c->pos_count, c->head_dim, c->rope_base)) return false;
   if (c->out_dtype != KVRING_OUT_BF16 && c->out_dtype != KVRING_OUT_F32) return false;
   if (c->max_queries < 1 || c->max_queries > (1 << 20)) return false;
   if (c->n_global < 0 || c->n_global >= c->n_slots) return false;
@@ -103,22 +109,6 @@ Layout layout_of(const kvring_config* c) {
   off = round_up(off + 2 * H * sizeof(float), 1024);
   L.total = off;
   return L;
-}
-
-// omega_{a,j} = base^(-2j/d_a), fp64
-double omega(double base, int d_axis, int j) { return std::pow(base, -2.0 * j / d_axis); }
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
 }
 
 // Query codes [n_rows][H][D] at q_codes: box of D channels x 1 head x 128

@@ -1,0 +1,159 @@
+// Internal definitions of the paged FP8 KV cache: device views, the batch of
+// sequences a call works on, and the kernels' host-side entry points.
+#pragma once
+#include <type_traits>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace kvring_dev {
+
+// state words at the start of the workspace
+enum : int { PST_ERR = 0, PST_WORDS = 64 };
+// device error bits (beside DEVERR_POS_RANGE and DEVERR_TIMEOUT)
+enum : int { DEVERR_SEQ = 8, DEVERR_PAGE = 16 };
+
+constexpr int kPagedMaxSeqs = 2048;
+constexpr int kPagedMaxLen = 1 << 22;    // tokens of one sequence
+constexpr int kPagedMaxSms = 160;        // sizes the attention's scratch
+
+// Device view of one layer of the cache, passed by value to the kernels.
+struct PagedView {
+  int32_t* state;                 // PST_* words
+  const float2* rope[kMaxAxes];   // per axis: [pos_count][axis_dims/2] (cos, sin)
+  int32_t pos_min[kMaxAxes];
+  int32_t pos_count[kMaxAxes];
+  int32_t axis_pairs[kMaxAxes];
+  int32_t pair_off[kMaxAxes];
+  uint8_t* k_codes;               // [n_pages][H][P][D]
+  uint8_t* v_codes;
+  float* k_scale;                 // [n_pages][H]
+  float* v_scale;
+  int32_t H, QH, G, D, P, p_shift, n_pages, n_axes;   // G = QH / H query heads per key head
+  long long row0;                 // the layer's first row of the code arrays seen as rows of D
+};
+
+// The sequences of one call: sequence b's new tokens are rows seq_start[b] ..
+// seq_start[b+1]-1 of the packed inputs, kv_len[b] its tokens in the cache
+// once they are in, table[b * table_stride + j] its page j.
+struct PagedBatch {
+  const int32_t* seq_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  long long table_stride;
+  int32_t n_seqs, n_tokens, table_width;
+};
+
+// ---------------------------------------------------------------- attention work
+// Rows of queries: sequence b has n_b * G rows per key head (row r: token
+// r / G, query head h * G + r % G).  Two kernels share the sequences: those
+// of at most kRowsMax rows go to the register-tile kernel (16 rows per item),
+// the others to the tensor-memory kernel (256 rows per item).
+constexpr int kRowsTile = 16, kRowsKeys = 32, kRowsWarps = 8;
+constexpr int kRowsMax = 1 << 30;
+constexpr int kRowsWorkersMax = kPagedMaxSms * kRowsWarps;
+
+// What a worker leaves for the merge when an item it began ends in a later
+// worker's range: the item, and the last worker that holds a piece of it.
+struct PieceRec {
+  int32_t b, h, tile, last;       // b < 0: nothing to merge
+};
+
+// Partial results: slot 2w holds the piece of an item begun before worker w's
+// range, slot 2w + 1 the piece of an item that w began and did not end.
+// o [slot][rows][D] fp32 (unnormalised), ml [slot][rows] (running maximum in
+// log2 units, sum); m = -inf marks rows (or whole pieces) without a key.
+struct PieceScratch {
+  float* o;
+  float2* ml;
+  PieceRec* rec;
+};
+
+struct PagedAttn {
+  PagedView pv;
+  PagedBatch pb;
+  const void* q;
+  const int32_t* q_pos;
+  void* out;
+  long long q_stride, out_stride;   // elements between tokens
+  float scale_log2;                 // softmax scale * log2(e)
+  int32_t causal, window, max_new;
+  PieceScratch rows;
+};
+
+// bytes of the attention's scratch (the same for every device)
+size_t paged_scratch_bytes(int D);
+void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a);
+
+cudaError_t launch_paged_rope_table(float2* table, int pos_min, int pos_count, int pairs, const double* omega,
+                                    cudaStream_t st);
+cudaError_t launch_paged_append(const PagedView& pv, const PagedBatch& pb, const void* k, long long k_stride,
+                                const void* v, long long v_stride, const int32_t* pos, bool f16, cudaStream_t st);
+cudaError_t prepare_paged_attend(int D);
+// tmK, tmV: the code arrays as [rows][D] u8, box {D, min(P, 32)}
+cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
+                                cudaStream_t st);
+
+// ---------------------------------------------------------------- sequences
+struct SeqInfo {
+  int s0, n, len;
+};
+
+// Sequence b's numbers.  Ones that contradict each other or the call's sizes
+// give n = 0 (the sequence is left out) and ok = false.
+__device__ __forceinline__ SeqInfo seq_info(const PagedBatch& pb, int p_shift, int b, bool& ok) {
+  SeqInfo s;
+  s.s0 = __ldg(pb.seq_start + b);
+  const int s1 = __ldg(pb.seq_start + b + 1);
+  s.len = __ldg(pb.kv_len + b);
+  ok = s.s0 >= 0 && s1 >= s.s0 && s1 <= pb.n_tokens && s.len >= 0 &&
+       (long long)s.len <= ((long long)pb.table_width << p_shift);
+  s.n = ok ? s1 - s.s0 : 0;
+  if (!ok) s.s0 = s.len = 0;
+  return s;
+}
+
+// e4m3 block scale: the smallest power of two s with amax <= 448 s, and 1 / s
+// (both exact); 0 and 0 for a block below 2^-100.
+__device__ __forceinline__ void pow2_scale(float amax, float& scale, float& inv) {
+  if (amax < 0x1p-100f) {
+    scale = inv = 0.0f;
+    return;
+  }
+  const uint32_t u = __float_as_uint(amax);
+  // amax = 1.f * 2^e and 448 = 1.75 * 2^8: s = 2^(e - 8), or 2^(e - 7) when 1.f > 1.75
+  const int k = (int)(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+  scale = __uint_as_float((uint32_t)(k + 127) << 23);
+  inv = __uint_as_float((uint32_t)(127 - k) << 23);
+}
+
+// 8 halfs (one uint4) -> 8 fp32 (exact); T picks the 16-bit type.
+template <typename T>
+__device__ __forceinline__ void load8_f32(uint4 u, float* x) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  } else {
+    bf16x8_to_f32(u, x);
+  }
+}
+
+// Two fp32 -> packed 16-bit pair of type T, round to nearest even.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same_v<T, __half>) {
+    return cvt_f16x2(lo, hi);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+}  // namespace kvring_dev

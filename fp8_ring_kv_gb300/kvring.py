@@ -34,6 +34,14 @@ KVRING_OUT_F32 = 1
 KVRING_SCALES_TOKEN = 0
 KVRING_SCALES_STATIC = 1
 
+# the paged cache (include/kvring_paged.h)
+KVRING_DEVERR_SEQ = 8
+KVRING_DEVERR_PAGE = 16
+KVRING_IN_BF16 = 0
+KVRING_IN_F16 = 1
+KVRING_PAGED_MAX_SEQS = 2048
+KVRING_PAGED_MAX_LEN = 1 << 22
+
 EXPORTS = (
     "kvring_workspace_bytes", "kvring_create", "kvring_write", "kvring_write_global", "kvring_calibrate",
     "kvring_set_qk_norm",
@@ -41,6 +49,8 @@ EXPORTS = (
     "kvring_attend", "kvring_destroy", "kvring_status_string", "kvring_last_cuda_error",
     "kvring_layout", "kvring_debug_state", "kvring_debug_quantize", "kvring_attend_noalloc",
     "kvring_debug_wait_timeout",
+    "kvring_paged_workspace_bytes", "kvring_paged_create", "kvring_paged_append", "kvring_paged_attend",
+    "kvring_paged_destroy", "kvring_paged_layout", "kvring_paged_debug_state",
 )
 
 
@@ -58,6 +68,23 @@ class kvring_config(ctypes.Structure):
         ("max_queries", ctypes.c_int32),
         ("n_global", ctypes.c_int32),
         ("scale_mode", ctypes.c_int32),
+    ]
+
+
+class kvring_paged_config(ctypes.Structure):
+    _fields_ = [
+        ("layers", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis_dims", ctypes.c_int32 * 3),
+        ("pos_min", ctypes.c_int32 * 3),
+        ("pos_count", ctypes.c_int32 * 3),
+        ("rope_base", ctypes.c_double),
     ]
 
 
@@ -97,6 +124,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvring_debug_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i32)]),
         "kvring_debug_quantize": (ctypes.c_int, [vp, i64, i32, vp, vp, vp]),
         "kvring_debug_wait_timeout": (ctypes.c_int, [i64, i32, vp, vp]),
+        "kvring_paged_workspace_bytes": (sz, [ctypes.POINTER(kvring_paged_config)]),
+        "kvring_paged_create": (ctypes.c_int, [ctypes.POINTER(kvring_paged_config), vp, sz, vp, ctypes.POINTER(vp)]),
+        "kvring_paged_append": (ctypes.c_int, [vp, i32, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i64, i32, vp]),
+        "kvring_paged_attend": (ctypes.c_int, [vp, i32, vp, i64, vp, vp, vp, i32, i32, i32, vp, i64, i32, i32, i32,
+                                               ctypes.c_float, vp, i64, vp]),
+        "kvring_paged_destroy": (ctypes.c_int, [vp]),
+        "kvring_paged_layout": (ctypes.c_int, [vp] + [ctypes.POINTER(vp)] * 5),
+        "kvring_paged_debug_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i32)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
