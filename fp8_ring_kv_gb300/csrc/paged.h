@@ -49,10 +49,14 @@ struct PagedBatch {
 // ---------------------------------------------------------------- attention work
 // Rows of queries: sequence b has n_b * G rows per key head (row r: token
 // r / G, query head h * G + r % G).  Two kernels share the sequences: those
-// of at most kRowsMax rows go to the register-tile kernel (16 rows per item),
-// the others to the tensor-memory kernel (256 rows per item).
-constexpr int kRowsTile = 16, kRowsKeys = 32, kRowsWarps = 8;
-constexpr int kRowsMax = 1 << 30;
+// of at most kRowsMax rows go to the register-tile kernel (an item is the
+// rows of one sequence and key head), the others to the tensor-memory kernel
+// (256 rows per item).  fp16 queries take two of the register tile's 16 rows
+// each (high and low part).
+constexpr int kRowsWarps = 8, kRowsKeys = 32;
+template <typename T>
+constexpr int kRowsMax = std::is_same_v<T, __half> ? 8 : 16;
+constexpr int kTilesRows = 256;
 constexpr int kRowsWorkersMax = kPagedMaxSms * kRowsWarps;
 
 // What a worker leaves for the merge when an item it began ends in a later
@@ -80,10 +84,10 @@ struct PagedAttn {
   long long q_stride, out_stride;   // elements between tokens
   float scale_log2;                 // softmax scale * log2(e)
   int32_t causal, window, max_new;
-  PieceScratch rows;
+  PieceScratch rows, tiles;
 };
 
-// bytes of the attention's scratch (the same for every device)
+// bytes of the attention's scratch (the same on every device)
 size_t paged_scratch_bytes(int D);
 void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a);
 
@@ -91,7 +95,13 @@ cudaError_t launch_paged_rope_table(float2* table, int pos_min, int pos_count, i
                                     cudaStream_t st);
 cudaError_t launch_paged_append(const PagedView& pv, const PagedBatch& pb, const void* k, long long k_stride,
                                 const void* v, long long v_stride, const int32_t* pos, bool f16, cudaStream_t st);
-cudaError_t prepare_paged_attend(int D);
+cudaError_t prepare_paged_rows(int D);
+cudaError_t prepare_paged_tiles(int D);
+// the kernel of few rows, and the kernel of many; ``blocks`` of either share its work
+cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
+                              cudaStream_t st);
+cudaError_t launch_paged_tiles(const PagedAttn& a, bool f16, int blocks, cudaStream_t st);
+cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int workers, cudaStream_t st);
 // tmK, tmV: the code arrays as [rows][D] u8, box {D, min(P, 32)}
 cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
                                 cudaStream_t st);

@@ -181,7 +181,8 @@ int kvring_paged_create(const kvring_paged_config* cfg, void* workspace, size_t 
                                 cfg->axis_dims[a] / 2, reinterpret_cast<const double*>(ws + L.omega) + a * 64, st);
   if (e == cudaSuccess && (!encode_codes(&p->k_map, pv.k_codes, *cfg) || !encode_codes(&p->v_map, pv.v_codes, *cfg)))
     e = cudaErrorInvalidValue;
-  if (e == cudaSuccess) e = prepare_paged_attend(pv.D);
+  if (e == cudaSuccess) e = prepare_paged_rows(pv.D);
+  if (e == cudaSuccess) e = prepare_paged_tiles(pv.D);
   if (e != cudaSuccess) {
     delete p;
     return cuda_fail(e);

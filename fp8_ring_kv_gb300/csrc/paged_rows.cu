@@ -26,9 +26,8 @@
 
 namespace kvring_dev {
 
-constexpr int RW = kRowsWarps, RT = kRowsTile, RK = kRowsKeys;
+constexpr int RW = kRowsWarps, RK = kRowsKeys;
 constexpr int RTHREADS = 32 * RW;
-using RowsShare = Share<RT, RK, 0, 0, kRowsMax>;
 
 template <int D>
 struct RowsLayout {
@@ -71,6 +70,12 @@ __global__ void __launch_bounds__(RTHREADS, 1)
   constexpr int NST = LY::NST;
   constexpr int KS = D / 16;                             // k steps of QK; also 2 x the V channel tiles per byte group
   constexpr int DG = D / 8;                              // channels of O per thread and column parity
+  // MMA rows 8 .. 15: eight more query rows, or, for fp16 queries, the low
+  // parts of rows 0 .. 7 (and of their weights): both parts of a product are
+  // summed at the end, at no further MMA
+  constexpr bool SPLIT = std::is_same_v<T, __half>;
+  constexpr int RT = kRowsMax<T>, E = SPLIT ? 1 : 2;
+  using RowsShare = Share<RT, RK, 0, 0, RT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
   if (tid == 0) *abort_flag = 0;
   pdl_wait();
   pdl_trigger();
-  RowsShare::prefix<RTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SUMS), blockIdx.x == 0);
+  RowsShare::template prefix<RTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SUMS), blockIdx.x == 0);
   const int H = a.pv.H, G = a.pv.G;
   const int worker = blockIdx.x * RW + warp;
   const int workers = gridDim.x * RW;
@@ -109,13 +114,13 @@ __global__ void __launch_bounds__(RTHREADS, 1)
       const int rows = pl.s.n * G;
       // ---------------------------------------------------------- queries
       // rows g and g + 8 of the tile, rotated, scaled by a power of two to
-      // below 2 and rounded to fp16 (an MMA operand; 2^-11 of a value, like
-      // the 16-bit type they came in)
+      // below 2 and rounded to fp16 (an MMA operand): a bf16 query loses
+      // nothing that its output could show, an fp16 one keeps a second part
       uint32_t qa[KS][4];
-      float rf[2];
-      int hi[2], lo[2];
+      float rf[E];
+      int hi[E], lo[E];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int r = pl.tile * RT + g + 8 * e;
         const bool live = r < rows;
         const int i = live ? r / G : 0;
@@ -152,8 +157,16 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         rf[e] = ldexpf(a.scale_log2, ex);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qa[k][e] = cvt_f16x2(x[4 * k] * down, x[4 * k + 1] * down);
-          qa[k][2 + e] = cvt_f16x2(x[4 * k + 2] * down, x[4 * k + 3] * down);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const float x0 = x[4 * k + 2 * f] * down, x1 = x[4 * k + 2 * f + 1] * down;
+            const uint32_t w = cvt_f16x2(x0, x1);
+            qa[k][2 * f + e] = w;
+            if constexpr (SPLIT) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
+              qa[k][2 * f + 1] = cvt_f16x2(x0 - y.x, x1 - y.y);
+            }
+          }
         }
         const int at = pl.s.len - pl.s.n + i;            // the row's own index
         hi[e] = !live ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
@@ -162,7 +175,12 @@ __global__ void __launch_bounds__(RTHREADS, 1)
       float o[DG][4];
 #pragma unroll
       for (int i = 0; i < DG; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      float m[E], l[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        m[e] = -INFINITY;
+        l[e] = 0.0f;
+      }
 
       // ---------------------------------------------------------- pages
       // lane i holds the page ids and scales of tile base + i (two pages when
@@ -269,34 +287,39 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             mma_16816(c[j], qa[q * 4 + 3], widen_lo(w.w), widen_hi(w.w));
           }
         }
-        // y of rows g (e = 0) and g + 8 (e = 1); columns 2 t4, 2 t4 + 1 of group j
+        // y of row g (and, e = 1, g + 8); columns 2 t4, 2 t4 + 1 of group j
         const float sk1 = a.pv.P == 16 ? mt.y : mt.x, sv1 = a.pv.P == 16 ? mt.w : mt.z;
-        const float off0 = __log2f(mt.z), off1 = __log2f(sv1);   // powers of two: whole numbers
+        const float off0 = __log2f(mt.z), off1 = __log2f(sv1);
         const int key0 = k * RK;
-        const bool cut = key0 + RK > min(hi[0], hi[1]) || key0 < max(lo[0], lo[1]);
-        float mx[2] = {-INFINITY, -INFINITY};
+        bool cut = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int e = 0; e < E; ++e) cut = cut || key0 + RK > hi[e] || key0 < lo[e];
+        float mx[E];
+        bool raise = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = i >> 1;
-            float y = fmaf(c[j][i], rf[e] * (j < 2 ? mt.x : sk1), j < 2 ? off0 : off1);
-            if (cut) {
-              const int key = key0 + j * 8 + key_row(2 * t4 + (i & 1));
-              if (key >= hi[e] || key < lo[e] || key >= pl.t.hi) y = -INFINITY;
+        for (int e = 0; e < E; ++e) {
+          mx[e] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float s = SPLIT ? c[j][i] + c[j][2 + i] : c[j][2 * e + i];
+              float y = fmaf(s, rf[e] * (j < 2 ? mt.x : sk1), j < 2 ? off0 : off1);
+              if (cut) {
+                const int key = key0 + j * 8 + key_row(2 * t4 + i);
+                if (key >= hi[e] || key < lo[e] || key >= pl.t.hi) y = -INFINITY;
+              }
+              c[j][2 * e + i] = y;
+              mx[e] = fmaxf(mx[e], y);
             }
-            c[j][i] = y;
-            mx[e] = fmaxf(mx[e], y);
-          }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+          raise = raise || mx[e] > m[e];
         }
-        if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
-          float al[2];
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          float al[E];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < E; ++e) {
             const float mn = fmaxf(m[e], mx[e]);
             al[e] = mn > m[e] ? ex2f(m[e] - mn) : 1.0f;      // 0 for the first keys of a row
             m[e] = mn;
@@ -306,27 +329,29 @@ __global__ void __launch_bounds__(RTHREADS, 1)
           for (int i = 0; i < DG; ++i) {
             o[i][0] *= al[0];
             o[i][1] *= al[0];
-            o[i][2] *= al[1];
-            o[i][3] *= al[1];
+            o[i][2] *= al[E - 1];
+            o[i][3] *= al[E - 1];
           }
         }
-        const float sub[2] = {m[0] == -INFINITY ? 0.0f : 8.0f - m[0], m[1] == -INFINITY ? 0.0f : 8.0f - m[1]};
         uint32_t pa[2][4];
-        float ls[2][2] = {{0, 0}, {0, 0}};               // [page][row]
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = ex2f(c[j][i] + sub[i >> 1]);
-            ls[j >> 1][i >> 1] += w[i];
-          }
-          pa[j >> 1][(j & 1) * 2] = cvt_f16x2(w[0], w[1]);
-          pa[j >> 1][(j & 1) * 2 + 1] = cvt_f16x2(w[2], w[3]);
-        }
         const float iv0 = 1.0f / mt.z, iv1 = 1.0f / sv1;
-        l[0] += ls[0][0] * iv0 + ls[1][0] * iv1;
-        l[1] += ls[0][1] * iv0 + ls[1][1] * iv1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float sub = m[e] == -INFINITY ? 0.0f : 8.0f - m[e];
+          float ls[2] = {0.0f, 0.0f};                    // of either page
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w0 = ex2f(c[j][2 * e] + sub), w1 = ex2f(c[j][2 * e + 1] + sub);
+            ls[j >> 1] += w0 + w1;
+            const uint32_t w = cvt_f16x2(w0, w1);
+            pa[j >> 1][(j & 1) * 2 + e] = w;
+            if constexpr (SPLIT) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
+              pa[j >> 1][(j & 1) * 2 + 1] = cvt_f16x2(w0 - y.x, w1 - y.y);
+            }
+          }
+          l[e] += ls[0] * iv0 + ls[1] * iv1;
+        }
         // O += P V: k pairs are keys (row(2 t4), row(2 t4 + 1)) of groups 2 kk and 2 kk + 1
         const bool edge = key0 + RK > pl.t.hi || key0 < pl.t.lo;
 #pragma unroll
@@ -373,13 +398,20 @@ __global__ void __launch_bounds__(RTHREADS, 1)
       }
       // ---------------------------------------------------------- results
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
         l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
       }
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < DG; ++i) {
+          o[i][0] += o[i][2];
+          o[i][1] += o[i][3];
+        }
+      }
       const int slot = 2 * worker + (u == pl.at ? 1 : 0);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int r = pl.tile * RT + g + 8 * e;
         if (r >= rows) continue;
         if (whole) {
@@ -419,125 +451,30 @@ __global__ void __launch_bounds__(RTHREADS, 1)
   }
 }
 
-// ---------------------------------------------------------------- join
-// The items that several workers share: out = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i over the pieces, in the workers' order (no atomics:
-// the result does not depend on which worker came first).  Block x looks at
-// the records of workers 8 x .. 8 x + 7; a record's rows are taken by the
-// blocks along y, a row by the whole block: warp w the pieces w, w + 8, ...
-template <int D, int TR, typename T>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttn a, PieceScratch ps,
-                                                         int workers) {
-  __shared__ float acc[8][D];
-  __shared__ float2 mls[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int V = D / 32;                              // channels per lane
-  pdl_wait();
-  pdl_trigger();
-  for (int w0 = 0; w0 < 8; ++w0) {
-    const int w = blockIdx.x * 8 + w0;
-    if (w >= workers) return;
-    const PieceRec rec = ps.rec[w];
-    if (rec.b < 0) continue;
-    bool ok;
-    const SeqInfo s = seq_info(a.pb, a.pv.p_shift, rec.b, ok);
-    const int rows = s.n * a.pv.G - rec.tile * TR;
-    for (int r = blockIdx.y; r < min(rows, TR); r += gridDim.y) {
-      // pieces: slot 2 w + 1, then slot 2 i of the workers i = w + 1 .. last
-      float m = -INFINITY, l = 0.0f, o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = 0.0f;
-      for (int p = w + warp; p <= rec.last; p += 8) {
-        const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * TR + r;
-        const float2 ml = ps.ml[row];
-        if (ml.x == -INFINITY) continue;
-        float x[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = ps.o[row * D + lane * V + i];
-        const float mn = fmaxf(m, ml.x);
-        const float f0 = ex2f(m - mn), f1 = ex2f(ml.x - mn);
-        m = mn;
-        l = l * f0 + ml.y * f1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + x[i] * f1;
-      }
-      if (lane == 0) mls[warp] = make_float2(m, l);
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[warp][lane * V + i] = o[i];
-      __syncthreads();
-      if (tid < D) {
-        float mm = -INFINITY, ll = 0.0f, oo = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mm = fmaxf(mm, mls[i].x);
-        if (mm != -INFINITY) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float f = ex2f(mls[i].x - mm);
-            ll += mls[i].y * f;
-            oo += acc[i][tid] * f;
-          }
-        }
-        const int rr = rec.tile * TR + r;
-        const int i = rr / a.pv.G;
-        T* dst = static_cast<T*>(a.out) + (s.s0 + i) * a.out_stride + (size_t)(rec.h * a.pv.G + rr - i * a.pv.G) * D;
-        const float v = ll > 0.0f ? oo / ll : 0.0f;
-        if constexpr (std::is_same_v<T, __half>) dst[tid] = __float2half_rn(v);
-        else dst[tid] = __float2bfloat16_rn(v);
-      }
-      __syncthreads();
-    }
-  }
-}
-
 // ---------------------------------------------------------------- host
-static size_t piece_bytes(int workers, int rows, int D) {
-  const size_t slots = (size_t)2 * workers * rows;
-  return slots * D * 4 + slots * 8 + (size_t)workers * sizeof(PieceRec);
-}
-
-static uint8_t* carve(uint8_t* at, int workers, int rows, int D, PieceScratch* ps) {
-  const size_t slots = (size_t)2 * workers * rows;
-  ps->o = reinterpret_cast<float*>(at);
-  at += slots * D * 4;
-  ps->ml = reinterpret_cast<float2*>(at);
-  at += slots * 8;
-  ps->rec = reinterpret_cast<PieceRec*>(at);
-  return at + (size_t)workers * sizeof(PieceRec);
-}
-
-size_t paged_scratch_bytes(int D) { return piece_bytes(kRowsWorkersMax, RT, D); }
-
-void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a) { carve(base, kRowsWorkersMax, RT, D, &a->rows); }
-
-template <int D>
+template <int D, typename T>
 static cudaError_t prepare_t() {
-  cudaError_t e = cudaFuncSetAttribute(paged_attend_rows_kernel<D, __half>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       RowsLayout<D>::ALLOC);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_attend_rows_kernel<D, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             RowsLayout<D>::ALLOC);
-  return e;
+  return cudaFuncSetAttribute(paged_attend_rows_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              RowsLayout<D>::ALLOC);
 }
 
-cudaError_t prepare_paged_attend(int D) { return D == 128 ? prepare_t<128>() : prepare_t<64>(); }
+cudaError_t prepare_paged_rows(int D) {
+  const cudaError_t e = D == 128 ? prepare_t<128, __half>() : prepare_t<64, __half>();
+  if (e != cudaSuccess) return e;
+  return D == 128 ? prepare_t<128, __nv_bfloat16>() : prepare_t<64, __nv_bfloat16>();
+}
 
 template <int D, typename T>
-static cudaError_t attend_t(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int sms,
-                            cudaStream_t st) {
-  const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
-  cudaError_t e = launch_pdl(paged_attend_rows_kernel<D, T>, dim3(blocks), dim3(RTHREADS), RowsLayout<D>::ALLOC, st,
-                             tmK, tmV, a);
-  if (e != cudaSuccess) return e;
-  const long long most = (long long)a.max_new * a.pv.G;
-  return launch_pdl(paged_join_kernel<D, RT, T>, dim3(blocks, (unsigned)(most < RT ? most : RT)), dim3(256), 0, st, a,
-                    a.rows, blocks * RW);
+static cudaError_t rows_t(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int blocks,
+                          cudaStream_t st) {
+  return launch_pdl(paged_attend_rows_kernel<D, T>, dim3(blocks), dim3(RTHREADS), RowsLayout<D>::ALLOC, st, tmK, tmV, a);
 }
 
-cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
-                                cudaStream_t st) {
+cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
+                              cudaStream_t st) {
   if (a.pv.D == 64)
-    return f16 ? attend_t<64, __half>(a, tmK, tmV, sms, st) : attend_t<64, __nv_bfloat16>(a, tmK, tmV, sms, st);
-  return f16 ? attend_t<128, __half>(a, tmK, tmV, sms, st) : attend_t<128, __nv_bfloat16>(a, tmK, tmV, sms, st);
+    return f16 ? rows_t<64, __half>(a, tmK, tmV, blocks, st) : rows_t<64, __nv_bfloat16>(a, tmK, tmV, blocks, st);
+  return f16 ? rows_t<128, __half>(a, tmK, tmV, blocks, st) : rows_t<128, __nv_bfloat16>(a, tmK, tmV, blocks, st);
 }
 
 }  // namespace kvring_dev
