@@ -22,10 +22,11 @@
 // Warp roles (512 threads, registers moved from the last two groups to the softmax):
 //   warps 0-3, 4-7   softmax of query tile 0, 1: one row per thread.  They also
 //                    load and rotate the rows' queries and write the output
-//   warps 8-11       K and V: page ids and codes of the next tile into
-//                    registers, the current ones widened into shared memory;
-//                    warp 8 the pages' scales
+//   warps 8-11       K and V: the codes of the next tile into registers, the
+//                    current ones widened into shared memory
 //   warp 12          MMA issue
+//   warp 13          the line of work: the stretches of items for the others,
+//                    and per tile the page ids and scales, up to TMETA tiles ahead
 // MMAs run in the order they are issued: QK of the next tile may overwrite
 // the P that the PV before it reads.
 #include "paged_sched.cuh"
@@ -37,9 +38,15 @@ constexpr int TM_ROWS = 128;                 // rows of one MMA
 constexpr int TTR = kTilesRows;              // rows of an item: two query tiles
 static_assert(TTR == 2 * TM_ROWS);
 constexpr int TTHREADS = 512;
-constexpr int TMETA = 4;                     // scale stages
+constexpr int TMETA = 8;                     // stages of page ids and scales
 constexpr float kRaise = 8.0f;               // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kTop = 6.0f;                 // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
+
+// What a block does of one item: its key tiles [k0, k1).
+struct Stretch {
+  int b, h, tile, s0, n, len, lo, hi, k0, k1, flags, pad;
+};
+enum : int { STRETCH_SOME = 1, STRETCH_WHOLE = 2, STRETCH_HEAD = 4 };   // else: the end; the whole item; its beginning
 
 template <int D, typename T>
 struct TilesLayout {
@@ -50,9 +57,11 @@ struct TilesLayout {
   static constexpr int Q = 0;                                    // [2 tiles][NQ]
   static constexpr int KH = Q + 2 * NQ * QB;                     // [2]
   static constexpr int VH = KH + 2 * KB;                         // [2]
-  static constexpr int META = VH + 2 * KB;                       // [TMETA][KT / 16] float4 {s_k, log2 s_v, 1 / s_v, -}
-  static constexpr int BAR = META + TMETA * (KT / 16) * 16;
-  static constexpr int NBAR = 2 + 2 + 2 + TMETA + 4 + 4 + 2 + 1;
+  static constexpr int META = VH + 2 * KB;                       // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, page}
+  static constexpr int RF = META + TMETA * (KT / 16) * 16;       // [256] logit factor of a row
+  static constexpr int SEG = RF + TTR * 4;                       // [2] Stretch
+  static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
+  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 4 + 4 + 2 + 4 + 1;
   static constexpr int SUMS = BAR + NBAR * 8;
   static constexpr int MISC = SUMS + 16 * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
@@ -66,19 +75,24 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
   constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16;
   using SH = Share<TTR, KT, 2, kRowsMax<T>, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
+  constexpr int kNone = -1;                // page of a group of keys that no query sees
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
-  uint64_t* q_full = bars;                 // [2] query tile written (once per stretch of an item)
+  uint64_t* q_full = bars;                 // [2] query tile written (once per stretch)
   uint64_t* kh_full = q_full + 2;          // [2] K tile widened
   uint64_t* vh_full = kh_full + 2;         // [2] V tile widened
-  uint64_t* meta_full = vh_full + 2;       // [TMETA] scales written
-  uint64_t* s_full = meta_full + TMETA;    // [2 query tiles][2] QK done; of tile 1: both, and the K tile is free
+  uint64_t* meta_full = vh_full + 2;       // [TMETA] page ids and scales of a tile written
+  uint64_t* meta_free = meta_full + TMETA; // [TMETA] the tile's softmax is done
+  uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][2] QK done; of tile 1: both, and the K tile is free
   uint64_t* o_done = s_full + 4;           // [2][2] PV done; of tile 1: both, and the V tile is free
   uint64_t* p_full = o_done + 4;           // [2] P stored
-  uint64_t* drain = p_full + 2;
+  uint64_t* seg_full = p_full + 2;         // [2] stretch written
+  uint64_t* seg_free = seg_full + 2;       // [2] every role is done with it
+  uint64_t* drain = seg_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
+  volatile Stretch* segs = reinterpret_cast<volatile Stretch*>(sm + LY::SEG);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -86,8 +100,13 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
       mbar_init(&kh_full[i], 4);
       mbar_init(&vh_full[i], 4);
       mbar_init(&p_full[i], 4);
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_free[i], 13);
     }
-    for (int i = 0; i < TMETA; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < TMETA; ++i) {
+      mbar_init(&meta_full[i], 1);
+      mbar_init(&meta_free[i], 8);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&o_done[i], 1);
@@ -113,31 +132,15 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
   long long stretch = (total + gridDim.x - 1) / gridDim.x;
   if (stretch < 6) stretch = 6;
   const int worker = blockIdx.x;
-  const long long begin = min(total, stretch * worker), end = min(total, begin + stretch);
+  long long u = min(total, stretch * worker);
+  const long long end = min(total, u + stretch);
   Place pl;
-  if (begin < end) pl = find_place<SH, TTR, KT>(a, pre, begin);
+  if (warp == 13 && u < end) pl = find_place<SH, TTR, KT>(a, pre, u);
   __syncthreads();                         // the prefix sums' room is the query tiles' now
-  long long u = begin;
-  // one step along the line: the stretch of the current item, its key tiles [k0, k1)
-  int k0 = 0, k1 = 0;
-  bool whole = false, heads = false;       // heads: the item begins here
-  long long item_end = 0;
-  auto cut_item = [&]() {
-    item_end = pl.at + pl.units;
-    const int n = pl.t.t1 - pl.t.t0;
-    k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - 2));
-    k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - 2));
-    heads = u == pl.at;
-    whole = heads && end >= item_end;
-  };
-  auto advance = [&]() -> bool {
-    u = min(end, item_end);
-    return u < end && next_place<SH, TTR, KT>(a, pl);
-  };
-  // tiles of the whole line that this block has done: parity and stage of every barrier
-  int done = 0;
-  const bool work = begin < end;
 
+  // ``done``: tiles of the line that a role has behind it; it gives the stage
+  // and phase of every per-tile barrier.  Waits tell a phase only from the one
+  // before it, so a role that has nothing to do in a tile still waits for it.
   if (warp < 8) {
     // ======================================================== softmax
     reg_inc<176>();
@@ -146,75 +149,87 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + TM_S + 128 * t;
     const uint32_t o_at = tmem + lanes + TM_O + 128 * t;
+    int done = 0;
     bool ok = true;
-    for (bool more = work; more && ok; more = advance()) {
-      cut_item();
-      const int rows = pl.s.n * G;
-      const int n = k1 - k0;
-      const int r = pl.tile * TTR + t * TM_ROWS + row;
-      if (pl.tile * TTR + t * TM_ROWS >= rows) {
-        // nothing in this query tile: keep step with the barriers, whose waits
-        // tell one phase from the next only
-        for (int j = 0; ok && j < n; ++j)
-          ok = warp_wait(&s_full[2 * t + ((done + j) & 1)], ((done + j) >> 1) & 1, abort_flag);
-        done += n;
-        if (ok && n > 0) ok = warp_wait(&o_done[2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort_flag);
-        continue;
-      }
-      const bool live = r < rows;
-      const int i = live ? r / G : 0;
-      const int hq = pl.h * G + (live ? r - i * G : 0);
-      const int at = pl.s.len - pl.s.n + i;            // the row's own index
-      const int hi = !live ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
-      const int lo = live && a.window > 0 ? at - a.window + 1 : 0;
+    for (int sg = 0; ok; ++sg) {
+      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      const volatile Stretch& seg = segs[sg & 1];
+      const int flags = seg.flags;
+      if (!(flags & STRETCH_SOME)) break;
+      const int k0 = seg.k0, n = seg.k1 - k0, len_n = seg.len - seg.n, s0 = seg.s0;
+      const int rows = min(TM_ROWS, seg.n * G - seg.tile * TTR - t * TM_ROWS);   // of this query tile
+      const int r0 = seg.tile * TTR + t * TM_ROWS;
+      const int head0 = seg.h * G;
+      const bool live = row < rows;
+      const int i = live ? (r0 + row) / G : 0;
+      const int hi = !live ? 0x7FFFFFFF : a.causal ? len_n + i + 1 : seg.len;
+      const int lo = live && a.window > 0 ? len_n + i - a.window + 1 : 0;
       float m = -INFINITY, l = 0.0f;
-      if (n > 0) {
-        // ------------------------------------------------------ the row's query
-        float x[D];
-        float amax = 0.0f;
-        if (live) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride +
-                                                            (size_t)hq * D);
-          const int32_t* pr = a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes;
-          bool bad = false;
+      if (n > 0 && rows > 0) {
+        // ------------------------------------------------------ queries
+        // a row by L lanes of 16 channels, 128 / L rows at a time
+        constexpr int L = D / 16;
+        const int ql = tid % L;
+        float* rfs = reinterpret_cast<float*>(sm + LY::RF) + t * TM_ROWS;
+        bool bad = false;
+#pragma unroll 2
+        for (int rr = row / L; rr < TM_ROWS; rr += TM_ROWS / L) {
+          const bool on = rr < rows;
+          const int qi = on ? (r0 + rr) / G : 0;
+          const int hq = head0 + (on ? r0 + rr - qi * G : 0);
+          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+          float2 cs[8];
+          if (on) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + qi) * a.q_stride +
+                                                              (size_t)hq * D + ql * 16);
+            w0 = __ldg(src);
+            w1 = __ldg(src + 1);
+            const int32_t* pr = a.q_pos + (size_t)(s0 + qi) * a.pv.n_axes;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) load8_f32<T>(__ldg(src + c), x + 8 * c);
+            for (int k = 0; k < 8; ++k) cs[k] = rope_cs(a.pv, pr, ql * 8 + k, bad);
+          } else {
 #pragma unroll
-          for (int k = 0; k < D / 2; ++k) {
-            const float2 cs = rope_cs(a.pv, pr, k, bad);
-            rope_pair(x[2 * k], x[2 * k + 1], cs.x, cs.y);
+            for (int k = 0; k < 8; ++k) cs[k] = make_float2(0.0f, 0.0f);
           }
-          if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
-        } else {
+          float x[16];
+          load8_f32<T>(w0, x);
+          load8_f32<T>(w1, x + 8);
+          float amax = 0.0f;
 #pragma unroll
-          for (int k = 0; k < D; ++k) x[k] = 0.0f;
-        }
+          for (int k = 0; k < 8; ++k) {
+            rope_pair(x[2 * k], x[2 * k + 1], cs[k].x, cs[k].y);
+            amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+          }
 #pragma unroll
-        for (int k = 0; k < D; ++k) amax = fmaxf(amax, fabsf(x[k]));
-        const int ex = amax > 0.0f ? max(-120, min(120, ilogbf(amax))) : 0;
-        const float down = ldexpf(1.0f, -ex);
-        const float rf = ldexpf(a.scale_log2, ex);
-        uint8_t* qs = sm + LY::Q + t * NQ * LY::QB + row * 128;
+          for (int off = L / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+          const int ex = amax > 0.0f ? max(-120, min(120, ilogbf(amax))) : 0;
+          const float down = ldexpf(1.0f, -ex);
+          if (ql == 0) rfs[rr] = ldexpf(a.scale_log2, ex);
+          uint8_t* dst = sm + LY::Q + t * NQ * LY::QB + (ql >> 2) * (TM_ROWS * 128) + rr * 128;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t w[4], v[4];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[4], v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = x[8 * c + 2 * k] * down, x1 = x[8 * c + 2 * k + 1] * down;
-            w[k] = cvt_f16x2(x0, x1);
-            if constexpr (NQ == 2) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-              v[k] = cvt_f16x2(x0 - f.x, x1 - f.y);
+            for (int k = 0; k < 4; ++k) {
+              const float x0 = x[8 * c + 2 * k] * down, x1 = x[8 * c + 2 * k + 1] * down;
+              w[k] = cvt_f16x2(x0, x1);
+              if constexpr (NQ == 2) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                v[k] = cvt_f16x2(x0 - f.x, x1 - f.y);
+              }
             }
+            uint8_t* at = dst + (((2 * ql + c) & 7) ^ (rr & 7)) * 16;
+            *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (NQ == 2) *reinterpret_cast<uint4*>(at + LY::QB) = make_uint4(v[0], v[1], v[2], v[3]);
           }
-          uint8_t* dst = qs + (c >> 3) * (TM_ROWS * 128) + (((c & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-          if constexpr (NQ == 2) *reinterpret_cast<uint4*>(dst + LY::QB) = make_uint4(v[0], v[1], v[2], v[3]);
         }
+        if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
         // ------------------------------------------------------ key tiles
+        float rf = 0.0f;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int g = done + j;
           if (!warp_wait(&meta_full[g % TMETA], (g / TMETA) & 1, abort_flag) ||
@@ -223,6 +238,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
             break;
           }
           tc_fence_after();
+          if (j == 0) rf = rfs[row];       // written before q_full, which S waited for
           uint32_t xr[KT];
           if constexpr (KT == 128) tmem_ld_32x32b_x128(s_at, xr);
           else tmem_ld_32x32b_x64(s_at, xr);
@@ -238,14 +254,14 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
           float my = -INFINITY;
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
-            const float4 mt = meta[q];
+            const float2 mt = *reinterpret_cast<const float2*>(meta + q);
             // never 0, so that a masked score stays -inf
             f[q] = fmaxf(rf * mt.x, 0x1p-100f);
             float* sq = s + 16 * q;
             const float a0 = max3f(sq[0], sq[1], sq[2]), a1 = max3f(sq[3], sq[4], sq[5]);
             const float a2 = max3f(sq[6], sq[7], sq[8]), a3 = max3f(sq[9], sq[10], sq[11]);
             const float a4 = max3f(sq[12], sq[13], fmaxf(sq[14], sq[15]));
-            my = fmaxf(my, fmaf(fmaxf(max3f(a0, a1, a2), fmaxf(a3, a4)), f[q], mt.y));
+            my = fmaxf(my, fmaf(max3f(max3f(a0, a1, a2), a3, a4), f[q], mt.y));
           }
           if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
             const float mn = my > m + kRaise ? my : m;
@@ -253,6 +269,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
             m = mn;
             l *= al;
             if (j > 0) {
+              // QK of this tile was issued after the PV before it, so that one is done
               if (!warp_wait(&o_done[2 * t + ((g - 1) & 1)], ((g - 1) >> 1) & 1, abort_flag)) {
                 ok = false;
                 break;
@@ -292,46 +309,60 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t]);
+          if (lane == 0) {
+            mbar_arrive(&p_full[t]);
+            mbar_arrive(&meta_free[g % TMETA]);
+          }
         }
-        if (ok && !warp_wait(&o_done[2 * t + ((done + n - 1) & 1)], ((done + n - 1) >> 1) & 1, abort_flag)) ok = false;
-        if (!ok) break;
-        tc_fence_after();
+      } else {
+        for (int j = 0; ok && j < n; ++j) {
+          const int g = done + j;
+          ok = warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag);
+          if (lane == 0) mbar_arrive(&meta_free[g % TMETA]);
+        }
       }
       done += n;
+      if (ok && n > 0) ok = warp_wait(&o_done[2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
       // -------------------------------------------------------- results
-      const size_t at_row = (size_t)(2 * worker + (heads ? 1 : 0)) * TTR + t * TM_ROWS + row;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      T* dst = static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride + (size_t)hq * D;
-      if (!whole && live) a.tiles.ml[at_row] = make_float2(m, l);
-      if (whole || n > 0) {
+      if (rows > 0) {
+        const bool whole = flags & STRETCH_WHOLE;
+        const size_t at_row = (size_t)(2 * worker + (flags & STRETCH_HEAD ? 1 : 0)) * TTR + t * TM_ROWS + row;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        T* dst = static_cast<T*>(a.out) + (s0 + i) * a.out_stride + (size_t)(head0 + (live ? r0 + row - i * G : 0)) * D;
+        if (!whole && live) a.tiles.ml[at_row] = make_float2(m, l);
+        if (whole || n > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld_32x32b_x32(o_at + c, o);
-          } else {
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld_32x32b_x32(o_at + c, o);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0u;
-          }
-          if (live && whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<T>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
-          } else if (live) {
+            if (live && whole) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(a.tiles.o + at_row * D + c + 4 * k) =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack2<T>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                *reinterpret_cast<uint4*>(dst + c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else if (live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(a.tiles.o + at_row * D + c + 4 * k) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
           }
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
   } else if (warp < 12) {
     // ======================================================== K, V
@@ -342,42 +373,28 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
     constexpr int STEP = KT / NT;                        // rows per round of the 128 threads
     const int sl0 = CH == 8 ? 8 * (ct >> 6) + (ct & 7) : 8 * (ct >> 5) + (ct & 7);
     const int ch = (ct >> 3) & (CH - 1);
-    const bool scales = warp == 8 && lane < NG;
-    constexpr int kNone = -0x7FFFFFFF - 1;               // no query sees the key
-    int id[NT], gid = kNone;
-    uint4 kr[NT], vr[NT];
-    float near = 0.0f;
+    const int in_page = a.pv.P - 1;
+    int done = 0;
     bool ok = true;
-    for (bool more = work; more && ok; more = advance()) {
-      cut_item();
-      const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
-      auto page_of = [&](int key) -> int {
-        if (key >= pl.t.hi || key < pl.t.lo) return kNone;
-        return __ldg(tab + (key >> a.pv.p_shift));
-      };
-      auto ids = [&](int k) {
-#pragma unroll
-        for (int it = 0; it < NT; ++it) id[it] = k < k1 ? page_of(k * KT + it * STEP + sl0) : kNone;
-        if (scales) {
-          // a group of 16 keys that any query sees lies in one page
-          const int key = k * KT + lane * 16;
-          gid = k < k1 && key < pl.t.hi && key + 16 > pl.t.lo ? __ldg(tab + (key >> a.pv.p_shift)) : kNone;
-        }
-      };
-      auto load = [&](const uint8_t* codes, int k, uint4 (&reg)[NT]) {
+    uint4 kr[NT], vr[NT];
+    for (int sg = 0; ok; ++sg) {
+      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      const volatile Stretch& seg = segs[sg & 1];
+      if (!(seg.flags & STRETCH_SOME)) break;
+      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi, h = seg.h;
+      // the codes of tile j of the stretch (rows that no query sees: zeros,
+      // whatever the page holds there)
+      auto load = [&](const uint8_t* codes, int j, uint4 (&reg)[NT]) {
+        const int4* meta = reinterpret_cast<const int4*>(sm + LY::META) + ((done + j) % TMETA) * NG;
+        const int key0 = (k0 + j) * KT + sl0;
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
-          const int key = k * KT + it * STEP + sl0;
+          const int key = key0 + it * STEP;
+          const int pg = meta[(it * STEP + sl0) >> 4].w;
           reg[it] = make_uint4(0, 0, 0, 0);
-          if (k < k1 && key < pl.t.hi && key >= pl.t.lo) {
-            int pg = id[it];
-            if (pg < 0 || pg >= a.pv.n_pages) {
-              atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
-              pg = 0;
-            }
-            const size_t at = (((size_t)pg * H + pl.h) << a.pv.p_shift) + (key & (a.pv.P - 1));
-            reg[it] = __ldg(reinterpret_cast<const uint4*>(codes + at * D) + ch);
-          }
+          if (key < hi && key >= lo)
+            reg[it] = __ldg(reinterpret_cast<const uint4*>(codes) +
+                            (size_t)(((pg * H + h) << a.pv.p_shift) + (key & in_page)) * CH + ch);
         }
       };
       auto widen = [&](uint8_t* dst, const uint4 (&reg)[NT]) {
@@ -397,56 +414,19 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
           *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       };
-      float sk = 0.0f, sv = 0.0f;
-      auto load_scales = [&]() {
-        sk = sv = 0.0f;
-        if (scales && gid != kNone) {
-          const int pg = gid < 0 || gid >= a.pv.n_pages ? 0 : gid;
-          sk = __ldg(a.pv.k_scale + (size_t)pg * H + pl.h);
-          sv = __ldg(a.pv.v_scale + (size_t)pg * H + pl.h);
-        }
-      };
-      auto warp_max = [&](float v) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
-        return v;
-      };
-      if (k0 < k1) {
-        near = 0.0f;
-        ids(k0);
-        load(a.pv.k_codes, k0, kr);
-        load(a.pv.v_codes, k0, vr);
-        load_scales();
-        ids(k0 + 1);
+      if (n > 0) {
+        ok = warp_wait(&meta_full[done % TMETA], (done / TMETA) & 1, abort_flag);
+        if (!ok) break;
+        load(a.pv.k_codes, 0, kr);
+        load(a.pv.v_codes, 0, vr);
       }
-      for (int k = k0; k < k1; ++k) {
-        const int g = done + k - k0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int g = done + j;
         const int buf = g & 1;
-        if (warp == 8) {
-          // pages of zero values take a V scale near by
-          float mx = warp_max(sv);
-          if (mx == 0.0f && near == 0.0f) {
-            for (int s = k + 1; mx == 0.0f && s < k1; ++s) {
-              const int key = s * KT + lane * 16;
-              float v = 0.0f;
-              if (lane < NG && key < pl.t.hi && key + 16 > pl.t.lo) {
-                const int pg = __ldg(tab + (key >> a.pv.p_shift));
-                if (pg >= 0 && pg < a.pv.n_pages) v = __ldg(a.pv.v_scale + (size_t)pg * H + pl.h);
-              }
-              mx = warp_max(v);
-            }
-            if (mx == 0.0f) mx = 1.0f;
-          }
-          if (mx > 0.0f) near = mx;
-          if (lane < NG) {
-            const float v = sv > 0.0f ? sv : near;
-            reinterpret_cast<float4*>(sm + LY::META)[(g % TMETA) * NG + lane] =
-                make_float4(sk, __log2f(v), 1.0f / v, 0.0f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&meta_full[g % TMETA]);
-        }
-        if (g >= 2 && !warp_wait(&s_full[2 + buf], ((g - 2) >> 1) & 1, abort_flag)) {
+        const bool next = j + 1 < n;
+        if ((g >= 2 && !warp_wait(&s_full[2 + buf], ((g - 2) >> 1) & 1, abort_flag)) ||
+            (next && !warp_wait(&meta_full[(g + 1) % TMETA], ((g + 1) / TMETA) & 1, abort_flag))) {
           ok = false;
           break;
         }
@@ -454,7 +434,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kh_full[buf]);
-        load(a.pv.k_codes, k + 1, kr);
+        if (next) load(a.pv.k_codes, j + 1, kr);
         if (g >= 2 && !warp_wait(&o_done[2 + buf], ((g - 2) >> 1) & 1, abort_flag)) {
           ok = false;
           break;
@@ -463,89 +443,195 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&vh_full[buf]);
-        load(a.pv.v_codes, k + 1, vr);
-        load_scales();
-        ids(k + 2);
+        if (next) load(a.pv.v_codes, j + 1, vr);
       }
-      done += k1 - k0;
+      done += n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
   } else {
-    // ======================================================== MMA issue
     reg_dec<56>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
+      // ====================================================== MMA issue
+      // the warp walks together, one lane issues
       constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, TM_ROWS, KT);
       constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, TM_ROWS, D);
       const uint32_t q0 = smem_u32(sm + LY::Q), kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
-      int nq[2] = {0, 0}, np[2] = {0, 0};                // stretches and tiles of each query tile so far
-      auto qk = [&](int t, int g) {
-#pragma unroll
-        for (int part = 0; part < NQ; ++part)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ss(tmem + TM_S + 128 * t,
-                       make_sdesc_sw128(q0 + (t * NQ + part) * LY::QB + (kk >> 2) * (TM_ROWS * 128) + (kk & 3) * 32, 16, 1024),
-                       make_sdesc_sw128(kh0 + (g & 1) * LY::KB + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
-                       idesc_qk, part > 0 || kk > 0 ? 1u : 0u);
+      const bool issuer = lane == 0;
+      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;       // stretches and tiles of each query tile so far
+      int done = 0;
+      // 64 channels (a column block of 128-byte rows) per step of the loop
+      auto qk = [&](uint32_t q, uint32_t kh, uint32_t s) {
+#pragma unroll 1
+        for (int c = 0; c < NQ * (D / 64); ++c) {
+          const int block = c & (D / 64 - 1), part = c / (D / 64);
+          mma4_f16_ss(s, make_sdesc_sw128(q + part * LY::QB + block * (TM_ROWS * 128), 16, 1024),
+                      make_sdesc_sw128(kh + block * (KT * 128), 16, 1024), idesc_qk, c);
+        }
+      };
+      // 64 keys per step
+      auto pv = [&](uint32_t o, uint32_t p, uint32_t vh, bool first) {
+#pragma unroll 1
+        for (int c = 0; c < KT / 64; ++c)
+          mma4_f16_ts(o, p + c * 32, make_sdesc_sw128(vh + c * 64 * 128, KT * 128, 1024), idesc_pv, first ? c : 1);
       };
       bool ok = true;
-      for (bool more = work; more && ok; more = advance()) {
-        cut_item();
-        const int n = k1 - k0;
-        if (n <= 0) continue;
-        const bool two = pl.s.n * G - pl.tile * TTR > TM_ROWS;
-        ok = mbar_wait(&q_full[0], nq[0]++ & 1, abort_flag) && (!two || mbar_wait(&q_full[1], nq[1]++ & 1, abort_flag)) &&
-             mbar_wait(&kh_full[done & 1], (done >> 1) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        qk(0, done);
-        mma_commit(&s_full[0 + (done & 1)]);
-        if (two) qk(1, done);
-        mma_commit(&s_full[2 + (done & 1)]);
-        for (int j = 0; j < n && ok; ++j) {
+      for (int sg = 0; ok; ++sg) {
+        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile Stretch& seg = segs[sg & 1];
+        if (!(seg.flags & STRETCH_SOME)) break;
+        const int n = seg.k1 - seg.k0;
+        const bool two = seg.n * G - seg.tile * TTR > TM_ROWS;
+        if (n > 0) {
+          ok = warp_wait(&q_full[0], nq0++ & 1, abort_flag) && (!two || warp_wait(&q_full[1], nq1++ & 1, abort_flag)) &&
+               warp_wait(&kh_full[done & 1], (done >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (issuer) {
+            const uint32_t kh = kh0 + (done & 1) * LY::KB;
+            qk(q0, kh, tmem + TM_S);
+            mma_commit(&s_full[done & 1]);
+            if (two) qk(q0 + NQ * LY::QB, kh, tmem + TM_S + 128);
+            mma_commit(&s_full[2 + (done & 1)]);
+          }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
           const int g = done + j;
-          for (int t = 0; t < 2; ++t) {
-            const bool on = t == 0 || two;
-            if (on) {
-              ok = mbar_wait(&p_full[t], np[t]++ & 1, abort_flag) &&
-                   (t == 1 || mbar_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < KT / 16; ++kk)
-                mma_f16_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + kk * 8,
-                           make_sdesc_sw128(vh0 + (g & 1) * LY::KB + kk * 16 * 128, KT * 128, 1024), idesc_pv,
-                           j > 0 || kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&o_done[2 * t + (g & 1)]);
-            if (j + 1 < n) {
-              if (t == 0) {
-                ok = mbar_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              if (on) qk(t, g + 1);
-              mma_commit(&s_full[2 * t + ((g + 1) & 1)]);
+          const uint32_t vh = vh0 + (g & 1) * LY::KB, kh = kh0 + ((g + 1) & 1) * LY::KB;
+          const bool next = j + 1 < n;
+          ok = warp_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag) &&
+               (!next || warp_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag)) &&
+               warp_wait(&p_full[0], np0++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (issuer) {
+            pv(tmem + TM_O, tmem + TM_S, vh, j == 0);
+            mma_commit(&o_done[g & 1]);
+            if (next) {
+              qk(q0, kh, tmem + TM_S);
+              mma_commit(&s_full[(g + 1) & 1]);
             }
           }
+          __syncwarp();
+          if (two) {
+            ok = warp_wait(&p_full[1], np1++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (issuer) {
+            if (two) pv(tmem + TM_O + 128, tmem + TM_S + 128, vh, j == 0);
+            mma_commit(&o_done[2 + (g & 1)]);
+            if (next) {
+              if (two) qk(q0 + NQ * LY::QB, kh, tmem + TM_S + 128);
+              mma_commit(&s_full[2 + ((g + 1) & 1)]);
+            }
+          }
+          __syncwarp();
         }
         done += n;
+        if (issuer) mbar_arrive(&seg_free[sg & 1]);
       }
       // every MMA issued so far is done before the block releases its tensor memory
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr, 100000000ull);
+      if (issuer) {
+        mma_commit(drain);
+        mbar_wait(drain, 0, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ====================================================== the line of work
+      PieceRec rec = {-1, 0, 0, 0};
+      int done = 0, sg = 0;
+      bool ok = true;
+      for (bool more = u < end; ok; ++sg) {
+        if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+        int k0 = 0, k1 = 0;
+        long long item_end = 0;
+        if (more) {
+          item_end = pl.at + pl.units;
+          const int n = pl.t.t1 - pl.t.t0;
+          k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - 2));
+          k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - 2));
+        }
+        if (lane == 0) {
+          volatile Stretch& seg = segs[sg & 1];
+          if (more) {
+            const bool head = u == pl.at;
+            seg.b = pl.b;
+            seg.h = pl.h;
+            seg.tile = pl.tile;
+            seg.s0 = pl.s.s0;
+            seg.n = pl.s.n;
+            seg.len = pl.s.len;
+            seg.lo = pl.t.lo;
+            seg.hi = pl.t.hi;
+            seg.k0 = k0;
+            seg.k1 = k1;
+            seg.flags = STRETCH_SOME | (head ? STRETCH_HEAD : 0) | (head && end >= item_end ? STRETCH_WHOLE : 0);
+          } else {
+            seg.flags = 0;
+          }
+          mbar_arrive(&seg_full[sg & 1]);
+        }
+        __syncwarp();
+        if (!more) break;
+        // page ids and scales of its tiles: lane i the keys 16 i .. 16 i + 15,
+        // which lie in one page.  Pages of zero values take a V scale near by.
+        const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
+        float near = 0.0f;
+        auto group = [&](int k, int& pg, float& sv) {
+          const int key = k * KT + lane * 16;
+          pg = kNone;
+          sv = 0.0f;
+          if (lane < NG && k < k1 && key < pl.t.hi && key + 16 > pl.t.lo) {
+            pg = __ldg(tab + (key >> a.pv.p_shift));
+            if (pg < 0 || pg >= a.pv.n_pages) {
+              atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
+              pg = 0;
+            }
+            sv = __ldg(a.pv.v_scale + (size_t)pg * H + pl.h);
+          }
+          float mx = sv;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+          return mx;
+        };
+        for (int k = k0; k < k1; ++k) {
+          const int g = done + k - k0;
+          int pg;
+          float sv;
+          float mx = group(k, pg, sv);
+          const float sk = pg != kNone ? __ldg(a.pv.k_scale + (size_t)pg * H + pl.h) : 0.0f;
+          if (mx == 0.0f && near == 0.0f) {
+            int unused;
+            float v;
+            for (int s = k + 1; mx == 0.0f && s < k1; ++s) mx = group(s, unused, v);
+            if (mx == 0.0f) mx = 1.0f;
+          }
+          if (mx > 0.0f) near = mx;
+          if (g >= TMETA && !warp_wait(&meta_free[g % TMETA], ((g - TMETA) / TMETA) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane < NG) {
+            const float v = sv > 0.0f ? sv : near;
+            reinterpret_cast<float4*>(sm + LY::META)[(g % TMETA) * NG + lane] =
+                make_float4(sk, __log2f(v), 1.0f / v, __int_as_float(pg));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&meta_full[g % TMETA]);
+        }
+        done += k1 - k0;
+        if (u == pl.at && end < item_end) rec = {pl.b, pl.h, pl.tile, (int)((item_end - 1) / stretch)};
+        u = min(end, item_end);
+        more = u < end && next_place<SH, TTR, KT>(a, pl);
+      }
+      if (lane == 0) a.tiles.rec[worker] = rec;
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    // the item that this block began and did not end
-    PieceRec rec = {-1, 0, 0, 0};
-    if (work) {
-      // replay of the last step: warp 0 has walked the line to its end
-      if (item_end > end && heads) rec = {pl.b, pl.h, pl.tile, (int)((item_end - 1) / stretch)};
-    }
-    a.tiles.rec[worker] = rec;
-    if (*abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
-  }
+  if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
