@@ -100,7 +100,8 @@ cudaError_t prepare_paged_tiles(int D);
 // the kernel of few rows, and the kernel of many; ``blocks`` of either share its work
 cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                               cudaStream_t st);
-cudaError_t launch_paged_tiles(const PagedAttn& a, bool f16, int blocks, cudaStream_t st);
+cudaError_t launch_paged_tiles(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
+                               cudaStream_t st);
 cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int workers, cudaStream_t st);
 // tmK, tmV: the code arrays as [rows][D] u8, box {D, min(P, 32)}
 cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
@@ -137,6 +138,49 @@ __device__ __forceinline__ void pow2_scale(float amax, float& scale, float& inv)
   const int k = (int)(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
   scale = __uint_as_float((uint32_t)(k + 127) << 23);
   inv = __uint_as_float((uint32_t)(127 - k) << 23);
+}
+
+// The eight RoPE pairs p0 .. p0 + 7 that one thread rotates for many tokens.
+// Where they lie in one axis at an even place (axes of a multiple of 16
+// channels), a token's (cos, sin) are four 16-byte loads at one table row;
+// else eight single ones.
+struct RopeLane {
+  const float2* row0;   // null: the pairs span axes, or start at an odd place
+  int axis, stride, pos_min, last, p0;
+};
+
+__device__ __forceinline__ RopeLane rope_lane(const PagedView& pv, int p0) {
+  RopeLane r;
+  r.p0 = p0;
+  r.axis = 0;
+  if (pv.n_axes > 1 && p0 >= pv.pair_off[1]) r.axis = 1;
+  if (pv.n_axes > 2 && p0 >= pv.pair_off[2]) r.axis = 2;
+  const int j0 = p0 - pv.pair_off[r.axis];
+  r.stride = pv.axis_pairs[r.axis];
+  r.pos_min = pv.pos_min[r.axis];
+  r.last = pv.pos_count[r.axis] - 1;
+  r.row0 = j0 + 8 <= r.stride && ((j0 | r.stride) & 1) == 0 ? pv.rope[r.axis] + j0 : nullptr;
+  return r;
+}
+
+// (cos, sin) of the lane's pairs at the positions pr[0 .. n_axes - 1]
+__device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, float2 (&cs)[8],
+                                          bool& bad) {
+  if (r.row0) {
+    const int idx = __ldg(pr + r.axis) - r.pos_min;
+    const int at = max(0, min(idx, r.last));
+    bad = bad || at != idx;
+    const float4* t = reinterpret_cast<const float4*>(r.row0 + (size_t)at * r.stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = __ldg(t + k);
+      cs[2 * k] = make_float2(v.x, v.y);
+      cs[2 * k + 1] = make_float2(v.z, v.w);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cs[k] = rope_cs(pv, pr, r.p0 + k, bad);
+  }
 }
 
 // 8 halfs (one uint4) -> 8 fp32 (exact); T picks the 16-bit type.

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedView pv, PagedBa
   float x[PASS][16];
   float amax = 0.0f;
   bool bad = false;
+  const RopeLane rl = rope_lane(pv, lane * 8);
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int r = p * ROWS + row;
@@ -87,12 +88,10 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedView pv, PagedBa
       load8_f32<T>(a0, x[p]);
       load8_f32<T>(a1, x[p] + 8);
       if (!is_v) {
-        const int32_t* pr = pos + (size_t)tok * pv.n_axes;
+        float2 cs[8];
+        rope_load(pv, rl, pos + (size_t)tok * pv.n_axes, cs, bad);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const float2 cs = rope_cs(pv, pr, lane * 8 + m, bad);
-          rope_pair(x[p][2 * m], x[p][2 * m + 1], cs.x, cs.y);
-        }
+        for (int m = 0; m < 8; ++m) rope_pair(x[p][2 * m], x[p][2 * m + 1], cs[m].x, cs[m].y);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[p][i]));

@@ -155,7 +155,7 @@ cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, cons
   const int few = f16 ? kRowsMax<__half> : kRowsMax<__nv_bfloat16>;
   const bool many = (long long)a.max_new * a.pv.G > few;
   cudaError_t e = launch_paged_rows(a, tmK, tmV, f16, blocks, st);
-  if (e == cudaSuccess && many) e = launch_paged_tiles(a, f16, blocks, st);
+  if (e == cudaSuccess && many) e = launch_paged_tiles(a, tmK, tmV, f16, blocks, st);
   if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks * kRowsWarps, st);
   if (e == cudaSuccess && many) e = launch_paged_join(a, true, f16, blocks, st);
   return e;

@@ -139,12 +139,10 @@ __global__ void __launch_bounds__(RTHREADS, 1)
           load8_f32<T>(w0, x + c * 16);
           load8_f32<T>(w1, x + c * 16 + 8);
           if (live) {
-            const int32_t* pr = a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes;
+            float2 cs[8];
+            rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, cs, bad);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const float2 cs = rope_cs(a.pv, pr, c * 32 + t4 * 8 + m, bad);
-              rope_pair(x[c * 16 + 2 * m], x[c * 16 + 2 * m + 1], cs.x, cs.y);
-            }
+            for (int m = 0; m < 8; ++m) rope_pair(x[c * 16 + 2 * m], x[c * 16 + 2 * m + 1], cs[m].x, cs[m].y);
           }
         }
         if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);

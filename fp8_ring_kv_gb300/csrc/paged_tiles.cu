@@ -22,11 +22,13 @@
 // Warp roles (512 threads, registers moved from the last two groups to the softmax):
 //   warps 0-3, 4-7   softmax of query tile 0, 1: one row per thread.  They also
 //                    load and rotate the rows' queries and write the output
-//   warps 8-11       K and V: the codes of the next tile into registers, the
-//                    current ones widened into shared memory
+//   warps 8-11       K and V codes widened to fp16, shared memory to shared memory
 //   warp 12          MMA issue
 //   warp 13          the line of work: the stretches of items for the others,
 //                    and per tile the page ids and scales, up to TMETA tiles ahead
+//   warp 14          TMA: the codes of a tile, page by page
+// The softmax takes a tile in chunks of 32 keys and hands P over in halves, so
+// that PV starts while the second half's exponentials run.
 // MMAs run in the order they are issued: QK of the next tile may overwrite
 // the P that the PV before it reads.
 #include "paged_sched.cuh"
@@ -57,27 +59,38 @@ struct TilesLayout {
   static constexpr int Q = 0;                                    // [2 tiles][NQ]
   static constexpr int KH = Q + 2 * NQ * QB;                     // [2]
   static constexpr int VH = KH + 2 * KB;                         // [2]
-  static constexpr int META = VH + 2 * KB;                       // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, page}
+  static constexpr int RAW = VH + 2 * KB;                        // K codes, V codes of one tile
+  static constexpr int META = RAW + 2 * KT * D;                  // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, page}
   static constexpr int RF = META + TMETA * (KT / 16) * 16;       // [256] logit factor of a row
   static constexpr int SEG = RF + TTR * 4;                       // [2] Stretch
   static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
-  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 4 + 4 + 2 + 4 + 1;
+  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 4 + 4 + 4 + 2 + 4 + 4 + 1;
   static constexpr int SUMS = BAR + NBAR * 8;
   static constexpr int MISC = SUMS + 16 * 8;
-  static constexpr int ALLOC = MISC + 16 + 1024;
+  static constexpr int ALLOC = MISC + 16;                        // the block's shared memory starts 1024-byte aligned
   static_assert(ALLOC <= 232448, "shared memory of a block");
   static_assert(KH >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the query tiles at first");
 };
 
+// byte offset of 16-byte chunk c of code row r as TMA left it (128- or 64-byte swizzle)
+template <int D>
+__device__ __forceinline__ int raw_chunk(int r, int c) {
+  if constexpr (D == 128)
+    return r * 128 + ((c ^ (r & 7)) << 4);
+  else
+    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const __grid_constant__ PagedAttn a) {
+__global__ void __launch_bounds__(TTHREADS, 1)
+    paged_attend_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                              const __grid_constant__ PagedAttn a) {
   using LY = TilesLayout<D, T>;
   constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16;
   using SH = Share<TTR, KT, 2, kRowsMax<T>, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr int kNone = -1;                // page of a group of keys that no query sees
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
   uint64_t* q_full = bars;                 // [2] query tile written (once per stretch)
   uint64_t* kh_full = q_full + 2;          // [2] K tile widened
@@ -86,8 +99,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
   uint64_t* meta_free = meta_full + TMETA; // [TMETA] the tile's softmax is done
   uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][2] QK done; of tile 1: both, and the K tile is free
   uint64_t* o_done = s_full + 4;           // [2][2] PV done; of tile 1: both, and the V tile is free
-  uint64_t* p_full = o_done + 4;           // [2] P stored
-  uint64_t* seg_full = p_full + 2;         // [2] stretch written
+  uint64_t* p_full = o_done + 4;           // [2 query tiles][2] a half of P stored
+  uint64_t* half_done = p_full + 4;        // [2] PV of the first half done
+  uint64_t* raw_full = half_done + 2;      // [2] K codes, V codes landed
+  uint64_t* raw_free = raw_full + 2;       // [2] and read
+  uint64_t* seg_full = raw_free + 2;       // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2] every role is done with it
   uint64_t* drain = seg_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
@@ -99,9 +115,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
       mbar_init(&q_full[i], 4);
       mbar_init(&kh_full[i], 4);
       mbar_init(&vh_full[i], 4);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&half_done[i], 1);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_free[i], 4);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], 13);
+      mbar_init(&seg_free[i], 14);
     }
     for (int i = 0; i < TMETA; ++i) {
       mbar_init(&meta_full[i], 1);
@@ -110,6 +128,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&o_done[i], 1);
+      mbar_init(&p_full[i], 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -118,6 +137,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
   if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+  }
+  if (warp == 14 && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   __syncthreads();
   tc_fence_after();
@@ -149,7 +172,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + TM_S + 128 * t;
     const uint32_t o_at = tmem + lanes + TM_O + 128 * t;
-    int done = 0;
+    int done = 0, tiles = 0;               // tiles: those of this query tile, of P's barriers
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -171,26 +194,18 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
         constexpr int L = D / 16;
         const int ql = tid % L;
         float* rfs = reinterpret_cast<float*>(sm + LY::RF) + t * TM_ROWS;
+        const RopeLane rl = rope_lane(a.pv, ql * 8);
         bool bad = false;
-#pragma unroll 2
+#pragma unroll 4
         for (int rr = row / L; rr < TM_ROWS; rr += TM_ROWS / L) {
-          const bool on = rr < rows;
-          const int qi = on ? (r0 + rr) / G : 0;
-          const int hq = head0 + (on ? r0 + rr - qi * G : 0);
-          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+          // rows past the last repeat it: their S and O are never looked at
+          const int rq = r0 + min(rr, rows - 1);
+          const int qi = rq / G;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + qi) * a.q_stride +
+                                                            (size_t)(head0 + rq - qi * G) * D + ql * 16);
+          const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
           float2 cs[8];
-          if (on) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + qi) * a.q_stride +
-                                                              (size_t)hq * D + ql * 16);
-            w0 = __ldg(src);
-            w1 = __ldg(src + 1);
-            const int32_t* pr = a.q_pos + (size_t)(s0 + qi) * a.pv.n_axes;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) cs[k] = rope_cs(a.pv, pr, ql * 8 + k, bad);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) cs[k] = make_float2(0.0f, 0.0f);
-          }
+          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + qi) * a.pv.n_axes, cs, bad);
           float x[16];
           load8_f32<T>(w0, x);
           load8_f32<T>(w1, x + 8);
@@ -229,90 +244,117 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
         if (lane == 0) mbar_arrive(&q_full[t]);
         // ------------------------------------------------------ key tiles
         float rf = 0.0f;
+        constexpr int NC = KT / 32;                      // chunks of 32 keys
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < n; ++j, ++tiles) {
           const int g = done + j;
-          if (!warp_wait(&meta_full[g % TMETA], (g / TMETA) & 1, abort_flag) ||
-              !warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag)) {
+          if (!warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          uint32_t xa[32], xb[32];
+          tmem_ld_32x32b_x32_start(s_at, xa);
           if (j == 0) rf = rfs[row];       // written before q_full, which S waited for
-          uint32_t xr[KT];
-          if constexpr (KT == 128) tmem_ld_32x32b_x128(s_at, xr);
-          else tmem_ld_32x32b_x64(s_at, xr);
-          float* s = reinterpret_cast<float*>(xr);
           const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + (g % TMETA) * NG;
           const int key0 = (k0 + j) * KT;
-          if (__any_sync(0xFFFFFFFFu, key0 + KT > hi || key0 < lo)) {
+          const bool cut = __any_sync(0xFFFFFFFFu, key0 + KT > hi || key0 < lo);
+          // one chunk of S (loaded) to P
+          auto chunk = [&](uint32_t (&xr)[32], int c) {
+            float* s = reinterpret_cast<float*>(xr);
+            if (cut) {
 #pragma unroll
-            for (int c = 0; c < KT; ++c)
-              if (key0 + c >= hi || key0 + c < lo) s[c] = -INFINITY;
-          }
-          float f[NG];
-          float my = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < NG; ++q) {
-            const float2 mt = *reinterpret_cast<const float2*>(meta + q);
+              for (int k = 0; k < 32; ++k)
+                if (key0 + 32 * c + k >= hi || key0 + 32 * c + k < lo) s[k] = -INFINITY;
+            }
+            const float4 ma = meta[2 * c], mb = meta[2 * c + 1];
             // never 0, so that a masked score stays -inf
-            f[q] = fmaxf(rf * mt.x, 0x1p-100f);
-            float* sq = s + 16 * q;
-            const float a0 = max3f(sq[0], sq[1], sq[2]), a1 = max3f(sq[3], sq[4], sq[5]);
-            const float a2 = max3f(sq[6], sq[7], sq[8]), a3 = max3f(sq[9], sq[10], sq[11]);
-            const float a4 = max3f(sq[12], sq[13], fmaxf(sq[14], sq[15]));
-            my = fmaxf(my, fmaf(max3f(max3f(a0, a1, a2), a3, a4), f[q], mt.y));
-          }
-          if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
-            const float mn = my > m + kRaise ? my : m;
-            const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
-            m = mn;
-            l *= al;
-            if (j > 0) {
-              // QK of this tile was issued after the PV before it, so that one is done
-              if (!warp_wait(&o_done[2 * t + ((g - 1) & 1)], ((g - 1) >> 1) & 1, abort_flag)) {
-                ok = false;
-                break;
+            const float fa = fmaxf(rf * ma.x, 0x1p-100f), fb = fmaxf(rf * mb.x, 0x1p-100f);
+            auto max16 = [](const float* v) {
+              const float a0 = max3f(v[0], v[1], v[2]), a1 = max3f(v[3], v[4], v[5]), a2 = max3f(v[6], v[7], v[8]);
+              const float a3 = max3f(v[9], v[10], v[11]), a4 = max3f(v[12], v[13], fmaxf(v[14], v[15]));
+              return max3f(max3f(a0, a1, a2), a3, a4);
+            };
+            const float my = fmaxf(fmaf(max16(s), fa, ma.y), fmaf(max16(s + 16), fb, mb.y));
+            if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
+              // rare after a row's first keys: what was summed with the old
+              // maximum is brought to the new one
+              const float mn = my > m + kRaise ? my : m;
+              const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
+              m = mn;
+              l *= al;
+              bool scale_o = j > 0;
+              if (2 * c >= NC) {
+                // the first half of this tile may be in O already
+                if (!warp_wait(&half_done[t], tiles & 1, abort_flag)) ok = false;
+                scale_o = true;
               }
-              tc_fence_after();
+              tc_fence_after();            // (QK of this tile was issued after the PV before it, so that one is done)
+              // P of this half
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(o_at + c, o);
+              for (int k = 2 * c >= NC ? NC / 2 : 0; k < c; ++k) {
+                uint32_t p[16];
+                tmem_ld_32x32b_x16(s_at + 16 * k, p);
+                const __half2 f = __float2half2_rn(al);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                tmem_st_32x32b_x16(o_at + c, o);
+                for (int e = 0; e < 16; ++e) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[e]), f);
+                  p[e] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                tmem_st_32x32b_x16(s_at + 16 * k, p);
+              }
+              if (scale_o) {
+#pragma unroll 1
+                for (int k = 0; k < D; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(o_at + k, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                  tmem_st_32x32b_x16(o_at + k, o);
+                }
               }
             }
-          }
-          const float sub = m == -INFINITY ? 0.0f : kTop - m;
-#pragma unroll
-          for (int q = 0; q < NG; q += 2) {
+            const float sub = m == -INFINITY ? 0.0f : kTop - m;
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float4 mt = meta[q + e];
-              const float2 ff = make_float2(f[q + e], f[q + e]), ad = make_float2(mt.y + sub, mt.y + sub);
+              const float f1 = e ? fb : fa, a1 = (e ? mb.y : ma.y) + sub;
+              const float2 ff = make_float2(f1, f1), ad = make_float2(a1, a1);
               float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                float2 y = fma2(make_float2(s[16 * (q + e) + 2 * c], s[16 * (q + e) + 2 * c + 1]), ff, ad);
+              for (int k = 0; k < 8; ++k) {
+                float2 y = fma2(make_float2(s[16 * e + 2 * k], s[16 * e + 2 * k + 1]), ff, ad);
                 y.x = ex2f(y.x);
                 y.y = ex2f(y.y);
                 sum = add2(sum, y);
-                p[8 * e + c] = cvt_f16x2(y.x, y.y);
+                p[8 * e + k] = cvt_f16x2(y.x, y.y);
               }
-              l = fmaf(sum.x + sum.y, mt.z, l);
+              l = fmaf(sum.x + sum.y, e ? mb.z : ma.z, l);
             }
-            tmem_st_32x32b_x16(s_at + 8 * q, p);
+            tmem_st_32x32b_x16(s_at + 16 * c, p);
+          };
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 2) {
+            tmem_ld_wait(xa);
+            tmem_ld_32x32b_x32_start(s_at + 32 * (c + 1), xb);
+            chunk(xa, c);
+            const bool half = NC == 2;     // this chunk ends a half
+            if (half) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[2 * t]);
+            }
+            tmem_ld_wait(xb);
+            if (c + 2 < NC) tmem_ld_32x32b_x32_start(s_at + 32 * (c + 2), xa);
+            chunk(xb, c + 1);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + (half || c > 0 ? 1 : 0)]);
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&p_full[t]);
-            mbar_arrive(&meta_free[g % TMETA]);
-          }
+          if (lane == 0) mbar_arrive(&meta_free[g % TMETA]);
+          if (!ok) break;
         }
       } else {
         for (int j = 0; ok && j < n; ++j) {
@@ -373,80 +415,65 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
     constexpr int STEP = KT / NT;                        // rows per round of the 128 threads
     const int sl0 = CH == 8 ? 8 * (ct >> 6) + (ct & 7) : 8 * (ct >> 5) + (ct & 7);
     const int ch = (ct >> 3) & (CH - 1);
-    const int in_page = a.pv.P - 1;
     int done = 0;
     bool ok = true;
-    uint4 kr[NT], vr[NT];
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile Stretch& seg = segs[sg & 1];
       if (!(seg.flags & STRETCH_SOME)) break;
-      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi, h = seg.h;
-      // the codes of tile j of the stretch (rows that no query sees: zeros,
-      // whatever the page holds there)
-      auto load = [&](const uint8_t* codes, int j, uint4 (&reg)[NT]) {
-        const int4* meta = reinterpret_cast<const int4*>(sm + LY::META) + ((done + j) % TMETA) * NG;
-        const int key0 = (k0 + j) * KT + sl0;
-#pragma unroll
-        for (int it = 0; it < NT; ++it) {
-          const int key = key0 + it * STEP;
-          const int pg = meta[(it * STEP + sl0) >> 4].w;
-          reg[it] = make_uint4(0, 0, 0, 0);
-          if (key < hi && key >= lo)
-            reg[it] = __ldg(reinterpret_cast<const uint4*>(codes) +
-                            (size_t)(((pg * H + h) << a.pv.p_shift) + (key & in_page)) * CH + ch);
-        }
-      };
-      auto widen = [&](uint8_t* dst, const uint4 (&reg)[NT]) {
-#pragma unroll
-        for (int it = 0; it < NT; ++it) {
-          const int sl = it * STEP + sl0;
-          uint32_t w[8];
-          const uint32_t c[4] = {reg[it].x, reg[it].y, reg[it].z, reg[it].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[2 * e] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] & 0xFFFFu));
-            w[2 * e + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] >> 16));
-          }
-          uint8_t* at = dst + (ch >> 2) * (KT * 128) + sl * 128;
-          const int cc = (2 * ch) & 7;
-          *reinterpret_cast<uint4*>(at + ((cc ^ (sl & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      };
-      if (n > 0) {
-        ok = warp_wait(&meta_full[done % TMETA], (done / TMETA) & 1, abort_flag);
-        if (!ok) break;
-        load(a.pv.k_codes, 0, kr);
-        load(a.pv.v_codes, 0, vr);
-      }
+      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n && ok; ++j) {
         const int g = done + j;
         const int buf = g & 1;
-        const bool next = j + 1 < n;
-        if ((g >= 2 && !warp_wait(&s_full[2 + buf], ((g - 2) >> 1) & 1, abort_flag)) ||
-            (next && !warp_wait(&meta_full[(g + 1) % TMETA], ((g + 1) / TMETA) & 1, abort_flag))) {
-          ok = false;
-          break;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {                    // K, then V
+          if (!warp_wait(&raw_full[v], g & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* src = sm + LY::RAW + v * KT * D;
+          uint4 reg[NT];
+#pragma unroll
+          for (int it = 0; it < NT; ++it) reg[it] = *reinterpret_cast<const uint4*>(src + raw_chunk<D>(it * STEP + sl0, ch));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_free[v]);
+          const int key0 = (k0 + j) * KT;
+          if (v && (key0 + KT > hi || key0 < lo)) {
+            // values that no query sees: zeros, whatever their page holds (a
+            // NaN code too); their scores are masked
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+              const int key = key0 + it * STEP + sl0;
+              if (key >= hi || key < lo) reg[it] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (g >= 2 && !warp_wait((v ? o_done : s_full) + 2 + buf, ((g - 2) >> 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = sm + (v ? LY::VH : LY::KH) + buf * LY::KB + (ch >> 2) * (KT * 128);
+          const int cc = (2 * ch) & 7;
+#pragma unroll
+          for (int it = 0; it < NT; ++it) {
+            const int sl = it * STEP + sl0;
+            uint32_t w[8];
+            const uint32_t c[4] = {reg[it].x, reg[it].y, reg[it].z, reg[it].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[2 * e] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] & 0xFFFFu));
+              w[2 * e + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] >> 16));
+            }
+            uint8_t* at = dst + sl * 128;
+            *reinterpret_cast<uint4*>(at + ((cc ^ (sl & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive((v ? vh_full : kh_full) + buf);
         }
-        widen(sm + LY::KH + buf * LY::KB, kr);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kh_full[buf]);
-        if (next) load(a.pv.k_codes, j + 1, kr);
-        if (g >= 2 && !warp_wait(&o_done[2 + buf], ((g - 2) >> 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        widen(sm + LY::VH + buf * LY::KB, vr);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&vh_full[buf]);
-        if (next) load(a.pv.v_codes, j + 1, vr);
       }
       done += n;
-      __syncwarp();
       if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
   } else {
@@ -469,11 +496,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
                       make_sdesc_sw128(kh + block * (KT * 128), 16, 1024), idesc_qk, c);
         }
       };
-      // 64 keys per step
-      auto pv = [&](uint32_t o, uint32_t p, uint32_t vh, bool first) {
-#pragma unroll 1
-        for (int c = 0; c < KT / 64; ++c)
-          mma4_f16_ts(o, p + c * 32, make_sdesc_sw128(vh + c * 64 * 128, KT * 128, 1024), idesc_pv, first ? c : 1);
+      // one half of the tile's keys
+      auto pv = [&](uint32_t o, uint32_t p, uint32_t vh, int half, bool first) {
+        const uint64_t b = make_sdesc_sw128(vh + half * (KT / 2) * 128, KT * 128, 1024);
+        if constexpr (KT == 128) mma4_f16_ts(o, p + half * 32, b, idesc_pv, first ? 0 : 1);
+        else mma2_f16_ts(o, p + half * 16, b, idesc_pv, first ? 0 : 1);
       };
       bool ok = true;
       for (int sg = 0; ok; ++sg) {
@@ -502,33 +529,36 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
           const uint32_t vh = vh0 + (g & 1) * LY::KB, kh = kh0 + ((g + 1) & 1) * LY::KB;
           const bool next = j + 1 < n;
           ok = warp_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag) &&
-               (!next || warp_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag)) &&
-               warp_wait(&p_full[0], np0++ & 1, abort_flag);
+               (!next || warp_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag));
+#pragma unroll 1
+          for (int t = 0; t < 2 && ok; ++t) {
+            const uint32_t o = tmem + TM_O + 128 * t, s = tmem + TM_S + 128 * t;
+            const bool on = t == 0 || two;
+            if (on) {
+              const uint32_t ph = (t ? np1++ : np0++) & 1;
+              ok = warp_wait(&p_full[2 * t], ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (issuer) {
+                pv(o, s, vh, 0, j == 0);
+                mma_commit(&half_done[t]);
+              }
+              __syncwarp();
+              ok = warp_wait(&p_full[2 * t + 1], ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (issuer) {
+              if (on) pv(o, s, vh, 1, false);
+              mma_commit(&o_done[2 * t + (g & 1)]);
+              if (next) {
+                if (on) qk(q0 + t * NQ * LY::QB, kh, s);
+                mma_commit(&s_full[2 * t + ((g + 1) & 1)]);
+              }
+            }
+            __syncwarp();
+          }
           if (!ok) break;
-          tc_fence_after();
-          if (issuer) {
-            pv(tmem + TM_O, tmem + TM_S, vh, j == 0);
-            mma_commit(&o_done[g & 1]);
-            if (next) {
-              qk(q0, kh, tmem + TM_S);
-              mma_commit(&s_full[(g + 1) & 1]);
-            }
-          }
-          __syncwarp();
-          if (two) {
-            ok = warp_wait(&p_full[1], np1++ & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (issuer) {
-            if (two) pv(tmem + TM_O + 128, tmem + TM_S + 128, vh, j == 0);
-            mma_commit(&o_done[2 + (g & 1)]);
-            if (next) {
-              if (two) qk(q0 + NQ * LY::QB, kh, tmem + TM_S + 128);
-              mma_commit(&s_full[2 + ((g + 1) & 1)]);
-            }
-          }
-          __syncwarp();
         }
         done += n;
         if (issuer) mbar_arrive(&seg_free[sg & 1]);
@@ -628,6 +658,52 @@ __global__ void __launch_bounds__(TTHREADS, 1) paged_attend_tiles_kernel(const _
         more = u < end && next_place<SH, TTR, KT>(a, pl);
       }
       if (lane == 0) a.tiles.rec[worker] = rec;
+    } else if (warp == 14) {
+      // ====================================================== TMA
+      // lane i a box of the tile: 32 rows of a page (16 where a page has no more)
+      const int rows = a.pv.P < 32 ? a.pv.P : 32;
+      const int boxes = KT / rows;
+      int done = 0, issued = 0;                          // tiles; copies (K, V, K, ...)
+      bool ok = true;
+      for (int sg = 0; ok; ++sg) {
+        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile Stretch& seg = segs[sg & 1];
+        if (!(seg.flags & STRETCH_SOME)) break;
+        const int k0 = seg.k0, n = seg.k1 - k0, h = seg.h;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int g = done + j;
+          ok = warp_wait(&meta_full[g % TMETA], (g / TMETA) & 1, abort_flag);
+          if (!ok) break;
+          int pg = kNone;
+          if (lane < boxes) {
+            const int4* meta = reinterpret_cast<const int4*>(sm + LY::META) + (g % TMETA) * NG;
+            pg = rows == 16 ? meta[lane].w : max(meta[2 * lane].w, meta[2 * lane + 1].w);
+          }
+          const int key = (k0 + j) * KT + lane * rows;
+          const int y = (int)(a.pv.row0 + (((long long)pg * H + h) << a.pv.p_shift)) + (key & (a.pv.P - 1));
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pg != kNone)) * rows * D;
+          for (int v = 0; v < 2; ++v) {
+            if (g >= 1 && !warp_wait(&raw_free[v], (g - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[v], bytes);
+            __syncwarp();
+            if (pg != kNone)
+              tma_load_2d(sm + LY::RAW + v * KT * D + lane * rows * D, v ? &tmV : &tmK, &raw_full[v], 0, y);
+            issued = 2 * g + v + 1;
+          }
+          if (!ok) break;
+        }
+        done += n;
+        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+      }
+      // after an abort: copies still in flight land in this block's shared memory
+      if (*abort_flag && issued > 0) {
+        mbar_wait(&raw_full[0], ((issued - 1) >> 1) & 1, nullptr, 100000000ull);
+        if (issued > 1) mbar_wait(&raw_full[1], ((issued - 2) >> 1) & 1, nullptr, 100000000ull);
+      }
     }
   }
   __syncthreads();
@@ -652,13 +728,17 @@ cudaError_t prepare_paged_tiles(int D) {
 }
 
 template <int D, typename T>
-static cudaError_t tiles_t(const PagedAttn& a, int blocks, cudaStream_t st) {
-  return launch_pdl(paged_attend_tiles_kernel<D, T>, dim3(blocks), dim3(TTHREADS), TilesLayout<D, T>::ALLOC, st, a);
+static cudaError_t tiles_t(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int blocks,
+                           cudaStream_t st) {
+  return launch_pdl(paged_attend_tiles_kernel<D, T>, dim3(blocks), dim3(TTHREADS), TilesLayout<D, T>::ALLOC, st, tmK,
+                    tmV, a);
 }
 
-cudaError_t launch_paged_tiles(const PagedAttn& a, bool f16, int blocks, cudaStream_t st) {
-  if (a.pv.D == 64) return f16 ? tiles_t<64, __half>(a, blocks, st) : tiles_t<64, __nv_bfloat16>(a, blocks, st);
-  return f16 ? tiles_t<128, __half>(a, blocks, st) : tiles_t<128, __nv_bfloat16>(a, blocks, st);
+cudaError_t launch_paged_tiles(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
+                               cudaStream_t st) {
+  if (a.pv.D == 64)
+    return f16 ? tiles_t<64, __half>(a, tmK, tmV, blocks, st) : tiles_t<64, __nv_bfloat16>(a, tmK, tmV, blocks, st);
+  return f16 ? tiles_t<128, __half>(a, tmK, tmV, blocks, st) : tiles_t<128, __nv_bfloat16>(a, tmK, tmV, blocks, st);
 }
 
 }  // namespace kvring_dev
