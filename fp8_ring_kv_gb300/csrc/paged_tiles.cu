@@ -16,21 +16,23 @@
 // beside which the softmax and the widening have to run.  A block works on two
 // tiles of 128 query rows over the same keys, so that each K and V tile is
 // loaded and widened once for 256 rows and the tensor cores work on one tile
-// while the softmax of the other runs.  Tensor memory is full: S (then P) of
-// both tiles and O of both.
+// while the softmax of the other runs.  S goes in steps of 64 keys through two
+// buffers per query tile, so that QK of a step runs while the softmax of the
+// one before it does (with one buffer of 128 keys, every tile was a chain of QK,
+// softmax and PV: 577 us for 512 tokens over 65,512 against XXX).  Tensor
+// memory is full: two S (then P) buffers and O of both query tiles.
 //
 // Warp roles (512 threads, registers moved from the last two groups to the softmax):
 //   warps 0-3, 4-7   softmax of query tile 0, 1: one row per thread.  They also
 //                    load and rotate the rows' queries and write the output
 //   warps 8-11       K and V codes widened to fp16, shared memory to shared memory
-//   warp 12          MMA issue
+//   warps 12, 15     MMA issue for query tile 0, 1
 //   warp 13          the line of work: the stretches of items for the others,
 //                    and per tile the page ids and scales, up to TMETA tiles ahead
 //   warp 14          TMA: the codes of a tile, page by page
-// The softmax takes a tile in chunks of 32 keys and hands P over in halves, so
-// that PV starts while the second half's exponentials run.
-// MMAs run in the order they are issued: QK of the next tile may overwrite
-// the P that the PV before it reads.
+// MMAs of one thread run in the order they are issued: QK may overwrite the P
+// that the PV before it reads.  A query tile has an issuing thread of its own,
+// since a wait costs a thread about as much as an MMA takes.
 #include "paged_sched.cuh"
 #include "launch.h"
 
@@ -40,6 +42,7 @@ constexpr int TM_ROWS = 128;                 // rows of one MMA
 constexpr int TTR = kTilesRows;              // rows of an item: two query tiles
 static_assert(TTR == 2 * TM_ROWS);
 constexpr int TTHREADS = 512;
+constexpr int STEP_KEYS = 64;                // keys of one S buffer
 constexpr int TMETA = 8;                     // stages of page ids and scales
 constexpr float kRaise = 8.0f;               // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kTop = 6.0f;                 // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
@@ -53,7 +56,8 @@ enum : int { STRETCH_SOME = 1, STRETCH_WHOLE = 2, STRETCH_HEAD = 4 };   // else:
 template <int D, typename T>
 struct TilesLayout {
   static constexpr int NQ = std::is_same_v<T, __half> ? 2 : 1;   // fp16 parts of a query
-  static constexpr int KT = NQ == 2 ? 64 : 128;                  // keys per tile
+  static constexpr int KT = NQ == 2 ? 64 : 128;                  // keys per K and V tile
+  static constexpr int SPT = KT / STEP_KEYS;                     // steps of S per tile
   static constexpr int QB = TM_ROWS * D * 2;                     // one part of one query tile
   static constexpr int KB = KT * D * 2;                          // one widened K or V tile
   static constexpr int Q = 0;                                    // [2 tiles][NQ]
@@ -64,7 +68,7 @@ struct TilesLayout {
   static constexpr int RF = META + TMETA * (KT / 16) * 16;       // [256] logit factor of a row
   static constexpr int SEG = RF + TTR * 4;                       // [2] Stretch
   static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
-  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 4 + 4 + 4 + 2 + 4 + 4 + 1;
+  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 8 + 8 + 4 + 4 + 4 + 2;
   static constexpr int SUMS = BAR + NBAR * 8;
   static constexpr int MISC = SUMS + 16 * 8;
   static constexpr int ALLOC = MISC + 16;                        // the block's shared memory starts 1024-byte aligned
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     paged_attend_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                               const __grid_constant__ PagedAttn a) {
   using LY = TilesLayout<D, T>;
-  constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16;
+  constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16, SPT = LY::SPT;
   using SH = Share<TTR, KT, 2, kRowsMax<T>, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr int kNone = -1;                // page of a group of keys that no query sees
@@ -97,15 +101,14 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   uint64_t* vh_full = kh_full + 2;         // [2] V tile widened
   uint64_t* meta_full = vh_full + 2;       // [TMETA] page ids and scales of a tile written
   uint64_t* meta_free = meta_full + TMETA; // [TMETA] the tile's softmax is done
-  uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][2] QK done; of tile 1: both, and the K tile is free
-  uint64_t* o_done = s_full + 4;           // [2][2] PV done; of tile 1: both, and the V tile is free
-  uint64_t* p_full = o_done + 4;           // [2 query tiles][2] a half of P stored
-  uint64_t* half_done = p_full + 4;        // [2] PV of the first half done
-  uint64_t* raw_full = half_done + 2;      // [2] K codes, V codes landed
+  uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][4 steps] QK done
+  uint64_t* pv_done = s_full + 8;          // [2][4] PV done
+  uint64_t* p_full = pv_done + 8;          // [2][2] P stored
+  uint64_t* raw_full = p_full + 4;         // [2] K codes, V codes landed
   uint64_t* raw_free = raw_full + 2;       // [2] and read
   uint64_t* seg_full = raw_free + 2;       // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2] every role is done with it
-  uint64_t* drain = seg_free + 2;
+  uint64_t* drain = seg_free + 2;          // [2] every MMA of an issuing thread done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile Stretch* segs = reinterpret_cast<volatile Stretch*>(sm + LY::SEG);
@@ -115,22 +118,21 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       mbar_init(&q_full[i], 4);
       mbar_init(&kh_full[i], 4);
       mbar_init(&vh_full[i], 4);
-      mbar_init(&half_done[i], 1);
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_free[i], 4);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], 14);
+      mbar_init(&seg_free[i], 15);
+      mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < TMETA; ++i) {
       mbar_init(&meta_full[i], 1);
       mbar_init(&meta_free[i], 8);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&o_done[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -162,8 +164,9 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   __syncthreads();                         // the prefix sums' room is the query tiles' now
 
   // ``done``: tiles of the line that a role has behind it; it gives the stage
-  // and phase of every per-tile barrier.  Waits tell a phase only from the one
-  // before it, so a role that has nothing to do in a tile still waits for it.
+  // and phase of every barrier of a tile or of its steps.  Waits tell a phase
+  // only from the one before it, so a role that has nothing to do in a tile
+  // still waits for it.
   if (warp < 8) {
     // ======================================================== softmax
     reg_inc<176>();
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + TM_S + 128 * t;
     const uint32_t o_at = tmem + lanes + TM_O + 128 * t;
-    int done = 0, tiles = 0;               // tiles: those of this query tile, of P's barriers
+    int done = 0, steps = 0;               // steps: those of this query tile, of P's barriers
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -244,21 +247,22 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         if (lane == 0) mbar_arrive(&q_full[t]);
         // ------------------------------------------------------ key tiles
         float rf = 0.0f;
-        constexpr int NC = KT / 32;                      // chunks of 32 keys
 #pragma unroll 1
-        for (int j = 0; j < n; ++j, ++tiles) {
-          const int g = done + j;
-          if (!warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag)) {
+        for (int j = 0; j < n * SPT; ++j, ++steps) {
+          const int x = done * SPT + j;
+          if (!warp_wait(&s_full[4 * t + (x & 3)], (x >> 2) & 1, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t sb = s_at + 64 * (x & 1);
           uint32_t xa[32], xb[32];
-          tmem_ld_32x32b_x32_start(s_at, xa);
+          tmem_ld_32x32b_x32_start(sb, xa);
           if (j == 0) rf = rfs[row];       // written before q_full, which S waited for
-          const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + (g % TMETA) * NG;
-          const int key0 = (k0 + j) * KT;
-          const bool cut = __any_sync(0xFFFFFFFFu, key0 + KT > hi || key0 < lo);
+          const int stage = (x / SPT) % TMETA;
+          const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + stage * NG + (x % SPT) * 4;
+          const int key0 = k0 * KT + j * STEP_KEYS;
+          const bool cut = __any_sync(0xFFFFFFFFu, key0 + STEP_KEYS > hi || key0 < lo);
           // one chunk of S (loaded) to P
           auto chunk = [&](uint32_t (&xr)[32], int c) {
             float* s = reinterpret_cast<float*>(xr);
@@ -283,27 +287,20 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
               m = mn;
               l *= al;
-              bool scale_o = j > 0;
-              if (2 * c >= NC) {
-                // the first half of this tile may be in O already
-                if (!warp_wait(&half_done[t], tiles & 1, abort_flag)) ok = false;
-                scale_o = true;
-              }
-              tc_fence_after();            // (QK of this tile was issued after the PV before it, so that one is done)
-              // P of this half
-#pragma unroll 1
-              for (int k = 2 * c >= NC ? NC / 2 : 0; k < c; ++k) {
+              if (c == 1) {                // the chunk before it, in P already
                 uint32_t p[16];
-                tmem_ld_32x32b_x16(s_at + 16 * k, p);
+                tmem_ld_32x32b_x16(sb, p);
                 const __half2 f = __float2half2_rn(al);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[e]), f);
                   p[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                tmem_st_32x32b_x16(s_at + 16 * k, p);
+                tmem_st_32x32b_x16(sb, p);
               }
-              if (scale_o) {
+              if (j > 0) {
+                if (!warp_wait(&pv_done[4 * t + ((x - 1) & 3)], ((x - 1) >> 2) & 1, abort_flag)) ok = false;
+                tc_fence_after();
 #pragma unroll 1
                 for (int k = 0; k < D; k += 16) {
                   uint32_t o[16];
@@ -331,40 +328,34 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               }
               l = fmaf(sum.x + sum.y, e ? mb.z : ma.z, l);
             }
-            tmem_st_32x32b_x16(s_at + 16 * c, p);
+            tmem_st_32x32b_x16(sb + 16 * c, p);
           };
-#pragma unroll 1
-          for (int c = 0; c < NC; c += 2) {
-            tmem_ld_wait(xa);
-            tmem_ld_32x32b_x32_start(s_at + 32 * (c + 1), xb);
-            chunk(xa, c);
-            const bool half = NC == 2;     // this chunk ends a half
-            if (half) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&p_full[2 * t]);
-            }
-            tmem_ld_wait(xb);
-            if (c + 2 < NC) tmem_ld_32x32b_x32_start(s_at + 32 * (c + 2), xa);
-            chunk(xb, c + 1);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * t + (half || c > 0 ? 1 : 0)]);
+          tmem_ld_wait(xa);
+          tmem_ld_32x32b_x32_start(sb + 32, xb);
+          chunk(xa, 0);
+          tmem_ld_wait(xb);
+          chunk(xb, 1);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&p_full[2 * t + (steps & 1)]);
+            if (x % SPT == SPT - 1) mbar_arrive(&meta_free[stage]);
           }
-          if (lane == 0) mbar_arrive(&meta_free[g % TMETA]);
           if (!ok) break;
         }
       } else {
-        for (int j = 0; ok && j < n; ++j) {
-          const int g = done + j;
-          ok = warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag);
-          if (lane == 0) mbar_arrive(&meta_free[g % TMETA]);
+        for (int j = 0; ok && j < n * SPT; ++j) {
+          const int x = done * SPT + j;
+          ok = warp_wait(&s_full[4 * t + (x & 3)], (x >> 2) & 1, abort_flag);
+          if (lane == 0 && x % SPT == SPT - 1) mbar_arrive(&meta_free[(x / SPT) % TMETA]);
         }
       }
       done += n;
-      if (ok && n > 0) ok = warp_wait(&o_done[2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort_flag);
+      if (ok && n > 0) {
+        const int x = done * SPT - 1;
+        ok = warp_wait(&pv_done[4 * t + (x & 3)], (x >> 2) & 1, abort_flag);
+      }
       if (!ok) break;
       tc_fence_after();
       // -------------------------------------------------------- results
@@ -448,9 +439,12 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               if (key >= hi || key < lo) reg[it] = make_uint4(0, 0, 0, 0);
             }
           }
-          if (g >= 2 && !warp_wait((v ? o_done : s_full) + 2 + buf, ((g - 2) >> 1) & 1, abort_flag)) {
-            ok = false;
-            break;
+          if (g >= 2) {
+            // the last step of the tile before the last, of both query tiles
+            const int x = (g - 1) * SPT - 1;
+            uint64_t* free = (v ? pv_done : s_full) + (x & 3);
+            ok = warp_wait(free, (x >> 2) & 1, abort_flag) && warp_wait(free + 4, (x >> 2) & 1, abort_flag);
+            if (!ok) break;
           }
           uint8_t* dst = sm + (v ? LY::VH : LY::KH) + buf * LY::KB + (ch >> 2) * (KT * 128);
           const int cc = (2 * ch) & 7;
@@ -478,95 +472,71 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     }
   } else {
     reg_dec<56>();
-    if (warp == 12) {
+    if (warp == 12 || warp == 15) {
       // ====================================================== MMA issue
-      // the warp walks together, one lane issues
-      constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, TM_ROWS, KT);
-      constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, TM_ROWS, D);
-      const uint32_t q0 = smem_u32(sm + LY::Q), kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
-      const bool issuer = lane == 0;
-      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;       // stretches and tiles of each query tile so far
-      int done = 0;
-      // 64 channels (a column block of 128-byte rows) per step of the loop
-      auto qk = [&](uint32_t q, uint32_t kh, uint32_t s) {
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, TM_ROWS, STEP_KEYS);
+        constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, TM_ROWS, D);
+        const int t = warp == 12 ? 0 : 1;
+        const uint32_t q = smem_u32(sm + LY::Q) + t * NQ * LY::QB;
+        const uint32_t kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
+        const uint32_t o = tmem + TM_O + 128 * t, s = tmem + TM_S + 128 * t;
+        uint32_t nq = 0, np = 0;                         // stretches and steps of this query tile so far
+        int done = 0;
+        // S of step x: 64 channels (a column block of 128-byte rows) per turn of the loop
+        auto qk = [&](int x) {
+          const uint32_t kh = kh0 + ((x / SPT) & 1) * LY::KB + (x % SPT) * (STEP_KEYS * 128);
 #pragma unroll 1
-        for (int c = 0; c < NQ * (D / 64); ++c) {
-          const int block = c & (D / 64 - 1), part = c / (D / 64);
-          mma4_f16_ss(s, make_sdesc_sw128(q + part * LY::QB + block * (TM_ROWS * 128), 16, 1024),
-                      make_sdesc_sw128(kh + block * (KT * 128), 16, 1024), idesc_qk, c);
-        }
-      };
-      // one half of the tile's keys
-      auto pv = [&](uint32_t o, uint32_t p, uint32_t vh, int half, bool first) {
-        const uint64_t b = make_sdesc_sw128(vh + half * (KT / 2) * 128, KT * 128, 1024);
-        if constexpr (KT == 128) mma4_f16_ts(o, p + half * 32, b, idesc_pv, first ? 0 : 1);
-        else mma2_f16_ts(o, p + half * 16, b, idesc_pv, first ? 0 : 1);
-      };
-      bool ok = true;
-      for (int sg = 0; ok; ++sg) {
-        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
-        const volatile Stretch& seg = segs[sg & 1];
-        if (!(seg.flags & STRETCH_SOME)) break;
-        const int n = seg.k1 - seg.k0;
-        const bool two = seg.n * G - seg.tile * TTR > TM_ROWS;
-        if (n > 0) {
-          ok = warp_wait(&q_full[0], nq0++ & 1, abort_flag) && (!two || warp_wait(&q_full[1], nq1++ & 1, abort_flag)) &&
-               warp_wait(&kh_full[done & 1], (done >> 1) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (issuer) {
-            const uint32_t kh = kh0 + (done & 1) * LY::KB;
-            qk(q0, kh, tmem + TM_S);
-            mma_commit(&s_full[done & 1]);
-            if (two) qk(q0 + NQ * LY::QB, kh, tmem + TM_S + 128);
-            mma_commit(&s_full[2 + (done & 1)]);
+          for (int c = 0; c < NQ * (D / 64); ++c) {
+            const int block = c & (D / 64 - 1), part = c / (D / 64);
+            mma4_f16_ss(s + 64 * (x & 1), make_sdesc_sw128(q + part * LY::QB + block * (TM_ROWS * 128), 16, 1024),
+                        make_sdesc_sw128(kh + block * (KT * 128), 16, 1024), idesc_qk, c);
           }
-          __syncwarp();
-        }
+        };
+        auto k_ready = [&](int x) -> bool {              // the tile of step x, at its first step
+          const int g = x / SPT;
+          return x % SPT != 0 || mbar_wait(&kh_full[g & 1], (g >> 1) & 1, abort_flag);
+        };
+        bool ok = true;
+        for (int sg = 0; ok; ++sg) {
+          if (!mbar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+          const volatile Stretch& seg = segs[sg & 1];
+          if (!(seg.flags & STRETCH_SOME)) break;
+          const int ns = (seg.k1 - seg.k0) * SPT;
+          const bool on = seg.n * G - seg.tile * TTR > t * TM_ROWS;   // the query tile has rows
+          if (ns > 0 && on && !mbar_wait(&q_full[t], nq++ & 1, abort_flag)) break;
+          // QK of the first two steps; then PV of a step and QK of the one two after it
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int g = done + j;
-          const uint32_t vh = vh0 + (g & 1) * LY::KB, kh = kh0 + ((g + 1) & 1) * LY::KB;
-          const bool next = j + 1 < n;
-          ok = warp_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag) &&
-               (!next || warp_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag));
-#pragma unroll 1
-          for (int t = 0; t < 2 && ok; ++t) {
-            const uint32_t o = tmem + TM_O + 128 * t, s = tmem + TM_S + 128 * t;
-            const bool on = t == 0 || two;
-            if (on) {
-              const uint32_t ph = (t ? np1++ : np0++) & 1;
-              ok = warp_wait(&p_full[2 * t], ph, abort_flag);
+          for (int j = -2; j < ns; ++j) {
+            const int x = done * SPT + j;
+            if (j >= 0) {
+              const int g = x / SPT;
+              ok = (x % SPT != 0 || mbar_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag)) &&
+                   (!on || mbar_wait(&p_full[2 * t + (np & 1)], (np >> 1) & 1, abort_flag));
+              if (!ok) break;
+              ++np;
+              tc_fence_after();
+              if (on)
+                mma4_f16_ts(o, s + 64 * (x & 1),
+                            make_sdesc_sw128(vh0 + (g & 1) * LY::KB + (x % SPT) * (STEP_KEYS * 128), KT * 128, 1024),
+                            idesc_pv, j > 0);
+              mma_commit(&pv_done[4 * t + (x & 3)]);
+            }
+            if (j + 2 < ns) {
+              ok = k_ready(x + 2);
               if (!ok) break;
               tc_fence_after();
-              if (issuer) {
-                pv(o, s, vh, 0, j == 0);
-                mma_commit(&half_done[t]);
-              }
-              __syncwarp();
-              ok = warp_wait(&p_full[2 * t + 1], ph, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
+              if (on) qk(x + 2);
+              mma_commit(&s_full[4 * t + ((x + 2) & 3)]);
             }
-            if (issuer) {
-              if (on) pv(o, s, vh, 1, false);
-              mma_commit(&o_done[2 * t + (g & 1)]);
-              if (next) {
-                if (on) qk(q0 + t * NQ * LY::QB, kh, s);
-                mma_commit(&s_full[2 * t + ((g + 1) & 1)]);
-              }
-            }
-            __syncwarp();
           }
-          if (!ok) break;
+          if (!on) np -= ns;                             // P's barriers count the steps of this query tile only
+          done += seg.k1 - seg.k0;
+          mbar_arrive(&seg_free[sg & 1]);
         }
-        done += n;
-        if (issuer) mbar_arrive(&seg_free[sg & 1]);
-      }
-      // every MMA issued so far is done before the block releases its tensor memory
-      if (issuer) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, nullptr, 100000000ull);
+        // every MMA issued so far is done before the block releases its tensor memory
+        mma_commit(&drain[t]);
+        mbar_wait(&drain[t], 0, nullptr, 100000000ull);
       }
       __syncwarp();
     } else if (warp == 13) {
