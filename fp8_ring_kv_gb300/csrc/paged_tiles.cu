@@ -246,6 +246,9 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
         // ------------------------------------------------------ key tiles
+        // steps below j_lo and from j_hi on hold keys that some row of the warp does not see
+        const int j_hi = __reduce_min_sync(0xFFFFFFFFu, hi >= k0 * KT ? (hi - k0 * KT) / STEP_KEYS : 0);
+        const int j_lo = __reduce_max_sync(0xFFFFFFFFu, (lo - k0 * KT + STEP_KEYS - 1) / STEP_KEYS);
         float rf = 0.0f;
 #pragma unroll 1
         for (int j = 0; j < n * SPT; ++j, ++steps) {
@@ -256,85 +259,71 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           }
           tc_fence_after();
           const uint32_t sb = s_at + 64 * (x & 1);
-          uint32_t xa[32], xb[32];
-          tmem_ld_32x32b_x32_start(sb, xa);
+          uint32_t xr[64];
+          tmem_ld_32x32b_x64(sb, xr);
+          float* s = reinterpret_cast<float*>(xr);
           if (j == 0) rf = rfs[row];       // written before q_full, which S waited for
           const int stage = (x / SPT) % TMETA;
           const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + stage * NG + (x % SPT) * 4;
-          const int key0 = k0 * KT + j * STEP_KEYS;
-          const bool cut = __any_sync(0xFFFFFFFFu, key0 + STEP_KEYS > hi || key0 < lo);
-          // one chunk of S (loaded) to P
-          auto chunk = [&](uint32_t (&xr)[32], int c) {
-            float* s = reinterpret_cast<float*>(xr);
-            if (cut) {
+          if (j >= j_hi || j < j_lo) {
+            const int key0 = k0 * KT + j * STEP_KEYS;
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (key0 + 32 * c + k >= hi || key0 + 32 * c + k < lo) s[k] = -INFINITY;
-            }
-            const float4 ma = meta[2 * c], mb = meta[2 * c + 1];
-            // never 0, so that a masked score stays -inf
-            const float fa = fmaxf(rf * ma.x, 0x1p-100f), fb = fmaxf(rf * mb.x, 0x1p-100f);
-            auto max16 = [](const float* v) {
-              const float a0 = max3f(v[0], v[1], v[2]), a1 = max3f(v[3], v[4], v[5]), a2 = max3f(v[6], v[7], v[8]);
-              const float a3 = max3f(v[9], v[10], v[11]), a4 = max3f(v[12], v[13], fmaxf(v[14], v[15]));
-              return max3f(max3f(a0, a1, a2), a3, a4);
-            };
-            const float my = fmaxf(fmaf(max16(s), fa, ma.y), fmaf(max16(s + 16), fb, mb.y));
-            if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
-              // rare after a row's first keys: what was summed with the old
-              // maximum is brought to the new one
-              const float mn = my > m + kRaise ? my : m;
-              const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
-              m = mn;
-              l *= al;
-              if (c == 1) {                // the chunk before it, in P already
-                uint32_t p[16];
-                tmem_ld_32x32b_x16(sb, p);
-                const __half2 f = __float2half2_rn(al);
+            for (int k = 0; k < STEP_KEYS; ++k)
+              if (key0 + k >= hi || key0 + k < lo) s[k] = -INFINITY;
+          }
+          float4 mt[4];
+          float f[4], my = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[e]), f);
-                  p[e] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                tmem_st_32x32b_x16(sb, p);
-              }
-              if (j > 0) {
-                if (!warp_wait(&pv_done[4 * t + ((x - 1) & 3)], ((x - 1) >> 2) & 1, abort_flag)) ok = false;
-                tc_fence_after();
+          for (int q = 0; q < 4; ++q) {
+            mt[q] = meta[q];
+            f[q] = fmaxf(rf * mt[q].x, 0x1p-100f);       // never 0, so that a masked score stays -inf
+            const float* v = s + 16 * q;
+            const float a0 = max3f(v[0], v[1], v[2]), a1 = max3f(v[3], v[4], v[5]), a2 = max3f(v[6], v[7], v[8]);
+            const float a3 = max3f(v[9], v[10], v[11]), a4 = max3f(v[12], v[13], fmaxf(v[14], v[15]));
+            my = fmaxf(my, fmaf(max3f(max3f(a0, a1, a2), a3, a4), f[q], mt[q].y));
+          }
+          if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
+            // rare after a row's first keys: what was summed with the old
+            // maximum is brought to the new one
+            const float mn = my > m + kRaise ? my : m;
+            const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
+            m = mn;
+            l *= al;
+            if (j > 0) {
+              if (!warp_wait(&pv_done[4 * t + ((x - 1) & 3)], ((x - 1) >> 2) & 1, abort_flag)) ok = false;
+              tc_fence_after();
 #pragma unroll 1
-                for (int k = 0; k < D; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld_32x32b_x16(o_at + k, o);
+              for (int k = 0; k < D; k += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_at + k, o);
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                  tmem_st_32x32b_x16(o_at + k, o);
-                }
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st_32x32b_x16(o_at + k, o);
               }
             }
-            const float sub = m == -INFINITY ? 0.0f : kTop - m;
+          }
+          const float sub = m == -INFINITY ? 0.0f : kTop - m;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float f1 = e ? fb : fa, a1 = (e ? mb.y : ma.y) + sub;
-              const float2 ff = make_float2(f1, f1), ad = make_float2(a1, a1);
+              const int q = 2 * c + e;
+              const float ad = mt[q].y + sub;
               float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                float2 y = fma2(make_float2(s[16 * e + 2 * k], s[16 * e + 2 * k + 1]), ff, ad);
+                float2 y = fma2(make_float2(s[16 * q + 2 * k], s[16 * q + 2 * k + 1]), make_float2(f[q], f[q]),
+                                make_float2(ad, ad));
                 y.x = ex2f(y.x);
                 y.y = ex2f(y.y);
                 sum = add2(sum, y);
                 p[8 * e + k] = cvt_f16x2(y.x, y.y);
               }
-              l = fmaf(sum.x + sum.y, e ? mb.z : ma.z, l);
+              l = fmaf(sum.x + sum.y, mt[q].z, l);
             }
             tmem_st_32x32b_x16(sb + 16 * c, p);
-          };
-          tmem_ld_wait(xa);
-          tmem_ld_32x32b_x32_start(sb + 32, xb);
-          chunk(xa, 0);
-          tmem_ld_wait(xb);
-          chunk(xb, 1);
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
