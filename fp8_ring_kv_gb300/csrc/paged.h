@@ -199,6 +199,32 @@ __device__ __forceinline__ void load8_f32(uint4 u, float* x) {
   }
 }
 
+// Largest magnitude of 8 values in 16 bits, as a pair of 16-bit patterns (the
+// order of non-negative bf16 or fp16 numbers is that of their bits).
+__device__ __forceinline__ uint32_t max8_bits(uint4 u) {
+  constexpr uint32_t A = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(u.x & A, u.y & A), __vmaxu2(u.z & A, u.w & A));
+}
+
+// The power of two that queries of a row are divided by on their way to fp16:
+// 2^ex <= amax < 2^(ex + 1) for the row's largest magnitude (m: max8_bits of all
+// of it), so that what a rotation leaves is below 2 sqrt(2).
+template <typename T>
+__device__ __forceinline__ int query_exponent(uint32_t m) {
+  const uint32_t top = max(m & 0xFFFFu, m >> 16);
+  float amax;
+  if constexpr (std::is_same_v<T, __half>) amax = __half2float(__ushort_as_half((unsigned short)top));
+  else amax = __uint_as_float(top << 16);
+  return max(-120, min(120, (int)(__float_as_uint(amax) >> 23) - 127));
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
+
+// One RoPE pair of a query: fp32, fused.
+__device__ __forceinline__ float2 rope_query(float x0, float x1, float2 cs) {
+  return make_float2(fmaf(x0, cs.x, -x1 * cs.y), fmaf(x0, cs.y, x1 * cs.x));
+}
+
 // Two fp32 -> packed 16-bit pair of type T, round to nearest even.
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

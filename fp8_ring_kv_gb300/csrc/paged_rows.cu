@@ -124,45 +124,44 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         const int r = pl.tile * RT + g + 8 * e;
         const bool live = r < rows;
         const int i = live ? r / G : 0;
-        float x[D / 4];
-        float amax = 0.0f;
+        uint4 w[D / 32];
+        float2 cs[D / 8];
+        uint32_t mb = 0;
         bool bad = false;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+          w[2 * c] = w[2 * c + 1] = make_uint4(0, 0, 0, 0);
           if (live) {
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + r - i * G) * D + c * 64 + t4 * 16);
-            w0 = __ldg(src);
-            w1 = __ldg(src + 1);
+            w[2 * c] = __ldg(src);
+            w[2 * c + 1] = __ldg(src + 1);
           }
-          load8_f32<T>(w0, x + c * 16);
-          load8_f32<T>(w1, x + c * 16 + 8);
-          if (live) {
-            float2 cs[8];
-            rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, cs, bad);
+          float2 part[8];
+          rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, part, bad);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) rope_pair(x[c * 16 + 2 * m], x[c * 16 + 2 * m + 1], cs[m].x, cs[m].y);
-          }
+          for (int k = 0; k < 8; ++k) cs[8 * c + k] = part[k];
+          mb = __vmaxu2(mb, __vmaxu2(max8_bits(w[2 * c]), max8_bits(w[2 * c + 1])));
         }
         if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
-#pragma unroll
-        for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(x[k]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        const int ex = amax > 0.0f ? max(-120, min(120, ilogbf(amax))) : 0;
-        const float down = ldexpf(1.0f, -ex);
-        rf[e] = ldexpf(a.scale_log2, ex);
+        mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 1));
+        mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 2));
+        const int ex = query_exponent<T>(mb);
+        const float down = pow2f(-ex);
+        rf[e] = a.scale_log2 * pow2f(ex);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
+          float x[8];
+          load8_f32<T>(w[k / 2], x);
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const float x0 = x[4 * k + 2 * f] * down, x1 = x[4 * k + 2 * f + 1] * down;
-            const uint32_t w = cvt_f16x2(x0, x1);
-            qa[k][2 * f + e] = w;
+            const int at = 4 * (k & 1) + 2 * f;          // of the 8 values of the chunk
+            const float2 y = mul2(rope_query(x[at], x[at + 1], cs[2 * k + f]), make_float2(down, down));
+            const uint32_t p = cvt_f16x2(y.x, y.y);
+            qa[k][2 * f + e] = p;
             if constexpr (SPLIT) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
-              qa[k][2 * f + 1] = cvt_f16x2(x0 - y.x, x1 - y.y);
+              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&p));
+              qa[k][2 * f + 1] = cvt_f16x2(y.x - z.x, y.y - z.y);
             }
           }
         }

@@ -199,41 +199,49 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         float* rfs = reinterpret_cast<float*>(sm + LY::RF) + t * TM_ROWS;
         const RopeLane rl = rope_lane(a.pv, ql * 8);
         bool bad = false;
+        // the token and head of a row, carried from one turn to the next
+        constexpr int RSTEP = TM_ROWS / L;
+        const int step_i = RSTEP / G, step_g = RSTEP - step_i * G;
+        int qi = (r0 + row / L) / G, qg = r0 + row / L - qi * G;
+        const T* qp = static_cast<const T*>(a.q) + (size_t)head0 * D + ql * 16;
 #pragma unroll 4
-        for (int rr = row / L; rr < TM_ROWS; rr += TM_ROWS / L) {
-          // rows past the last repeat it: their S and O are never looked at
-          const int rq = r0 + min(rr, rows - 1);
-          const int qi = rq / G;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + qi) * a.q_stride +
-                                                            (size_t)(head0 + rq - qi * G) * D + ql * 16);
-          const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+        for (int rr = row / L; rr < TM_ROWS; rr += RSTEP) {
+          // rows past the last: zeros
+          const bool on = rr < rows;
+          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+          if (on) {
+            const uint4* src = reinterpret_cast<const uint4*>(qp + (s0 + qi) * a.q_stride + qg * D);
+            w0 = __ldg(src);
+            w1 = __ldg(src + 1);
+          }
           float2 cs[8];
-          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + qi) * a.pv.n_axes, cs, bad);
+          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + (on ? qi : 0)) * a.pv.n_axes, cs, bad);
+          qi += step_i;
+          qg += step_g;
+          if (qg >= G) {
+            qg -= G;
+            ++qi;
+          }
+          uint32_t mb = __vmaxu2(max8_bits(w0), max8_bits(w1));
+#pragma unroll
+          for (int off = L / 2; off > 0; off >>= 1) mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
+          const int ex = query_exponent<T>(mb);
+          const float down = pow2f(-ex);
+          if (ql == 0) rfs[rr] = a.scale_log2 * pow2f(ex);
           float x[16];
           load8_f32<T>(w0, x);
           load8_f32<T>(w1, x + 8);
-          float amax = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            rope_pair(x[2 * k], x[2 * k + 1], cs[k].x, cs[k].y);
-            amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
-          }
-#pragma unroll
-          for (int off = L / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-          const int ex = amax > 0.0f ? max(-120, min(120, ilogbf(amax))) : 0;
-          const float down = ldexpf(1.0f, -ex);
-          if (ql == 0) rfs[rr] = ldexpf(a.scale_log2, ex);
           uint8_t* dst = sm + LY::Q + t * NQ * LY::QB + (ql >> 2) * (TM_ROWS * 128) + rr * 128;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t w[4], v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float x0 = x[8 * c + 2 * k] * down, x1 = x[8 * c + 2 * k + 1] * down;
-              w[k] = cvt_f16x2(x0, x1);
+              const float2 y = mul2(rope_query(x[8 * c + 2 * k], x[8 * c + 2 * k + 1], cs[4 * c + k]), make_float2(down, down));
+              w[k] = cvt_f16x2(y.x, y.y);
               if constexpr (NQ == 2) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                v[k] = cvt_f16x2(x0 - f.x, x1 - f.y);
+                v[k] = cvt_f16x2(y.x - f.x, y.y - f.y);
               }
             }
             uint8_t* at = dst + (((2 * ql + c) & 7) ^ (rr & 7)) * 16;
