@@ -34,34 +34,26 @@ def kvring_paged_workspace_bytes(cfg: kvring_paged_config) -> int:
     return int(_k.load().kvring_paged_workspace_bytes(ctypes.byref(cfg)))
 
 
-def _check_ints(t, shape, device, what):
-    """int32, contiguous, on the cache's device, of that shape (None: any size)."""
+def _bad_ints(t, shape, index, what):
+    """Why an int32 tensor is not as the kernels read it (None in ``shape``: any size)."""
     if t.dtype is not torch.int32:
-        raise KVRingError(f"{what}: {t.dtype}; the kernels read torch.int32")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-        raise KVRingError(f"{what}: shape {tuple(got)}; [{', '.join('*' if w is None else str(w) for w in shape)}] is read")
+        return f"{what}: {t.dtype}; the kernels read torch.int32"
+    if t.get_device() != index:
+        return f"{what}: on {t.device}, the cache is on cuda:{index}"
     if not t.is_contiguous():
-        raise KVRingError(f"{what}: not contiguous")
-    if t.device != device:
-        raise KVRingError(f"{what}: on {t.device}, the cache is on {device}")
+        return f"{what}: not contiguous"
+    return f"{what}: shape {tuple(t.shape)}; [{', '.join('*' if w is None else str(w) for w in shape)}] is read"
 
 
-def _check_heads(t, n, heads, dim, dtype, device, what):
-    """[n, heads, dim] with a token's heads side by side and a token stride
-    that is a multiple of 8 elements (q, k, v may be slices of one tensor);
-    returns the stride."""
+def _bad_heads(t, n, heads, dim, dtype, index, what):
+    """Why a tensor is not [n, heads, dim] with a token's heads side by side."""
     if t.dtype is not dtype:
-        raise KVRingError(f"{what}: {t.dtype}; the cache was made for {dtype}")
+        return f"{what}: {t.dtype}; the cache was made for {dtype}"
     if tuple(t.shape) != (n, heads, dim):
-        raise KVRingError(f"{what}: shape {tuple(t.shape)}; [{n}, {heads}, {dim}] is read")
-    if t.device != device:
-        raise KVRingError(f"{what}: on {t.device}, the cache is on {device}")
-    st = t.stride()
-    row = st[0] if n > 1 else heads * dim      # the only token's stride is not used
-    if n and (st[2] != 1 or (heads > 1 and st[1] != dim) or row < heads * dim or row % 8):
-        raise KVRingError(f"{what}: strides {st}; heads side by side and tokens a multiple of 8 elements apart")
-    return row
+        return f"{what}: shape {tuple(t.shape)}; [{n}, {heads}, {dim}] is read"
+    if t.get_device() != index:
+        return f"{what}: on {t.device}, the cache is on cuda:{index}"
+    return f"{what}: strides {t.stride()}; heads side by side and tokens a multiple of 8 elements apart"
 
 
 class PagedKV:
@@ -89,6 +81,7 @@ class PagedKV:
             raise KVRingError("workspace: a uint8 CUDA tensor of kvring_paged_workspace_bytes, 256-byte aligned")
         self.workspace = workspace
         self.device = workspace.device
+        self._index = workspace.get_device()
         lib = _k.load()
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
@@ -107,32 +100,60 @@ class PagedKV:
 
     def _stream(self, stream):
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def _check_batch(self, layer, n, pos, seq_start, kv_len, page_table):
-        dev = self.device
+    # The checks run before every call, beside kernels of a few microseconds:
+    # the good case first, the reason only for a bad one.
+    def _row_stride(self, t, n, heads, what):
+        """Elements between the tokens of [n, heads, head_dim] (q, k and v may be
+        slices of one tensor)."""
+        dim = self.head_dim
+        if t.dtype is self.dtype and t.shape == (n, heads, dim) and t.get_device() == self._index:
+            row, head, one = t.stride()
+            if n <= 1:
+                row = heads * dim              # the only token's stride is not used
+            if not n or one == 1 and (head == dim or heads == 1) and row >= heads * dim and row % 8 == 0:
+                return row
+        raise KVRingError(_bad_heads(t, n, heads, dim, self.dtype, self._index, what))
+
+    def _ints(self, t, shape, what):
+        if t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == self._index:
+            return t.data_ptr()
+        raise KVRingError(_bad_ints(t, shape, self._index, what))
+
+    def _batch(self, layer, n, pos, pos_name, seq_start, kv_len, page_table):
+        """The batch's arguments in the library's order."""
         if self.handle is None:
             raise KVRingError("the cache is closed")
         if not 0 <= layer < self.layers:
             raise KVRingError(f"layer: {layer} of {self.layers}")
-        n_seqs = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        shape = page_table.shape
+        if len(shape) != 2 or shape[1] < 1:
+            raise KVRingError(f"page_table: shape {tuple(shape)}; [sequences, at least 1] is read")
+        n_seqs, width = shape
         if n_seqs > _k.KVRING_PAGED_MAX_SEQS:
-            raise KVRingError(f"kv_len: {n_seqs} sequences; a call takes at most {_k.KVRING_PAGED_MAX_SEQS}")
-        _check_ints(kv_len, (None,), dev, "kv_len")
-        _check_ints(seq_start, (n_seqs + 1,), dev, "seq_start")
-        _check_ints(pos, (n, self.n_axes), dev, "pos")
-        if page_table.dim() != 2 or page_table.shape[0] != n_seqs or page_table.shape[1] < 1:
-            raise KVRingError(f"page_table: shape {tuple(page_table.shape)}; [{n_seqs}, at least 1] is read")
-        if page_table.dtype is not torch.int32 or page_table.device != dev:
-            raise KVRingError(f"page_table: {page_table.dtype} on {page_table.device}; torch.int32 on {dev} is read")
-        width = page_table.shape[1]
-        st = page_table.stride()
-        if (width > 1 and st[1] != 1) or (n_seqs > 1 and st[0] < width):
-            raise KVRingError(f"page_table: strides {st}; a row's entries side by side")
+            raise KVRingError(f"page_table: {n_seqs} sequences; a call takes at most {_k.KVRING_PAGED_MAX_SEQS}")
         if width * self.page_tokens > _k.KVRING_PAGED_MAX_LEN:
             raise KVRingError(f"page_table: {width} pages a row, more than {_k.KVRING_PAGED_MAX_LEN} tokens")
-        return n_seqs, max(st[0], width), width
+        if page_table.dtype is not torch.int32 or page_table.get_device() != self._index:
+            raise KVRingError(f"page_table: {page_table.dtype} on {page_table.device}; torch.int32 on cuda:{self._index} is read")
+        row, one = page_table.stride()
+        if (width > 1 and one != 1) or (n_seqs > 1 and row < width):
+            raise KVRingError(f"page_table: strides {(row, one)}; a row's entries side by side")
+        return (self._ints(pos, (n, self.n_axes), pos_name), self._ints(seq_start, (n_seqs + 1,), "seq_start"),
+                self._ints(kv_len, (n_seqs,), "kv_len"), n_seqs, page_table.data_ptr(), max(row, width), width)
+
+    def _call(self, name, *args):
+        """The library's function with the cache's device current."""
+        fn = getattr(_k.load(), name)
+        if torch._C._cuda_getDevice() == self._index:
+            status = fn(self.handle, *args)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(self.handle, *args)
+        if status:
+            check(status, name)
 
     def append(self, k, v, pos, seq_start, kv_len, page_table, layer=0, stream=None):
         """Write the new tokens' keys (rotated at ``pos``) and values.
@@ -142,16 +163,11 @@ class PagedKV:
         are rows seq_start[b] .. seq_start[b+1]-1; kv_len[b] counts its tokens
         with them; page_table[b] lists its pages in order."""
         n = k.shape[0]
-        ks = _check_heads(k, n, self.kv_heads, self.head_dim, self.dtype, self.device, "k")
-        vs = _check_heads(v, n, self.kv_heads, self.head_dim, self.dtype, self.device, "v")
-        n_seqs, ts, width = self._check_batch(layer, n, pos, seq_start, kv_len, page_table)
-        if n == 0 or n_seqs == 0:
-            return
-        with torch.cuda.device(self.device):
-            check(_k.load().kvring_paged_append(
-                self.handle, layer, k.data_ptr(), ks, v.data_ptr(), vs, pos.data_ptr(), seq_start.data_ptr(),
-                kv_len.data_ptr(), n_seqs, n, page_table.data_ptr(), ts, width, self._stream(stream)),
-                "kvring_paged_append")
+        ks, vs = self._row_stride(k, n, self.kv_heads, "k"), self._row_stride(v, n, self.kv_heads, "v")
+        p, start, length, n_seqs, table, ts, width = self._batch(layer, n, pos, "pos", seq_start, kv_len, page_table)
+        if n and n_seqs:
+            self._call("kvring_paged_append", layer, k.data_ptr(), ks, v.data_ptr(), vs, p, start, length, n_seqs, n,
+                       table, ts, width, self._stream(stream))
 
     def attend(self, q, q_pos, seq_start, kv_len, page_table, out=None, layer=0, causal=True, window=None, scale=None,
                max_new=None, stream=None):
@@ -163,8 +179,8 @@ class PagedKV:
         most new tokens that a sequence of this call has, where the caller
         knows it (a sequence with more is left out and flagged)."""
         n = q.shape[0]
-        qs = _check_heads(q, n, self.q_heads, self.head_dim, self.dtype, self.device, "q")
-        n_seqs, ts, width = self._check_batch(layer, n, q_pos, seq_start, kv_len, page_table)
+        qs = self._row_stride(q, n, self.q_heads, "q")
+        p, start, length, n_seqs, table, ts, width = self._batch(layer, n, q_pos, "q_pos", seq_start, kv_len, page_table)
         if window is not None and (not causal or window < 1):
             raise KVRingError("window: a positive number of tokens, with causal")
         if scale is not None and not 0.0 < scale < float("inf"):
@@ -179,14 +195,11 @@ class PagedKV:
                 s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
                 with torch.cuda.stream(s):
                     out = torch.empty((n, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
-        os_ = _check_heads(out, n, self.q_heads, self.head_dim, self.dtype, self.device, "out")
-        if n == 0 or n_seqs == 0:
-            return out
-        with torch.cuda.device(self.device):
-            check(_k.load().kvring_paged_attend(
-                self.handle, layer, q.data_ptr(), qs, q_pos.data_ptr(), seq_start.data_ptr(), kv_len.data_ptr(),
-                n_seqs, n, n if max_new is None else max_new, page_table.data_ptr(), ts, width, 1 if causal else 0,
-                window or 0, scale or 0.0, out.data_ptr(), os_, self._stream(stream)), "kvring_paged_attend")
+        os_ = self._row_stride(out, n, self.q_heads, "out")
+        if n and n_seqs:
+            self._call("kvring_paged_attend", layer, q.data_ptr(), qs, p, start, length, n_seqs, n,
+                       n if max_new is None else max_new, table, ts, width, 1 if causal else 0, window or 0,
+                       scale or 0.0, out.data_ptr(), os_, self._stream(stream))
         return out
 
     def debug_state(self, stream=None):
