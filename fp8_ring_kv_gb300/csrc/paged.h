@@ -53,7 +53,7 @@ struct PagedBatch {
 // rows of one sequence and key head), the others to the tensor-memory kernel
 // (256 rows per item).  fp16 queries take two of the register tile's 16 rows
 // each (high and low part).
-constexpr int kRowsWarps = 8, kRowsKeys = 32;
+constexpr int kRowsWarps = 12, kRowsKeys = 32;   // warps of a block, at most; keys of a tile
 template <typename T>
 constexpr int kRowsMax = std::is_same_v<T, __half> ? 8 : 16;
 constexpr int kTilesRows = 256;
@@ -98,6 +98,7 @@ cudaError_t launch_paged_append(const PagedView& pv, const PagedBatch& pb, const
 cudaError_t prepare_paged_rows(int D);
 cudaError_t prepare_paged_tiles(int D);
 // the kernel of few rows, and the kernel of many; ``blocks`` of either share its work
+int paged_rows_warps(const PagedAttn& a, bool f16);   // workers per block of this call
 cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                               cudaStream_t st);
 cudaError_t launch_paged_tiles(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,

@@ -46,45 +46,65 @@ __device__ __forceinline__ void sum_pieces(const PieceScratch& ps, int w, int p,
   }
 }
 
-// Block x looks at the records of workers RECS x .. RECS x + RECS - 1, and
-// takes a record's rows y, y + gridDim.y, ... in groups.  An item of few
-// pieces gives a row to each warp; one of many (a long sequence spread over
-// the GPU) gives a row to all eight, warp i the pieces i, i + 8, ...
-template <int D, int TR, int RECS, typename T>
+// Block x looks at the records of workers 8 x .. 8 x + 7 (TR <= 16) or at that
+// of worker x, and takes rows y, y + gridDim.y, ... of its items.  An item of
+// few pieces: a row to a warp (a record to a warp, or the rows shared by the
+// warps); one of many (a long sequence spread over the GPU): a row to all eight
+// warps, warp i the pieces i, i + 8, ...
+template <int D, int TR, typename T>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttn a, PieceScratch ps,
                                                          int workers) {
+  constexpr int RECS = TR <= 16 ? 8 : 1;
+  constexpr int V = D / 32;                              // channels per lane
+  constexpr int MANY = 12;                               // pieces
   __shared__ float acc[8][D];
   __shared__ float2 mls[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int V = D / 32;                              // channels per lane
   pdl_wait();
   pdl_trigger();
-  for (int w0 = 0; w0 < RECS; ++w0) {
-    const int w = blockIdx.x * RECS + w0;
-    if (w >= workers) return;
-    const PieceRec rec = ps.rec[w];
-    if (rec.b < 0) continue;
-    bool ok;
-    const SeqInfo s = seq_info(a.pb, a.pv.p_shift, rec.b, ok);
-    const int rows = min(s.n * a.pv.G - rec.tile * TR, TR);
-    auto out_row = [&](int r) {
-      const int rr = rec.tile * TR + r;
-      const int i = rr / a.pv.G;
-      return static_cast<T*>(a.out) + (s.s0 + i) * a.out_stride + (size_t)(rec.h * a.pv.G + rr - i * a.pv.G) * D;
-    };
-    float m, l, o[V];
-    if (rec.last - w < 12) {
-      for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        sum_pieces<V, TR>(ps, w, w, 1, rec.last, r, m, l, o);
+  struct Item {
+    PieceRec rec;
+    int w, rows, s0;
+  };
+  auto item = [&](int w) {
+    Item it;
+    it.w = w;
+    it.rec.b = -1;
+    if (w < workers) it.rec = ps.rec[w];
+    it.rows = 0;
+    if (it.rec.b >= 0) {
+      bool ok;
+      const SeqInfo s = seq_info(a.pb, a.pv.p_shift, it.rec.b, ok);
+      it.rows = min(s.n * a.pv.G - it.rec.tile * TR, TR);
+      it.s0 = s.s0;
+    }
+    return it;
+  };
+  auto out_row = [&](const Item& it, int r) {
+    const int rr = it.rec.tile * TR + r;
+    const int i = rr / a.pv.G;
+    return static_cast<T*>(a.out) + (it.s0 + i) * a.out_stride + (size_t)(it.rec.h * a.pv.G + rr - i * a.pv.G) * D;
+  };
+  float m, l, o[V];
+  bool many;
+  {
+    const Item it = item(RECS == 8 ? blockIdx.x * 8 + warp : blockIdx.x);
+    many = it.rec.b >= 0 && it.rec.last - it.w >= MANY;
+    if (!many)
+      for (int r = RECS == 8 ? blockIdx.y : blockIdx.y * 8 + warp; r < it.rows; r += gridDim.y * (RECS == 8 ? 1 : 8)) {
+        sum_pieces<V, TR>(ps, it.w, it.w, 1, it.rec.last, r, m, l, o);
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(out_row(r)) + lane * (V / 2);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(out_row(it, r)) + lane * (V / 2);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) dst[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
       }
-      continue;
-    }
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-      sum_pieces<V, TR>(ps, w, w + warp, 8, rec.last, r, m, l, o);
+  }
+  if (!__syncthreads_or(many)) return;
+  for (int w0 = 0; w0 < RECS; ++w0) {
+    const Item it = item(blockIdx.x * RECS + w0);
+    if (it.rec.b < 0 || it.rec.last - it.w < MANY) continue;
+    for (int r = blockIdx.y; r < it.rows; r += gridDim.y) {
+      sum_pieces<V, TR>(ps, it.w, it.w + warp, 8, it.rec.last, r, m, l, o);
       if (lane == 0) mls[warp] = make_float2(m, l);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[warp][lane * V + i] = o[i];
@@ -103,7 +123,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
           }
         }
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        reinterpret_cast<uint32_t*>(out_row(r))[tid] = pack2<T>(o0 * inv, o1 * inv);
+        reinterpret_cast<uint32_t*>(out_row(it, r))[tid] = pack2<T>(o0 * inv, o1 * inv);
       }
       __syncthreads();
     }
@@ -135,10 +155,10 @@ void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a) {
 template <int D, typename T>
 static cudaError_t join_t(const PagedAttn& a, bool tiles, int workers, cudaStream_t st) {
   if (tiles)
-    return launch_pdl(paged_join_kernel<D, kTilesRows, 1, T>, dim3(workers, 8), dim3(256), 0, st, a, a.tiles, workers);
+    return launch_pdl(paged_join_kernel<D, kTilesRows, T>, dim3(workers, 8), dim3(256), 0, st, a, a.tiles, workers);
   const long long most = (long long)a.max_new * a.pv.G;
   const unsigned rows = (unsigned)(most < kRowsMax<T> ? most : kRowsMax<T>);
-  return launch_pdl(paged_join_kernel<D, kRowsMax<T>, 8, T>, dim3((workers + 7) / 8, rows), dim3(256), 0, st, a, a.rows,
+  return launch_pdl(paged_join_kernel<D, kRowsMax<T>, T>, dim3((workers + 7) / 8, rows), dim3(256), 0, st, a, a.rows,
                     workers);
 }
 
@@ -156,7 +176,7 @@ cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, cons
   const bool many = (long long)a.max_new * a.pv.G > few;
   cudaError_t e = launch_paged_rows(a, tmK, tmV, f16, blocks, st);
   if (e == cudaSuccess && many) e = launch_paged_tiles(a, tmK, tmV, f16, blocks, st);
-  if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks * kRowsWarps, st);
+  if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks * paged_rows_warps(a, f16), st);
   if (e == cudaSuccess && many) e = launch_paged_join(a, true, f16, blocks, st);
   return e;
 }

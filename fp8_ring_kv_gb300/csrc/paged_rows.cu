@@ -9,16 +9,24 @@
 // s_v = 0; any scale serves it, and the nearest page's is taken.
 //
 // What bounds it: every key and value byte is read once for at most 16 rows,
-// so HBM bandwidth.  The codes go from memory to shared memory by TMA (32 keys
-// and values per stage, a ring of stages per warp) and from there, widened to
-// fp16 (exact), straight into the registers of mma.m16n8k16: a warp works by
-// itself, with no barrier between warps, and at 16 rows the products cost a
-// fraction of what the bytes do.  tcgen05 would want 128 rows.
+// so HBM bandwidth, if the warps get through their instructions: a byte costs
+// half a conversion and its share of the MMAs, whatever the number of rows.
+// The codes go from memory to shared memory by TMA (32 keys and values per
+// stage, a ring of stages per warp) and from there, widened to fp16 (exact),
+// straight into the registers of mma.m16n8k16; a warp works by itself, with no
+// barrier between warps.  tcgen05 would want 128 rows.
 //
-// Register layouts: a thread of lane 4g + t holds, of a K tile, 16-byte chunks
-// of key row g (its channels are the MMA's k in a permuted order, the same for
-// Q), and of a V tile 16 bytes of each of the four keys whose weights it
-// holds: byte pairs of two keys at one channel become the MMA's k pair.  The
+// The products are S^T = K Q^T and O^T = V^T P^T: keys and channels are the
+// MMA's 16 rows and the queries its 8 columns, so up to 8 query rows waste
+// nothing (with the queries as rows, half of the products and of the
+// accumulators were padding, two warps per sub-partition fitted, and a decoding
+// batch of 64 contexts took 129 us against XXX).
+//
+// Register layouts (lane 4 g + t): of a K tile a thread holds 16-byte chunks of
+// key rows g and g + 8 (its channels are the MMA's k in a permuted order, the
+// same for Q), of a V tile 16 bytes of each of four keys: byte pairs of two
+// keys at one channel become the MMA's k pairs.  S^T has key g and queries
+// 2 t, 2 t + 1 in a thread; movmatrix turns the weights into P^T's layout.  The
 // key rows of an 8-key group are taken in the order 0 5 2 7 4 1 6 3, with
 // which both patterns read 128-byte-swizzled rows without bank conflicts.
 #include "paged_sched.cuh"
@@ -26,29 +34,41 @@
 
 namespace kvring_dev {
 
-constexpr int RW = kRowsWarps, RK = kRowsKeys;
-constexpr int RTHREADS = 32 * RW;
+constexpr int RK = kRowsKeys;
 
-template <int D>
+// NT: MMA column tiles.  1: up to 8 query rows; 2: up to 16, or, for fp16
+// queries, the high parts of up to 8 and their low parts (whose products are
+// summed: an fp16 result shows more than the 11 bits of one operand)
+template <int D, int NT>
 struct RowsLayout {
-  static constexpr int NST = D == 128 ? 3 : 6;           // stages per warp
+  static constexpr int RW = NT == 1 ? kRowsWarps : 8;    // warps, as their registers allow
+  static constexpr int NST = (NT == 1 ? 2 : 3) * (128 / D);   // stages per warp
   static constexpr int STAGE = 2 * RK * D;               // K codes, then V codes
-  static constexpr int META = RW * NST * STAGE;          // per warp and stage: s_k of two pages, s_v of two pages
-  static constexpr int BAR = META + RW * NST * 16;
+  static constexpr int META = RW * NST * STAGE;          // per warp and stage: {s_k, log2 s_v, 1 / s_v, -} of two pages
+  static constexpr int BAR = META + RW * NST * 32;
   static constexpr int PRE = BAR + RW * NST * 8;
   static constexpr int SUMS = PRE + (kPagedMaxSeqs + 1) * 8;
   static constexpr int MISC = SUMS + RW * 8;
-  static constexpr int ALLOC = MISC + 16 + 1024;         // slack for 1024-byte alignment
+  static constexpr int ALLOC = MISC + 16;                // the block's shared memory starts 1024-byte aligned
+  static_assert(ALLOC <= 232448, "shared memory of a block");
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// key row of MMA column n of an 8-key group
+// Transpose of an 8 x 8 matrix of 16-bit values held as MMA fragments.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// key row of MMA index n of an 8-key group
 __device__ __forceinline__ int key_row(int n) { return ((((n >> 2) ^ n) & 1) << 2) | (n & 3); }
 
 template <int D>
@@ -62,27 +82,25 @@ __device__ __forceinline__ int code_chunk(int r, int c) {
 __device__ __forceinline__ uint32_t widen_lo(uint32_t w) { return cvt_e4m3x2_to_f16x2((uint16_t)(w & 0xFFFFu)); }
 __device__ __forceinline__ uint32_t widen_hi(uint32_t w) { return cvt_e4m3x2_to_f16x2((uint16_t)(w >> 16)); }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(RTHREADS, 1)
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
     paged_attend_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const __grid_constant__ PagedAttn a) {
-  using LY = RowsLayout<D>;
-  constexpr int NST = LY::NST;
-  constexpr int KS = D / 16;                             // k steps of QK; also 2 x the V channel tiles per byte group
-  constexpr int DG = D / 8;                              // channels of O per thread and column parity
-  // MMA rows 8 .. 15: eight more query rows, or, for fp16 queries, the low
-  // parts of rows 0 .. 7 (and of their weights): both parts of a product are
-  // summed at the end, at no further MMA
+  using LY = RowsLayout<D, NT>;
+  constexpr int NST = LY::NST, RW = LY::RW;
   constexpr bool SPLIT = std::is_same_v<T, __half>;
-  constexpr int RT = kRowsMax<T>, E = SPLIT ? 1 : 2;
+  constexpr int E = SPLIT ? 1 : NT;                      // tiles of 8 query rows
+  constexpr int RT = kRowsMax<T>;                        // rows of an item, at most
   using RowsShare = Share<RT, RK, 0, 0, RT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  constexpr int KS = D / 16;                             // k steps of QK
+  constexpr int NJ = D / 16;                             // channel tiles of O
+  constexpr int DG = D / 8;                              // channels per thread
+  extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR) + warp * NST;
   uint8_t* stages = sm + warp * NST * LY::STAGE;
-  float4* metas = reinterpret_cast<float4*>(sm + LY::META) + warp * NST;
+  float4* metas = reinterpret_cast<float4*>(sm + LY::META) + warp * NST * 2;
   long long* pre = reinterpret_cast<long long*>(sm + LY::PRE);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC);
   if (lane == 0) {
@@ -94,7 +112,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
   if (tid == 0) *abort_flag = 0;
   pdl_wait();
   pdl_trigger();
-  RowsShare::template prefix<RTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SUMS), blockIdx.x == 0);
+  RowsShare::template prefix<32 * RW>(a, pre, reinterpret_cast<long long*>(sm + LY::SUMS), blockIdx.x == 0);
   const int H = a.pv.H, G = a.pv.G;
   const int worker = blockIdx.x * RW + warp;
   const int workers = gridDim.x * RW;
@@ -112,16 +130,103 @@ __global__ void __launch_bounds__(RTHREADS, 1)
       const int k1 = min(pl.t.t1, pl.t.t0 + (int)(min(end, item_end) - pl.at));
       const bool whole = u == pl.at && end >= item_end;
       const int rows = pl.s.n * G;
+      // ---------------------------------------------------------- pages
+      // lane i holds the page ids and scales of tile base + i (two pages when
+      // P = 16); v_near: a non-zero V scale near by, for pages of zeros
+      int base = k0;
+      int id[2] = {-1, -1};
+      float sk[2] = {0.0f, 0.0f}, sv[2] = {0.0f, 0.0f};
+      float v_near = 0.0f;
+      auto load_ids = [&](int tb, int (&ids)[2]) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ids[p] = -1;
+          const int key = (tb + lane) * RK + p * 16;
+          if (tb + lane < k1 && (p == 0 || a.pv.P == 16) && key < pl.t.hi &&
+              key + (a.pv.P == 16 ? 16 : RK) > pl.t.lo) {
+            ids[p] = __ldg(a.pb.table + pl.b * a.pb.table_stride + (key >> a.pv.p_shift));
+            if (ids[p] < 0 || ids[p] >= a.pv.n_pages) {
+              atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
+              ids[p] = 0;
+            }
+          }
+        }
+      };
+      auto load_scales = [&](const int (&ids)[2], float (&ks)[2], float (&vs)[2]) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ks[p] = ids[p] >= 0 ? __ldg(a.pv.k_scale + (size_t)ids[p] * H + pl.h) : 0.0f;
+          vs[p] = ids[p] >= 0 ? __ldg(a.pv.v_scale + (size_t)ids[p] * H + pl.h) : 0.0f;
+        }
+      };
+      auto near_scale = [&]() {
+        auto top = [](float v) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+          return v;
+        };
+        float mx = top(fmaxf(sv[0], sv[1]));
+        if (mx == 0.0f && v_near == 0.0f) {
+          for (int tb = base + 32; mx == 0.0f && tb < k1; tb += 32) {
+            int di[2];
+            float dk[2], dv[2];
+            load_ids(tb, di);
+            load_scales(di, dk, dv);
+            mx = top(fmaxf(dv[0], dv[1]));
+          }
+          if (mx == 0.0f) mx = 1.0f;
+        }
+        if (mx > 0.0f) v_near = mx;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (sv[p] == 0.0f) sv[p] = v_near;
+      };
+      // tile k's codes on their way to the next stage, by the lane that holds its pages
+      auto issue = [&](int k) {
+        if (lane == k - base) {
+          const int st = used % NST;
+          uint8_t* dst = stages + st * LY::STAGE;
+          if (a.pv.P == 16) {
+            mbar_arrive_expect_tx(&bars[st], (uint32_t)((id[0] >= 0) + (id[1] >= 0)) * 2 * 16 * D);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              if (id[p] >= 0) {
+                const int y = (int)(a.pv.row0 + ((long long)id[p] * H + pl.h) * 16);
+                tma_load_2d(dst + p * 16 * D, &tmK, &bars[st], 0, y);
+                tma_load_2d(dst + RK * D + p * 16 * D, &tmV, &bars[st], 0, y);
+              }
+          } else {
+            const int y = (int)(a.pv.row0 + (((long long)id[0] * H + pl.h) << a.pv.p_shift)) + ((k * RK) & (a.pv.P - 1));
+            mbar_arrive_expect_tx(&bars[st], LY::STAGE);
+            tma_load_2d(dst, &tmK, &bars[st], 0, y);
+            tma_load_2d(dst + RK * D, &tmV, &bars[st], 0, y);
+          }
+        }
+        ++used;
+      };
+      auto write_meta = [&](int k, int n) {
+        if (lane == k - base) {
+          float4* m = metas + (n % NST) * 2;
+          const int p1 = a.pv.P == 16 ? 1 : 0;
+          m[0] = make_float4(sk[0], __log2f(sv[0]), 1.0f / sv[0], 0.0f);
+          m[1] = make_float4(sk[p1], __log2f(sv[p1]), 1.0f / sv[p1], 0.0f);
+        }
+      };
+      const int first = used;
+      int issued = k0;
+      load_ids(base, id);
+      while (issued < k1 && issued < k0 + NST) issue(issued++);
+      load_scales(id, sk, sv);
       // ---------------------------------------------------------- queries
-      // rows g and g + 8 of the tile, rotated, scaled by a power of two to
-      // below 2 and rounded to fp16 (an MMA operand): a bf16 query loses
-      // nothing that its output could show, an fp16 one keeps a second part
-      uint32_t qa[KS][4];
-      float rf[E];
-      int hi[E], lo[E];
+      // row g of each tile, rotated, scaled by a power of two and rounded to
+      // fp16 (an MMA operand): a bf16 query loses nothing that its output
+      // could show, an fp16 one keeps a second part
+      uint32_t qb[NT][KS][2];
+      float rf[E][2];                                    // logit factors of rows 2 t, 2 t + 1
+      int hi[E][2], lo[E][2];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int r = pl.tile * RT + g + 8 * e;
+        const int r = e * 8 + g;
         const bool live = r < rows;
         const int i = live ? r / G : 0;
         uint4 w[D / 32];
@@ -148,7 +253,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 2));
         const int ex = query_exponent<T>(mb);
         const float down = pow2f(-ex);
-        rf[e] = a.scale_log2 * pow2f(ex);
+        const float rfg = a.scale_log2 * pow2f(ex);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           float x[8];
@@ -158,108 +263,50 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             const int at = 4 * (k & 1) + 2 * f;          // of the 8 values of the chunk
             const float2 y = mul2(rope_query(x[at], x[at + 1], cs[2 * k + f]), make_float2(down, down));
             const uint32_t p = cvt_f16x2(y.x, y.y);
-            qa[k][2 * f + e] = p;
+            qb[e][k][f] = p;
             if constexpr (SPLIT) {
               const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&p));
-              qa[k][2 * f + 1] = cvt_f16x2(y.x - z.x, y.y - z.y);
+              qb[1][k][f] = cvt_f16x2(y.x - z.x, y.y - z.y);
             }
           }
         }
-        const int at = pl.s.len - pl.s.n + i;            // the row's own index
-        hi[e] = !live ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
-        lo[e] = live && a.window > 0 ? at - a.window + 1 : 0;
-      }
-      float o[DG][4];
 #pragma unroll
-      for (int i = 0; i < DG; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-      float m[E], l[E];
+        for (int f = 0; f < 2; ++f) {
+          const int rr = e * 8 + 2 * t4 + f;
+          const int at = pl.s.len - pl.s.n + (rr < rows ? rr / G : 0);   // the row's own index
+          rf[e][f] = __shfl_sync(0xFFFFFFFFu, rfg, 4 * (2 * t4 + f));
+          hi[e][f] = rr >= rows ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
+          lo[e][f] = rr < rows && a.window > 0 ? at - a.window + 1 : 0;
+        }
+      }
+      if (k0 < k1) {
+        near_scale();
+        for (int k = k0; k < issued; ++k) write_meta(k, first + k - k0);
+        __syncwarp();
+      }
+      // tiles below c_lo and from c_hi on hold keys that some row of the thread does not see
+      int c_hi = pl.t.hi / RK, c_lo = (pl.t.lo + RK - 1) / RK;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          c_hi = min(c_hi, hi[e][f] / RK);
+          c_lo = max(c_lo, (lo[e][f] + RK - 1) / RK);
+        }
+      float o[NJ][NT][4];
+#pragma unroll
+      for (int i = 0; i < NJ; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+      float m[E][2], l[E][2];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        m[e] = -INFINITY;
-        l[e] = 0.0f;
+        m[e][0] = m[e][1] = -INFINITY;
+        l[e][0] = l[e][1] = 0.0f;
       }
-
-      // ---------------------------------------------------------- pages
-      // lane i holds the page ids and scales of tile base + i (two pages when
-      // P = 16); v_near: a non-zero V scale near by, for pages of zeros
-      int base = k0 - 32;
-      int id[2] = {-1, -1};
-      float sk[2] = {0, 0}, sv[2] = {0, 0};
-      float v_near = 0.0f;
-      auto load_pages = [&](int tb, int (&ids)[2], float (&ks)[2], float (&vs)[2]) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          ids[p] = -1;
-          ks[p] = vs[p] = 0.0f;
-          const int key = (tb + lane) * RK + p * 16;
-          if (tb + lane < k1 && (p == 0 || a.pv.P == 16) && key < pl.t.hi &&
-              key + (a.pv.P == 16 ? 16 : RK) > pl.t.lo) {
-            int pg = __ldg(a.pb.table + pl.b * a.pb.table_stride + (key >> a.pv.p_shift));
-            if (pg < 0 || pg >= a.pv.n_pages) {
-              atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
-              pg = 0;
-            }
-            ids[p] = pg;
-            ks[p] = __ldg(a.pv.k_scale + (size_t)pg * H + pl.h);
-            vs[p] = __ldg(a.pv.v_scale + (size_t)pg * H + pl.h);
-          }
-        }
-        float mx = fmaxf(vs[0], vs[1]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        return mx;
-      };
-      auto issue = [&](int k) {
-        if (k >= base + 32) {
-          base += 32;
-          float mx = load_pages(base, id, sk, sv);
-          if (mx == 0.0f && v_near == 0.0f) {
-            for (int tb = base + 32; mx == 0.0f && tb < k1; tb += 32) {
-              int di[2];
-              float dk[2], dv[2];
-              mx = load_pages(tb, di, dk, dv);
-            }
-            if (mx == 0.0f) mx = 1.0f;
-          }
-          if (mx > 0.0f) v_near = mx;
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            if (sv[p] == 0.0f) sv[p] = v_near;
-        }
-        const int src = k - base;
-        const int p0 = __shfl_sync(0xFFFFFFFFu, id[0], src), p1 = __shfl_sync(0xFFFFFFFFu, id[1], src);
-        const float4 mt = make_float4(__shfl_sync(0xFFFFFFFFu, sk[0], src), __shfl_sync(0xFFFFFFFFu, sk[1], src),
-                                      __shfl_sync(0xFFFFFFFFu, sv[0], src), __shfl_sync(0xFFFFFFFFu, sv[1], src));
-        const int st = used % NST;
-        if (lane == 0) {
-          uint8_t* dst = stages + st * LY::STAGE;
-          metas[st] = mt;
-          if (a.pv.P == 16) {
-            mbar_arrive_expect_tx(&bars[st], (uint32_t)((p0 >= 0) + (p1 >= 0)) * 2 * 16 * D);
-            if (p0 >= 0) {
-              const int y = (int)(a.pv.row0 + ((long long)p0 * H + pl.h) * 16);
-              tma_load_2d(dst, &tmK, &bars[st], 0, y);
-              tma_load_2d(dst + RK * D, &tmV, &bars[st], 0, y);
-            }
-            if (p1 >= 0) {
-              const int y = (int)(a.pv.row0 + ((long long)p1 * H + pl.h) * 16);
-              tma_load_2d(dst + 16 * D, &tmK, &bars[st], 0, y);
-              tma_load_2d(dst + RK * D + 16 * D, &tmV, &bars[st], 0, y);
-            }
-          } else {
-            const int y = (int)(a.pv.row0 + (((long long)p0 * H + pl.h) << a.pv.p_shift)) + ((k * RK) & (a.pv.P - 1));
-            mbar_arrive_expect_tx(&bars[st], LY::STAGE);
-            tma_load_2d(dst, &tmK, &bars[st], 0, y);
-            tma_load_2d(dst + RK * D, &tmV, &bars[st], 0, y);
-          }
-        }
-        ++used;
-      };
       // ---------------------------------------------------------- keys
-      const int first = used;
-      int issued = k0;
-      while (issued < k1 && issued < k0 + NST) issue(issued++);
       bool alive = true;
+#pragma unroll 1
       for (int k = k0; k < k1; ++k) {
         const int n = first + (k - k0);
         const int st = n % NST;
@@ -267,96 +314,109 @@ __global__ void __launch_bounds__(RTHREADS, 1)
           alive = false;
           break;
         }
-        __syncwarp();
         const uint8_t* kc = stages + st * LY::STAGE;
         const uint8_t* vc = kc + RK * D;
-        const float4 mt = metas[st];
-        float c[4][4];
+        const float4 m0 = metas[2 * st], m1 = metas[2 * st + 1];
+        float c[2][NT][4];                               // 16 keys each
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) c[j][nt][0] = c[j][nt][1] = c[j][nt][2] = c[j][nt][3] = 0.0f;
 #pragma unroll
           for (int q = 0; q < D / 64; ++q) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kc + code_chunk<D>(j * 8 + key_row(g), q * 4 + t4));
-            mma_16816(c[j], qa[q * 4 + 0], widen_lo(w.x), widen_hi(w.x));
-            mma_16816(c[j], qa[q * 4 + 1], widen_lo(w.y), widen_hi(w.y));
-            mma_16816(c[j], qa[q * 4 + 2], widen_lo(w.z), widen_hi(w.z));
-            mma_16816(c[j], qa[q * 4 + 3], widen_lo(w.w), widen_hi(w.w));
+            const uint4 w = *reinterpret_cast<const uint4*>(kc + code_chunk<D>(j * 16 + key_row(g), q * 4 + t4));
+            const uint4 v = *reinterpret_cast<const uint4*>(kc + code_chunk<D>(j * 16 + 8 + key_row(g), q * 4 + t4));
+            const uint32_t wa[4] = {w.x, w.y, w.z, w.w}, va[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0 = widen_lo(wa[i]), a1 = widen_lo(va[i]), a2 = widen_hi(wa[i]), a3 = widen_hi(va[i]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816(c[j][nt], a0, a1, a2, a3, qb[nt][q * 4 + i][0], qb[nt][q * 4 + i][1]);
+            }
           }
         }
-        // y of row g (and, e = 1, g + 8); columns 2 t4, 2 t4 + 1 of group j
-        const float sk1 = a.pv.P == 16 ? mt.y : mt.x, sv1 = a.pv.P == 16 ? mt.w : mt.z;
-        const float off0 = __log2f(mt.z), off1 = __log2f(sv1);
+        // y: keys key_row(g) (+ 8) of group j, rows 2 t4 + f of tile e
         const int key0 = k * RK;
-        bool cut = false;
-#pragma unroll
-        for (int e = 0; e < E; ++e) cut = cut || key0 + RK > hi[e] || key0 < lo[e];
-        float mx[E];
+        const bool cut = k >= c_hi || k < c_lo;
+        float mx[E][2];
         bool raise = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          mx[e] = -INFINITY;
+        for (int e = 0; e < E; ++e)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int f = 0; f < 2; ++f) {
+            mx[e][f] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float s = SPLIT ? c[j][i] + c[j][2 + i] : c[j][2 * e + i];
-              float y = fmaf(s, rf[e] * (j < 2 ? mt.x : sk1), j < 2 ? off0 : off1);
-              if (cut) {
-                const int key = key0 + j * 8 + key_row(2 * t4 + i);
-                if (key >= hi[e] || key < lo[e] || key >= pl.t.hi) y = -INFINITY;
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h8 = 0; h8 < 2; ++h8) {
+                const int i = 2 * h8 + f;
+                const float s = SPLIT ? c[j][0][i] + c[j][NT - 1][i] : c[j][e][i];
+                float y = fmaf(s, rf[e][f] * (j ? m1.x : m0.x), j ? m1.y : m0.y);
+                if (cut) {
+                  const int key = key0 + j * 16 + h8 * 8 + key_row(g);
+                  if (key >= hi[e][f] || key < lo[e][f] || key >= pl.t.hi) y = -INFINITY;
+                }
+                c[j][e][i] = y;
+                mx[e][f] = fmaxf(mx[e][f], y);
               }
-              c[j][2 * e + i] = y;
-              mx[e] = fmaxf(mx[e], y);
-            }
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-          raise = raise || mx[e] > m[e];
-        }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx[e][f] = fmaxf(mx[e][f], __shfl_xor_sync(0xFFFFFFFFu, mx[e][f], off));
+            raise = raise || mx[e][f] > m[e][f];
+          }
         if (__any_sync(0xFFFFFFFFu, raise)) {
-          float al[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float mn = fmaxf(m[e], mx[e]);
-            al[e] = mn > m[e] ? ex2f(m[e] - mn) : 1.0f;      // 0 for the first keys of a row
-            m[e] = mn;
-            l[e] *= al[e];
-          }
+          for (int e = 0; e < E; ++e)
 #pragma unroll
-          for (int i = 0; i < DG; ++i) {
-            o[i][0] *= al[0];
-            o[i][1] *= al[0];
-            o[i][2] *= al[E - 1];
-            o[i][3] *= al[E - 1];
-          }
+            for (int f = 0; f < 2; ++f) {
+              const float mn = fmaxf(m[e][f], mx[e][f]);
+              const float al = mn > m[e][f] ? ex2f(m[e][f] - mn) : 1.0f;     // 0 for the first keys of a row
+              m[e][f] = mn;
+              l[e][f] *= al;
+#pragma unroll
+              for (int i = 0; i < NJ; ++i) {
+                o[i][e][f] *= al;
+                o[i][e][2 + f] *= al;
+                if constexpr (SPLIT) {
+                  o[i][1][f] *= al;
+                  o[i][1][2 + f] *= al;
+                }
+              }
+            }
         }
-        uint32_t pa[2][4];
-        const float iv0 = 1.0f / mt.z, iv1 = 1.0f / sv1;
+        // weights, and P^T as the MMA's second operand
+        uint32_t pb[2][NT][2];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float sub = m[e] == -INFINITY ? 0.0f : 8.0f - m[e];
-          float ls[2] = {0.0f, 0.0f};                    // of either page
+          const float sub0 = m[e][0] == -INFINITY ? 0.0f : 8.0f - m[e][0], sub1 = m[e][1] == -INFINITY ? 0.0f : 8.0f - m[e][1];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float w0 = ex2f(c[j][2 * e] + sub), w1 = ex2f(c[j][2 * e + 1] + sub);
-            ls[j >> 1] += w0 + w1;
-            const uint32_t w = cvt_f16x2(w0, w1);
-            pa[j >> 1][(j & 1) * 2 + e] = w;
-            if constexpr (SPLIT) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
-              pa[j >> 1][(j & 1) * 2 + 1] = cvt_f16x2(w0 - y.x, w1 - y.y);
+          for (int j = 0; j < 2; ++j) {
+            const float iv = j ? m1.z : m0.z;
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int h8 = 0; h8 < 2; ++h8) {
+              const float w0 = ex2f(c[j][e][2 * h8] + sub0), w1 = ex2f(c[j][e][2 * h8 + 1] + sub1);
+              s0 += w0;
+              s1 += w1;
+              const uint32_t w = cvt_f16x2(w0, w1);
+              pb[j][e][h8] = transpose8(w);
+              if constexpr (SPLIT) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                pb[j][1][h8] = transpose8(cvt_f16x2(w0 - y.x, w1 - y.y));
+              }
             }
+            l[e][0] = fmaf(s0, iv, l[e][0]);
+            l[e][1] = fmaf(s1, iv, l[e][1]);
           }
-          l[e] += ls[0] * iv0 + ls[1] * iv1;
         }
-        // O += P V: k pairs are keys (row(2 t4), row(2 t4 + 1)) of groups 2 kk and 2 kk + 1
+        // O^T += V^T P^T: k pairs are keys (row(2 t4), row(2 t4 + 1)) of either 8-key group
         const bool edge = key0 + RK > pl.t.hi || key0 < pl.t.lo;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int j = 0; j < 2; ++j) {
           uint32_t w[4][D / 32];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int kr = kk * 16 + (r >> 1) * 8 + key_row(2 * t4 + (r & 1));
+            const int kr = j * 16 + (r >> 1) * 8 + key_row(2 * t4 + (r & 1));
             if constexpr (D == 128) {
               const uint4 v = *reinterpret_cast<const uint4*>(vc + code_chunk<D>(kr, g));
               w[r][0] = v.x;
@@ -375,17 +435,29 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint32_t a01 = __byte_perm(w[0][i], w[1][i], 0x5140), a23 = __byte_perm(w[0][i], w[1][i], 0x7362);
-            const uint32_t b01 = __byte_perm(w[2][i], w[3][i], 0x5140), b23 = __byte_perm(w[2][i], w[3][i], 0x7362);
-            mma_16816(o[4 * i + 0], pa[kk], widen_lo(a01), widen_lo(b01));
-            mma_16816(o[4 * i + 1], pa[kk], widen_hi(a01), widen_hi(b01));
-            mma_16816(o[4 * i + 2], pa[kk], widen_lo(a23), widen_lo(b23));
-            mma_16816(o[4 * i + 3], pa[kk], widen_hi(a23), widen_hi(b23));
-          }
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t sel = f ? 0x7362 : 0x5140;
+              const uint32_t x = __byte_perm(w[0][i], w[1][i], sel), y = __byte_perm(w[2][i], w[3][i], sel);
+              const uint32_t a0 = widen_lo(x), a1 = widen_hi(x), a2 = widen_lo(y), a3 = widen_hi(y);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816(o[2 * i + f][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
+            }
         }
         __syncwarp();                                    // every lane is done with the stage
-        if (issued < k1) issue(issued++);
+        if (issued < k1) {
+          if (issued >= base + 32) {
+            base += 32;
+            load_ids(base, id);
+            load_scales(id, sk, sv);
+            near_scale();
+          }
+          issue(issued);
+          write_meta(issued, used - 1);
+          ++issued;
+          __syncwarp();
+        }
       }
       if (!alive) {
         // copies still in flight land in this block's shared memory: wait (bounded)
@@ -394,49 +466,40 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         break;
       }
       // ---------------------------------------------------------- results
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-      }
-      if constexpr (SPLIT) {
-#pragma unroll
-        for (int i = 0; i < DG; ++i) {
-          o[i][0] += o[i][2];
-          o[i][1] += o[i][3];
-        }
-      }
+      // a thread: rows 2 t4 + f of each tile, channels DG g ..
       const int slot = 2 * worker + (u == pl.at ? 1 : 0);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int r = pl.tile * RT + g + 8 * e;
-        if (r >= rows) continue;
-        if (whole) {
-          const int i = r / G;
-          const float inv = l[e] > 0.0f ? 1.0f / l[e] : 0.0f;
-          T* dst = static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride + (size_t)(pl.h * G + r - i * G) * D;
+      for (int e = 0; e < E; ++e)
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            uint4* at = reinterpret_cast<uint4*>(dst + (2 * t4 + f) * DG);
+        for (int f = 0; f < 2; ++f) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[e][f] += __shfl_xor_sync(0xFFFFFFFFu, l[e][f], off);
+          const int r = e * 8 + 2 * t4 + f;
+          if (r >= rows) continue;
+          float v[DG];
+#pragma unroll
+          for (int i = 0; i < NJ; ++i) {
+            v[2 * i] = SPLIT ? o[i][0][f] + o[i][NT - 1][f] : o[i][e][f];
+            v[2 * i + 1] = SPLIT ? o[i][0][2 + f] + o[i][NT - 1][2 + f] : o[i][e][2 + f];
+          }
+          if (whole) {
+            const int i = r / G;
+            const float inv = l[e][f] > 0.0f ? 1.0f / l[e][f] : 0.0f;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride +
+                                                  (size_t)(pl.h * G + r - i * G) * D + g * DG);
 #pragma unroll
             for (int c = 0; c < DG / 8; ++c)
-              at[c] = make_uint4(pack2<T>(o[8 * c][2 * e + f] * inv, o[8 * c + 1][2 * e + f] * inv),
-                                 pack2<T>(o[8 * c + 2][2 * e + f] * inv, o[8 * c + 3][2 * e + f] * inv),
-                                 pack2<T>(o[8 * c + 4][2 * e + f] * inv, o[8 * c + 5][2 * e + f] * inv),
-                                 pack2<T>(o[8 * c + 6][2 * e + f] * inv, o[8 * c + 7][2 * e + f] * inv));
+              dst[c] = make_uint4(pack2<T>(v[8 * c] * inv, v[8 * c + 1] * inv), pack2<T>(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
+                                  pack2<T>(v[8 * c + 4] * inv, v[8 * c + 5] * inv),
+                                  pack2<T>(v[8 * c + 6] * inv, v[8 * c + 7] * inv));
+          } else {
+            const size_t at_row = (size_t)slot * RT + r;
+            float4* dst = reinterpret_cast<float4*>(a.rows.o + at_row * D + g * DG);
+#pragma unroll
+            for (int c = 0; c < DG / 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
           }
-        } else {
-          const size_t at_row = (size_t)slot * RT + g + 8 * e;
-          float* dst = a.rows.o + at_row * D;
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int c = 0; c < DG / 4; ++c)
-              reinterpret_cast<float4*>(dst + (2 * t4 + f) * DG)[c] =
-                  make_float4(o[4 * c][2 * e + f], o[4 * c + 1][2 * e + f], o[4 * c + 2][2 * e + f], o[4 * c + 3][2 * e + f]);
-          if (t4 == 0) a.rows.ml[at_row] = make_float2(m[e], l[e]);
         }
-      }
       if (u == pl.at && end < item_end) rec = {pl.b, pl.h, pl.tile, (int)((item_end - 1) / stretch)};
       u = min(end, item_end);
       if (u >= end || !next_place<RowsShare, RT, RK>(a, pl)) break;
@@ -449,29 +512,45 @@ __global__ void __launch_bounds__(RTHREADS, 1)
 }
 
 // ---------------------------------------------------------------- host
-template <int D, typename T>
+template <int D, int NT, typename T>
 static cudaError_t prepare_t() {
-  return cudaFuncSetAttribute(paged_attend_rows_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              RowsLayout<D>::ALLOC);
+  return cudaFuncSetAttribute(paged_attend_rows_kernel<D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              RowsLayout<D, NT>::ALLOC);
 }
 
-cudaError_t prepare_paged_rows(int D) {
-  const cudaError_t e = D == 128 ? prepare_t<128, __half>() : prepare_t<64, __half>();
-  if (e != cudaSuccess) return e;
-  return D == 128 ? prepare_t<128, __nv_bfloat16>() : prepare_t<64, __nv_bfloat16>();
+template <int D>
+static cudaError_t prepare_d() {
+  cudaError_t e = prepare_t<D, 2, __half>();
+  if (e == cudaSuccess) e = prepare_t<D, 1, __nv_bfloat16>();
+  return e == cudaSuccess ? prepare_t<D, 2, __nv_bfloat16>() : e;
 }
 
-template <int D, typename T>
+cudaError_t prepare_paged_rows(int D) { return D == 128 ? prepare_d<128>() : prepare_d<64>(); }
+
+// One column tile where no sequence of the call has more than 8 rows, as far
+// as the host knows: half of the MMAs, and half as many warps again.
+static int column_tiles(const PagedAttn& a, bool f16) { return f16 || (long long)a.max_new * a.pv.G > 8 ? 2 : 1; }
+
+int paged_rows_warps(const PagedAttn& a, bool f16) { return column_tiles(a, f16) == 1 ? kRowsWarps : 8; }
+
+template <int D, int NT, typename T>
 static cudaError_t rows_t(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int blocks,
                           cudaStream_t st) {
-  return launch_pdl(paged_attend_rows_kernel<D, T>, dim3(blocks), dim3(RTHREADS), RowsLayout<D>::ALLOC, st, tmK, tmV, a);
+  using LY = RowsLayout<D, NT>;
+  return launch_pdl(paged_attend_rows_kernel<D, NT, T>, dim3(blocks), dim3(32 * LY::RW), LY::ALLOC, st, tmK, tmV, a);
+}
+
+template <int D>
+static cudaError_t rows_d(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
+                          cudaStream_t st) {
+  if (f16) return rows_t<D, 2, __half>(a, tmK, tmV, blocks, st);
+  return column_tiles(a, f16) == 1 ? rows_t<D, 1, __nv_bfloat16>(a, tmK, tmV, blocks, st)
+                                   : rows_t<D, 2, __nv_bfloat16>(a, tmK, tmV, blocks, st);
 }
 
 cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                               cudaStream_t st) {
-  if (a.pv.D == 64)
-    return f16 ? rows_t<64, __half>(a, tmK, tmV, blocks, st) : rows_t<64, __nv_bfloat16>(a, tmK, tmV, blocks, st);
-  return f16 ? rows_t<128, __half>(a, tmK, tmV, blocks, st) : rows_t<128, __nv_bfloat16>(a, tmK, tmV, blocks, st);
+  return a.pv.D == 64 ? rows_d<64>(a, tmK, tmV, f16, blocks, st) : rows_d<128>(a, tmK, tmV, f16, blocks, st);
 }
 
 }  // namespace kvring_dev
