@@ -61,8 +61,10 @@ constexpr int kRowsWorkersMax = kPagedMaxSms * kRowsWarps;
 
 // What a worker leaves for the merge when an item it began ends in a later
 // worker's range: the item, and the last worker that holds a piece of it.
-struct PieceRec {
-  int32_t b, h, tile, last;       // b < 0: nothing to merge
+struct alignas(16) PieceRec {
+  int32_t rows;                   // of the item; 0: nothing to merge
+  int32_t last, h, s0, row0;      // row0: its first row among the sequence's
+  int32_t pad[3];
 };
 
 // Partial results: slot 2w holds the piece of an item begun before worker w's
@@ -103,7 +105,7 @@ cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const 
                               cudaStream_t st);
 cudaError_t launch_paged_tiles(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                                cudaStream_t st);
-cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int workers, cudaStream_t st);
+cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int blocks, cudaStream_t st);
 // tmK, tmV: the code arrays as [rows][D] u8, box {D, min(P, 32)}
 cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
                                 cudaStream_t st);

@@ -20,7 +20,7 @@ __device__ __forceinline__ void sum_pieces(const PieceScratch& ps, int w, int p,
   l = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (; p <= last; p += step) {
     const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * TR + r;
     const float2 ml = ps.ml[row];
@@ -46,84 +46,81 @@ __device__ __forceinline__ void sum_pieces(const PieceScratch& ps, int w, int p,
   }
 }
 
-// Block x looks at the records of workers 8 x .. 8 x + 7 (TR <= 16) or at that
-// of worker x, and takes rows y, y + gridDim.y, ... of its items.  An item of
-// few pieces: a row to a warp (a record to a warp, or the rows shared by the
-// warps); one of many (a long sequence spread over the GPU): a row to all eight
-// warps, warp i the pieces i, i + 8, ...
+// Block x looks at the records of ``per`` workers (at most 32, a lane each).
+// Few rows per item (TR <= 16): of an item of few pieces, row y to the warp
+// that has the record; of one of many pieces (a long sequence spread over the
+// GPU), row y to the whole block, warp i the pieces i, i + JW, ...
+// Many rows (one record per block): a row to a warp.
+constexpr int JW = 8;                                   // warps
 template <int D, int TR, typename T>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttn a, PieceScratch ps,
-                                                         int workers) {
-  constexpr int RECS = TR <= 16 ? 8 : 1;
+__global__ void __launch_bounds__(32 * JW) paged_join_kernel(const __grid_constant__ PagedAttn a, PieceScratch ps,
+                                                             int workers, int per) {
   constexpr int V = D / 32;                              // channels per lane
   constexpr int MANY = 12;                               // pieces
-  __shared__ float acc[8][D];
-  __shared__ float2 mls[8];
+  constexpr bool TALL = TR > 16;
+  __shared__ float acc[JW][D];
+  __shared__ float2 mls[JW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  struct Item {
-    PieceRec rec;
-    int w, rows, s0;
+  const int w0 = blockIdx.x * per;
+  PieceRec mine = {};
+  if (lane < per && w0 + lane < workers) mine = ps.rec[w0 + lane];
+  const bool long_ = !TALL && mine.last - (w0 + lane) >= MANY;
+  unsigned few = __ballot_sync(0xFFFFFFFFu, mine.rows > 0 && !long_);
+  unsigned many = __ballot_sync(0xFFFFFFFFu, mine.rows > 0 && long_);
+  auto record = [&](int i) {
+    PieceRec r;
+    r.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, i);
+    r.last = __shfl_sync(0xFFFFFFFFu, mine.last, i);
+    r.h = __shfl_sync(0xFFFFFFFFu, mine.h, i);
+    r.s0 = __shfl_sync(0xFFFFFFFFu, mine.s0, i);
+    r.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, i);
+    return r;
   };
-  auto item = [&](int w) {
-    Item it;
-    it.w = w;
-    it.rec.b = -1;
-    if (w < workers) it.rec = ps.rec[w];
-    it.rows = 0;
-    if (it.rec.b >= 0) {
-      bool ok;
-      const SeqInfo s = seq_info(a.pb, a.pv.p_shift, it.rec.b, ok);
-      it.rows = min(s.n * a.pv.G - it.rec.tile * TR, TR);
-      it.s0 = s.s0;
-    }
-    return it;
-  };
-  auto out_row = [&](const Item& it, int r) {
-    const int rr = it.rec.tile * TR + r;
+  auto out_row = [&](const PieceRec& it, int r) {
+    const int rr = it.row0 + r;
     const int i = rr / a.pv.G;
-    return static_cast<T*>(a.out) + (it.s0 + i) * a.out_stride + (size_t)(it.rec.h * a.pv.G + rr - i * a.pv.G) * D;
+    return reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + (it.s0 + i) * a.out_stride +
+                                       (size_t)(it.h * a.pv.G + rr - i * a.pv.G) * D);
   };
   float m, l, o[V];
-  bool many;
-  {
-    const Item it = item(RECS == 8 ? blockIdx.x * 8 + warp : blockIdx.x);
-    many = it.rec.b >= 0 && it.rec.last - it.w >= MANY;
-    if (!many)
-      for (int r = RECS == 8 ? blockIdx.y : blockIdx.y * 8 + warp; r < it.rows; r += gridDim.y * (RECS == 8 ? 1 : 8)) {
-        sum_pieces<V, TR>(ps, it.w, it.w, 1, it.rec.last, r, m, l, o);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(out_row(it, r)) + lane * (V / 2);
+  for (int k = 0; few; ++k, few &= few - 1) {
+    const int i = __ffs(few) - 1;
+    if (!TALL && k % JW != warp) continue;
+    const PieceRec it = record(i);
+    for (int r = TALL ? blockIdx.y * JW + warp : blockIdx.y; r < it.rows; r += gridDim.y * (TALL ? JW : 1)) {
+      sum_pieces<V, TR>(ps, w0 + i, w0 + i, 1, it.last, r, m, l, o);
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      uint32_t* dst = out_row(it, r) + lane * (V / 2);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) dst[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
-      }
+      for (int c = 0; c < V / 2; ++c) dst[c] = pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
+    }
   }
-  if (!__syncthreads_or(many)) return;
-  for (int w0 = 0; w0 < RECS; ++w0) {
-    const Item it = item(blockIdx.x * RECS + w0);
-    if (it.rec.b < 0 || it.rec.last - it.w < MANY) continue;
+  for (; many; many &= many - 1) {                       // the same in every warp
+    const int i = __ffs(many) - 1;
+    const PieceRec it = record(i);
     for (int r = blockIdx.y; r < it.rows; r += gridDim.y) {
-      sum_pieces<V, TR>(ps, it.w, it.w + warp, 8, it.rec.last, r, m, l, o);
+      sum_pieces<V, TR>(ps, w0 + i, w0 + i + warp, JW, it.last, r, m, l, o);
       if (lane == 0) mls[warp] = make_float2(m, l);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[warp][lane * V + i] = o[i];
+      for (int c = 0; c < V; ++c) acc[warp][lane * V + c] = o[c];
       __syncthreads();
       if (tid < D / 2) {
         float mm = -INFINITY, ll = 0.0f, o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mm = fmaxf(mm, mls[i].x);
+        for (int k = 0; k < JW; ++k) mm = fmaxf(mm, mls[k].x);
         if (mm != -INFINITY) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float f = ex2f(mls[i].x - mm);
-            ll += mls[i].y * f;
-            o0 += acc[i][2 * tid] * f;
-            o1 += acc[i][2 * tid + 1] * f;
+          for (int k = 0; k < JW; ++k) {
+            const float f = ex2f(mls[k].x - mm);
+            ll += mls[k].y * f;
+            o0 += acc[k][2 * tid] * f;
+            o1 += acc[k][2 * tid + 1] * f;
           }
         }
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        reinterpret_cast<uint32_t*>(out_row(it, r))[tid] = pack2<T>(o0 * inv, o1 * inv);
+        out_row(it, r)[tid] = pack2<T>(o0 * inv, o1 * inv);
       }
       __syncthreads();
     }
@@ -153,19 +150,22 @@ void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a) {
 }
 
 template <int D, typename T>
-static cudaError_t join_t(const PagedAttn& a, bool tiles, int workers, cudaStream_t st) {
+static cudaError_t join_t(const PagedAttn& a, bool tiles, int blocks, cudaStream_t st) {
   if (tiles)
-    return launch_pdl(paged_join_kernel<D, kTilesRows, T>, dim3(workers, 8), dim3(256), 0, st, a, a.tiles, workers);
+    return launch_pdl(paged_join_kernel<D, kTilesRows, T>, dim3(blocks, kTilesRows / JW / 4), dim3(32 * JW), 0, st, a,
+                      a.tiles, blocks, 1);
   const long long most = (long long)a.max_new * a.pv.G;
   const unsigned rows = (unsigned)(most < kRowsMax<T> ? most : kRowsMax<T>);
-  return launch_pdl(paged_join_kernel<D, kRowsMax<T>, T>, dim3((workers + 7) / 8, rows), dim3(256), 0, st, a, a.rows,
-                    workers);
+  const int workers = blocks * paged_rows_warps(a, std::is_same_v<T, __half>);
+  constexpr int per = 8;
+  return launch_pdl(paged_join_kernel<D, kRowsMax<T>, T>, dim3((workers + per - 1) / per, rows), dim3(32 * JW), 0, st, a,
+                    a.rows, workers, per);
 }
 
-cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int workers, cudaStream_t st) {
+cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int blocks, cudaStream_t st) {
   if (a.pv.D == 64)
-    return f16 ? join_t<64, __half>(a, tiles, workers, st) : join_t<64, __nv_bfloat16>(a, tiles, workers, st);
-  return f16 ? join_t<128, __half>(a, tiles, workers, st) : join_t<128, __nv_bfloat16>(a, tiles, workers, st);
+    return f16 ? join_t<64, __half>(a, tiles, blocks, st) : join_t<64, __nv_bfloat16>(a, tiles, blocks, st);
+  return f16 ? join_t<128, __half>(a, tiles, blocks, st) : join_t<128, __nv_bfloat16>(a, tiles, blocks, st);
 }
 
 // ---------------------------------------------------------------- one call
@@ -176,7 +176,7 @@ cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, cons
   const bool many = (long long)a.max_new * a.pv.G > few;
   cudaError_t e = launch_paged_rows(a, tmK, tmV, f16, blocks, st);
   if (e == cudaSuccess && many) e = launch_paged_tiles(a, tmK, tmV, f16, blocks, st);
-  if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks * paged_rows_warps(a, f16), st);
+  if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks, st);
   if (e == cudaSuccess && many) e = launch_paged_join(a, true, f16, blocks, st);
   return e;
 }

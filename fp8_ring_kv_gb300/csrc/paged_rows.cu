@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
   const long long stretch = (total + workers - 1) / workers;
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
-  PieceRec rec = {-1, 0, 0, 0};
+  PieceRec rec = {};
   int used = 0;                                          // stages issued so far: stage and phase of the next
   if (u < end) {
     Place pl = find_place<RowsShare, RT, RK>(a, pre, u);
@@ -215,6 +215,30 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       const int first = used;
       int issued = k0;
       load_ids(base, id);
+      // the queries' loads ahead of the first codes, which keep the memory busy for some microseconds
+      uint4 qw[E][D / 32];
+      float2 cs[E][D / 8];
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int r = e * 8 + g;
+        const bool live = r < rows;
+        const int i = live ? r / G : 0;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          qw[e][2 * c] = qw[e][2 * c + 1] = make_uint4(0, 0, 0, 0);
+          if (live) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + r - i * G) * D + c * 64 + t4 * 16);
+            qw[e][2 * c] = __ldg(src);
+            qw[e][2 * c + 1] = __ldg(src + 1);
+          }
+          float2 part8[8];
+          rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, part8, bad);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) cs[e][8 * c + k] = part8[k];
+        }
+      }
       while (issued < k1 && issued < k0 + NST) issue(issued++);
       load_scales(id, sk, sv);
       // ---------------------------------------------------------- queries
@@ -226,29 +250,9 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       int hi[E][2], lo[E][2];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int r = e * 8 + g;
-        const bool live = r < rows;
-        const int i = live ? r / G : 0;
-        uint4 w[D / 32];
-        float2 cs[D / 8];
         uint32_t mb = 0;
-        bool bad = false;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          w[2 * c] = w[2 * c + 1] = make_uint4(0, 0, 0, 0);
-          if (live) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + r - i * G) * D + c * 64 + t4 * 16);
-            w[2 * c] = __ldg(src);
-            w[2 * c + 1] = __ldg(src + 1);
-          }
-          float2 part[8];
-          rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, part, bad);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) cs[8 * c + k] = part[k];
-          mb = __vmaxu2(mb, __vmaxu2(max8_bits(w[2 * c]), max8_bits(w[2 * c + 1])));
-        }
-        if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
+        for (int c = 0; c < D / 32; ++c) mb = __vmaxu2(mb, max8_bits(qw[e][c]));
         mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 1));
         mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 2));
         const int ex = query_exponent<T>(mb);
@@ -257,11 +261,11 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           float x[8];
-          load8_f32<T>(w[k / 2], x);
+          load8_f32<T>(qw[e][k / 2], x);
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int at = 4 * (k & 1) + 2 * f;          // of the 8 values of the chunk
-            const float2 y = mul2(rope_query(x[at], x[at + 1], cs[2 * k + f]), make_float2(down, down));
+            const float2 y = mul2(rope_query(x[at], x[at + 1], cs[e][2 * k + f]), make_float2(down, down));
             const uint32_t p = cvt_f16x2(y.x, y.y);
             qb[e][k][f] = p;
             if constexpr (SPLIT) {
@@ -279,6 +283,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           lo[e][f] = rr < rows && a.window > 0 ? at - a.window + 1 : 0;
         }
       }
+      if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
       if (k0 < k1) {
         near_scale();
         for (int k = k0; k < issued; ++k) write_meta(k, first + k - k0);
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
           }
         }
-      if (u == pl.at && end < item_end) rec = {pl.b, pl.h, pl.tile, (int)((item_end - 1) / stretch)};
+      if (u == pl.at && end < item_end) rec = {rows, (int)((item_end - 1) / stretch), pl.h, pl.s.s0, 0};
       u = min(end, item_end);
       if (u >= end || !next_place<RowsShare, RT, RK>(a, pl)) break;
     }

@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       __syncwarp();
     } else if (warp == 13) {
       // ====================================================== the line of work
-      PieceRec rec = {-1, 0, 0, 0};
+      PieceRec rec = {};
       int done = 0, sg = 0;
       bool ok = true;
       for (bool more = u < end; ok; ++sg) {
@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           if (lane == 0) mbar_arrive(&meta_full[g % TMETA]);
         }
         done += k1 - k0;
-        if (u == pl.at && end < item_end) rec = {pl.b, pl.h, pl.tile, (int)((item_end - 1) / stretch)};
+        if (u == pl.at && end < item_end) 
+          rec = {min(pl.s.n * G - pl.tile * TTR, TTR), (int)((item_end - 1) / stretch), pl.h, pl.s.s0, pl.tile * TTR};
         u = min(end, item_end);
         more = u < end && next_place<SH, TTR, KT>(a, pl);
       }
