@@ -36,9 +36,10 @@ namespace kvring_dev {
 
 constexpr int RK = kRowsKeys;
 
-// NT: MMA column tiles.  1: up to 8 query rows; 2: up to 16, or, for fp16
-// queries, the high parts of up to 8 and their low parts (whose products are
-// summed: an fp16 result shows more than the 11 bits of one operand)
+// NT: MMA column tiles.  1: up to 8 query rows; 2: up to 16.  fp16 queries take
+// two columns a row, a high and a low part whose products are summed (an fp16
+// result shows more than the 11 bits of one operand): up to 4 rows in one tile,
+// the low parts in columns 4 .. 7, up to 8 in two, the low parts in the second.
 template <int D, int NT>
 struct RowsLayout {
   static constexpr int RW = NT == 1 ? kRowsWarps : 8;    // warps, as their registers allow
@@ -89,7 +90,9 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
   using LY = RowsLayout<D, NT>;
   constexpr int NST = LY::NST, RW = LY::RW;
   constexpr bool SPLIT = std::is_same_v<T, __half>;
-  constexpr int E = SPLIT ? 1 : NT;                      // tiles of 8 query rows
+  constexpr bool SIDE = SPLIT && NT == 1;                // low parts beside the high ones
+  constexpr int E = SPLIT ? 1 : NT;                      // tiles of query rows
+  constexpr int COLS = SIDE ? 4 : 8;                     // rows of a tile
   constexpr int RT = kRowsMax<T>;                        // rows of an item, at most
   using RowsShare = Share<RT, RK, 0, 0, RT>;
   constexpr int KS = D / 16;                             // k steps of QK
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       bool bad = false;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int r = e * 8 + g;
+        const int r = e * COLS + g % COLS;
         const bool live = r < rows;
         const int i = live ? r / G : 0;
 #pragma unroll
@@ -270,13 +273,15 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             qb[e][k][f] = p;
             if constexpr (SPLIT) {
               const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&p));
-              qb[1][k][f] = cvt_f16x2(y.x - z.x, y.y - z.y);
+              const uint32_t low = cvt_f16x2(y.x - z.x, y.y - z.y);
+              if constexpr (SIDE) qb[0][k][f] = g < COLS ? p : low;
+              else qb[1][k][f] = low;
             }
           }
         }
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int rr = e * 8 + 2 * t4 + f;
+          const int rr = e * COLS + (2 * t4 + f) % COLS;
           const int at = pl.s.len - pl.s.n + (rr < rows ? rr / G : 0);   // the row's own index
           rf[e][f] = __shfl_sync(0xFFFFFFFFu, rfg, 4 * (2 * t4 + f));
           hi[e][f] = rr >= rows ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
@@ -356,7 +361,9 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
 #pragma unroll
               for (int h8 = 0; h8 < 2; ++h8) {
                 const int i = 2 * h8 + f;
-                const float s = SPLIT ? c[j][0][i] + c[j][NT - 1][i] : c[j][e][i];
+                float s = c[j][e][i];
+                if constexpr (SIDE) s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+                else if constexpr (SPLIT) s += c[j][NT - 1][i];
                 float y = fmaf(s, rf[e][f] * (j ? m1.x : m0.x), j ? m1.y : m0.y);
                 if (cut) {
                   const int key = key0 + j * 16 + h8 * 8 + key_row(g);
@@ -382,9 +389,9 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
               for (int i = 0; i < NJ; ++i) {
                 o[i][e][f] *= al;
                 o[i][e][2 + f] *= al;
-                if constexpr (SPLIT) {
-                  o[i][1][f] *= al;
-                  o[i][1][2 + f] *= al;
+                if constexpr (SPLIT && !SIDE) {
+                  o[i][NT - 1][f] *= al;
+                  o[i][NT - 1][2 + f] *= al;
                 }
               }
             }
@@ -403,12 +410,14 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
               const float w0 = ex2f(c[j][e][2 * h8] + sub0), w1 = ex2f(c[j][e][2 * h8 + 1] + sub1);
               s0 += w0;
               s1 += w1;
-              const uint32_t w = cvt_f16x2(w0, w1);
-              pb[j][e][h8] = transpose8(w);
+              uint32_t w = cvt_f16x2(w0, w1);
               if constexpr (SPLIT) {
                 const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                pb[j][1][h8] = transpose8(cvt_f16x2(w0 - y.x, w1 - y.y));
+                const uint32_t low = cvt_f16x2(w0 - y.x, w1 - y.y);
+                if constexpr (SIDE) w = t4 < 2 ? w : low;
+                else pb[j][NT - 1][h8] = transpose8(low);
               }
+              pb[j][e][h8] = transpose8(w);
             }
             l[e][0] = fmaf(s0, iv, l[e][0]);
             l[e][1] = fmaf(s1, iv, l[e][1]);
@@ -479,14 +488,18 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
         for (int f = 0; f < 2; ++f) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) l[e][f] += __shfl_xor_sync(0xFFFFFFFFu, l[e][f], off);
-          const int r = e * 8 + 2 * t4 + f;
-          if (r >= rows) continue;
+          const int r = e * COLS + 2 * t4 + f;
           float v[DG];
 #pragma unroll
-          for (int i = 0; i < NJ; ++i) {
-            v[2 * i] = SPLIT ? o[i][0][f] + o[i][NT - 1][f] : o[i][e][f];
-            v[2 * i + 1] = SPLIT ? o[i][0][2 + f] + o[i][NT - 1][2 + f] : o[i][e][2 + f];
-          }
+          for (int i = 0; i < NJ; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float x = o[i][e][2 * k + f];
+              if constexpr (SIDE) x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+              else if constexpr (SPLIT) x += o[i][NT - 1][2 * k + f];
+              v[2 * i + k] = x;
+            }
+          if (r >= rows || 2 * t4 + f >= COLS) continue;
           if (whole) {
             const int i = r / G;
             const float inv = l[e][f] > 0.0f ? 1.0f / l[e][f] : 0.0f;
@@ -525,16 +538,17 @@ static cudaError_t prepare_t() {
 
 template <int D>
 static cudaError_t prepare_d() {
-  cudaError_t e = prepare_t<D, 2, __half>();
+  cudaError_t e = prepare_t<D, 1, __half>();
+  if (e == cudaSuccess) e = prepare_t<D, 2, __half>();
   if (e == cudaSuccess) e = prepare_t<D, 1, __nv_bfloat16>();
   return e == cudaSuccess ? prepare_t<D, 2, __nv_bfloat16>() : e;
 }
 
 cudaError_t prepare_paged_rows(int D) { return D == 128 ? prepare_d<128>() : prepare_d<64>(); }
 
-// One column tile where no sequence of the call has more than 8 rows, as far
-// as the host knows: half of the MMAs, and half as many warps again.
-static int column_tiles(const PagedAttn& a, bool f16) { return f16 || (long long)a.max_new * a.pv.G > 8 ? 2 : 1; }
+// One column tile where no sequence of the call has more rows than it holds,
+// as far as the host knows: half of the MMAs, and half as many warps again.
+static int column_tiles(const PagedAttn& a, bool f16) { return (long long)a.max_new * a.pv.G > (f16 ? 4 : 8) ? 2 : 1; }
 
 int paged_rows_warps(const PagedAttn& a, bool f16) { return column_tiles(a, f16) == 1 ? kRowsWarps : 8; }
 
@@ -548,7 +562,9 @@ static cudaError_t rows_t(const PagedAttn& a, const CUtensorMap& tmK, const CUte
 template <int D>
 static cudaError_t rows_d(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                           cudaStream_t st) {
-  if (f16) return rows_t<D, 2, __half>(a, tmK, tmV, blocks, st);
+  if (f16)
+    return column_tiles(a, f16) == 1 ? rows_t<D, 1, __half>(a, tmK, tmV, blocks, st)
+                                     : rows_t<D, 2, __half>(a, tmK, tmV, blocks, st);
   return column_tiles(a, f16) == 1 ? rows_t<D, 1, __nv_bfloat16>(a, tmK, tmV, blocks, st)
                                    : rows_t<D, 2, __nv_bfloat16>(a, tmK, tmV, blocks, st);
 }

@@ -193,60 +193,72 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       float m = -INFINITY, l = 0.0f;
       if (n > 0 && rows > 0) {
         // ------------------------------------------------------ queries
-        // a row by L lanes of 16 channels, 128 / L rows at a time
+        // a warp its own 32 rows, each by L lanes of 16 channels; four turns'
+        // loads in flight
         constexpr int L = D / 16;
+        constexpr int RSTEP = 32 / L;                    // rows per turn
+        constexpr int BATCH = 4;
+        static_assert(32 % (RSTEP * BATCH) == 0);
         const int ql = tid % L;
+        const int rr0 = 32 * (warp & 3) + lane / L;
         float* rfs = reinterpret_cast<float*>(sm + LY::RF) + t * TM_ROWS;
         const RopeLane rl = rope_lane(a.pv, ql * 8);
         bool bad = false;
         // the token and head of a row, carried from one turn to the next
-        constexpr int RSTEP = TM_ROWS / L;
         const int step_i = RSTEP / G, step_g = RSTEP - step_i * G;
-        int qi = (r0 + row / L) / G, qg = r0 + row / L - qi * G;
+        int qi = (r0 + rr0) / G, qg = r0 + rr0 - qi * G;
         const T* qp = static_cast<const T*>(a.q) + (size_t)head0 * D + ql * 16;
-#pragma unroll 4
-        for (int rr = row / L; rr < TM_ROWS; rr += RSTEP) {
-          // rows past the last: zeros
-          const bool on = rr < rows;
-          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-          if (on) {
-            const uint4* src = reinterpret_cast<const uint4*>(qp + (s0 + qi) * a.q_stride + qg * D);
-            w0 = __ldg(src);
-            w1 = __ldg(src + 1);
-          }
-          float2 cs[8];
-          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + (on ? qi : 0)) * a.pv.n_axes, cs, bad);
-          qi += step_i;
-          qg += step_g;
-          if (qg >= G) {
-            qg -= G;
-            ++qi;
-          }
-          uint32_t mb = __vmaxu2(max8_bits(w0), max8_bits(w1));
+#pragma unroll 1
+        for (int rr = rr0; rr < 32 * (warp & 3) + 32; rr += RSTEP * BATCH) {
+          uint4 w0[BATCH], w1[BATCH];
+          float2 cs[BATCH][8];
 #pragma unroll
-          for (int off = L / 2; off > 0; off >>= 1) mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
-          const int ex = query_exponent<T>(mb);
-          const float down = pow2f(-ex);
-          if (ql == 0) rfs[rr] = a.scale_log2 * pow2f(ex);
-          float x[16];
-          load8_f32<T>(w0, x);
-          load8_f32<T>(w1, x + 8);
-          uint8_t* dst = sm + LY::Q + t * NQ * LY::QB + (ql >> 2) * (TM_ROWS * 128) + rr * 128;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[4], v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 y = mul2(rope_query(x[8 * c + 2 * k], x[8 * c + 2 * k + 1], cs[4 * c + k]), make_float2(down, down));
-              w[k] = cvt_f16x2(y.x, y.y);
-              if constexpr (NQ == 2) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                v[k] = cvt_f16x2(y.x - f.x, y.y - f.y);
-              }
+          for (int k = 0; k < BATCH; ++k) {
+            const bool on = rr + k * RSTEP < rows;       // rows past the last: zeros
+            w0[k] = w1[k] = make_uint4(0, 0, 0, 0);
+            if (on) {
+              const uint4* src = reinterpret_cast<const uint4*>(qp + (s0 + qi) * a.q_stride + qg * D);
+              w0[k] = __ldg(src);
+              w1[k] = __ldg(src + 1);
             }
-            uint8_t* at = dst + (((2 * ql + c) & 7) ^ (rr & 7)) * 16;
-            *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-            if constexpr (NQ == 2) *reinterpret_cast<uint4*>(at + LY::QB) = make_uint4(v[0], v[1], v[2], v[3]);
+            rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + (on ? qi : 0)) * a.pv.n_axes, cs[k], bad);
+            qi += step_i;
+            qg += step_g;
+            if (qg >= G) {
+              qg -= G;
+              ++qi;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int rk = rr + k * RSTEP;
+            uint32_t mb = __vmaxu2(max8_bits(w0[k]), max8_bits(w1[k]));
+#pragma unroll
+            for (int off = L / 2; off > 0; off >>= 1) mb = __vmaxu2(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
+            const int ex = query_exponent<T>(mb);
+            const float down = pow2f(-ex);
+            if (ql == 0) rfs[rk] = a.scale_log2 * pow2f(ex);
+            float x[16];
+            load8_f32<T>(w0[k], x);
+            load8_f32<T>(w1[k], x + 8);
+            uint8_t* dst = sm + LY::Q + t * NQ * LY::QB + (ql >> 2) * (TM_ROWS * 128) + rk * 128;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[4], v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = mul2(rope_query(x[8 * c + 2 * e], x[8 * c + 2 * e + 1], cs[k][4 * c + e]),
+                                      make_float2(down, down));
+                w[e] = cvt_f16x2(y.x, y.y);
+                if constexpr (NQ == 2) {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                  v[e] = cvt_f16x2(y.x - f.x, y.y - f.y);
+                }
+              }
+              uint8_t* at = dst + (((2 * ql + c) & 7) ^ (rk & 7)) * 16;
+              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+              if constexpr (NQ == 2) *reinterpret_cast<uint4*>(at + LY::QB) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
         }
         if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
@@ -356,13 +368,30 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       if (!ok) break;
       tc_fence_after();
       // -------------------------------------------------------- results
+      // A thread has a row, memory wants rows side by side in a warp: through
+      // the warp's own rows of the query tile, which every MMA is done with.
       if (rows > 0) {
         const bool whole = flags & STRETCH_WHOLE;
         const size_t at_row = (size_t)(2 * worker + (flags & STRETCH_HEAD ? 1 : 0)) * TTR + t * TM_ROWS + row;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        T* dst = static_cast<T*>(a.out) + (s0 + i) * a.out_stride + (size_t)(head0 + (live ? r0 + row - i * G : 0)) * D;
-        if (!whole && live) a.tiles.ml[at_row] = make_float2(m, l);
-        if (whole || n > 0) {
+        uint8_t* own = sm + LY::Q + t * NQ * LY::QB + 32 * (warp & 3) * 128;
+        auto put = [&](int c, uint4 v) {                 // 16-byte chunk c of the thread's row
+          *reinterpret_cast<uint4*>(own + (c >> 3) * (TM_ROWS * 128) + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) = v;
+        };
+        auto flush = [&](auto chunks, void* dst) {       // that many chunks of every row to the row's dst
+          constexpr int N = decltype(chunks)::value;
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < N; ++i) {
+            const int rr = i * (32 / N) + lane / N, c = lane % N;
+            const unsigned long long p = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(dst), rr);
+            const uint4 v = *reinterpret_cast<const uint4*>(own + (c >> 3) * (TM_ROWS * 128) + rr * 128 +
+                                                            (((c & 7) ^ (rr & 7)) << 4));
+            if (p) reinterpret_cast<uint4*>(p)[c] = v;
+          }
+          __syncwarp();
+        };
+        if (whole) {
+          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -372,20 +401,32 @@ __global__ void __launch_bounds__(TTHREADS, 1)
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
-            if (live && whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t w[4];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = pack2<T>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                *reinterpret_cast<uint4*>(dst + c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<T>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+              put(c / 8 + k, make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          T* dst = static_cast<T*>(a.out) + (s0 + i) * a.out_stride + (size_t)(head0 + (live ? r0 + row - i * G : 0)) * D;
+          flush(std::integral_constant<int, D / 8>{}, live ? dst : nullptr);
+        } else {
+          if (live) a.tiles.ml[at_row] = make_float2(m, l);
+          if (n > 0) {
+            // half of the row at a time: a row has D * 2 bytes there
+#pragma unroll 1
+            for (int half = 0; half < D; half += D / 2) {
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + half + c, o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  put(c / 4 + k, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
               }
-            } else if (live) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(a.tiles.o + at_row * D + c + 4 * k) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              flush(std::integral_constant<int, D / 8>{}, live ? a.tiles.o + at_row * D + half : nullptr);
             }
           }
         }
