@@ -14,105 +14,156 @@
 
 namespace kvring_dev {
 
-// Block = 128 threads on one (page task, key head, K or V).  A row is handled
-// by L = D / 16 lanes of 16 channels each, ROWS = 128 / L rows at a time, and
-// a thread keeps the 16 fp32 values of up to P / ROWS rows until the block's
-// maximum is known, so the input is read once.
-//
+constexpr int kAppendFew = 4;   // tokens per sequence, on average, up to which the row kernel is taken
+
 // Tasks: sequence b touches at most floor(n_b / P) + 2 pages, so it owns the
 // task numbers base(b) .. base(b + 1) - 1 with base(b) = floor(seq_start[b] /
-// P) + 2 b; the block finds its b by counting the bases at or below its own
-// number, all sequences in parallel.
-template <int L, int P, typename T>
-__global__ void __launch_bounds__(128) paged_append_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k,
-                                                           long long k_stride, const T* __restrict__ v,
-                                                           long long v_stride, const int32_t* __restrict__ pos) {
-  constexpr int D = L * 16;
-  constexpr int ROWS = 128 / L;                         // rows per pass
-  constexpr int PASS = P > ROWS ? P / ROWS : 1;
+// P) + 2 b; a block finds its b by counting the bases at or below its own
+// number, all sequences in parallel, and with them loads the lengths.
+struct AppendTask {
+  int held;       // rows of the page that were there before
+  int cnt;        // new rows
+  int tok0;       // the first one's token
+  int page;       // -1: nothing to do
+};
+
+__device__ AppendTask append_task(const PagedView& pv, const PagedBatch& pb, int task, int* found) {
   const int tid = threadIdx.x;
-  // K and V of every head of a page are neighbouring blocks: together they
-  // read whole input rows, and the same rows of the RoPE table
+  AppendTask t = {0, 0, 0, -1};
+  int below = 0;
+  for (int i0 = 0; i0 < pb.n_seqs; i0 += blockDim.x) {
+    const int i = i0 + tid;
+    bool mine = false;
+    int s0 = 0, s1 = 0, len = 0, base = 0;
+    if (i < pb.n_seqs) {
+      s0 = __ldg(pb.seq_start + i);
+      s1 = __ldg(pb.seq_start + i + 1);
+      len = __ldg(pb.kv_len + i);
+      base = (min(max(s0, 0), pb.n_tokens) >> pv.p_shift) + 2 * i;
+      mine = base <= task;
+    }
+    const int upto = __syncthreads_count(mine);
+    below += upto;
+    // the last sequence so far whose tasks begin at or below this one
+    if (upto > 0 && tid == upto - 1) {
+      found[0] = s0;
+      found[1] = s1;
+      found[2] = len;
+      found[3] = base;
+    }
+    __syncthreads();
+  }
+  if (below == 0) return t;
+  const int b = below - 1;
+  const int s0 = found[0], s1 = found[1], len = found[2], j = task - found[3];
+  if (s0 < 0 || s1 < s0 || s1 > pb.n_tokens || len < s1 - s0 || (long long)len > ((long long)pb.table_width << pv.p_shift)) {
+    if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_SEQ);
+    return t;
+  }
+  const int first = len - (s1 - s0);                    // cache index of the first new token
+  const int slot = (first >> pv.p_shift) + j;           // the task's page of the sequence
+  const int lo = max(first, slot << pv.p_shift);
+  const int hi = min(len, (slot + 1) << pv.p_shift);
+  if (j < 0 || lo >= hi) return t;
+  t.held = lo - (slot << pv.p_shift);
+  t.cnt = hi - lo;
+  t.tok0 = s0 + (lo - first);
+  t.page = __ldg(pb.table + b * pb.table_stride + slot);
+  if (t.page < 0 || t.page >= pv.n_pages) {
+    if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_PAGE);
+    t.page = -1;
+  }
+  return t;
+}
+
+// The scale that a block of codes takes, and its inverse; true where it grew.
+__device__ __forceinline__ bool block_scale(float amax, float old, float& scale, float& inv) {
+  pow2_scale(amax, scale, inv);
+  if (scale > old) return true;
+  scale = old;
+  inv = old > 0.0f ? 1.0f / old : 0.0f;                 // a power of two: exact
+  return false;
+}
+
+// Whole pages: a block on one (page task, key head, K or V).  A row is handled
+// by L = D / 16 lanes of 16 channels each; a thread keeps the fp32 values of two
+// rows (where the page has as many) until the block's maximum is known, so the
+// input is read once.  More rows per thread would take the registers of the
+// warps that hide the loads' latency.
+// K and V of every head of a page are neighbouring blocks: together they read
+// whole input rows, and the same rows of the RoPE table.
+template <int L, int P>
+constexpr int append_threads = P * L / 2 < 128 ? 128 : P * L / 2;
+
+template <int L, int P, typename T>
+__global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L, P>)
+    paged_append_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k, long long k_stride,
+                        const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
+  constexpr int D = L * 16;
+  constexpr int THREADS = append_threads<L, P>;
+  constexpr int ROWS = THREADS / L;                     // rows per pass
+  constexpr int PASS = P > ROWS ? P / ROWS : 1;
+  __shared__ int found[4];
+  __shared__ float wmax[THREADS / 32];
+  const int tid = threadIdx.x;
   const int task = blockIdx.x / (2 * pv.H);
   const int h = (blockIdx.x - task * 2 * pv.H) >> 1;
   const bool is_v = blockIdx.x & 1;
   pdl_wait();
   pdl_trigger();
-  int b = -1;
-  for (int i0 = 0; i0 < pb.n_seqs; i0 += 128) {
-    const int i = i0 + tid;
-    const bool below = i < pb.n_seqs && (min(max(__ldg(pb.seq_start + i), 0), pb.n_tokens) >> pv.p_shift) + 2 * i <= task;
-    b += __syncthreads_count(below);
-  }
-  if (b < 0) return;
-  bool ok;
-  const SeqInfo s = seq_info(pb, pv.p_shift, b, ok);
-  ok = ok && s.n <= s.len;
-  const int j = ok ? task - ((s.s0 >> pv.p_shift) + 2 * b) : 0;
-  if (!ok) {
-    if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_SEQ);
-    return;
-  }
-  const int first = s.len - s.n;                        // cache index of the first new token
-  const int slot = (first >> pv.p_shift) + j;           // the task's page of the sequence
-  const int lo = max(first, slot << pv.p_shift);
-  const int hi = min(s.len, (slot + 1) << pv.p_shift);
-  if (j < 0 || lo >= hi) return;
-  const int page = __ldg(pb.table + b * pb.table_stride + slot);
-  if (page < 0 || page >= pv.n_pages) {
-    if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_PAGE);
-    return;
-  }
-  const int held = lo - (slot << pv.p_shift);           // rows of the page that were there before
-  const int cnt = hi - lo;
-  const int tok0 = s.s0 + (lo - first);
+  const AppendTask t = append_task(pv, pb, task, found);
+  if (t.cnt == 0) return;                               // the whole block
   const int lane = tid % L;
   const int row = tid / L;
-  const size_t blk = (size_t)page * pv.H + h;
-  uint8_t* codes = (is_v ? pv.v_codes : pv.k_codes) + blk * (size_t)(P * D) + lane * 16;
-  float* scale_at = (is_v ? pv.v_scale : pv.k_scale) + blk;
-  const float old = held > 0 ? *scale_at : 0.0f;
-
+  const T* src0 = (is_v ? v + t.tok0 * v_stride : k + t.tok0 * k_stride) + (size_t)h * D + lane * 16;
+  const long long stride = is_v ? v_stride : k_stride;
   float x[PASS][16];
   float amax = 0.0f;
   bool bad = false;
   const RopeLane rl = rope_lane(pv, lane * 8);
+  uint4 raw[PASS][2];
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int r = p * ROWS + row;
-    if (r < cnt) {
-      const int tok = tok0 + r;
-      const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + tok * v_stride : k + tok * k_stride) +
-                                                        (size_t)h * D + lane * 16);
-      const uint4 a0 = __ldg(src), a1 = __ldg(src + 1);
-      load8_f32<T>(a0, x[p]);
-      load8_f32<T>(a1, x[p] + 8);
-      if (!is_v) {
-        float2 cs[8];
-        rope_load(pv, rl, pos + (size_t)tok * pv.n_axes, cs, bad);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) rope_pair(x[p][2 * m], x[p][2 * m + 1], cs[m].x, cs[m].y);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[p][i]));
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (r < t.cnt) {
+      const uint4* src = reinterpret_cast<const uint4*>(src0 + r * stride);
+      raw[p][0] = __ldg(src);
+      raw[p][1] = __ldg(src + 1);
     }
   }
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+    const int r = p * ROWS + row;
+    load8_f32<T>(raw[p][0], x[p]);
+    load8_f32<T>(raw[p][1], x[p] + 8);
+    if (!is_v && r < t.cnt) {
+      float2 cs[8];
+      rope_load(pv, rl, pos + (size_t)(t.tok0 + r) * pv.n_axes, cs, bad);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) rope_pair(x[p][2 * m], x[p][2 * m + 1], cs[m].x, cs[m].y);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[p][i]));
+  }
   if (bad) atomicOr(&pv.state[PST_ERR], DEVERR_POS_RANGE);
-  __shared__ float wmax[4];
+  if (t.page < 0) return;                               // the whole block
+  const size_t blk = (size_t)t.page * pv.H + h;
+  uint8_t* codes = (is_v ? pv.v_codes : pv.k_codes) + blk * (size_t)(P * D) + lane * 16;
+  float* scale_at = (is_v ? pv.v_scale : pv.k_scale) + blk;
+  const float old = t.held > 0 ? *scale_at : 0.0f;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   if ((tid & 31) == 0) wmax[tid >> 5] = amax;
   __syncthreads();                                      // also: every thread has read the old scale
-  amax = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  amax = wmax[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 32; ++i) amax = fmaxf(amax, wmax[i]);
   float scale, inv;
-  pow2_scale(amax, scale, inv);
-  if (scale <= old) {
-    scale = old;
-    inv = old > 0.0f ? 1.0f / old : 0.0f;               // a power of two: exact
-  } else if (held > 0) {
+  if (block_scale(amax, old, scale, inv) && t.held > 0) {
     // the page's older codes at the larger scale (a row of zeros for old = 0)
     const float ratio = old * inv;
-    for (int r = row; r < held; r += ROWS) {
+    for (int r = row; r < t.held; r += ROWS) {
       uint4* at = reinterpret_cast<uint4*>(codes + r * D);
       float y[16];
       dequant16_codes(*at, y);
@@ -122,9 +173,81 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedView pv, PagedBa
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int r = p * ROWS + row;
-    if (r < cnt) *reinterpret_cast<uint4*>(codes + (held + r) * D) = quant16(x[p], inv);
+    if (r < t.cnt) *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = quant16(x[p], inv);
   }
   if (tid == 0) *scale_at = scale;
+}
+
+// A few tokens per sequence (decoding): a block on one page task, L lanes on
+// each (key head, K or V) of it, its rows one after the other: the lanes of a
+// row are all that its maximum needs, so nothing waits for a barrier, and a
+// token's heads are one block instead of 2 H.  Right for any number of rows (it
+// reads them twice), slow for many.
+template <int L, typename T>
+__global__ void __launch_bounds__(512)
+    paged_append_few_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k, long long k_stride,
+                            const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
+  constexpr int D = L * 16;
+  __shared__ int found[4];
+  pdl_wait();
+  pdl_trigger();
+  const AppendTask t = append_task(pv, pb, blockIdx.x, found);
+  if (t.cnt == 0) return;
+  const int lane = threadIdx.x % L;
+  const unsigned group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+  const RopeLane rl = rope_lane(pv, lane * 8);
+  bool bad = false;
+  for (int unit = threadIdx.x / L; unit < 2 * pv.H; unit += blockDim.x / L) {
+    const int h = unit >> 1;
+    const bool is_v = unit & 1;
+    const T* src0 = (is_v ? v + t.tok0 * v_stride : k + t.tok0 * k_stride) + (size_t)h * D + lane * 16;
+    const long long stride = is_v ? v_stride : k_stride;
+    auto load = [&](int r, float (&x)[16]) {
+      const uint4* src = reinterpret_cast<const uint4*>(src0 + r * stride);
+      const uint4 a0 = __ldg(src), a1 = __ldg(src + 1);
+      float2 cs[8];
+      if (!is_v) rope_load(pv, rl, pos + (size_t)(t.tok0 + r) * pv.n_axes, cs, bad);
+      load8_f32<T>(a0, x);
+      load8_f32<T>(a1, x + 8);
+      if (!is_v) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) rope_pair(x[2 * m], x[2 * m + 1], cs[m].x, cs[m].y);
+      }
+    };
+    float x[16];
+    float amax = 0.0f;
+#pragma unroll 2
+    for (int r = t.cnt - 1; r >= 0; --r) {              // ends with row 0's values in x
+      load(r, x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    }
+    if (t.page < 0) continue;
+    const size_t blk = (size_t)t.page * pv.H + h;
+    uint8_t* codes = (is_v ? pv.v_codes : pv.k_codes) + (blk << pv.p_shift) * D + lane * 16;
+    float* scale_at = (is_v ? pv.v_scale : pv.k_scale) + blk;
+    const float old = t.held > 0 ? *scale_at : 0.0f;
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, off));
+    float scale, inv;
+    if (block_scale(amax, old, scale, inv) && t.held > 0) {
+      const float ratio = old * inv;
+      for (int r = 0; r < t.held; ++r) {
+        uint4* at = reinterpret_cast<uint4*>(codes + r * D);
+        float y[16];
+        dequant16_codes(*at, y);
+        *at = quant16(y, ratio);
+      }
+    }
+#pragma unroll 2
+    for (int r = 0; r < t.cnt; ++r) {
+      if (r > 0) load(r, x);
+      *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = quant16(x, inv);
+    }
+    __syncwarp(group);                                  // every lane has read the old scale
+    if (lane == 0) *scale_at = scale;
+  }
+  if (bad) atomicOr(&pv.state[PST_ERR], DEVERR_POS_RANGE);
 }
 
 // ---------------------------------------------------------------- RoPE table
@@ -152,9 +275,17 @@ cudaError_t launch_paged_rope_table(float2* table, int pos_min, int pos_count, i
 template <int L, int P, typename T>
 static cudaError_t append_t(const PagedView& pv, const PagedBatch& pb, const void* k, long long k_stride,
                             const void* v, long long v_stride, const int32_t* pos, cudaStream_t st) {
-  const dim3 grid((unsigned)((pb.n_tokens / P + 2 * pb.n_seqs) * 2 * pv.H));
-  return launch_pdl(paged_append_kernel<L, P, T>, grid, dim3(128), 0, st, pv, pb, static_cast<const T*>(k), k_stride,
-                    static_cast<const T*>(v), v_stride, pos);
+  const long long tasks = pb.n_tokens / P + 2 * pb.n_seqs;
+  const T* kt = static_cast<const T*>(k);
+  const T* vt = static_cast<const T*>(v);
+  if (pb.n_tokens <= kAppendFew * pb.n_seqs) {
+    const int units = 2 * pv.H * L;                     // threads that a token's heads keep busy
+    const int threads = units < 128 ? 128 : units > 512 ? 512 : (units + 31) / 32 * 32;
+    return launch_pdl(paged_append_few_kernel<L, T>, dim3((unsigned)tasks), dim3(threads), 0, st, pv, pb, kt, k_stride,
+                      vt, v_stride, pos);
+  }
+  return launch_pdl(paged_append_kernel<L, P, T>, dim3((unsigned)(tasks * 2 * pv.H)), dim3(append_threads<L, P>), 0,
+                    st, pv, pb, kt, k_stride, vt, v_stride, pos);
 }
 
 template <int L, typename T>
