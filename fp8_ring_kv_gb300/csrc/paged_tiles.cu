@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   __syncthreads();                         // the prefix sums' room is the query tiles' now
 
   // ``done``: tiles of the line that a role has behind it; it gives the stage
-  // and phase of every barrier of a tile or of its steps.  Waits tell a phase
-  // only from the one before it, so a role that has nothing to do in a tile
-  // still waits for it.
+  // and phase of every barrier of a tile or of its steps.  A wait tells a phase
+  // only from the one before it, so no barrier may complete twice before all of
+  // its waiters have seen the first: a role that has nothing to do in a tile
+  // still waits, and arrives where the next phase needs that it has.
   if (warp < 8) {
     // ======================================================== softmax
     reg_inc<176>();
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + TM_S + 128 * t;
     const uint32_t o_at = tmem + lanes + TM_O + 128 * t;
-    int done = 0, steps = 0;               // steps: those of this query tile, of P's barriers
+    int done = 0, steps = 0;               // steps: of P's barriers
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -354,10 +355,13 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           if (!ok) break;
         }
       } else {
-        for (int j = 0; ok && j < n * SPT; ++j) {
+        for (int j = 0; ok && j < n * SPT; ++j, ++steps) {
           const int x = done * SPT + j;
           ok = warp_wait(&s_full[4 * t + (x & 3)], (x >> 2) & 1, abort_flag);
-          if (lane == 0 && x % SPT == SPT - 1) mbar_arrive(&meta_free[(x / SPT) % TMETA]);
+          if (lane == 0) {
+            mbar_arrive(&p_full[2 * t + (steps & 1)]);
+            if (x % SPT == SPT - 1) mbar_arrive(&meta_free[(x / SPT) % TMETA]);
+          }
         }
       }
       done += n;
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         const uint32_t q = smem_u32(sm + LY::Q) + t * NQ * LY::QB;
         const uint32_t kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
         const uint32_t o = tmem + TM_O + 128 * t, s = tmem + TM_S + 128 * t;
-        uint32_t nq = 0, np = 0;                         // stretches and steps of this query tile so far
+        uint32_t nq = 0, np = 0;                         // stretches of this query tile, and steps, so far
         int done = 0;
         // S of step x: 64 channels (a column block of 128-byte rows) per turn of the loop
         auto qk = [&](int x) {
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             if (j >= 0) {
               const int g = x / SPT;
               ok = (x % SPT != 0 || mbar_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag)) &&
-                   (!on || mbar_wait(&p_full[2 * t + (np & 1)], (np >> 1) & 1, abort_flag));
+                   mbar_wait(&p_full[2 * t + (np & 1)], (np >> 1) & 1, abort_flag);
               if (!ok) break;
               ++np;
               tc_fence_after();
@@ -568,7 +572,6 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               mma_commit(&s_full[4 * t + ((x + 2) & 3)]);
             }
           }
-          if (!on) np -= ns;                             // P's barriers count the steps of this query tile only
           done += seg.k1 - seg.k0;
           mbar_arrive(&seg_free[sg & 1]);
         }
