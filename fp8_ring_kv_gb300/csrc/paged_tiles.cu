@@ -16,23 +16,21 @@
 // beside which the softmax and the widening have to run.  A block works on two
 // tiles of 128 query rows over the same keys, so that each K and V tile is
 // loaded and widened once for 256 rows and the tensor cores work on one tile
-// while the softmax of the other runs.  S goes in steps of 64 keys through two
-// buffers per query tile, so that QK of a step runs while the softmax of the
-// one before it does (with one buffer of 128 keys, every tile was a chain of QK,
-// softmax and PV: 577 us for 512 tokens over 65,512 against XXX).  Tensor
-// memory is full: two S (then P) buffers and O of both query tiles.
+// while the softmax of the other runs.  Tensor memory is full: S (then P) and O
+// of both.  S is 128 keys wide in one product: with two buffers of 64 keys QK
+// could run ahead of the softmax, but a 128 x 64 x 16 product from shared memory
+// takes 58 cycles, hardly less than a 128 x 128 x 16 one.
 //
-// Warp roles (512 threads, registers moved from the last two groups to the softmax):
-//   warps 0-3, 4-7   softmax of query tile 0, 1: one row per thread.  They also
-//                    load and rotate the rows' queries and write the output
-//   warps 8-11       K and V codes widened to fp16, shared memory to shared memory
-//   warps 12, 15     MMA issue for query tile 0, 1
-//   warp 13          the line of work: the stretches of items for the others,
-//                    and per tile the page ids and scales, up to TMETA tiles ahead
-//   warp 14          TMA: the codes of a tile, page by page
+// Warp roles (640 threads, registers moved from the last group to the softmax):
+//   warps 0-15       softmax: of query tile t and half p of its keys, warps
+//                    8 p + 4 t .. + 3, one row per thread: two warps share a row.
+//                    They also load and rotate the rows' queries and write the output
+//   warp 16          MMA issue
+//   warp 17          the line of work: the stretches of items for the others,
+//                    per tile the page ids and scales, and TMA of the codes
+//   warps 18, 19     K and V codes widened to fp16, shared memory to shared memory
 // MMAs of one thread run in the order they are issued: QK may overwrite the P
-// that the PV before it reads.  A query tile has an issuing thread of its own,
-// since a wait costs a thread about as much as an MMA takes.
+// that the PV before it reads.
 #include "paged_sched.cuh"
 #include "launch.h"
 
@@ -41,9 +39,8 @@ namespace kvring_dev {
 constexpr int TM_ROWS = 128;                 // rows of one MMA
 constexpr int TTR = kTilesRows;              // rows of an item: two query tiles
 static_assert(TTR == 2 * TM_ROWS);
-constexpr int TTHREADS = 512;
-constexpr int STEP_KEYS = 64;                // keys of one S buffer
-constexpr int TMETA = 8;                     // stages of page ids and scales
+constexpr int TTHREADS = 640;
+constexpr int TMETA = 3;                     // stages of page ids and scales
 constexpr float kRaise = 8.0f;               // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kTop = 6.0f;                 // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
 
@@ -57,7 +54,6 @@ template <int D, typename T>
 struct TilesLayout {
   static constexpr int NQ = std::is_same_v<T, __half> ? 2 : 1;   // fp16 parts of a query
   static constexpr int KT = NQ == 2 ? 64 : 128;                  // keys per K and V tile
-  static constexpr int SPT = KT / STEP_KEYS;                     // steps of S per tile
   static constexpr int QB = TM_ROWS * D * 2;                     // one part of one query tile
   static constexpr int KB = KT * D * 2;                          // one widened K or V tile
   static constexpr int Q = 0;                                    // [2 tiles][NQ]
@@ -65,12 +61,11 @@ struct TilesLayout {
   static constexpr int VH = KH + 2 * KB;                         // [2]
   static constexpr int RAW = VH + 2 * KB;                        // K codes, V codes of one tile
   static constexpr int META = RAW + 2 * KT * D;                  // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, page}
-  static constexpr int RF = META + TMETA * (KT / 16) * 16;       // [256] logit factor of a row
-  static constexpr int SEG = RF + TTR * 4;                       // [2] Stretch
+  static constexpr int SLOT = META + TMETA * (KT / 16) * 16;     // [2 halves][256] a row's logit factor; maxima; sums
+  static constexpr int SEG = SLOT + 2 * TTR * 4;                 // [2] Stretch
   static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
-  static constexpr int NBAR = 2 + 2 + 2 + 2 * TMETA + 8 + 8 + 4 + 4 + 4 + 2;
-  static constexpr int SUMS = BAR + NBAR * 8;
-  static constexpr int MISC = SUMS + 16 * 8;
+  static constexpr int NBAR = 2 + 2 + 2 + TMETA + 4 + 4 + 2 + 4 + 4 + 1 + 16 + 8;
+  static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;                        // the block's shared memory starts 1024-byte aligned
   static_assert(ALLOC <= 232448, "shared memory of a block");
   static_assert(KH >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the query tiles at first");
@@ -90,7 +85,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     paged_attend_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                               const __grid_constant__ PagedAttn a) {
   using LY = TilesLayout<D, T>;
-  constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16, SPT = LY::SPT;
+  constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16;
+  constexpr int SC = KT / 2;               // keys of a tile that a softmax warp looks at
   using SH = Share<TTR, KT, 2, kRowsMax<T>, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr int kNone = -1;                // page of a group of keys that no query sees
@@ -99,48 +95,50 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   uint64_t* q_full = bars;                 // [2] query tile written (once per stretch)
   uint64_t* kh_full = q_full + 2;          // [2] K tile widened
   uint64_t* vh_full = kh_full + 2;         // [2] V tile widened
-  uint64_t* meta_full = vh_full + 2;       // [TMETA] page ids and scales of a tile written
-  uint64_t* meta_free = meta_full + TMETA; // [TMETA] the tile's softmax is done
-  uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][4 steps] QK done
-  uint64_t* pv_done = s_full + 8;          // [2][4] PV done
-  uint64_t* p_full = pv_done + 8;          // [2][2] P stored
-  uint64_t* raw_full = p_full + 4;         // [2] K codes, V codes landed
+  uint64_t* meta_free = vh_full + 2;       // [TMETA] the tile's softmax is done
+  uint64_t* s_full = meta_free + TMETA;    // [2 query tiles][2] QK done
+  uint64_t* o_done = s_full + 4;           // [2][2] PV done
+  uint64_t* p_full = o_done + 4;           // [2] P stored
+  uint64_t* raw_full = p_full + 2;         // [2] K codes, V codes landed
   uint64_t* raw_free = raw_full + 2;       // [2] and read
   uint64_t* seg_full = raw_free + 2;       // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2] every role is done with it
-  uint64_t* drain = seg_free + 2;          // [2] every MMA of an issuing thread done
+  uint64_t* drain = seg_free + 2;          // every MMA done
+  uint64_t* m_ready = drain + 1;           // [2][4 warps][2 halves] a half's maxima written
+  uint64_t* both = m_ready + 16;           // [2][4] both warps of a row are here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile Stretch* segs = reinterpret_cast<volatile Stretch*>(sm + LY::SEG);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
-      mbar_init(&kh_full[i], 4);
-      mbar_init(&vh_full[i], 4);
+      mbar_init(&q_full[i], 8);
+      mbar_init(&kh_full[i], 2);
+      mbar_init(&vh_full[i], 2);
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_free[i], 4);
+      mbar_init(&raw_free[i], 2);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], 15);
-      mbar_init(&drain[i], 1);
+      mbar_init(&seg_free[i], 19);
     }
     for (int i = 0; i < TMETA; ++i) {
-      mbar_init(&meta_full[i], 1);
-      mbar_init(&meta_free[i], 8);
+      mbar_init(&meta_free[i], 16);
     }
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 8);
+    for (int i = 0; i < 16; ++i) mbar_init(&m_ready[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&both[i], 2);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 14 && lane == 0) {
+  if (warp == 17 && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -151,7 +149,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   pdl_trigger();
   // this block's stretch of the line of items
   long long* pre = reinterpret_cast<long long*>(sm + LY::Q);
-  SH::template prefix<TTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SUMS), false);
+  SH::template prefix<TTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SLOT), false);
   const int H = a.pv.H, G = a.pv.G;
   const long long total = pre[a.pb.n_seqs] * H;
   long long stretch = (total + gridDim.x - 1) / gridDim.x;
@@ -160,23 +158,34 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
   Place pl;
-  if (warp == 13 && u < end) pl = find_place<SH, TTR, KT>(a, pre, u);
+  if (warp == 17 && u < end) pl = find_place<SH, TTR, KT>(a, pre, u);
   __syncthreads();                         // the prefix sums' room is the query tiles' now
 
   // ``done``: tiles of the line that a role has behind it; it gives the stage
-  // and phase of every barrier of a tile or of its steps.  A wait tells a phase
-  // only from the one before it, so no barrier may complete twice before all of
-  // its waiters have seen the first: a role that has nothing to do in a tile
-  // still waits, and arrives where the next phase needs that it has.
-  if (warp < 8) {
+  // and phase of every per-tile barrier.  Waits tell a phase only from the one
+  // before it, so no barrier may complete twice before all of its waiters have
+  // seen the first: a role that has nothing to do in a tile still waits, and
+  // arrives where the next phase needs that it has.
+  if (warp < 16) {
     // ======================================================== softmax
-    reg_inc<176>();
-    const int t = warp >> 2;
+    reg_inc<104>();
+    const int t = (warp >> 2) & 1;
+    const int par = warp >> 3;
     const int row = tid & 127;
+    float* slots = reinterpret_cast<float*>(sm + LY::SLOT) + t * TM_ROWS + row;
+    float *mine = slots + par * TTR, *other = slots + (par ^ 1) * TTR;
+    const int pair = 4 * t + (warp & 3);   // the two warps of these rows
+    uint32_t nb = 0, tiles = 0;            // phases of ``both``, and of the barriers of this query tile's key tiles
+    auto meet = [&]() {                    // the other warp need not be here yet
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&both[pair]);
+      ++nb;
+    };
+    auto met = [&]() -> bool { return warp_wait(&both[pair], (nb - 1) & 1, abort_flag); };
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_at = tmem + lanes + TM_S + 128 * t;
+    const uint32_t s_at = tmem + lanes + TM_S + 128 * t + SC * par;
     const uint32_t o_at = tmem + lanes + TM_O + 128 * t;
-    int done = 0, steps = 0;               // steps: of P's barriers
+    int done = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -192,17 +201,18 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       const int hi = !live ? 0x7FFFFFFF : a.causal ? len_n + i + 1 : seg.len;
       const int lo = live && a.window > 0 ? len_n + i - a.window + 1 : 0;
       float m = -INFINITY, l = 0.0f;
+      if (nb > 0 && !met()) break;                       // the other warp is done with the last stretch
       if (n > 0 && rows > 0) {
         // ------------------------------------------------------ queries
-        // a warp its own 32 rows, each by L lanes of 16 channels; four turns'
-        // loads in flight
+        // the pair its own 32 rows, a warp every other turn, a row by L lanes of
+        // 16 channels; the turns' loads in flight together
         constexpr int L = D / 16;
         constexpr int RSTEP = 32 / L;                    // rows per turn
-        constexpr int BATCH = 4;
-        static_assert(32 % (RSTEP * BATCH) == 0);
+        constexpr int BATCH = 2;
+        static_assert(32 % (2 * RSTEP * BATCH) == 0);
         const int ql = tid % L;
-        const int rr0 = 32 * (warp & 3) + lane / L;
-        float* rfs = reinterpret_cast<float*>(sm + LY::RF) + t * TM_ROWS;
+        const int rr0 = 32 * (warp & 3) + 16 * par + lane / L;
+        float* rfs = reinterpret_cast<float*>(sm + LY::SLOT) + t * TM_ROWS;
         const RopeLane rl = rope_lane(a.pv, ql * 8);
         bool bad = false;
         // the token and head of a row, carried from one turn to the next
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         int qi = (r0 + rr0) / G, qg = r0 + rr0 - qi * G;
         const T* qp = static_cast<const T*>(a.q) + (size_t)head0 * D + ql * 16;
 #pragma unroll 1
-        for (int rr = rr0; rr < 32 * (warp & 3) + 32; rr += RSTEP * BATCH) {
+        for (int rr = rr0; rr < 32 * (warp & 3) + 16 * par + 16; rr += RSTEP * BATCH) {
           uint4 w0[BATCH], w1[BATCH];
           float2 cs[BATCH][8];
 #pragma unroll
@@ -266,55 +276,66 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
+        meet();
+        if (!met()) ok = false;
+        const float rf = slots[0];
+        meet();                                          // (both have read it: waited for before the first maxima)
         // ------------------------------------------------------ key tiles
-        // steps below j_lo and from j_hi on hold keys that some row of the warp does not see
-        const int j_hi = __reduce_min_sync(0xFFFFFFFFu, hi >= k0 * KT ? (hi - k0 * KT) / STEP_KEYS : 0);
-        const int j_lo = __reduce_max_sync(0xFFFFFFFFu, (lo - k0 * KT + STEP_KEYS - 1) / STEP_KEYS);
-        float rf = 0.0f;
+        // tiles below j_lo and from j_hi on hold keys that some row of the warp does not see
+        const int past = hi - k0 * KT - (par + 1) * SC, before = lo - k0 * KT - par * SC;
+        const int j_hi = __reduce_min_sync(0xFFFFFFFFu, past >= 0 ? past / KT + 1 : 0);
+        const int j_lo = __reduce_max_sync(0xFFFFFFFFu, before > 0 ? (before + KT - 1) / KT : 0);
 #pragma unroll 1
-        for (int j = 0; j < n * SPT; ++j, ++steps) {
-          const int x = done * SPT + j;
-          if (!warp_wait(&s_full[4 * t + (x & 3)], (x >> 2) & 1, abort_flag)) {
+        for (int j = 0; ok && j < n; ++j, ++tiles) {
+          const int g = done + j;
+          if (!warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sb = s_at + 64 * (x & 1);
-          uint32_t xr[64];
-          tmem_ld_32x32b_x64(sb, xr);
-          float* s = reinterpret_cast<float*>(xr);
-          if (j == 0) rf = rfs[row];       // written before q_full, which S waited for
-          const int stage = (x / SPT) % TMETA;
-          const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + stage * NG + (x % SPT) * 4;
+          const int stage = g % TMETA;
+          const float4* meta = reinterpret_cast<const float4*>(sm + LY::META) + stage * NG + par * (NG / 2);
+          uint32_t xr[SC];
+          if constexpr (SC == 64) tmem_ld_32x32b_x64(s_at, xr);
+          else tmem_ld_32x32b_x32(s_at, xr);
           if (j >= j_hi || j < j_lo) {
-            const int key0 = k0 * KT + j * STEP_KEYS;
+            const int key0 = (k0 + j) * KT + par * SC;
 #pragma unroll
-            for (int k = 0; k < STEP_KEYS; ++k)
-              if (key0 + k >= hi || key0 + k < lo) s[k] = -INFINITY;
+            for (int k = 0; k < SC; ++k)
+              if (key0 + k >= hi || key0 + k < lo) xr[k] = 0xFF800000u;   // -inf
           }
-          float4 mt[4];
-          float f[4], my = -INFINITY;
+          const float* s = reinterpret_cast<const float*>(xr);
+          // a factor is never 0, so that a masked score stays -inf
+          float my = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mt[q] = meta[q];
-            f[q] = fmaxf(rf * mt[q].x, 0x1p-100f);       // never 0, so that a masked score stays -inf
+          for (int q = 0; q < SC / 16; ++q) {
+            const float2 mt = *reinterpret_cast<const float2*>(meta + q);
             const float* v = s + 16 * q;
             const float a0 = max3f(v[0], v[1], v[2]), a1 = max3f(v[3], v[4], v[5]), a2 = max3f(v[6], v[7], v[8]);
             const float a3 = max3f(v[9], v[10], v[11]), a4 = max3f(v[12], v[13], fmaxf(v[14], v[15]));
-            my = fmaxf(my, fmaf(max3f(max3f(a0, a1, a2), a3, a4), f[q], mt[q].y));
+            my = fmaxf(my, fmaf(max3f(max3f(a0, a1, a2), a3, a4), fmaxf(rf * mt.x, 0x1p-100f), mt.y));
           }
-          if (__any_sync(0xFFFFFFFFu, my > m + kRaise)) {
+          // the row's maximum: the other half's keys are the other warp's.  Both
+          // see the same numbers and do the same.
+          if (j == 0 && !met()) ok = false;
+          *mine = my;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m_ready[2 * pair + par]);
+          if (!warp_wait(&m_ready[2 * pair + (par ^ 1)], tiles & 1, abort_flag)) ok = false;
+          const float mm = fmaxf(my, *other);
+          if (__any_sync(0xFFFFFFFFu, mm > m + kRaise)) {
             // rare after a row's first keys: what was summed with the old
             // maximum is brought to the new one
-            const float mn = my > m + kRaise ? my : m;
+            const float mn = mm > m + kRaise ? mm : m;
             const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
             m = mn;
             l *= al;
             if (j > 0) {
-              if (!warp_wait(&pv_done[4 * t + ((x - 1) & 3)], ((x - 1) >> 2) & 1, abort_flag)) ok = false;
+              // QK of this tile was issued after the PV before it, so that one is done
+              if (!warp_wait(&o_done[2 * t + ((g - 1) & 1)], ((g - 1) >> 1) & 1, abort_flag)) ok = false;
               tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < D; k += 16) {
+              for (int k = par * (D / 2); k < (par + 1) * (D / 2); k += 16) {
                 uint32_t o[16];
                 tmem_ld_32x32b_x16(o_at + k, o);
 #pragma unroll
@@ -325,71 +346,76 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           }
           const float sub = m == -INFINITY ? 0.0f : kTop - m;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < SC / 32; ++c) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int q = 2 * c + e;
-              const float ad = mt[q].y + sub;
-              float2 sum = make_float2(0.0f, 0.0f);
+              const float4 mt = meta[q];
+              const float f = fmaxf(rf * mt.x, 0x1p-100f), ad = mt.y + sub;
+              float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                float2 y = fma2(make_float2(s[16 * q + 2 * k], s[16 * q + 2 * k + 1]), make_float2(f[q], f[q]),
+                float2 y = fma2(make_float2(s[16 * q + 2 * k], s[16 * q + 2 * k + 1]), make_float2(f, f),
                                 make_float2(ad, ad));
                 y.x = ex2f(y.x);
                 y.y = ex2f(y.y);
-                sum = add2(sum, y);
+                part = add2(part, y);
                 p[8 * e + k] = cvt_f16x2(y.x, y.y);
               }
-              l = fmaf(sum.x + sum.y, mt[q].z, l);
+              l = fmaf(part.x + part.y, mt.z, l);
             }
-            tmem_st_32x32b_x16(sb + 16 * c, p);
+            tmem_st_32x32b_x16(s_at + 16 * c, p);
           }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&p_full[2 * t + (steps & 1)]);
-            if (x % SPT == SPT - 1) mbar_arrive(&meta_free[stage]);
+            mbar_arrive(&p_full[t]);
+            mbar_arrive(&meta_free[stage]);
           }
-          if (!ok) break;
         }
       } else {
-        for (int j = 0; ok && j < n * SPT; ++j, ++steps) {
-          const int x = done * SPT + j;
-          ok = warp_wait(&s_full[4 * t + (x & 3)], (x >> 2) & 1, abort_flag);
+        for (int j = 0; ok && j < n; ++j) {
+          const int g = done + j;
+          ok = warp_wait(&s_full[2 * t + (g & 1)], (g >> 1) & 1, abort_flag);
           if (lane == 0) {
-            mbar_arrive(&p_full[2 * t + (steps & 1)]);
-            if (x % SPT == SPT - 1) mbar_arrive(&meta_free[(x / SPT) % TMETA]);
+            mbar_arrive(&p_full[t]);
+            mbar_arrive(&meta_free[g % TMETA]);
           }
         }
       }
       done += n;
-      if (ok && n > 0) {
-        const int x = done * SPT - 1;
-        ok = warp_wait(&pv_done[4 * t + (x & 3)], (x >> 2) & 1, abort_flag);
-      }
+      if (ok && n > 0) ok = warp_wait(&o_done[2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
+      if (n > 0 && rows > 0) {
+        // the row's sum: both halves
+        *mine = l;
+        meet();
+        if (!met()) break;
+        l = slots[0] + slots[TTR];
+      }
       // -------------------------------------------------------- results
-      // A thread has a row, memory wants rows side by side in a warp: through
-      // the warp's own rows of the query tile, which every MMA is done with.
+      // Half of the channels per warp.  A thread has a row, memory wants rows side
+      // by side in a warp: through half of the warp's rows of the query tile,
+      // which every MMA is done with.
       if (rows > 0) {
         const bool whole = flags & STRETCH_WHOLE;
         const size_t at_row = (size_t)(2 * worker + (flags & STRETCH_HEAD ? 1 : 0)) * TTR + t * TM_ROWS + row;
-        uint8_t* own = sm + LY::Q + t * NQ * LY::QB + 32 * (warp & 3) * 128;
-        auto put = [&](int c, uint4 v) {                 // 16-byte chunk c of the thread's row
-          *reinterpret_cast<uint4*>(own + (c >> 3) * (TM_ROWS * 128) + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) = v;
+        constexpr int HC = D / 16;                       // 16-byte chunks of half a row of the tile
+        uint8_t* own = sm + LY::Q + t * NQ * LY::QB + 32 * (warp & 3) * 128 + (D == 128 ? par * (TM_ROWS * 128) : 0);
+        const int c0 = D == 128 ? 0 : par * HC;          // the warp's chunks of the 128-byte row
+        auto put = [&](int c, uint4 v) {                 // chunk c of the thread's row
+          *reinterpret_cast<uint4*>(own + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4)) = v;
         };
-        auto flush = [&](auto chunks, void* dst) {       // that many chunks of every row to the row's dst
-          constexpr int N = decltype(chunks)::value;
+        auto flush = [&](void* dst) {                    // the chunks of every row to the row's dst
           __syncwarp();
-#pragma unroll 4
-          for (int i = 0; i < N; ++i) {
-            const int rr = i * (32 / N) + lane / N, c = lane % N;
+#pragma unroll
+          for (int i = 0; i < HC; ++i) {
+            const int rr = i * (32 / HC) + lane / HC, c = lane % HC;
             const unsigned long long p = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(dst), rr);
-            const uint4 v = *reinterpret_cast<const uint4*>(own + (c >> 3) * (TM_ROWS * 128) + rr * 128 +
-                                                            (((c & 7) ^ (rr & 7)) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(own + rr * 128 + (((c0 + c) ^ (rr & 7)) << 4));
             if (p) reinterpret_cast<uint4*>(p)[c] = v;
           }
           __syncwarp();
@@ -397,16 +423,16 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         if (whole) {
           const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
+          for (int c = 0; c < D / 2; c += 16) {
+            uint32_t o[16];
             if (n > 0) {
-              tmem_ld_32x32b_x32(o_at + c, o);
+              tmem_ld_32x32b_x16(o_at + par * (D / 2) + c, o);
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = 0u;
+              for (int k = 0; k < 16; ++k) o[k] = 0u;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -414,176 +440,117 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               put(c / 8 + k, make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
-          T* dst = static_cast<T*>(a.out) + (s0 + i) * a.out_stride + (size_t)(head0 + (live ? r0 + row - i * G : 0)) * D;
-          flush(std::integral_constant<int, D / 8>{}, live ? dst : nullptr);
+          T* dst = static_cast<T*>(a.out) + (s0 + i) * a.out_stride +
+                   (size_t)(head0 + (live ? r0 + row - i * G : 0)) * D + par * (D / 2);
+          flush(live ? dst : nullptr);
         } else {
-          if (live) a.tiles.ml[at_row] = make_float2(m, l);
+          if (live && par == 0) a.tiles.ml[at_row] = make_float2(m, l);
           if (n > 0) {
-            // half of the row at a time: a row has D * 2 bytes there
+            // fp32: half of the warp's channels at a time
 #pragma unroll 1
-            for (int half = 0; half < D; half += D / 2) {
+            for (int h4 = par * (D / 2); h4 < (par + 1) * (D / 2); h4 += D / 4) {
 #pragma unroll 1
-              for (int c = 0; c < D / 2; c += 32) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_at + half + c, o);
+              for (int c = 0; c < D / 4; c += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_at + h4 + c, o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 4; ++k)
                   put(c / 4 + k, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
               }
-              flush(std::integral_constant<int, D / 8>{}, live ? a.tiles.o + at_row * D + half : nullptr);
+              flush(live ? a.tiles.o + at_row * D + h4 : nullptr);
             }
           }
         }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
-    }
-  } else if (warp < 12) {
-    // ======================================================== K, V
-    reg_dec<104>();
-    const int ct = tid - 256;
-    constexpr int CH = D / 16;                           // 16-byte code chunks of a row
-    constexpr int NT = KT * CH / 128;                    // chunks of K, and of V, per thread
-    constexpr int STEP = KT / NT;                        // rows per round of the 128 threads
-    const int sl0 = CH == 8 ? 8 * (ct >> 6) + (ct & 7) : 8 * (ct >> 5) + (ct & 7);
-    const int ch = (ct >> 3) & (CH - 1);
-    int done = 0;
-    bool ok = true;
-    for (int sg = 0; ok; ++sg) {
-      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
-      const volatile Stretch& seg = segs[sg & 1];
-      if (!(seg.flags & STRETCH_SOME)) break;
-      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
-#pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        const int g = done + j;
-        const int buf = g & 1;
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {                    // K, then V
-          if (!warp_wait(&raw_full[v], g & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint8_t* src = sm + LY::RAW + v * KT * D;
-          uint4 reg[NT];
-#pragma unroll
-          for (int it = 0; it < NT; ++it) reg[it] = *reinterpret_cast<const uint4*>(src + raw_chunk<D>(it * STEP + sl0, ch));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_free[v]);
-          const int key0 = (k0 + j) * KT;
-          if (v && (key0 + KT > hi || key0 < lo)) {
-            // values that no query sees: zeros, whatever their page holds (a
-            // NaN code too); their scores are masked
-#pragma unroll
-            for (int it = 0; it < NT; ++it) {
-              const int key = key0 + it * STEP + sl0;
-              if (key >= hi || key < lo) reg[it] = make_uint4(0, 0, 0, 0);
-            }
-          }
-          if (g >= 2) {
-            // the last step of the tile before the last, of both query tiles
-            const int x = (g - 1) * SPT - 1;
-            uint64_t* free = (v ? pv_done : s_full) + (x & 3);
-            ok = warp_wait(free, (x >> 2) & 1, abort_flag) && warp_wait(free + 4, (x >> 2) & 1, abort_flag);
-            if (!ok) break;
-          }
-          uint8_t* dst = sm + (v ? LY::VH : LY::KH) + buf * LY::KB + (ch >> 2) * (KT * 128);
-          const int cc = (2 * ch) & 7;
-#pragma unroll
-          for (int it = 0; it < NT; ++it) {
-            const int sl = it * STEP + sl0;
-            uint32_t w[8];
-            const uint32_t c[4] = {reg[it].x, reg[it].y, reg[it].z, reg[it].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[2 * e] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] & 0xFFFFu));
-              w[2 * e + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] >> 16));
-            }
-            uint8_t* at = dst + sl * 128;
-            *reinterpret_cast<uint4*>(at + ((cc ^ (sl & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive((v ? vh_full : kh_full) + buf);
-        }
-      }
-      done += n;
+      // sums read, rows of the query tile free: waited for before the next queries
+      meet();
       if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
   } else {
-    reg_dec<56>();
-    if (warp == 12 || warp == 15) {
+    reg_dec<64>();
+    if (warp == 16) {
       // ====================================================== MMA issue
       if (lane == 0) {
-        constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, TM_ROWS, STEP_KEYS);
+        constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, TM_ROWS, KT);
         constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, TM_ROWS, D);
-        const int t = warp == 12 ? 0 : 1;
-        const uint32_t q = smem_u32(sm + LY::Q) + t * NQ * LY::QB;
-        const uint32_t kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
-        const uint32_t o = tmem + TM_O + 128 * t, s = tmem + TM_S + 128 * t;
-        uint32_t nq = 0, np = 0;                         // stretches of this query tile, and steps, so far
+        const uint32_t q0 = smem_u32(sm + LY::Q), kh0 = smem_u32(sm + LY::KH), vh0 = smem_u32(sm + LY::VH);
+        uint32_t nq0 = 0, nq1 = 0;                       // stretches of either query tile so far
         int done = 0;
-        // S of step x: 64 channels (a column block of 128-byte rows) per turn of the loop
-        auto qk = [&](int x) {
-          const uint32_t kh = kh0 + ((x / SPT) & 1) * LY::KB + (x % SPT) * (STEP_KEYS * 128);
+        // 64 channels (a column block of 128-byte rows) per turn of the loop
+        auto qk = [&](int t, int g) {
+          const uint32_t q = q0 + t * NQ * LY::QB, kh = kh0 + (g & 1) * LY::KB;
 #pragma unroll 1
           for (int c = 0; c < NQ * (D / 64); ++c) {
             const int block = c & (D / 64 - 1), part = c / (D / 64);
-            mma4_f16_ss(s + 64 * (x & 1), make_sdesc_sw128(q + part * LY::QB + block * (TM_ROWS * 128), 16, 1024),
+            mma4_f16_ss(tmem + TM_S + 128 * t, make_sdesc_sw128(q + part * LY::QB + block * (TM_ROWS * 128), 16, 1024),
                         make_sdesc_sw128(kh + block * (KT * 128), 16, 1024), idesc_qk, c);
           }
         };
-        auto k_ready = [&](int x) -> bool {              // the tile of step x, at its first step
-          const int g = x / SPT;
-          return x % SPT != 0 || mbar_wait(&kh_full[g & 1], (g >> 1) & 1, abort_flag);
+        // both halves of the tile's keys, each half's P over its S
+        auto pv = [&](int t, int g, uint32_t accumulate) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint64_t b = make_sdesc_sw128(vh0 + (g & 1) * LY::KB + half * SC * 128, KT * 128, 1024);
+            const uint32_t p = tmem + TM_S + 128 * t + half * SC;
+            if constexpr (SC == 64) mma4_f16_ts(tmem + TM_O + 128 * t, p, b, idesc_pv, accumulate | half);
+            else mma2_f16_ts(tmem + TM_O + 128 * t, p, b, idesc_pv, accumulate | half);
+          }
         };
         bool ok = true;
         for (int sg = 0; ok; ++sg) {
           if (!mbar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
           const volatile Stretch& seg = segs[sg & 1];
           if (!(seg.flags & STRETCH_SOME)) break;
-          const int ns = (seg.k1 - seg.k0) * SPT;
-          const bool on = seg.n * G - seg.tile * TTR > t * TM_ROWS;   // the query tile has rows
-          if (ns > 0 && on && !mbar_wait(&q_full[t], nq++ & 1, abort_flag)) break;
-          // QK of the first two steps; then PV of a step and QK of the one two after it
-#pragma unroll 1
-          for (int j = -2; j < ns; ++j) {
-            const int x = done * SPT + j;
-            if (j >= 0) {
-              const int g = x / SPT;
-              ok = (x % SPT != 0 || mbar_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag)) &&
-                   mbar_wait(&p_full[2 * t + (np & 1)], (np >> 1) & 1, abort_flag);
+          const int n = seg.k1 - seg.k0;
+          const bool two = seg.n * G - seg.tile * TTR > TM_ROWS;   // the second query tile has rows
+          if (n > 0) {
+            ok = mbar_wait(&kh_full[done & 1], (done >> 1) & 1, abort_flag) && mbar_wait(&q_full[0], nq0++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            qk(0, done);
+            mma_commit(&s_full[done & 1]);
+            if (two) {
+              ok = mbar_wait(&q_full[1], nq1++ & 1, abort_flag);
               if (!ok) break;
-              ++np;
               tc_fence_after();
-              if (on)
-                mma4_f16_ts(o, s + 64 * (x & 1),
-                            make_sdesc_sw128(vh0 + (g & 1) * LY::KB + (x % SPT) * (STEP_KEYS * 128), KT * 128, 1024),
-                            idesc_pv, j > 0);
-              mma_commit(&pv_done[4 * t + (x & 3)]);
+              qk(1, done);
             }
-            if (j + 2 < ns) {
-              ok = k_ready(x + 2);
+            mma_commit(&s_full[2 + (done & 1)]);
+          }
+#pragma unroll 1
+          for (int j = 0; j < n && ok; ++j) {
+            const int g = done + j;
+            ok = mbar_wait(&vh_full[g & 1], (g >> 1) & 1, abort_flag) &&
+                 (j + 1 >= n || mbar_wait(&kh_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort_flag));
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+              const bool on = t == 0 || two;
+              ok = mbar_wait(&p_full[t], g & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              if (on) qk(x + 2);
-              mma_commit(&s_full[4 * t + ((x + 2) & 3)]);
+              if (on) pv(t, g, j > 0);
+              mma_commit(&o_done[2 * t + (g & 1)]);
+              if (j + 1 < n) {
+                if (on) qk(t, g + 1);
+                mma_commit(&s_full[2 * t + ((g + 1) & 1)]);
+              }
             }
           }
-          done += seg.k1 - seg.k0;
+          if (!ok) break;
+          done += n;
           mbar_arrive(&seg_free[sg & 1]);
         }
         // every MMA issued so far is done before the block releases its tensor memory
-        mma_commit(&drain[t]);
-        mbar_wait(&drain[t], 0, nullptr, 100000000ull);
+        mma_commit(drain);
+        mbar_wait(drain, 0, nullptr, 100000000ull);
       }
       __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
       // ====================================================== the line of work
       PieceRec rec = {};
-      int done = 0, sg = 0;
+      const int rows = a.pv.P < 32 ? a.pv.P : 32;
+      int done = 0, sg = 0, issued = 0;                  // tiles, stretches; copies (K, V, K, ...)
       bool ok = true;
       for (bool more = u < end; ok; ++sg) {
         if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
@@ -661,7 +628,26 @@ __global__ void __launch_bounds__(TTHREADS, 1)
                 make_float4(sk, __log2f(v), 1.0f / v, __int_as_float(pg));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&meta_full[g % TMETA]);
+          // the codes, lane i a box of the tile: 32 rows of a page (16 where a
+          // page has no more)
+          const int box_pg = rows == 16 ? pg : max(__shfl_sync(0xFFFFFFFFu, pg, (2 * lane) & 31),
+                                                   __shfl_sync(0xFFFFFFFFu, pg, (2 * lane + 1) & 31));
+          const bool on = lane < KT / rows && box_pg != kNone;
+          const int key = k * KT + lane * rows;
+          const int y = (int)(a.pv.row0 + (((long long)box_pg * H + pl.h) << a.pv.p_shift)) + (key & (a.pv.P - 1));
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * rows * D;
+#pragma unroll 1
+          for (int v = 0; v < 2; ++v) {
+            if (g >= 1 && !warp_wait(&raw_free[v], (g - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[v], bytes);
+            __syncwarp();
+            if (on) tma_load_2d(sm + LY::RAW + v * KT * D + lane * rows * D, v ? &tmV : &tmK, &raw_full[v], 0, y);
+            issued = 2 * g + v + 1;
+          }
+          if (!ok) break;
         }
         done += k1 - k0;
         if (u == pl.at && end < item_end) 
@@ -670,57 +656,91 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         more = u < end && next_place<SH, TTR, KT>(a, pl);
       }
       if (lane == 0) a.tiles.rec[worker] = rec;
-    } else if (warp == 14) {
-      // ====================================================== TMA
-      // lane i a box of the tile: 32 rows of a page (16 where a page has no more)
-      const int rows = a.pv.P < 32 ? a.pv.P : 32;
-      const int boxes = KT / rows;
-      int done = 0, issued = 0;                          // tiles; copies (K, V, K, ...)
-      bool ok = true;
-      for (int sg = 0; ok; ++sg) {
-        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
-        const volatile Stretch& seg = segs[sg & 1];
-        if (!(seg.flags & STRETCH_SOME)) break;
-        const int k0 = seg.k0, n = seg.k1 - k0, h = seg.h;
-#pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int g = done + j;
-          ok = warp_wait(&meta_full[g % TMETA], (g / TMETA) & 1, abort_flag);
-          if (!ok) break;
-          int pg = kNone;
-          if (lane < boxes) {
-            const int4* meta = reinterpret_cast<const int4*>(sm + LY::META) + (g % TMETA) * NG;
-            pg = rows == 16 ? meta[lane].w : max(meta[2 * lane].w, meta[2 * lane + 1].w);
-          }
-          const int key = (k0 + j) * KT + lane * rows;
-          const int y = (int)(a.pv.row0 + (((long long)pg * H + h) << a.pv.p_shift)) + (key & (a.pv.P - 1));
-          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pg != kNone)) * rows * D;
-          for (int v = 0; v < 2; ++v) {
-            if (g >= 1 && !warp_wait(&raw_free[v], (g - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&raw_full[v], bytes);
-            __syncwarp();
-            if (pg != kNone)
-              tma_load_2d(sm + LY::RAW + v * KT * D + lane * rows * D, v ? &tmV : &tmK, &raw_full[v], 0, y);
-            issued = 2 * g + v + 1;
-          }
-          if (!ok) break;
-        }
-        done += n;
-        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
-      }
       // after an abort: copies still in flight land in this block's shared memory
       if (*abort_flag && issued > 0) {
         mbar_wait(&raw_full[0], ((issued - 1) >> 1) & 1, nullptr, 100000000ull);
         if (issued > 1) mbar_wait(&raw_full[1], ((issued - 2) >> 1) & 1, nullptr, 100000000ull);
       }
+    } else {
+      // ====================================================== K, V
+      const int ct = tid - 18 * 32;
+      constexpr int CH = D / 16;                         // 16-byte code chunks of a row
+      constexpr int NT = KT * CH / 64;                   // chunks of K, and of V, per thread
+      constexpr int STEP = 64 / CH;                      // rows per round of the 64 threads
+      const int sl0 = CH == 8 ? ct & 7 : 8 * (ct >> 5) + (ct & 7);
+      const int ch = (ct >> 3) & (CH - 1);
+      int done = 0;
+      bool ok = true;
+      for (int sg = 0; ok; ++sg) {
+        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile Stretch& seg = segs[sg & 1];
+        if (!(seg.flags & STRETCH_SOME)) break;
+        const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
+  #pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int g = done + j;
+          const int buf = g & 1;
+  #pragma unroll 1
+          for (int v = 0; v < 2; ++v) {                    // K, then V
+            if (!warp_wait(&raw_full[v], g & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint64_t* free = (v ? o_done : s_full) + buf;  // both query tiles are done with the buffer
+            if (g >= 2 && (!warp_wait(free, ((g - 2) >> 1) & 1, abort_flag) ||
+                           !warp_wait(free + 2, ((g - 2) >> 1) & 1, abort_flag))) {
+              ok = false;
+              break;
+            }
+            const uint8_t* src = sm + LY::RAW + v * KT * D;
+            uint8_t* dst = sm + (v ? LY::VH : LY::KH) + buf * LY::KB + (ch >> 2) * (KT * 128);
+            const int cc = (2 * ch) & 7;
+            const int key0 = (k0 + j) * KT;
+            const bool edge = v && (key0 + KT > hi || key0 < lo);
+            constexpr int BATCH = NT < 4 ? NT : 4;
+  #pragma unroll 1
+            for (int i0 = 0; i0 < NT; i0 += BATCH) {
+              uint4 reg[BATCH];
+  #pragma unroll
+              for (int it = 0; it < BATCH; ++it) {
+                const int sl = (i0 + it) * STEP + sl0;
+                reg[it] = *reinterpret_cast<const uint4*>(src + raw_chunk<D>(sl, ch));
+                // values that no query sees: zeros, whatever their page holds (a
+                // NaN code too); their scores are masked
+                if (edge && (key0 + sl >= hi || key0 + sl < lo)) reg[it] = make_uint4(0, 0, 0, 0);
+              }
+              if (i0 + BATCH == NT) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&raw_free[v]);
+              }
+  #pragma unroll
+              for (int it = 0; it < BATCH; ++it) {
+                const int sl = (i0 + it) * STEP + sl0;
+                uint32_t w[8];
+                const uint32_t c[4] = {reg[it].x, reg[it].y, reg[it].z, reg[it].w};
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  w[2 * e] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] & 0xFFFFu));
+                  w[2 * e + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(c[e] >> 16));
+                }
+                uint8_t* at = dst + sl * 128;
+                *reinterpret_cast<uint4*>(at + ((cc ^ (sl & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive((v ? vh_full : kh_full) + buf);
+          }
+        }
+        done += n;
+        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+      }
     }
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
