@@ -60,7 +60,7 @@ struct TilesLayout {
   static constexpr int KH = Q + 2 * NQ * QB;                     // [2]
   static constexpr int VH = KH + 2 * KB;                         // [2]
   static constexpr int RAW = VH + 2 * KB;                        // K codes, V codes of one tile
-  static constexpr int META = RAW + 2 * KT * D;                  // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, page}
+  static constexpr int META = RAW + 2 * KT * D;                  // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, -}
   static constexpr int SLOT = META + TMETA * (KT / 16) * 16;     // [2 halves][256] a row's logit factor; maxima; sums
   static constexpr int SEG = SLOT + 2 * TTR * 4;                 // [2] Stretch
   static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
@@ -588,33 +588,41 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         // which lie in one page.  Pages of zero values take a V scale near by.
         const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
         float near = 0.0f;
-        auto group = [&](int k, int& pg, float& sv) {
+        // (Loads run a tile ahead: TMA of the next tile waits for nothing else than its stage.)
+        auto page = [&](int k) -> int {
           const int key = k * KT + lane * 16;
-          pg = kNone;
-          sv = 0.0f;
-          if (lane < NG && k < k1 && key < pl.t.hi && key + 16 > pl.t.lo) {
-            pg = __ldg(tab + (key >> a.pv.p_shift));
-            if (pg < 0 || pg >= a.pv.n_pages) {
-              atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
-              pg = 0;
-            }
-            sv = __ldg(a.pv.v_scale + (size_t)pg * H + pl.h);
-          }
-          float mx = sv;
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-          return mx;
+          return lane < NG && k < k1 && key < pl.t.hi && key + 16 > pl.t.lo ? __ldg(tab + (key >> a.pv.p_shift))
+                                                                            : -0x7FFFFFFF;
         };
+        auto known = [&](int pg) -> int {                // a page that can be read
+          if (pg == -0x7FFFFFFF) return kNone;
+          if (pg < 0 || pg >= a.pv.n_pages) {
+            atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
+            return 0;
+          }
+          return pg;
+        };
+        auto scale = [&](const float* scales, int pg) {
+          return pg != kNone ? __ldg(scales + (size_t)pg * H + pl.h) : 0.0f;
+        };
+        auto top = [](float v) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+          return v;
+        };
+        int pg = kNone;
+        float sk = 0.0f, sv = 0.0f;
+        if (k0 < k1) {
+          pg = known(page(k0));
+          sk = scale(a.pv.k_scale, pg);
+          sv = scale(a.pv.v_scale, pg);
+        }
         for (int k = k0; k < k1; ++k) {
           const int g = done + k - k0;
-          int pg;
-          float sv;
-          float mx = group(k, pg, sv);
-          const float sk = pg != kNone ? __ldg(a.pv.k_scale + (size_t)pg * H + pl.h) : 0.0f;
+          const int next = page(k + 1);
+          float mx = top(sv);
           if (mx == 0.0f && near == 0.0f) {
-            int unused;
-            float v;
-            for (int s = k + 1; mx == 0.0f && s < k1; ++s) mx = group(s, unused, v);
+            for (int s = k + 1; mx == 0.0f && s < k1; ++s) mx = top(scale(a.pv.v_scale, known(page(s))));
             if (mx == 0.0f) mx = 1.0f;
           }
           if (mx > 0.0f) near = mx;
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           if (lane < NG) {
             const float v = sv > 0.0f ? sv : near;
             reinterpret_cast<float4*>(sm + LY::META)[(g % TMETA) * NG + lane] =
-                make_float4(sk, __log2f(v), 1.0f / v, __int_as_float(pg));
+                make_float4(sk, __log2f(v), 1.0f / v, 0.0f);
           }
           __syncwarp();
           // the codes, lane i a box of the tile: 32 rows of a page (16 where a
@@ -646,6 +654,11 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             __syncwarp();
             if (on) tma_load_2d(sm + LY::RAW + v * KT * D + lane * rows * D, v ? &tmV : &tmK, &raw_full[v], 0, y);
             issued = 2 * g + v + 1;
+            if (v == 0) {
+              pg = known(next);
+              sk = scale(a.pv.k_scale, pg);
+              sv = scale(a.pv.v_scale, pg);
+            }
           }
           if (!ok) break;
         }
