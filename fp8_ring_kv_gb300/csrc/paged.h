@@ -105,7 +105,6 @@ cudaError_t launch_paged_rows(const PagedAttn& a, const CUtensorMap& tmK, const 
                               cudaStream_t st);
 cudaError_t launch_paged_tiles(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int blocks,
                                cudaStream_t st);
-cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int blocks, cudaStream_t st);
 // tmK, tmV: the code arrays as [rows][D] u8, box {D, min(P, 32)}
 cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
                                 cudaStream_t st);

@@ -1,4 +1,5 @@
-// paged_join: the items of the paged attention that several workers share.
+// paged_join: the items of the paged attention that several workers (warps of
+// the row kernel, blocks of the tile kernel) share.
 //
 //   out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
 // over the pieces in the workers' order (no atomics: the result does not
@@ -51,18 +52,14 @@ __device__ __forceinline__ void sum_pieces(const PieceScratch& ps, int w, int p,
 // that has the record; of one of many pieces (a long sequence spread over the
 // GPU), row y to the whole block, warp i the pieces i, i + JW, ...
 // Many rows (one record per block): a row to a warp.
-constexpr int JW = 8;                                   // warps
+constexpr int JW = 8;                                    // warps
 template <int D, int TR, typename T>
-__global__ void __launch_bounds__(32 * JW) paged_join_kernel(const __grid_constant__ PagedAttn a, PieceScratch ps,
-                                                             int workers, int per) {
+__device__ __forceinline__ void join_items(const PagedAttn& a, const PieceScratch& ps, int workers, int per,
+                                           float (&acc)[JW][D], float2 (&mls)[JW]) {
   constexpr int V = D / 32;                              // channels per lane
   constexpr int MANY = 12;                               // pieces
   constexpr bool TALL = TR > 16;
-  __shared__ float acc[JW][D];
-  __shared__ float2 mls[JW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
   const int w0 = blockIdx.x * per;
   PieceRec mine = {};
   if (lane < per && w0 + lane < workers) mine = ps.rec[w0 + lane];
@@ -127,6 +124,18 @@ __global__ void __launch_bounds__(32 * JW) paged_join_kernel(const __grid_consta
   }
 }
 
+// The row kernel's items and, blockIdx.z = 1, the tile kernel's.
+constexpr int JOIN_RECORDS = 8;                          // of the row kernel's, per block
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * JW) paged_join_kernel(const __grid_constant__ PagedAttn a, int workers, int blocks) {
+  __shared__ float acc[JW][D];
+  __shared__ float2 mls[JW];
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.z == 0) join_items<D, kRowsMax<T>, T>(a, a.rows, workers, JOIN_RECORDS, acc, mls);
+  else join_items<D, kTilesRows, T>(a, a.tiles, blocks, 1, acc, mls);
+}
+
 // ---------------------------------------------------------------- scratch
 static size_t piece_bytes(int workers, int rows, int D) {
   const size_t slots = (size_t)2 * workers * rows;
@@ -151,24 +160,24 @@ void paged_carve_scratch(uint8_t* base, int D, PagedAttn* a) {
 
 template <int D, typename T>
 static cudaError_t join_t(const PagedAttn& a, bool tiles, int blocks, cudaStream_t st) {
-  if (tiles)
-    return launch_pdl(paged_join_kernel<D, kTilesRows, T>, dim3(blocks, kTilesRows / JW / 4), dim3(32 * JW), 0, st, a,
-                      a.tiles, blocks, 1);
   const long long most = (long long)a.max_new * a.pv.G;
-  const unsigned rows = (unsigned)(most < kRowsMax<T> ? most : kRowsMax<T>);
   const int workers = blocks * paged_rows_warps(a, std::is_same_v<T, __half>);
-  constexpr int per = 8;
-  return launch_pdl(paged_join_kernel<D, kRowsMax<T>, T>, dim3((workers + per - 1) / per, rows), dim3(32 * JW), 0, st, a,
-                    a.rows, workers, per);
+  const int x = (workers + JOIN_RECORDS - 1) / JOIN_RECORDS;
+  static_assert(kTilesRows % (4 * JW) == 0);
+  const dim3 grid = tiles ? dim3(x > blocks ? x : blocks, kTilesRows / JW / 4, 2)
+                          : dim3(x, (unsigned)(most < kRowsMax<T> ? most : kRowsMax<T>));
+  return launch_pdl(paged_join_kernel<D, T>, grid, dim3(32 * JW), 0, st, a, workers, blocks);
 }
 
-cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int blocks, cudaStream_t st) {
+static cudaError_t launch_paged_join(const PagedAttn& a, bool tiles, bool f16, int blocks, cudaStream_t st) {
   if (a.pv.D == 64)
     return f16 ? join_t<64, __half>(a, tiles, blocks, st) : join_t<64, __nv_bfloat16>(a, tiles, blocks, st);
   return f16 ? join_t<128, __half>(a, tiles, blocks, st) : join_t<128, __nv_bfloat16>(a, tiles, blocks, st);
 }
 
 // ---------------------------------------------------------------- one call
+// The kernel of few rows always runs (only the device knows how many new
+// tokens each sequence has), the kernel of many where max_new allows such.
 cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, const CUtensorMap& tmV, bool f16, int sms,
                                 cudaStream_t st) {
   const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
@@ -176,9 +185,7 @@ cudaError_t launch_paged_attend(const PagedAttn& a, const CUtensorMap& tmK, cons
   const bool many = (long long)a.max_new * a.pv.G > few;
   cudaError_t e = launch_paged_rows(a, tmK, tmV, f16, blocks, st);
   if (e == cudaSuccess && many) e = launch_paged_tiles(a, tmK, tmV, f16, blocks, st);
-  if (e == cudaSuccess) e = launch_paged_join(a, false, f16, blocks, st);
-  if (e == cudaSuccess && many) e = launch_paged_join(a, true, f16, blocks, st);
-  return e;
+  return e == cudaSuccess ? launch_paged_join(a, many, f16, blocks, st) : e;
 }
 
 }  // namespace kvring_dev
