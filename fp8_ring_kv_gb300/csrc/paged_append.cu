@@ -18,8 +18,9 @@ constexpr int kAppendFew = 4;   // tokens per sequence, on average, up to which 
 
 // Tasks: sequence b touches at most floor(n_b / P) + 2 pages, so it owns the
 // task numbers base(b) .. base(b + 1) - 1 with base(b) = floor(seq_start[b] /
-// P) + 2 b; a block finds its b by counting the bases at or below its own
-// number, all sequences in parallel, and with them loads the lengths.
+// P) + 2 b; a block looks for the sequence that owns its number, all sequences
+// in parallel.  (Sequences whose numbers hold own separate tasks, however wrong
+// those of others are, unless starts that decrease make them overlap.)
 struct AppendTask {
   int held;       // rows of the page that were there before
   int cnt;        // new rows
@@ -27,44 +28,28 @@ struct AppendTask {
   int page;       // -1: nothing to do
 };
 
+// ``found``: one word of shared memory, -1 at first.
 __device__ AppendTask append_task(const PagedView& pv, const PagedBatch& pb, int task, int* found) {
   const int tid = threadIdx.x;
   AppendTask t = {0, 0, 0, -1};
-  int below = 0;
-  for (int i0 = 0; i0 < pb.n_seqs; i0 += blockDim.x) {
-    const int i = i0 + tid;
-    bool mine = false;
-    int s0 = 0, s1 = 0, len = 0, base = 0;
-    if (i < pb.n_seqs) {
-      s0 = __ldg(pb.seq_start + i);
-      s1 = __ldg(pb.seq_start + i + 1);
-      len = __ldg(pb.kv_len + i);
-      base = (min(max(s0, 0), pb.n_tokens) >> pv.p_shift) + 2 * i;
-      mine = base <= task;
-    }
-    const int upto = __syncthreads_count(mine);
-    below += upto;
-    // the last sequence so far whose tasks begin at or below this one
-    if (upto > 0 && tid == upto - 1) {
-      found[0] = s0;
-      found[1] = s1;
-      found[2] = len;
-      found[3] = base;
-    }
-    __syncthreads();
+  for (int i = tid; i < pb.n_seqs; i += blockDim.x) {
+    bool ok;
+    const SeqInfo s = seq_info(pb, pv.p_shift, i, ok);
+    ok = ok && s.n <= s.len;
+    if (!ok && blockIdx.x == 0) atomicOr(&pv.state[PST_ERR], DEVERR_SEQ);
+    const int j = task - (s.s0 >> pv.p_shift) - 2 * i;
+    const int first = s.len - s.n;
+    if (ok && s.n > 0 && j >= 0 && j <= ((s.len - 1) >> pv.p_shift) - (first >> pv.p_shift)) atomicMax(found, i);
   }
-  if (below == 0) return t;
-  const int b = below - 1;
-  const int s0 = found[0], s1 = found[1], len = found[2], j = task - found[3];
-  if (s0 < 0 || s1 < s0 || s1 > pb.n_tokens || len < s1 - s0 || (long long)len > ((long long)pb.table_width << pv.p_shift)) {
-    if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_SEQ);
-    return t;
-  }
+  __syncthreads();
+  const int b = *found;
+  if (b < 0) return t;
+  const int s0 = __ldg(pb.seq_start + b), s1 = __ldg(pb.seq_start + b + 1), len = __ldg(pb.kv_len + b);
+  const int j = task - (s0 >> pv.p_shift) - 2 * b;
   const int first = len - (s1 - s0);                    // cache index of the first new token
   const int slot = (first >> pv.p_shift) + j;           // the task's page of the sequence
   const int lo = max(first, slot << pv.p_shift);
   const int hi = min(len, (slot + 1) << pv.p_shift);
-  if (j < 0 || lo >= hi) return t;
   t.held = lo - (slot << pv.p_shift);
   t.cnt = hi - lo;
   t.tok0 = s0 + (lo - first);
@@ -103,15 +88,17 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
   constexpr int THREADS = append_threads<L, P>;
   constexpr int ROWS = THREADS / L;                     // rows per pass
   constexpr int PASS = P > ROWS ? P / ROWS : 1;
-  __shared__ int found[4];
+  __shared__ int found;
   __shared__ float wmax[THREADS / 32];
   const int tid = threadIdx.x;
   const int task = blockIdx.x / (2 * pv.H);
   const int h = (blockIdx.x - task * 2 * pv.H) >> 1;
   const bool is_v = blockIdx.x & 1;
+  if (tid == 0) found = -1;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const AppendTask t = append_task(pv, pb, task, found);
+  const AppendTask t = append_task(pv, pb, task, &found);
   if (t.cnt == 0) return;                               // the whole block
   const int lane = tid % L;
   const int row = tid / L;
@@ -188,10 +175,12 @@ __global__ void __launch_bounds__(512)
     paged_append_few_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k, long long k_stride,
                             const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
   constexpr int D = L * 16;
-  __shared__ int found[4];
+  __shared__ int found;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const AppendTask t = append_task(pv, pb, blockIdx.x, found);
+  const AppendTask t = append_task(pv, pb, blockIdx.x, &found);
   if (t.cnt == 0) return;
   const int lane = threadIdx.x % L;
   const unsigned group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
@@ -259,7 +248,7 @@ __global__ void __launch_bounds__(256) paged_rope_kernel(float2* table, int pos_
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
     const int p = (int)(i / pairs);
     double s, c;
-    sincos((double)(pos_min + p) * omega[(int)(i - (long long)p * pairs)], &s, &c);
+    sincos(((double)pos_min + p) * omega[(int)(i - (long long)p * pairs)], &s, &c);
     table[i] = make_float2((float)c, (float)s);
   }
 }
