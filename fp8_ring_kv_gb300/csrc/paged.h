@@ -185,6 +185,13 @@ __device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r
   }
 }
 
+// NaN codes (e4m3 S.1111.111) of four become zeros; true where there was one.
+__device__ __forceinline__ bool drop_nan_codes(uint32_t& w) {
+  const uint32_t n = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // the top bit of each NaN byte
+  w &= ~((n >> 7) * 0xFFu);
+  return n != 0;
+}
+
 // 8 halfs (one uint4) -> 8 fp32 (exact); T picks the 16-bit type.
 template <typename T>
 __device__ __forceinline__ void load8_f32(uint4 u, float* x) {

@@ -222,6 +222,7 @@ int kvring_paged_attend(kvring_paged* p, int32_t layer, const void* q, int64_t q
   if (!stride_ok(q_stride, a.pv.QH, a.pv.D) || !stride_ok(out_stride, a.pv.QH, a.pv.D)) return KVRING_ERR_INVALID_ARG;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return KVRING_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || !std::isfinite(scale)) return KVRING_ERR_INVALID_ARG;
+  if ((long long)n_tokens * a.pv.G > (1ll << 30)) return KVRING_ERR_INVALID_ARG;   // rows are 32-bit numbers
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_pos, 4)) return KVRING_ERR_MISALIGNED;
   if (n_seqs == 0 || n_tokens == 0) return KVRING_OK;
   if (max_new < 1 || max_new > n_tokens) return KVRING_ERR_INVALID_ARG;
@@ -232,7 +233,7 @@ int kvring_paged_attend(kvring_paged* p, int32_t layer, const void* q, int64_t q
   a.out_stride = out_stride;
   a.scale_log2 = (float)((scale > 0.0f ? (double)scale : 1.0 / std::sqrt((double)a.pv.D)) * 1.4426950408889634);
   a.causal = causal;
-  a.window = window;
+  a.window = window < KVRING_PAGED_MAX_LEN ? window : 0;   // wider than any sequence: none
   a.max_new = max_new;
   paged_carve_scratch(p->scratch, a.pv.D, &a);
   const cudaError_t e = launch_paged_attend(a, p->k_map, p->v_map, p->cfg.in_dtype == KVRING_IN_F16, p->sms,

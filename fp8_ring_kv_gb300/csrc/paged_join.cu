@@ -41,7 +41,7 @@ __device__ __forceinline__ void sum_pieces(const PieceScratch& ps, int w, int p,
     const float mn = some ? fmaxf(m, ml.x) : m;
     const float f0 = mn > m ? ex2f(m - mn) : 1.0f, f1 = some ? ex2f(ml.x - mn) : 0.0f;
     m = mn;
-    l = l * f0 + (some ? ml.y * f1 : 0.0f);
+    l = l * f0 + (some ? ml.y * f1 : ml.y);              // no key: 0; scores all NaN: NaN
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = some ? o[i] * f0 + x[i] * f1 : o[i];
   }
@@ -88,7 +88,7 @@ __device__ __forceinline__ void join_items(const PagedAttn& a, const PieceScratc
     const PieceRec it = record(i);
     for (int r = TALL ? blockIdx.y * JW + warp : blockIdx.y; r < it.rows; r += gridDim.y * (TALL ? JW : 1)) {
       sum_pieces<V, TR>(ps, w0 + i, w0 + i, 1, it.last, r, m, l, o);
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       uint32_t* dst = out_row(it, r) + lane * (V / 2);
 #pragma unroll
       for (int c = 0; c < V / 2; ++c) dst[c] = pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
@@ -107,16 +107,14 @@ __device__ __forceinline__ void join_items(const PagedAttn& a, const PieceScratc
         float mm = -INFINITY, ll = 0.0f, o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
         for (int k = 0; k < JW; ++k) mm = fmaxf(mm, mls[k].x);
-        if (mm != -INFINITY) {
 #pragma unroll
-          for (int k = 0; k < JW; ++k) {
-            const float f = ex2f(mls[k].x - mm);
-            ll += mls[k].y * f;
-            o0 += acc[k][2 * tid] * f;
-            o1 += acc[k][2 * tid + 1] * f;
-          }
+        for (int k = 0; k < JW; ++k) {
+          const float f = mls[k].x != -INFINITY ? ex2f(mls[k].x - mm) : 1.0f;   // no key: zeros
+          ll += mls[k].y * f;
+          o0 += acc[k][2 * tid] * f;
+          o1 += acc[k][2 * tid + 1] * f;
         }
-        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+        const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
         out_row(it, r)[tid] = pack2<T>(o0 * inv, o1 * inv);
       }
       __syncthreads();

@@ -20,7 +20,7 @@
 // MMA's 16 rows and the queries its 8 columns, so up to 8 query rows waste
 // nothing (with the queries as rows, half of the products and of the
 // accumulators were padding, two warps per sub-partition fitted, and a decoding
-// batch of 64 contexts took 129 us against XXX).
+// batch of 64 contexts took 129 us against 103).
 //
 // Register layouts (lane 4 g + t): of a K tile a thread holds 16-byte chunks of
 // key rows g and g + 8 (its channels are the MMA's k in a permuted order, the
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
         for (int k = k0; k < issued; ++k) write_meta(k, first + k - k0);
         __syncwarp();
       }
-      // tiles below c_lo and from c_hi on hold keys that some row of the thread does not see
+      // tiles below c_lo and from c_hi on hold keys that some row does not see
       int c_hi = pl.t.hi / RK, c_lo = (pl.t.lo + RK - 1) / RK;
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -303,6 +303,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           c_hi = min(c_hi, hi[e][f] / RK);
           c_lo = max(c_lo, (lo[e][f] + RK - 1) / RK);
         }
+      c_hi = __reduce_min_sync(0xFFFFFFFFu, c_hi);
+      c_lo = __reduce_max_sync(0xFFFFFFFFu, c_lo);
       float o[NJ][NT][4];
 #pragma unroll
       for (int i = 0; i < NJ; ++i)
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           break;
         }
         const uint8_t* kc = stages + st * LY::STAGE;
-        const uint8_t* vc = kc + RK * D;
+        uint8_t* vc = stages + st * LY::STAGE + RK * D;
         const float4 m0 = metas[2 * st], m1 = metas[2 * st + 1];
         float c[2][NT][4];                               // 16 keys each
 #pragma unroll
@@ -424,7 +426,38 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           }
         }
         // O^T += V^T P^T: k pairs are keys (row(2 t4), row(2 t4 + 1)) of either 8-key group
-        const bool edge = key0 + RK > pl.t.hi || key0 < pl.t.lo;
+        if (cut) {
+          // A lane looks at one key's values.  Those that no query sees become
+          // zeros, whatever their page holds.  A NaN that some rows see and
+          // others do not must not meet the latter's zero weights: it is left
+          // out, and the sums of the rows that see it get it.
+          const int key = key0 + lane;
+          const bool hidden = key >= pl.t.hi || key < pl.t.lo;
+          bool nan = false;
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(vc + code_chunk<D>(lane, i));
+            uint4 w = *at;
+            const bool n = drop_nan_codes(w.x) | drop_nan_codes(w.y) | drop_nan_codes(w.z) | drop_nan_codes(w.w);
+            nan = nan || n;
+            if (hidden) w = make_uint4(0, 0, 0, 0);
+            if (hidden || n) *at = w;
+          }
+          fence_proxy_async_smem();                      // before the stage's next TMA
+          const unsigned nans = __ballot_sync(0xFFFFFFFFu, nan && !hidden);
+          if (nans) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int kr = i * 8 + key_row(g);
+                  if ((nans >> kr & 1) && key0 + kr < hi[e][f] && key0 + kr >= lo[e][f]) l[e][f] = __int_as_float(0x7FFFFFFF);
+                }
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t w[4][D / 32];
@@ -441,11 +474,6 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
               const uint2 v = *reinterpret_cast<const uint2*>(vc + code_chunk<D>(kr, g >> 1) + (g & 1) * 8);
               w[r][0] = v.x;
               w[r][1] = v.y;
-            }
-            // rows no query sees may hold anything, NaN codes too
-            if (edge && (key0 + kr >= pl.t.hi || key0 + kr < pl.t.lo)) {
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) w[r][i] = 0u;
             }
           }
 #pragma unroll
@@ -502,7 +530,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           if (r >= rows || 2 * t4 + f >= COLS) continue;
           if (whole) {
             const int i = r / G;
-            const float inv = l[e][f] > 0.0f ? 1.0f / l[e][f] : 0.0f;
+            const float inv = l[e][f] != 0.0f ? 1.0f / l[e][f] : 0.0f;
             uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride +
                                                   (size_t)(pl.h * G + r - i * G) * D + g * DG);
 #pragma unroll

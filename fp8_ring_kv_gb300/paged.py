@@ -183,8 +183,8 @@ class PagedKV:
         p, start, length, n_seqs, table, ts, width = self._batch(layer, n, q_pos, "q_pos", seq_start, kv_len, page_table)
         if window is not None and (not causal or window < 1):
             raise KVRingError("window: a positive number of tokens, with causal")
-        if scale is not None and not 0.0 < scale < float("inf"):
-            raise KVRingError("scale: positive and finite")
+        if scale is not None and not 2.0 ** -100 <= scale <= 2.0 ** 100:
+            raise KVRingError(f"scale: {scale}; 2^-100 .. 2^100")
         if max_new is not None and not 1 <= max_new <= max(n, 1):
             raise KVRingError(f"max_new: {max_new}; 1 .. {n}")
         if out is None:
@@ -198,7 +198,7 @@ class PagedKV:
         os_ = self._row_stride(out, n, self.q_heads, "out")
         if n and n_seqs:
             self._call("kvring_paged_attend", layer, q.data_ptr(), qs, p, start, length, n_seqs, n,
-                       n if max_new is None else max_new, table, ts, width, 1 if causal else 0, window or 0,
+                       n if max_new is None else max_new, table, ts, width, 1 if causal else 0, min(window or 0, _k.KVRING_PAGED_MAX_LEN),
                        scale or 0.0, out.data_ptr(), os_, self._stream(stream))
         return out
 

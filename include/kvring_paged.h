@@ -42,11 +42,16 @@
  * out and flagged (KVRING_DEVERR_SEQ); a page id outside 0 .. n_pages - 1 is
  * flagged (KVRING_DEVERR_PAGE): such a page is not written, and attention reads
  * page 0 in its place.  The kernels never trap.
- * Non-finite inputs spread to what is computed from them and no further.
- * A handle must not be used by two host threads at once; the attention's
- * scratch belongs to the handle, so two kvring_paged_attend calls on one
- * handle must not run at the same time (one stream, or events; graphs that
- * captured them included).
+ * (Where seq_start decreases, sequences whose rows overlap may be left out of
+ * an append as well.)
+ * Non-finite inputs spread to what is computed from them and no further: a
+ * query or key with a NaN to the outputs of the query heads that it belongs to
+ * or that see it, a value's NaN to the same channel or the whole of them.  An
+ * infinity in k or v gives its page and head the scale 2^120.
+ * A handle must not be used by two host threads at once.  The caller orders
+ * calls that touch the same pages, and the attention's scratch belongs to the
+ * handle: two kvring_paged_attend calls on one handle must not run at the same
+ * time (one stream, or events; graphs that captured them included).
  *
  * Status codes and the device error bits are kvring.h's, with two more bits.
  */
@@ -126,7 +131,7 @@ int kvring_paged_create(const kvring_paged_config* cfg, void* workspace, size_t 
  * kv_len must count the new tokens (n <= kv_len).  Pages written by a call
  * belong to one sequence each: a page that two sequences of the batch append
  * to ends up with rows of either.
- * N or B of 0: nothing to do.
+ * N (at most 2^24) or B of 0: nothing to do.
  */
 int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k_stride, const void* v,
                         int64_t v_stride, const int32_t* pos, const int32_t* seq_start, const int32_t* kv_len,
@@ -137,8 +142,8 @@ int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k
  * Attention of the new tokens' queries over the cache (paged_attend).
  *   q        device [N][q_heads][D], tokens q_stride elements apart (a multiple
  *            of 8, >= q_heads * D), 16-byte aligned
- *   out      the same for the output, out_stride apart; rows past
- *            seq_start[B] are left as they were
+ *   out      the same for the output, out_stride apart, apart from q; rows
+ *            past seq_start[B] are left as they were
  *   max_new  the largest number of new tokens a sequence of this call has, as
  *            far as the host knows (1 .. N): it chooses what is launched.  A
  *            sequence with more is left out and flagged (KVRING_DEVERR_SEQ).
@@ -150,7 +155,7 @@ int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k
  * Queries are rotated by RoPE at q_pos (fp32) and then held in fp16 at a
  * power-of-two scale of their row; out = softmax(scale q.k) v with fp32 sums
  * and statistics and weights of V in fp16.  A query that sees nothing gives
- * zeros.
+ * zeros.  N * q_heads / kv_heads is at most 2^30.
  */
 int kvring_paged_attend(kvring_paged* p, int32_t layer, const void* q, int64_t q_stride, const int32_t* q_pos,
                         const int32_t* seq_start, const int32_t* kv_len, int32_t n_seqs, int32_t n_tokens,

@@ -2,10 +2,12 @@
 the attention over it in fp64.
 
 Block scale of rows whose largest magnitude is a: the smallest power of two s
-with a <= 448 s, 0 when a < 2^-100.  Codes are e4m3_rn(fl32(x / s)), the
+with a <= 448 s, 0 when a < 2^-100; 2^120 for an infinity, whose code is the
+largest.  Codes are e4m3_rn(fl32(x / s)), the
 division exact.  A page that already holds rows of the sequence keeps its scale
 unless the new rows need a larger one; its older codes then become
-e4m3_rn(code * (old / new)).
+e4m3_rn(code * (old / new)).  A NaN is left out of the maximum; its code is
+0x7F.
 """
 import numpy as np
 
@@ -16,6 +18,8 @@ def pow2_scale(amax):
     """fp32 amax [...] -> fp32 scale [...]."""
     amax = np.asarray(amax, dtype=np.float32)
     m, e = np.frexp(amax)                       # amax = m 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
+    e = np.where(np.isinf(amax), 129, e)        # an infinity: 2^120
+    m = np.where(np.isinf(amax), 0.5, m)
     k = np.where(m <= 0.875, e - 9, e - 8)
     return np.where(amax < np.float32(2.0) ** -100, np.float32(0), np.ldexp(np.float32(1), k)).astype(np.float32)
 
@@ -24,7 +28,8 @@ def encode(x, scale):
     """fp32 x [..., rows, D] at scale [...] -> codes."""
     s = np.asarray(scale, dtype=np.float32)[..., None, None]
     y = np.where(s > 0, x / np.where(s > 0, s, 1), 0).astype(np.float32)
-    return np.where(s > 0, e4m3.encode_rn_satfinite(y), np.uint8(0)).astype(np.uint8)
+    codes = np.where(s > 0, e4m3.encode_rn_satfinite(np.where(np.isnan(y), 0, y)), np.uint8(0))
+    return np.where(np.isnan(x), np.uint8(0x7F), codes).astype(np.uint8)
 
 
 class PagedOracle:
@@ -49,13 +54,15 @@ class PagedOracle:
 
     def _write(self, name, page, off, x):
         codes, scales = self.codes[name][page], self.scales[name][page]
-        need = pow2_scale(np.abs(x).max(axis=(1, 2)))
+        need = pow2_scale(np.fmax.reduce(np.abs(x).reshape(len(x), -1), axis=1, initial=0.0))   # NaN left out
         old = scales if off else np.zeros_like(scales)
         new = np.maximum(need, old)
         for h in range(len(new)):
             if off and new[h] > old[h]:
                 held = e4m3.decode(codes[h, :off]) * (np.float64(old[h]) / np.float64(new[h]))
-                codes[h, :off] = e4m3.encode_rn_satfinite(held) if old[h] > 0 else 0
+                nan = np.isnan(held)
+                codes[h, :off] = e4m3.encode_rn_satfinite(np.where(nan, 0, held)) if old[h] > 0 else 0
+                codes[h, :off][nan] = 0x7F
         codes[:, off:off + x.shape[1]] = encode(x, new)
         self.scales[name][page] = new
 
