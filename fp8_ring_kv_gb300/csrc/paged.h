@@ -165,11 +165,14 @@ __device__ __forceinline__ RopeLane rope_lane(const PagedView& pv, int p0) {
   return r;
 }
 
-// (cos, sin) of the lane's pairs at the positions pr[0 .. n_axes - 1]
-__device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, float2 (&cs)[8],
-                                          bool& bad) {
+// The lane's table row (before its bounds are applied) at the positions
+// pr[0 .. n_axes - 1]
+__device__ __forceinline__ int rope_index(const RopeLane& r, const int32_t* pr) { return __ldg(pr + r.axis) - r.pos_min; }
+
+// (cos, sin) of the lane's pairs at the positions pr[0 .. n_axes - 1], idx = rope_index
+__device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, int idx,
+                                          float2 (&cs)[8], bool& bad) {
   if (r.row0) {
-    const int idx = __ldg(pr + r.axis) - r.pos_min;
     const int at = max(0, min(idx, r.last));
     bad = bad || at != idx;
     const float4* t = reinterpret_cast<const float4*>(r.row0 + (size_t)at * r.stride);
@@ -183,6 +186,11 @@ __device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r
 #pragma unroll
     for (int k = 0; k < 8; ++k) cs[k] = rope_cs(pv, pr, r.p0 + k, bad);
   }
+}
+
+__device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, float2 (&cs)[8],
+                                          bool& bad) {
+  rope_load(pv, r, pr, rope_index(r, pr), cs, bad);
 }
 
 // NaN codes (e4m3 S.1111.111) of four become zeros; true where there was one.

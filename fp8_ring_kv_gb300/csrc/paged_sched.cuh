@@ -6,6 +6,12 @@
 // lengths and a single long sequence load the GPU alike; an item cut by the
 // ends of stretches leaves partial results that a second kernel joins.  The
 // lengths are read on the device: a captured call follows them.
+//
+// Where a kernel's items cost much beside their tiles (FIX > 0), a cut is worth
+// avoiding: with fewer items than workers, every item gets the same number of
+// workers to itself (one, if there are no more), as if all were as long as the
+// longest, unless that makes a stretch longer than the equal one by more than a
+// cut costs (kCut).
 #pragma once
 #include "paged.h"
 
@@ -30,11 +36,19 @@ __device__ __forceinline__ Tiles item_tiles(const PagedAttn& a, const SeqInfo& s
   return t;
 }
 
+// How long every item counts (0: as long as it is), and a worker's stretch then.
+struct Cut {
+  int pad, stretch;
+};
+
 // One kernel's share of the sequences: those with rows in (MIN, MAX].  FIX:
 // what an item costs beside its tiles, in tiles.
 template <int TR, int KT, int FIX, int MIN, int MAX>
 struct Share {
-  static __device__ __forceinline__ int units(const Tiles& t) { return max(t.t1 - t.t0, FIX ? 0 : 1) + FIX; }
+  // pad: 0, or what every item counts
+  static __device__ __forceinline__ int units(const Tiles& t, int pad) {
+    return pad ? pad : max(t.t1 - t.t0, FIX ? 0 : 1) + FIX;
+  }
 
   // tiles of rows of sequence s that this kernel works on
   static __device__ __forceinline__ int row_tiles(const PagedAttn& a, const SeqInfo& s) {
@@ -44,9 +58,11 @@ struct Share {
   }
 
   // pre[b] = units of one key head of the sequences before b, pre[n_seqs] the
-  // total; all threads of the block.  warp_sums: one entry per warp.
+  // total; all threads of the block.  warp_sums: one entry per warp.  With
+  // FIX > 0 (``sums``: three zeros at first, shared): may set pad and a stretch.
   template <int NT>
-  static __device__ void prefix(const PagedAttn& a, long long* pre, long long* warp_sums, bool report) {
+  static __device__ Cut prefix(const PagedAttn& a, long long* pre, long long* warp_sums, bool report,
+                               unsigned long long* sums = nullptr, int workers = 0) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.pb.n_seqs;
     constexpr int kAlone = 4;            // row tiles that one thread sums by itself
@@ -57,7 +73,13 @@ struct Share {
       const int nt = row_tiles(a, s);
       long long u = 0;
       if (nt <= kAlone) {
-        for (int t = 0; t < nt; ++t) u += units(item_tiles<TR, KT>(a, s, t));
+        int most = 0;
+        for (int t = 0; t < nt; ++t) {
+          const int n = units(item_tiles<TR, KT>(a, s, t), 0);
+          u += n;
+          most = max(most, n);
+        }
+        if (FIX > 0 && nt > 0) add_items(sums, u, nt, most);
       } else {
         u = -1;
       }
@@ -70,13 +92,40 @@ struct Share {
       const SeqInfo s = seq_info(a.pb, a.pv.p_shift, b, ok);
       const int nt = row_tiles(a, s);
       long long u = 0;
-      for (int t = lane; t < nt; t += 32) u += units(item_tiles<TR, KT>(a, s, t));
+      int most = 0;
+      for (int t = lane; t < nt; t += 32) {
+        const int n = units(item_tiles<TR, KT>(a, s, t), 0);
+        u += n;
+        most = max(most, n);
+      }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
+      if (FIX > 0) most = __reduce_max_sync(0xFFFFFFFFu, most);
       __syncwarp();
-      if (lane == 0) pre[b + 1] = u;
+      if (lane == 0) {
+        pre[b + 1] = u;
+        if (FIX > 0) add_items(sums, u, nt, most);
+      }
     }
     __syncthreads();
+    Cut cut = {0, 0};
+    if constexpr (FIX > 0) {
+      const long long total = (long long)sums[0] * a.pv.H, items = (long long)sums[1] * a.pv.H;
+      const int most = (int)sums[2];
+      if (items > 0 && items <= workers) {
+        const int per = workers / (int)items;            // workers of an item
+        const int part = max((most + per - 1) / per, kLeast);
+        if (part <= max((total + workers - 1) / workers, (long long)kLeast) + kCut)
+          cut = {(most + part - 1) / part * part, part};
+      }
+      if (cut.pad) {
+        for (int b = tid; b < B; b += NT) {
+          bool ok;
+          pre[b + 1] = (long long)row_tiles(a, seq_info(a.pb, a.pv.p_shift, b, ok)) * cut.pad;
+        }
+        __syncthreads();
+      }
+    }
     // inclusive scan: each thread a run of entries, then the runs' sums
     const int run = (B + NT - 1) / NT;
     const int b0 = min(B, tid * run), b1 = min(B, b0 + run);
@@ -98,7 +147,24 @@ struct Share {
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
+    return cut;
   }
+
+  // units, items, and the longest item
+  static __device__ __forceinline__ void add_items(unsigned long long* sums, long long u, int items, int most) {
+    atomicAdd(&sums[0], (unsigned long long)u);
+    atomicAdd(&sums[1], (unsigned long long)items);
+    atomicMax(&sums[2], (unsigned long long)most);
+  }
+
+  // Units of a stretch, at least (64 tokens over 4,000, 8 key heads: 38.5 us;
+  // with 6: 41.5, with 9: 44.4), and what a cut costs: a second piece's
+  // queries, fp32 results and their joining (1,100 tokens over 4,000: 100.4 us;
+  // with 4, which cuts there: 107.8; with 12, which does not cut 512 tokens
+  // over 16,000: 152.7 instead of 140.7).  Items to themselves take 22.9 us for
+  // a prompt of 128 and 38 us for one of 1,024, cut ones 31.6 and 47.
+  static constexpr int kLeast = 4;
+  static constexpr int kCut = 8;
 };
 
 // A place on the line of items: (sequence, key head, row tile), the unit at
@@ -113,7 +179,7 @@ struct Place {
 
 // The item that holds unit u (0 <= u < H * pre[n_seqs]); one warp.
 template <class SH, int TR, int KT>
-__device__ Place find_place(const PagedAttn& a, const long long* pre, long long u) {
+__device__ Place find_place(const PagedAttn& a, const long long* pre, long long u, int pad = 0) {
   const int lane = threadIdx.x & 31;
   const int H = a.pv.H;
   int lo = 0, hi = a.pb.n_seqs - 1;      // the last b with pre[b] * H <= u
@@ -134,7 +200,7 @@ __device__ Place find_place(const PagedAttn& a, const long long* pre, long long 
   p.tile = 0;
   for (int t0 = 0; t0 < p.row_tiles; t0 += 32) {
     const int t = t0 + lane;
-    const int n = t < p.row_tiles ? SH::units(item_tiles<TR, KT>(a, p.s, t)) : 0;
+    const int n = t < p.row_tiles ? SH::units(item_tiles<TR, KT>(a, p.s, t), pad) : 0;
     long long inc = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -154,13 +220,13 @@ __device__ Place find_place(const PagedAttn& a, const long long* pre, long long 
     p.at += all;
   }
   p.t = item_tiles<TR, KT>(a, p.s, p.tile);
-  p.units = SH::units(p.t);
+  p.units = SH::units(p.t, pad);
   return p;
 }
 
 // The next item; false at the end of the line.
 template <class SH, int TR, int KT>
-__device__ __forceinline__ bool next_place(const PagedAttn& a, Place& p) {
+__device__ __forceinline__ bool next_place(const PagedAttn& a, Place& p, int pad = 0) {
   p.at += p.units;
   if (++p.tile >= p.row_tiles) {
     p.tile = 0;
@@ -175,7 +241,7 @@ __device__ __forceinline__ bool next_place(const PagedAttn& a, Place& p) {
     }
   }
   p.t = item_tiles<TR, KT>(a, p.s, p.tile);
-  p.units = SH::units(p.t);
+  p.units = SH::units(p.t, pad);
   return true;
 }
 

@@ -63,6 +63,7 @@ struct TilesLayout {
   static constexpr int RAW = VH + 2 * KB;                        // K codes, V codes of one tile
   static constexpr int META = RAW + 2 * KT * D;                  // [TMETA][KT / 16] {s_k, log2 s_v, 1 / s_v, -}
   static constexpr int SLOT = META + TMETA * (KT / 16) * 16;     // [2 halves][256] a row's logit factor; maxima; sums
+  static constexpr int SUMS = SLOT + 1024;                       // (at first) sums over the items, behind the warps'
   static constexpr int SEG = SLOT + 2 * TTR * 4;                 // [2] Stretch
   static constexpr int BAR = SEG + 2 * (int)sizeof(Stretch);
   static constexpr int NBAR = 2 + 2 + 2 + TMETA + 4 + 4 + 2 + 4 + 4 + 1 + 16 + 8;
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     *nan_seen = 0;
+    for (int i = 0; i < 3; ++i) reinterpret_cast<unsigned long long*>(sm + LY::SUMS)[i] = 0;
     fence_mbar_init();
   }
   if (warp == 16) {
@@ -173,16 +175,18 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   pdl_trigger();
   // this block's stretch of the line of items
   long long* pre = reinterpret_cast<long long*>(sm + LY::Q);
-  SH::template prefix<TTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SLOT), false);
+  const Cut cut = SH::template prefix<TTHREADS>(a, pre, reinterpret_cast<long long*>(sm + LY::SLOT), false,
+                                                reinterpret_cast<unsigned long long*>(sm + LY::SUMS), gridDim.x);
   const int H = a.pv.H, G = a.pv.G;
   const long long total = pre[a.pb.n_seqs] * H;
   long long stretch = (total + gridDim.x - 1) / gridDim.x;
-  if (stretch < 6) stretch = 6;
+  if (stretch < SH::kLeast) stretch = SH::kLeast;
+  if (cut.pad) stretch = cut.stretch;
   const int worker = blockIdx.x;
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
   Place pl;
-  if (warp == 17 && u < end) pl = find_place<SH, TTR, KT>(a, pre, u);
+  if (warp == 17 && u < end) pl = find_place<SH, TTR, KT>(a, pre, u, cut.pad);
   __syncthreads();                         // the prefix sums' room is the query tiles' now
 
   // ``done``: tiles of the line that a role has behind it; it gives the stage
@@ -243,6 +247,25 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         const int step_i = RSTEP / G, step_g = RSTEP - step_i * G;
         int qi = (r0 + rr0) / G, qg = r0 + rr0 - qi * G;
         const T* qp = static_cast<const T*>(a.q) + (size_t)head0 * D + ql * 16;
+        const int32_t* pr0 = a.q_pos + (size_t)s0 * a.pv.n_axes;
+        auto step = [&](int& i2, int& g2) {
+          i2 += step_i;
+          g2 += step_g;
+          if (g2 >= G) {
+            g2 -= G;
+            ++i2;
+          }
+        };
+        // positions of a turn's rows, a turn ahead of its loads from the table
+        int idx[BATCH];
+        auto positions = [&](int rr, int i2, int g2) {
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            idx[k] = rope_index(rl, pr0 + (size_t)(rr + k * RSTEP < rows ? i2 : 0) * a.pv.n_axes);
+            step(i2, g2);
+          }
+        };
+        positions(rr0, qi, qg);
 #pragma unroll 1
         for (int rr = rr0; rr < 32 * (warp & 3) + 16 * par + 16; rr += RSTEP * BATCH) {
           uint4 w0[BATCH], w1[BATCH];
@@ -256,14 +279,10 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               w0[k] = __ldg(src);
               w1[k] = __ldg(src + 1);
             }
-            rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + (on ? qi : 0)) * a.pv.n_axes, cs[k], bad);
-            qi += step_i;
-            qg += step_g;
-            if (qg >= G) {
-              qg -= G;
-              ++qi;
-            }
+            rope_load(a.pv, rl, pr0 + (size_t)(on ? qi : 0) * a.pv.n_axes, idx[k], cs[k], bad);
+            step(qi, qg);
           }
+          positions(rr + RSTEP * BATCH, qi, qg);         // (rows past the last turn's: a row's position all the same)
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             const int rk = rr + k * RSTEP;
@@ -451,16 +470,16 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         if (whole) {
           const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
-            uint32_t o[16];
+          for (int c = 0; c < D / 2; c += 32) {
+            uint32_t o[32];
             if (n > 0) {
-              tmem_ld_32x32b_x16(o_at + par * (D / 2) + c, o);
+              tmem_ld_32x32b_x32(o_at + par * (D / 2) + c, o);
             } else {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = 0u;
+              for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -477,14 +496,11 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             // fp32: half of the warp's channels at a time
 #pragma unroll 1
             for (int h4 = par * (D / 2); h4 < (par + 1) * (D / 2); h4 += D / 4) {
-#pragma unroll 1
-              for (int c = 0; c < D / 4; c += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(o_at + h4 + c, o);
+              uint32_t o[D / 4];
+              if constexpr (D == 128) tmem_ld_32x32b_x32(o_at + h4, o);
+              else tmem_ld_32x32b_x16(o_at + h4, o);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  put(c / 4 + k, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
-              }
+              for (int k = 0; k < D / 16; ++k) put(k, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
               flush(live ? a.tiles.o + at_row * D + h4 : nullptr);
             }
           }
@@ -700,7 +716,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         if (u == pl.at && end < item_end)
           rec = {min(pl.s.n * G - pl.tile * TTR, TTR), (int)((item_end - 1) / stretch), pl.h, pl.s.s0, pl.tile * TTR};
         u = min(end, item_end);
-        more = u < end && next_place<SH, TTR, KT>(a, pl);
+        more = u < end && next_place<SH, TTR, KT>(a, pl, cut.pad);
       }
       if (lane == 0) a.tiles.rec[worker] = rec;
       // after an abort: copies still in flight land in this block's shared memory
@@ -743,8 +759,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             uint8_t* dst = sm + (v ? LY::VH : LY::KH) + buf * LY::KB + (ch >> 2) * (KT * 128);
             const int cc = (2 * ch) & 7;
             const int key0 = (k0 + j) * KT;
-            const bool cut = v && (key0 + KT > all_hi || key0 < all_lo);
-            if (cut) {
+            const bool mixed = v && (key0 + KT > all_hi || key0 < all_lo);
+            if (mixed) {
               // Values that no query sees become zeros, whatever their page
               // holds; their scores are masked.  A NaN that some rows see and
               // others do not must not meet the latter's zero weights: it is
