@@ -189,12 +189,12 @@ class PagedKV:
             raise KVRingError(f"max_new: {max_new}; 1 .. {n}")
         if out is None:
             if stream is None:
-                out = torch.empty((n, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                out = q.new_empty((n, self.q_heads, self.head_dim))
             else:
                 # memory that the allocator knows to be in use on that stream
                 s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
                 with torch.cuda.stream(s):
-                    out = torch.empty((n, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                    out = q.new_empty((n, self.q_heads, self.head_dim))
         os_ = self._row_stride(out, n, self.q_heads, "out")
         if n and n_seqs:
             self._call("kvring_paged_attend", layer, q.data_ptr(), qs, p, start, length, n_seqs, n,
