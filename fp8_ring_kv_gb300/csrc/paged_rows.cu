@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
   const int worker = blockIdx.x * RW + warp;
   const int workers = gridDim.x * RW;
   const long long total = pre[a.pb.n_seqs] * H;
-  const long long stretch = (total + workers - 1) / workers;
+  const long long stretch = quotient(total + workers - 1, workers);
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
   PieceRec rec = {};
@@ -184,10 +184,11 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
         for (int p = 0; p < 2; ++p)
           if (sv[p] == 0.0f) sv[p] = v_near;
       };
-      // tile k's codes on their way to the next stage, by the lane that holds its pages
-      auto issue = [&](int k) {
-        if (lane == k - base) {
-          const int st = used % NST;
+      // the codes of tiles [k, to) on their way to the next stages, each by the lane that holds its pages
+      auto issue = [&](int k, int to) {
+        const int mine = base + lane;
+        if (mine >= k && mine < to) {
+          const int st = (used + mine - k) % NST;
           uint8_t* dst = stages + st * LY::STAGE;
           if (a.pv.P == 16) {
             mbar_arrive_expect_tx(&bars[st], (uint32_t)((id[0] >= 0) + (id[1] >= 0)) * 2 * 16 * D);
@@ -199,13 +200,13 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
                 tma_load_2d(dst + RK * D + p * 16 * D, &tmV, &bars[st], 0, y);
               }
           } else {
-            const int y = (int)(a.pv.row0 + (((long long)id[0] * H + pl.h) << a.pv.p_shift)) + ((k * RK) & (a.pv.P - 1));
+            const int y = (int)(a.pv.row0 + (((long long)id[0] * H + pl.h) << a.pv.p_shift)) + ((mine * RK) & (a.pv.P - 1));
             mbar_arrive_expect_tx(&bars[st], LY::STAGE);
             tma_load_2d(dst, &tmK, &bars[st], 0, y);
             tma_load_2d(dst + RK * D, &tmV, &bars[st], 0, y);
           }
         }
-        ++used;
+        used += to - k;
       };
       auto write_meta = [&](int k, int n) {
         if (lane == k - base) {
@@ -242,7 +243,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           for (int k = 0; k < 8; ++k) cs[e][8 * c + k] = part8[k];
         }
       }
-      while (issued < k1 && issued < k0 + NST) issue(issued++);
+      issued = min(k1, k0 + NST);
+      issue(k0, issued);
       load_scales(id, sk, sv);
       // ---------------------------------------------------------- queries
       // row g of each tile, rotated, scaled by a power of two and rounded to
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             load_scales(id, sk, sv);
             near_scale();
           }
-          issue(issued);
+          issue(issued, issued + 1);
           write_meta(issued, used - 1);
           ++issued;
           __syncwarp();
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
           }
         }
-      if (u == pl.at && end < item_end) rec = {rows, (int)((item_end - 1) / stretch), pl.h, pl.s.s0, 0};
+      if (u == pl.at && end < item_end) rec = {rows, (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, 0};
       u = min(end, item_end);
       if (u >= end || !next_place<RowsShare, RT, RK>(a, pl)) break;
     }

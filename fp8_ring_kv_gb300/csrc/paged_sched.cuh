@@ -17,6 +17,11 @@
 
 namespace kvring_dev {
 
+// a / b, both >= 0 (b > 0): 32-bit numbers nearly always, whose division is several times shorter
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct Tiles {
   int lo, hi;          // keys that some row of the item sees: [lo, hi), empty when hi <= lo
   int t0, t1;          // tiles of KT keys that hold them
@@ -25,8 +30,11 @@ struct Tiles {
 template <int TR, int KT>
 __device__ __forceinline__ Tiles item_tiles(const PagedAttn& a, const SeqInfo& s, int tile) {
   const int g = a.pv.G;
-  const int i0 = tile * TR / g;
-  const int i1 = min(s.n, (tile * TR + TR + g - 1) / g) - 1;
+  int i0 = 0, i1 = s.n - 1;
+  if (s.n * g > TR) {
+    i0 = tile * TR / g;
+    i1 = min(s.n, (tile * TR + TR + g - 1) / g) - 1;
+  }
   Tiles t;
   t.hi = a.causal ? max(0, s.len - s.n + i1 + 1) : s.len;
   t.lo = a.window > 0 ? max(0, s.len - s.n + i0 - a.window + 1) : 0;
@@ -85,29 +93,32 @@ struct Share {
       }
       pre[b + 1] = u;
     }
-    __syncthreads();
-    for (int b = warp; b < B; b += NT / 32) {
-      if (pre[b + 1] >= 0) continue;
-      bool ok;
-      const SeqInfo s = seq_info(a.pb, a.pv.p_shift, b, ok);
-      const int nt = row_tiles(a, s);
-      long long u = 0;
-      int most = 0;
-      for (int t = lane; t < nt; t += 32) {
-        const int n = units(item_tiles<TR, KT>(a, s, t), 0);
-        u += n;
-        most = max(most, n);
-      }
+    // (with an entry for each thread, a thread scans its own)
+    if (MAX > kAlone * TR || B > NT) __syncthreads();
+    if constexpr (MAX > kAlone * TR) {
+      for (int b = warp; b < B; b += NT / 32) {
+        if (pre[b + 1] >= 0) continue;
+        bool ok;
+        const SeqInfo s = seq_info(a.pb, a.pv.p_shift, b, ok);
+        const int nt = row_tiles(a, s);
+        long long u = 0;
+        int most = 0;
+        for (int t = lane; t < nt; t += 32) {
+          const int n = units(item_tiles<TR, KT>(a, s, t), 0);
+          u += n;
+          most = max(most, n);
+        }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
-      if (FIX > 0) most = __reduce_max_sync(0xFFFFFFFFu, most);
-      __syncwarp();
-      if (lane == 0) {
-        pre[b + 1] = u;
-        if (FIX > 0) add_items(sums, u, nt, most);
+        for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
+        if (FIX > 0) most = __reduce_max_sync(0xFFFFFFFFu, most);
+        __syncwarp();
+        if (lane == 0) {
+          pre[b + 1] = u;
+          if (FIX > 0) add_items(sums, u, nt, most);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
     Cut cut = {0, 0};
     if constexpr (FIX > 0) {
       const long long total = (long long)sums[0] * a.pv.H, items = (long long)sums[1] * a.pv.H;
@@ -115,7 +126,7 @@ struct Share {
       if (items > 0 && items <= workers) {
         const int per = workers / (int)items;            // workers of an item
         const int part = max((most + per - 1) / per, kLeast);
-        if (part <= max((total + workers - 1) / workers, (long long)kLeast) + kCut)
+        if (part <= max(quotient(total + workers - 1, workers), (long long)kLeast) + kCut)
           cut = {(most + part - 1) / part * part, part};
       }
       if (cut.pad) {
@@ -126,7 +137,7 @@ struct Share {
         __syncthreads();
       }
     }
-    // inclusive scan: each thread a run of entries, then the runs' sums
+    // inclusive scan: each thread a run of entries (at most one, nearly always), then the runs' sums
     const int run = (B + NT - 1) / NT;
     const int b0 = min(B, tid * run), b1 = min(B, b0 + run);
     long long sum = 0;
@@ -194,7 +205,7 @@ __device__ Place find_place(const PagedAttn& a, const long long* pre, long long 
   p.row_tiles = SH::row_tiles(a, p.s);
   const long long per_head = pre[lo + 1] - pre[lo];
   long long rest = u - pre[lo] * H;
-  p.h = per_head > 0 ? (int)(rest / per_head) : 0;
+  p.h = per_head > 0 ? (int)quotient(rest, per_head) : 0;
   rest -= p.h * per_head;
   p.at = u - rest;
   p.tile = 0;

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
                                                 reinterpret_cast<unsigned long long*>(sm + LY::SUMS), gridDim.x);
   const int H = a.pv.H, G = a.pv.G;
   const long long total = pre[a.pb.n_seqs] * H;
-  long long stretch = (total + gridDim.x - 1) / gridDim.x;
+  long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
   if (stretch < SH::kLeast) stretch = SH::kLeast;
   if (cut.pad) stretch = cut.stretch;
   const int worker = blockIdx.x;
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         }
         done += k1 - k0;
         if (u == pl.at && end < item_end)
-          rec = {min(pl.s.n * G - pl.tile * TTR, TTR), (int)((item_end - 1) / stretch), pl.h, pl.s.s0, pl.tile * TTR};
+          rec = {min(pl.s.n * G - pl.tile * TTR, TTR), (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, pl.tile * TTR};
         u = min(end, item_end);
         more = u < end && next_place<SH, TTR, KT>(a, pl, cut.pad);
       }
