@@ -8,8 +8,8 @@
 // page's weights is divided by s_v (exactly).  A page of zero V codes has
 // s_v = 0; any scale serves it, and the nearest page's is taken.
 //
-// What bounds it: every key and value byte is read once for at most 16 rows,
-// so HBM bandwidth, if the warps get through their instructions: a byte costs
+// What bounds it: every key and value byte is read once for up to 16 rows (8 in
+// fp16), again for the next of up to 32, so HBM bandwidth, if the warps get through their instructions: a byte costs
 // half a conversion and its share of the MMAs, whatever the number of rows.
 // The codes go from memory to shared memory by TMA (32 keys and values per
 // stage, a ring of stages per warp) and from there, widened to fp16 (exact),
@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
   constexpr bool SIDE = SPLIT && NT == 1;                // low parts beside the high ones
   constexpr int E = SPLIT ? 1 : NT;                      // tiles of query rows
   constexpr int COLS = SIDE ? 4 : 8;                     // rows of a tile
-  constexpr int RT = kRowsMax<T>;                        // rows of an item, at most
-  using RowsShare = Share<RT, RK, 0, 0, RT>;
+  constexpr int RT = kRowsTile<T>;                       // rows of an item, at most
+  using RowsShare = Share<RT, RK, 0, 0, kRowsMax>;
   constexpr int KS = D / 16;                             // k steps of QK
   constexpr int NJ = D / 16;                             // channel tiles of O
   constexpr int DG = D / 8;                              // channels per thread
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       const int k0 = pl.t.t0 + (int)(u - pl.at);
       const int k1 = min(pl.t.t1, pl.t.t0 + (int)(min(end, item_end) - pl.at));
       const bool whole = u == pl.at && end >= item_end;
-      const int rows = pl.s.n * G;
+      const int row0 = pl.tile * RT, rows = min(RT, pl.s.n * G - row0);
       // ---------------------------------------------------------- pages
       // lane i holds the page ids and scales of tile base + i (two pages when
       // P = 16); v_near: a non-zero V scale near by, for pages of zeros
@@ -227,13 +227,13 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       for (int e = 0; e < E; ++e) {
         const int r = e * COLS + g % COLS;
         const bool live = r < rows;
-        const int i = live ? r / G : 0;
+        const int i = live ? (row0 + r) / G : 0;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           qw[e][2 * c] = qw[e][2 * c + 1] = make_uint4(0, 0, 0, 0);
           if (live) {
             const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + r - i * G) * D + c * 64 + t4 * 16);
+                static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + row0 + r - i * G) * D + c * 64 + t4 * 16);
             qw[e][2 * c] = __ldg(src);
             qw[e][2 * c + 1] = __ldg(src + 1);
           }
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const int rr = e * COLS + (2 * t4 + f) % COLS;
-          const int at = pl.s.len - pl.s.n + (rr < rows ? rr / G : 0);   // the row's own index
+          const int at = pl.s.len - pl.s.n + (rr < rows ? (row0 + rr) / G : 0);   // the row's own index
           rf[e][f] = __shfl_sync(0xFFFFFFFFu, rfg, 4 * (2 * t4 + f));
           hi[e][f] = rr >= rows ? 0x7FFFFFFF : a.causal ? at + 1 : pl.s.len;
           lo[e][f] = rr < rows && a.window > 0 ? at - a.window + 1 : 0;
@@ -531,10 +531,10 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             }
           if (r >= rows || 2 * t4 + f >= COLS) continue;
           if (whole) {
-            const int i = r / G;
+            const int i = (row0 + r) / G;
             const float inv = l[e][f] != 0.0f ? 1.0f / l[e][f] : 0.0f;
             uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride +
-                                                  (size_t)(pl.h * G + r - i * G) * D + g * DG);
+                                                  (size_t)(pl.h * G + row0 + r - i * G) * D + g * DG);
 #pragma unroll
             for (int c = 0; c < DG / 8; ++c)
               dst[c] = make_uint4(pack2<T>(v[8 * c] * inv, v[8 * c + 1] * inv), pack2<T>(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
             if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
           }
         }
-      if (u == pl.at && end < item_end) rec = {rows, (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, 0};
+      if (u == pl.at && end < item_end) rec = {rows, (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, row0};
       u = min(end, item_end);
       if (u >= end || !next_place<RowsShare, RT, RK>(a, pl)) break;
     }

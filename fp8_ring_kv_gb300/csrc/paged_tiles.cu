@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   using LY = TilesLayout<D, T>;
   constexpr int KT = LY::KT, NQ = LY::NQ, NG = KT / 16;
   constexpr int SC = KT / 2;               // keys of a tile that a softmax warp looks at
-  using SH = Share<TTR, KT, 2, kRowsMax<T>, 0x7FFFFFFF>;
+  using SH = Share<TTR, KT, 2, kRowsMax, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr int kNone = -1;                // page of a group of keys that no query sees
   extern __shared__ __align__(1024) uint8_t sm[];

@@ -730,3 +730,20 @@ def test_a_window_wider_than_everything():
         want = c.kv.attend(q, *args)
         for window in (64, 2 ** 22, 2 ** 31 - 1, 2 ** 40):
             assert bool((c.kv.attend(q, *args, window=window) == want).all()), window
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("case,how", [
+    (dict(seqs=[(1, 900), (2, 300), (3, 5000), (4, 40), (5, 700), (4, 0)], group=8), {}),
+    (dict(seqs=[(3, 5000), (4, 900), (2, 33)], group=8, page=16, dim=64), dict(window=130)),
+    (dict(seqs=[(1, 2000), (1, 3), (2, 70)], kv_heads=1, group=16), dict(max_new=2)),
+    (dict(seqs=[(31, 2), (32, 500), (33, 500), (9, 100), (17, 100), (25, 1000)], group=1, page=32), {}),
+    (dict(seqs=[(31, 2), (32, 500), (8, 100), (16, 100), (24, 3000)], group=1, dim=64, page=128), dict(causal=False)),
+    (dict(seqs=[(3, 600), (1, 10)], kv_heads=3, group=11), dict(max_new=3)),
+], ids=range(6))
+def test_several_row_tiles_of_a_few_tokens(case, how, dtype):
+    """Sequences whose query rows fill one to four of the register tiles, or one more."""
+    c = Case(dtype=dtype, **case)
+    c.fill(2)
+    c.attend(**how)
+    assert c.kv.debug_state() == 0
