@@ -9,12 +9,24 @@
 // what a page holds does not depend on how many calls filled it, but for
 // codes that become e4m3 subnormals (half a step of 2^-10 s).  That is why
 // the scale is not a / 448, which would round every older code at each growth.
+//
+// What bounds it: a thread's chain of dependent loads (the sequences' numbers,
+// positions, table rows) with as many threads on an SM as the registers of two
+// rows each allow.  16,662 tokens of 8 heads x 128: 26.5 us, 3.9 TB/s of the
+// input's and codes' bytes, 57% of a copy (one row per thread: 43 us, two
+// without the bound on registers: 31 us; several units per block one after the
+// other: 39 us, the loop's registers spilt).
 #include "paged.h"
 #include "launch.h"
 
 namespace kvring_dev {
 
-constexpr int kAppendFew = 4;   // tokens per sequence, on average, up to which the row kernel is taken
+// Tokens per sequence, on average, up to which the kernel of few tokens is
+// taken.  128 sequences, 8 heads x 128, pages of 64, in us, against whole pages:
+// 1 token each 2.9 : 12.9, 4 tokens 5.3 : 13.2, 16 tokens 14.4 : 15.2, 64 tokens
+// 56 : 21; 16 sequences of 256 tokens 47 : 9.  Well below the crossing, because
+// the average may hide one long sequence.
+constexpr int kAppendFew = 4;
 
 // Tasks: sequence b touches at most floor(n_b / P) + 2 pages, so it owns the
 // task numbers base(b) .. base(b + 1) - 1 with base(b) = floor(seq_start[b] /

@@ -9,12 +9,16 @@
 // s_v = 0; any scale serves it, and the nearest page's is taken.
 //
 // What bounds it: every key and value byte is read once for up to 16 rows (8 in
-// fp16), again for the next of up to 32, so HBM bandwidth, if the warps get through their instructions: a byte costs
-// half a conversion and its share of the MMAs, whatever the number of rows.
+// fp16), and again for the next of up to 32, so HBM bandwidth, if the warps get
+// through their instructions: a byte costs half a conversion and its share of
+// the MMAs, whatever the number of rows.
 // The codes go from memory to shared memory by TMA (32 keys and values per
 // stage, a ring of stages per warp) and from there, widened to fp16 (exact),
 // straight into the registers of mma.m16n8k16; a warp works by itself, with no
-// barrier between warps.  tcgen05 would want 128 rows.
+// barrier between warps.  tcgen05 would want 128 rows.  Measured: a batch of 64
+// ragged contexts of 200 to 8,000 tokens (4 rows, 542 MB) 102 us with joining,
+// 5.3 TB/s; the stretch after the first codes runs at 6.3 TB/s (93% of a copy),
+// some 15 us go into the start (lengths, prefix sums, pages: 5 us) and the end.
 //
 // The products are S^T = K Q^T and O^T = V^T P^T: keys and channels are the
 // MMA's 16 rows and the queries its 8 columns, so up to 8 query rows waste
@@ -577,7 +581,9 @@ static cudaError_t prepare_d() {
 cudaError_t prepare_paged_rows(int D) { return D == 128 ? prepare_d<128>() : prepare_d<64>(); }
 
 // One column tile where no sequence of the call has more rows than it holds,
-// as far as the host knows: half of the MMAs, and half as many warps again.
+// as far as the host knows: half of the MMAs, and half as many warps again
+// (64 ragged contexts, 4 rows: 108 us against 129 with two; fp16, 1 row: 42
+// against 46).
 static int column_tiles(const PagedAttn& a, bool f16) { return (long long)a.max_new * a.pv.G > (f16 ? 4 : 8) ? 2 : 1; }
 
 int paged_rows_warps(const PagedAttn& a, bool f16) { return column_tiles(a, f16) == 1 ? kRowsWarps : 8; }

@@ -20,6 +20,14 @@
 // of both.  S is 128 keys wide in one product: with two buffers of 64 keys QK
 // could run ahead of the softmax, but a 128 x 64 x 16 product from shared memory
 // takes 58 cycles, hardly less than a 128 x 128 x 16 one.
+// Measured: 512 tokens over 65,000, 32 query heads on 8 key heads: 440 us by
+// itself (1.24 PFLOP/s, 66% of a library product), 490 us in a row of such
+// calls; three prompts of 1,731 to 3,644 tokens 283 us (0.72 PFLOP/s).  128 keys
+// of 256 rows take some 3,800 cycles: the products 2,200, the chain of one query
+// tile (softmax 2,000, its two products 1,100, hand-overs 500) the rest, beside
+// widening that is nearly as long; without any exponential, or any conversion,
+// the kernel is no more than 2% faster.  A piece of an item costs 12,000 cycles
+// beside its tiles (queries 6,500, the last product and the results 5,000).
 //
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15       softmax: of query tile t and half p of its keys, warps
