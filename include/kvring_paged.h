@@ -129,8 +129,9 @@ int kvring_paged_create(const kvring_paged_config* cfg, void* workspace, size_t 
  * e4m3(x / scale), round to nearest even.  Rows of the page past the last new
  * one are left as they are.
  * kv_len must count the new tokens (n <= kv_len).  Pages written by a call
- * belong to one sequence each: a page that two sequences of the batch append
- * to ends up with rows of either.
+ * belong to one place of one sequence each: a page that two sequences of the
+ * batch append to, or that a table names twice among its new tokens, ends up
+ * with rows of either.
  * N (at most 2^24) or B of 0: nothing to do.
  */
 int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k_stride, const void* v,
