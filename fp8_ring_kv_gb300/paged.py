@@ -12,6 +12,8 @@ import torch
 from . import kvring as _k
 from .kvring import KVRingError, check, kvring_paged_config
 
+_I32 = torch.int32
+_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _IN = {torch.bfloat16: _k.KVRING_IN_BF16, torch.float16: _k.KVRING_IN_F16}
 
 
@@ -88,6 +90,7 @@ class PagedKV:
             check(lib.kvring_paged_create(ctypes.byref(self.cfg), workspace.data_ptr(), workspace.numel(),
                                           self._stream(stream), ctypes.byref(h)), "kvring_paged_create")
         self.handle = h
+        self._append, self._attend = lib.kvring_paged_append, lib.kvring_paged_attend
         ptrs = [ctypes.c_void_p() for _ in range(5)]
         check(lib.kvring_paged_layout(h, *[ctypes.byref(p) for p in ptrs]), "kvring_paged_layout")
         kc, vc, ks, vs, _ = [p.value - workspace.data_ptr() for p in ptrs]
@@ -100,7 +103,7 @@ class PagedKV:
 
     def _stream(self, stream):
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self._index)
+            return _get_stream(self._index)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     # The checks run before every call, beside kernels of a few microseconds:
@@ -118,7 +121,7 @@ class PagedKV:
         raise KVRingError(_bad_heads(t, n, heads, dim, self.dtype, self._index, what))
 
     def _ints(self, t, shape, what):
-        if t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == self._index:
+        if t.dtype is _I32 and t.shape == shape and t.is_contiguous() and t.get_device() == self._index:
             return t.data_ptr()
         raise KVRingError(_bad_ints(t, shape, self._index, what))
 
@@ -136,7 +139,7 @@ class PagedKV:
             raise KVRingError(f"page_table: {n_seqs} sequences; a call takes at most {_k.KVRING_PAGED_MAX_SEQS}")
         if width * self.page_tokens > _k.KVRING_PAGED_MAX_LEN:
             raise KVRingError(f"page_table: {width} pages a row, more than {_k.KVRING_PAGED_MAX_LEN} tokens")
-        if page_table.dtype is not torch.int32 or page_table.get_device() != self._index:
+        if page_table.dtype is not _I32 or page_table.get_device() != self._index:
             raise KVRingError(f"page_table: {page_table.dtype} on {page_table.device}; torch.int32 on cuda:{self._index} is read")
         row, one = page_table.stride()
         if (width > 1 and one != 1) or (n_seqs > 1 and row < width):
@@ -144,16 +147,15 @@ class PagedKV:
         return (self._ints(pos, (n, self.n_axes), pos_name), self._ints(seq_start, (n_seqs + 1,), "seq_start"),
                 self._ints(kv_len, (n_seqs,), "kv_len"), n_seqs, page_table.data_ptr(), max(row, width), width)
 
-    def _call(self, name, *args):
+    def _call(self, fn, *args):
         """The library's function with the cache's device current."""
-        fn = getattr(_k.load(), name)
-        if torch._C._cuda_getDevice() == self._index:
+        if _get_device() == self._index:
             status = fn(self.handle, *args)
         else:
             with torch.cuda.device(self.device):
                 status = fn(self.handle, *args)
         if status:
-            check(status, name)
+            check(status, fn.__name__)
 
     def append(self, k, v, pos, seq_start, kv_len, page_table, layer=0, stream=None):
         """Write the new tokens' keys (rotated at ``pos``) and values.
@@ -166,7 +168,7 @@ class PagedKV:
         ks, vs = self._row_stride(k, n, self.kv_heads, "k"), self._row_stride(v, n, self.kv_heads, "v")
         p, start, length, n_seqs, table, ts, width = self._batch(layer, n, pos, "pos", seq_start, kv_len, page_table)
         if n and n_seqs:
-            self._call("kvring_paged_append", layer, k.data_ptr(), ks, v.data_ptr(), vs, p, start, length, n_seqs, n,
+            self._call(self._append, layer, k.data_ptr(), ks, v.data_ptr(), vs, p, start, length, n_seqs, n,
                        table, ts, width, self._stream(stream))
 
     def attend(self, q, q_pos, seq_start, kv_len, page_table, out=None, layer=0, causal=True, window=None, scale=None,
@@ -189,15 +191,17 @@ class PagedKV:
             raise KVRingError(f"max_new: {max_new}; 1 .. {n}")
         if out is None:
             if stream is None:
-                out = q.new_empty((n, self.q_heads, self.head_dim))
+                out = torch.empty_like(q, memory_format=torch.contiguous_format)
             else:
                 # memory that the allocator knows to be in use on that stream
                 s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
                 with torch.cuda.stream(s):
-                    out = q.new_empty((n, self.q_heads, self.head_dim))
-        os_ = self._row_stride(out, n, self.q_heads, "out")
+                    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            os_ = self.q_heads * self.head_dim
+        else:
+            os_ = self._row_stride(out, n, self.q_heads, "out")
         if n and n_seqs:
-            self._call("kvring_paged_attend", layer, q.data_ptr(), qs, p, start, length, n_seqs, n,
+            self._call(self._attend, layer, q.data_ptr(), qs, p, start, length, n_seqs, n,
                        n if max_new is None else max_new, table, ts, width, 1 if causal else 0, min(window or 0, _k.KVRING_PAGED_MAX_LEN),
                        scale or 0.0, out.data_ptr(), os_, self._stream(stream))
         return out
