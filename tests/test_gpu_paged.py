@@ -747,3 +747,36 @@ def test_several_row_tiles_of_a_few_tokens(case, how, dtype):
     c.fill(2)
     c.attend(**how)
     assert c.kv.debug_state() == 0
+
+
+@pytest.mark.parametrize("dtype,n,dim,page", [(BF, 1, 64, 128), (HF, 3, 128, 64), (BF, 50, 128, 64), (HF, 40, 64, 128)])
+def test_the_longest_sequence(dtype, n, dim, page):
+    """2^22 tokens whose table names the same few pages again and again: the
+    attention over those pages once."""
+    c = Case([(0, 4 * page)], kv_heads=1, group=2, dim=dim, page=page, dtype=dtype)
+    c.fill(1)
+    times = 2 ** 22 // (4 * page)
+    table = np.tile(c.table[:, :4], (1, times))
+    q = c.draw(n, 2)
+    pos = np.zeros((n, 1), np.int32)
+    start = np.array([0, n], np.int32)
+    # not causal: every query sees every page equally often
+    out = c.kv.attend(q.cuda(), cu(pos), cu(start), cu(np.array([2 ** 22], np.int32)), cu(table), causal=False)
+    c.n = n
+    c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, [4 * page], c.table, False))
+    # a window that reaches back over whole rounds of the pages
+    if n == 1:
+        out = c.kv.attend(q.cuda(), cu(pos), cu(start), cu(np.array([2 ** 22], np.int32)), cu(table), window=4 * page * 1000)
+        c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, [4 * page], c.table, False))
+    assert c.kv.debug_state() == 0
+
+
+def test_many_sequences_of_both_kinds():
+    """2,048 sequences, some without new tokens, some with prompts' worth of rows."""
+    seqs = [(0 if i % 5 == 3 else 300 if i % 401 == 7 else 40 if i % 97 == 0 else 1 + i % 2, i % 50) for i in range(2048)]
+    c = Case(seqs, kv_heads=1, group=3, dim=64, page=32)
+    c.fill(2)
+    c.check_cache()
+    c.attend()
+    c.attend(window=9)
+    assert c.kv.debug_state() == 0
