@@ -48,6 +48,7 @@ constexpr int TM_ROWS = 128;                 // rows of one MMA
 constexpr int TTR = kTilesRows;              // rows of an item: two query tiles
 static_assert(TTR == 2 * TM_ROWS);
 constexpr int TTHREADS = 640;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;   // per thread: 16 warps and 4
 constexpr int TMETA = 3;                     // stages of page ids and scales
 constexpr float kRaise = 8.0f;               // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kTop = 6.0f;                 // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
   // arrives where the next phase needs that it has.
   if (warp < 16) {
     // ======================================================== softmax
-    reg_inc<104>();
+    reg_inc<kSoftmaxRegs>();
     const int t = (warp >> 2) & 1;
     const int par = warp >> 3;
     const int row = tid & 127;
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
   } else {
-    reg_dec<64>();
+    reg_dec<kOtherRegs>();
     if (warp == 16) {
       // ====================================================== MMA issue
       if (lane == 0) {
@@ -844,6 +845,12 @@ __global__ void __launch_bounds__(TTHREADS, 1)
 // ---------------------------------------------------------------- host
 template <int D, typename T>
 static cudaError_t prepare_t() {
+  // reg_inc draws on the registers that the block was launched with: fewer
+  // would make it wait for ever
+  cudaFuncAttributes fa;
+  const cudaError_t e = cudaFuncGetAttributes(&fa, paged_attend_tiles_kernel<D, T>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * TTHREADS < 32 * (16 * kSoftmaxRegs + 4 * kOtherRegs)) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(paged_attend_tiles_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               TilesLayout<D, T>::ALLOC);
 }

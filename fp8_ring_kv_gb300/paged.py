@@ -64,7 +64,8 @@ class PagedKV:
 
     ``k_codes``, ``v_codes`` (uint8 [layers, n_pages, kv_heads, page_tokens,
     head_dim], e4m3) and ``k_scales``, ``v_scales`` (fp32 [layers, n_pages,
-    kv_heads]) are views of the workspace; a cached value is code * scale."""
+    kv_heads]) are views of the workspace; a cached value is code * scale.
+    For inference: nothing here has a gradient."""
 
     def __init__(self, kv_heads, q_heads, head_dim, n_pages, page_tokens, axis_dims, pos_min, pos_count,
                  rope_base=10000.0, dtype=torch.bfloat16, layers=1, device="cuda", stream=None, workspace=None):
