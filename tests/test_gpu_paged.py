@@ -780,3 +780,14 @@ def test_many_sequences_of_both_kinds():
     c.attend()
     c.attend(window=9)
     assert c.kv.debug_state() == 0
+
+
+def test_rows_are_32_bit_numbers():
+    from fp8_ring_kv_gb300 import kvring as K
+    kv = paged(1, 1024, 64, 2, 16, (64,), (0,), (8,))
+    p = kv.workspace.data_ptr()                              # never read: the call is refused
+    args = [kv.handle, 0, p, 65536, p, p, p, 1, 1 << 21, 1, p, 2, 2, 1, 0, 0.0, p, 65536, None]
+    assert K.load().kvring_paged_attend(*args) == K.KVRING_ERR_INVALID_ARG
+    args[8] = (1 << 24) + 1
+    assert K.load().kvring_paged_attend(*args) == K.KVRING_ERR_INVALID_ARG
+    assert kv.debug_state() == 0
