@@ -13,9 +13,9 @@
 // What bounds it: a thread's chain of dependent loads (the sequences' numbers,
 // positions, table rows) with as many threads on an SM as the registers of two
 // rows each allow.  16,662 tokens of 8 heads x 128: 26.5 us, 3.9 TB/s of the
-// input's and codes' bytes, 57% of a copy (one row per thread: 43 us, two
-// without the bound on registers: 31 us; several units per block one after the
-// other: 39 us, the loop's registers spilt).
+// input's and codes' bytes, 57% of a copy (without the bound on registers
+// 31 us; several units per block one after the other 39 us, the loop's registers
+// spilt).
 #include "paged.h"
 #include "launch.h"
 
@@ -82,19 +82,17 @@ __device__ __forceinline__ bool block_scale(float amax, float old, float& scale,
   return false;
 }
 
-// Whole pages: a block on one unit (page task, key head, K or V), or on K and V
-// of a head where a unit has rows for no more than half of the smallest block
-// (20,540 tokens of 24 heads in pages of 16 x 64: 90 us against 134).  A row is handled
-// by L = D / 16 lanes of 16 channels each; a thread keeps the fp32 values of two
-// rows (where the page has as many) until the block's maximum is known, so the
-// input is read once.  More rows per thread would take the registers of the
-// warps that hide the loads' latency.
+// Whole pages: a block on one unit (page task, key head, K or V).  A row is
+// handled by L = D / 16 lanes of 16 channels each; a thread keeps the fp32
+// values of two rows until the block's maximum is known, so the input is read
+// once.  More rows per thread would take the registers of the warps that hide
+// the loads' latency, fewer make blocks whose barrier waits for more warps
+// (pages of 64 x 128: one row 41 us against 26.5, four rows 28; pages of 16 x 64,
+// 20,540 tokens of 24 heads: blocks of 128 threads 134 us, of 32 threads 66).
 // K and V of every head of a page are neighbouring blocks: together they read
 // whole input rows, and the same rows of the RoPE table.
 template <int L, int P>
-constexpr int append_threads = P * L / 2 < 128 ? 128 : P * L / 2;
-template <int L, int P>
-constexpr int append_unit = P * L < append_threads<L, P> ? P * L : append_threads<L, P>;
+constexpr int append_threads = P * L / 2;
 
 template <int L, int P, typename T>
 __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L, P>)
@@ -102,18 +100,15 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
                         const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
   constexpr int D = L * 16;
   constexpr int THREADS = append_threads<L, P>;
-  constexpr int UT = append_unit<L, P>;                 // threads of a unit
-  constexpr int SIDE = THREADS / UT;                    // units of the block
-  constexpr int ROWS = UT / L;                          // rows per pass
-  constexpr int PASS = P / ROWS;
-  static_assert(SIDE <= 2 && UT % 32 == 0 && ROWS * PASS == P);
+  constexpr int ROWS = THREADS / L;                     // rows per pass
+  constexpr int PASS = 2;
+  static_assert(THREADS % 32 == 0 && ROWS * PASS == P);
   __shared__ int found;
   __shared__ float wmax[THREADS / 32];
   const int tid = threadIdx.x;
-  const int unit = blockIdx.x * SIDE + tid / UT;
-  const int task = blockIdx.x / (2 / SIDE * pv.H);
-  const int h = (unit - task * 2 * pv.H) >> 1;
-  const bool is_v = unit & 1;
+  const int task = blockIdx.x / (2 * pv.H);
+  const int h = (blockIdx.x - task * 2 * pv.H) >> 1;
+  const bool is_v = blockIdx.x & 1;
   if (tid == 0) found = -1;
   __syncthreads();
   pdl_wait();
@@ -121,7 +116,7 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
   const AppendTask t = append_task(pv, pb, task, &found);
   if (t.cnt == 0) return;                               // the whole block
   const int lane = tid % L;
-  const int row = tid % UT / L;
+  const int row = tid / L;
   const T* src0 = (is_v ? v + t.tok0 * v_stride : k + t.tok0 * k_stride) + (size_t)h * D + lane * 16;
   const long long stride = is_v ? v_stride : k_stride;
   float x[PASS][16];
@@ -163,9 +158,9 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   if ((tid & 31) == 0) wmax[tid >> 5] = amax;
   __syncthreads();                                      // also: every thread has read the old scale
-  amax = 0.0f;
+  amax = wmax[0];
 #pragma unroll
-  for (int i = 0; i < UT / 32; ++i) amax = fmaxf(amax, wmax[tid / UT * (UT / 32) + i]);
+  for (int i = 1; i < THREADS / 32; ++i) amax = fmaxf(amax, wmax[i]);
   float scale, inv;
   if (block_scale(amax, old, scale, inv) && t.held > 0) {
     // the page's older codes at the larger scale (a row of zeros for old = 0)
@@ -182,7 +177,7 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
     const int r = p * ROWS + row;
     if (r < t.cnt) *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = quant16(x[p], inv);
   }
-  if (tid % UT == 0) *scale_at = scale;
+  if (tid == 0) *scale_at = scale;
 }
 
 // A few tokens per sequence (decoding): a block on one page task, L lanes on
@@ -293,8 +288,7 @@ static cudaError_t append_t(const PagedView& pv, const PagedBatch& pb, const voi
     return launch_pdl(paged_append_few_kernel<L, T>, dim3((unsigned)tasks), dim3(threads), 0, st, pv, pb, kt, k_stride,
                       vt, v_stride, pos);
   }
-  constexpr int side = append_threads<L, P> / append_unit<L, P>;
-  return launch_pdl(paged_append_kernel<L, P, T>, dim3((unsigned)(tasks * 2 / side * pv.H)), dim3(append_threads<L, P>), 0,
+  return launch_pdl(paged_append_kernel<L, P, T>, dim3((unsigned)(tasks * 2 * pv.H)), dim3(append_threads<L, P>), 0,
                     st, pv, pb, kt, k_stride, vt, v_stride, pos);
 }
 
