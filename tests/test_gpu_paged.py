@@ -791,3 +791,36 @@ def test_rows_are_32_bit_numbers():
     args[8] = (1 << 24) + 1
     assert K.load().kvring_paged_attend(*args) == K.KVRING_ERR_INVALID_ARG
     assert kv.debug_state() == 0
+
+
+def test_a_captured_fork_and_join():
+    """The append on a second stream of the capture, the attention after both;
+    memory copies in front, so that edges of either kind meet."""
+    c = Case([(1, 300), (40, 64), (3, 10)], group=4)
+    c.append([(0, 0)] * 3)                                   # nothing
+    c.append([(b, 0) for _, b in c.seqs])
+    start, ln, pos = c.batch(c.seqs)
+    k, v, q = c.draw(c.n, 2), c.draw(c.n, 2), c.draw(c.n, 8)
+    args = [cu(x) for x in (pos, start, ln, c.table)]
+    src = [t.cuda() for t in (k, v, q)]
+    kd, vd, qd = (torch.zeros_like(t) for t in src)
+    out = torch.full_like(qd, 7.0)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        kd.copy_(src[0]), vd.copy_(src[1])
+        two.wait_stream(one)
+        with torch.cuda.stream(two):
+            c.kv.append(kd, vd, *args)
+        qd.copy_(src[2])
+        one.wait_stream(two)
+        c.kv.attend(qd, *args, out=out)
+    c.oracle.append(k.float().numpy(), v.float().numpy(), pos, start, ln, c.table)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check_cache()
+        c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, ln, c.table))
+    assert c.kv.debug_state() == 0
