@@ -805,10 +805,6 @@ __global__ void __launch_bounds__(TTHREADS, 1)
                 const int sl = (i0 + it) * STEP + sl0;
                 reg[it] = *reinterpret_cast<const uint4*>(src + raw_chunk<D>(sl, ch));
               }
-              if (i0 + BATCH == NT) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&raw_free[v]);
-              }
 #pragma unroll
               for (int it = 0; it < BATCH; ++it) {
                 const int sl = (i0 + it) * STEP + sl0;
@@ -824,9 +820,16 @@ __global__ void __launch_bounds__(TTHREADS, 1)
                 *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (sl & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
               }
             }
+            // The codes are given back only here: an arrival waits for no load in
+            // flight, so the next codes' TMA could overwrite what a load issued
+            // before it has not fetched yet.  The stores needed their values, and
+            // the fence orders this proxy's reads before the copy's writes.
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive((v ? vh_full : kh_full) + buf);
+            if (lane == 0) {
+              mbar_arrive(&raw_free[v]);
+              mbar_arrive((v ? vh_full : kh_full) + buf);
+            }
           }
         }
         done += n;
