@@ -37,8 +37,9 @@
 //   warp 17          the line of work: the stretches of items for the others,
 //                    per tile the page ids and scales, and TMA of the codes
 //   warps 18, 19     K and V codes widened to fp16, shared memory to shared memory
-// MMAs of one thread run in the order they are issued: QK may overwrite the P
-// that the PV before it reads.
+// QK of the next tile overwrites the P that PV of this one reads, with another
+// accumulator: products of different accumulators have no documented order, so
+// it is issued once that PV has completed.
 #include "paged_sched.cuh"
 #include "launch.h"
 
@@ -585,7 +586,12 @@ __global__ void __launch_bounds__(TTHREADS, 1)
               if (on) pv(t, g, j > 0);
               mma_commit(&o_done[2 * t + (g & 1)]);
               if (j + 1 < n) {
-                if (on) qk(t, g + 1);
+                if (on) {
+                  ok = mbar_wait(&o_done[2 * t + (g & 1)], (g >> 1) & 1, abort_flag);
+                  if (!ok) break;
+                  tc_fence_after();
+                  qk(t, g + 1);
+                }
                 mma_commit(&s_full[2 * t + ((g + 1) & 1)]);
               }
             }
