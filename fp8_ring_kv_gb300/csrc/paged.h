@@ -119,13 +119,18 @@ struct SeqInfo {
   int s0, n, len;
 };
 
+// What another kernel may have written just before (the batch's numbers and
+// rows, codes and scales) is read with plain loads: a kernel launched ahead of
+// that one's end (dependent launch) must not use the read-only path, which may
+// answer with what the SM fetched before.  Only the RoPE tables never change.
+
 // Sequence b's numbers.  Ones that contradict each other or the call's sizes
 // give n = 0 (the sequence is left out) and ok = false.
 __device__ __forceinline__ SeqInfo seq_info(const PagedBatch& pb, int p_shift, int b, bool& ok) {
   SeqInfo s;
-  s.s0 = __ldg(pb.seq_start + b);
-  const int s1 = __ldg(pb.seq_start + b + 1);
-  s.len = __ldg(pb.kv_len + b);
+  s.s0 = pb.seq_start[b];
+  const int s1 = pb.seq_start[b + 1];
+  s.len = pb.kv_len[b];
   ok = s.s0 >= 0 && s1 >= s.s0 && s1 <= pb.n_tokens && s.len >= 0 &&
        (long long)s.len <= ((long long)pb.table_width << p_shift);
   s.n = ok ? s1 - s.s0 : 0;
@@ -172,7 +177,7 @@ __device__ __forceinline__ RopeLane rope_lane(const PagedView& pv, int p0) {
 
 // The lane's table row (before its bounds are applied) at the positions
 // pr[0 .. n_axes - 1]
-__device__ __forceinline__ int rope_index(const RopeLane& r, const int32_t* pr) { return __ldg(pr + r.axis) - r.pos_min; }
+__device__ __forceinline__ int rope_index(const RopeLane& r, const int32_t* pr) { return pr[r.axis] - r.pos_min; }
 
 // (cos, sin) of the lane's pairs at the positions pr[0 .. n_axes - 1], idx = rope_index
 __device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, int idx,

@@ -56,7 +56,7 @@ __device__ AppendTask append_task(const PagedView& pv, const PagedBatch& pb, int
   __syncthreads();
   const int b = *found;
   if (b < 0) return t;
-  const int s0 = __ldg(pb.seq_start + b), s1 = __ldg(pb.seq_start + b + 1), len = __ldg(pb.kv_len + b);
+  const int s0 = pb.seq_start[b], s1 = pb.seq_start[b + 1], len = pb.kv_len[b];
   const int j = task - (s0 >> pv.p_shift) - 2 * b;
   const int first = len - (s1 - s0);                    // cache index of the first new token
   const int slot = (first >> pv.p_shift) + j;           // the task's page of the sequence
@@ -65,7 +65,7 @@ __device__ AppendTask append_task(const PagedView& pv, const PagedBatch& pb, int
   t.held = lo - (slot << pv.p_shift);
   t.cnt = hi - lo;
   t.tok0 = s0 + (lo - first);
-  t.page = __ldg(pb.table + b * pb.table_stride + slot);
+  t.page = pb.table[b * pb.table_stride + slot];
   if (t.page < 0 || t.page >= pv.n_pages) {
     if (tid == 0) atomicOr(&pv.state[PST_ERR], DEVERR_PAGE);
     t.page = -1;
@@ -96,8 +96,8 @@ constexpr int append_threads = P * L / 2;
 
 template <int L, int P, typename T>
 __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L, P>)
-    paged_append_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k, long long k_stride,
-                        const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
+    paged_append_kernel(PagedView pv, PagedBatch pb, const T* k, long long k_stride,
+                        const T* v, long long v_stride, const int32_t* pos) {
   constexpr int D = L * 16;
   constexpr int THREADS = append_threads<L, P>;
   constexpr int ROWS = THREADS / L;                     // rows per pass
@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
     raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
     if (r < t.cnt) {
       const uint4* src = reinterpret_cast<const uint4*>(src0 + r * stride);
-      raw[p][0] = __ldg(src);
-      raw[p][1] = __ldg(src + 1);
+      raw[p][0] = src[0];
+      raw[p][1] = src[1];
     }
   }
 #pragma unroll
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
 // reads them twice), slow for many.
 template <int L, typename T>
 __global__ void __launch_bounds__(512)
-    paged_append_few_kernel(PagedView pv, PagedBatch pb, const T* __restrict__ k, long long k_stride,
-                            const T* __restrict__ v, long long v_stride, const int32_t* __restrict__ pos) {
+    paged_append_few_kernel(PagedView pv, PagedBatch pb, const T* k, long long k_stride,
+                            const T* v, long long v_stride, const int32_t* pos) {
   constexpr int D = L * 16;
   __shared__ int found;
   if (threadIdx.x == 0) found = -1;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(512)
     const long long stride = is_v ? v_stride : k_stride;
     auto load = [&](int r, float (&x)[16]) {
       const uint4* src = reinterpret_cast<const uint4*>(src0 + r * stride);
-      const uint4 a0 = __ldg(src), a1 = __ldg(src + 1);
+      const uint4 a0 = src[0], a1 = src[1];
       float2 cs[8];
       if (!is_v) rope_load(pv, rl, pos + (size_t)(t.tok0 + r) * pv.n_axes, cs, bad);
       load8_f32<T>(a0, x);

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           const int key = (tb + lane) * RK + p * 16;
           if (tb + lane < k1 && (p == 0 || a.pv.P == 16) && key < pl.t.hi &&
               key + (a.pv.P == 16 ? 16 : RK) > pl.t.lo) {
-            ids[p] = __ldg(a.pb.table + pl.b * a.pb.table_stride + (key >> a.pv.p_shift));
+            ids[p] = a.pb.table[pl.b * a.pb.table_stride + (key >> a.pv.p_shift)];
             if (ids[p] < 0 || ids[p] >= a.pv.n_pages) {
               atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
               ids[p] = 0;
@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       auto load_scales = [&](const int (&ids)[2], float (&ks)[2], float (&vs)[2]) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          ks[p] = ids[p] >= 0 ? __ldg(a.pv.k_scale + (size_t)ids[p] * H + pl.h) : 0.0f;
-          vs[p] = ids[p] >= 0 ? __ldg(a.pv.v_scale + (size_t)ids[p] * H + pl.h) : 0.0f;
+          ks[p] = ids[p] >= 0 ? a.pv.k_scale[(size_t)ids[p] * H + pl.h] : 0.0f;
+          vs[p] = ids[p] >= 0 ? a.pv.v_scale[(size_t)ids[p] * H + pl.h] : 0.0f;
         }
       };
       auto near_scale = [&]() {
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           if (live) {
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const T*>(a.q) + (pl.s.s0 + i) * a.q_stride + (size_t)(pl.h * G + row0 + r - i * G) * D + c * 64 + t4 * 16);
-            qw[e][2 * c] = __ldg(src);
-            qw[e][2 * c + 1] = __ldg(src + 1);
+            qw[e][2 * c] = src[0];
+            qw[e][2 * c + 1] = src[1];
           }
           float2 part8[8];
           rope_load(a.pv, rope_lane(a.pv, c * 32 + t4 * 8), a.q_pos + (size_t)(pl.s.s0 + i) * a.pv.n_axes, part8, bad);

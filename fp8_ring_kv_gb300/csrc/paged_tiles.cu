@@ -100,13 +100,13 @@ __device__ __noinline__ bool nan_among(const PagedAttn& a, int b, int h, int lo,
   for (int key = lo; key < hi; key += 2) {
     const int k = key / KT;
     if (k * KT >= all_lo && k * KT + KT <= all_hi) continue;
-    int pg = __ldg(a.pb.table + b * a.pb.table_stride + (key >> a.pv.p_shift));
+    int pg = a.pb.table[b * a.pb.table_stride + (key >> a.pv.p_shift)];
     if (pg < 0 || pg >= a.pv.n_pages) pg = 0;
     const uint4* v = reinterpret_cast<const uint4*>(
         a.pv.v_codes + (((((size_t)pg * a.pv.H + h) << a.pv.p_shift) + (key & (a.pv.P - 1))) * D));
 #pragma unroll 1
     for (int c = 0; c < D / 16; ++c) {
-      uint4 w = __ldg(v + c);
+      uint4 w = v[c];
       if (drop_nan_codes(w.x) | drop_nan_codes(w.y) | drop_nan_codes(w.z) | drop_nan_codes(w.w)) return true;
     }
   }
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             w0[k] = w1[k] = make_uint4(0, 0, 0, 0);
             if (on) {
               const uint4* src = reinterpret_cast<const uint4*>(qp + (s0 + qi) * a.q_stride + qg * D);
-              w0[k] = __ldg(src);
-              w1[k] = __ldg(src + 1);
+              w0[k] = src[0];
+              w1[k] = src[1];
             }
             rope_load(a.pv, rl, pr0 + (size_t)(on ? qi : 0) * a.pv.n_axes, idx[k], cs[k], bad);
             step(qi, qg);
@@ -656,8 +656,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         // (Loads run a tile ahead: TMA of the next tile waits for nothing else than its stage.)
         auto page = [&](int k) -> int {
           const int key = k * KT + lane * 16;
-          return lane < NG && k < k1 && key < pl.t.hi && key + 16 > pl.t.lo ? __ldg(tab + (key >> a.pv.p_shift))
-                                                                            : -0x7FFFFFFF;
+          return lane < NG && k < k1 && key < pl.t.hi && key + 16 > pl.t.lo ? tab[key >> a.pv.p_shift] : -0x7FFFFFFF;
         };
         auto known = [&](int pg) -> int {                // a page that can be read
           if (pg == -0x7FFFFFFF) return kNone;
@@ -668,7 +667,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           return pg;
         };
         auto scale = [&](const float* scales, int pg) {
-          return pg != kNone ? __ldg(scales + (size_t)pg * H + pl.h) : 0.0f;
+          return pg != kNone ? scales[(size_t)pg * H + pl.h] : 0.0f;
         };
         auto top = [](float v) {
 #pragma unroll

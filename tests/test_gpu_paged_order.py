@@ -62,3 +62,42 @@ def test_first_calls_on_fresh_caches(dtype, dim, window):
 def test_first_calls_of_few_rows(dtype):
     c = Case([(1, 900), (3, 200), (2, 0), (1, 3000), (4, 77)], kv_heads=2, group=8, page=16, dtype=dtype)
     first_call(c, {}, 200, (0xFF, 0xA5, 0x00, 0x7F))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128)])
+def test_steps_without_a_pause(page, dim, new):
+    """Append and attention step after step, every step's values twice those of
+    the step before, so that page scales grow and codes are rounded again while
+    the next kernels are already waiting: the outputs and the cache of the same
+    steps with a pause after each kernel."""
+    steps = 24
+    c = Case([(0, 30 + steps * new), (0, 5 + steps * new), (0, 300 + steps * new)], kv_heads=4, group=4, page=page, dim=dim)
+    table = cu(c.table)
+    have, work = [30, 5, 300], []
+    first = c.batch([(n, 0) for n in have])
+    prompt = [c.draw(int(first[0][-1]), 4).cuda() for _ in range(2)] + [cu(x) for x in (first[2], first[0], first[1])]
+    for step in range(steps):
+        start, ln, pos = c.batch([(new, n) for n in have])
+        have = [n + new for n in have]
+        k, v, q = (c.draw(3 * new, h) for h in (4, 4, 16))
+        grow = 2.0 ** (step - 12)
+        work.append([(x * s).cuda() for x, s in ((k, grow), (v, grow), (q, 1.0))] + [cu(x) for x in (pos, start, ln)])
+    got = []
+    for pause in (True, False, False, False):
+        c.kv.workspace[c.kv.k_codes.data_ptr() - c.kv.workspace.data_ptr():].zero_()   # an empty cache
+        wait = torch.cuda.synchronize if pause else lambda: None
+        wait()
+        c.kv.append(*prompt, table)
+        outs = []
+        for k, v, q, pos, start, ln in work:
+            wait()
+            c.kv.append(k, v, pos, start, ln, table)
+            wait()
+            outs.append(c.kv.attend(q, pos, start, ln, table, max_new=new))
+        torch.cuda.synchronize()
+        assert c.kv.debug_state() == 0
+        got.append(outs + [c.kv.k_codes.clone(), c.kv.v_codes.clone(), c.kv.k_scales.clone(), c.kv.v_scales.clone()])
+    for other in got[1:]:
+        for i, (a, b) in enumerate(zip(got[0], other)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
