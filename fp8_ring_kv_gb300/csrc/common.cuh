@@ -103,9 +103,8 @@ __device__ __forceinline__ void row_absmax_scale(float amax, float& scale, float
   }
 }
 
-// 16 values -> 16 e4m3 codes (round to nearest even, saturating) of x * inv.
-// A zero row (inv == 0) gives all-zero codes (+0).
-__device__ __forceinline__ uint4 quant16(const float* x, float inv) {
+// 16 values -> 16 e4m3 codes (round to nearest even, saturating; 0x7F for a NaN) of x * inv.
+__device__ __forceinline__ uint4 codes16(const float* x, float inv) {
   uint32_t w[4];
   const float2 iv = make_float2(inv, inv);
 #pragma unroll
@@ -116,8 +115,13 @@ __device__ __forceinline__ uint4 quant16(const float* x, float inv) {
     const uint32_t hi = cvt_e4m3x2(b.x, b.y);
     w[i] = lo | (hi << 16);
   }
-  if (inv == 0.0f) w[0] = w[1] = w[2] = w[3] = 0u;
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same, but a zero row (inv == 0) gives all-zero codes (+0).
+__device__ __forceinline__ uint4 quant16(const float* x, float inv) {
+  const uint4 w = codes16(x, inv);
+  return inv == 0.0f ? make_uint4(0, 0, 0, 0) : w;
 }
 
 // 16 e4m3 codes -> 16 fp32 values (exact).

@@ -73,6 +73,16 @@ __device__ AppendTask append_task(const PagedView& pv, const PagedBatch& pb, int
   return t;
 }
 
+// Codes of x * inv in a block of scale 2^k, or (zero) in one of scale 0: +0
+// there, but for a NaN, which is 0x7F in any block.
+__device__ __forceinline__ uint4 block_codes(const float* x, float inv, bool zero) {
+  if (!zero) return codes16(x, inv);
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = x[i] != x[i] ? x[i] : 0.0f;
+  return codes16(y, 1.0f);
+}
+
 // The scale that a block of codes takes, and its inverse; true where it grew.
 __device__ __forceinline__ bool block_scale(float amax, float old, float& scale, float& inv) {
   pow2_scale(amax, scale, inv);
@@ -163,19 +173,19 @@ __global__ void __launch_bounds__(append_threads<L, P>, 1024 / append_threads<L,
   for (int i = 1; i < THREADS / 32; ++i) amax = fmaxf(amax, wmax[i]);
   float scale, inv;
   if (block_scale(amax, old, scale, inv) && t.held > 0) {
-    // the page's older codes at the larger scale (a row of zeros for old = 0)
+    // the page's older codes at the larger scale (zeros and NaN for old = 0)
     const float ratio = old * inv;
     for (int r = row; r < t.held; r += ROWS) {
       uint4* at = reinterpret_cast<uint4*>(codes + r * D);
       float y[16];
       dequant16_codes(*at, y);
-      *at = quant16(y, ratio);
+      *at = block_codes(y, ratio, old == 0.0f);
     }
   }
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int r = p * ROWS + row;
-    if (r < t.cnt) *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = quant16(x[p], inv);
+    if (r < t.cnt) *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = block_codes(x[p], inv, scale == 0.0f);
   }
   if (tid == 0) *scale_at = scale;
 }
@@ -240,13 +250,13 @@ __global__ void __launch_bounds__(512)
         uint4* at = reinterpret_cast<uint4*>(codes + r * D);
         float y[16];
         dequant16_codes(*at, y);
-        *at = quant16(y, ratio);
+        *at = block_codes(y, ratio, old == 0.0f);
       }
     }
 #pragma unroll 2
     for (int r = 0; r < t.cnt; ++r) {
       if (r > 0) load(r, x);
-      *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = quant16(x, inv);
+      *reinterpret_cast<uint4*>(codes + (t.held + r) * D) = block_codes(x, inv, scale == 0.0f);
     }
     __syncwarp(group);                                  // every lane has read the old scale
     if (lane == 0) *scale_at = scale;

@@ -122,11 +122,12 @@ int kvring_paged_create(const kvring_paged_config* cfg, void* workspace, size_t 
  *             (multiples of 8, >= H * D), 16-byte aligned; not modified
  * K is rotated by RoPE at pos (fp32, the operations of kvring_write), V is
  * not.  For each page touched and each head, K and V apart: a = the largest
- * |value| of the new rows; need = the smallest power of two s with a <= 448 s
- * (0 if a < 2^-100).  A page that held no row of the sequence before gets
+ * |value| of the new rows, NaN left out; need = the smallest power of two s with
+ * a <= 448 s (0 if a < 2^-100).  A page that held no row of the sequence before gets
  * scale = need; another keeps its scale unless need is larger, and then its
  * older rows' codes become e4m3(code * (old scale / need)).  New codes are
- * e4m3(x / scale), round to nearest even.  Rows of the page past the last new
+ * e4m3(x / scale), round to nearest even; 0 where the scale is 0, and 0x7F for a
+ * NaN at any scale.  Rows of the page past the last new
  * one are left as they are.
  * kv_len must count the new tokens (n <= kv_len).  Pages written by a call
  * belong to one place of one sequence each: a page that two sequences of the
