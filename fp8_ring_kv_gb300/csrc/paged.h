@@ -74,8 +74,9 @@ struct alignas(16) PieceRec {
 
 // Partial results: slot 2w holds the piece of an item begun before worker w's
 // range, slot 2w + 1 the piece of an item that w began and did not end.
-// o [slot][rows][D] fp32 (unnormalised), ml [slot][rows] (running maximum in
-// log2 units, sum); m = -inf marks rows (or whole pieces) without a key.
+// o [slot][rows][D] fp32 (unnormalised), ml [slot][rows] (a reference in log2
+// units, near the running maximum, and the sum); m = -inf marks rows (or whole
+// pieces) without a key.
 struct PieceScratch {
   float* o;
   float2* ml;

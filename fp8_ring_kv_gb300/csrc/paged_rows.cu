@@ -33,6 +33,7 @@
 // 2 t, 2 t + 1 in a thread; movmatrix turns the weights into P^T's layout.  The
 // key rows of an 8-key group are taken in the order 0 5 2 7 4 1 6 3, with
 // which both patterns read 128-byte-swizzled rows without bank conflicts.
+#include "paged_exact.cuh"
 #include "paged_sched.cuh"
 #include "launch.h"
 
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       int id[2] = {-1, -1};
       float sk[2] = {0.0f, 0.0f}, sv[2] = {0.0f, 0.0f};
       float v_near = 0.0f;
+      ScaleSpan span;
       auto load_ids = [&](int tb, int (&ids)[2]) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -172,6 +174,8 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
           for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
           return v;
         };
+        span.add(sv[0]);
+        span.add(sv[1]);
         float mx = top(fmaxf(sv[0], sv[1]));
         if (mx == 0.0f && v_near == 0.0f) {
           for (int tb = base + 32; mx == 0.0f && tb < k1; tb += 32) {
@@ -516,42 +520,52 @@ __global__ void __launch_bounds__(32 * RowsLayout<D, NT>::RW, 1)
       // ---------------------------------------------------------- results
       // a thread: rows 2 t4 + f of each tile, channels DG g ..
       const int slot = 2 * worker + (u == pl.at ? 1 : 0);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) l[e][f] += __shfl_xor_sync(0xFFFFFFFFu, l[e][f], off);
-          const int r = e * COLS + 2 * t4 + f;
-          float v[DG];
-#pragma unroll
-          for (int i = 0; i < NJ; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float x = o[i][e][2 * k + f];
-              if constexpr (SIDE) x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-              else if constexpr (SPLIT) x += o[i][NT - 1][2 * k + f];
-              v[2 * i + k] = x;
-            }
-          if (r >= rows || 2 * t4 + f >= COLS) continue;
-          if (whole) {
-            const int i = (row0 + r) / G;
-            const float inv = l[e][f] != 0.0f ? 1.0f / l[e][f] : 0.0f;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride +
-                                                  (size_t)(pl.h * G + row0 + r - i * G) * D + g * DG);
-#pragma unroll
-            for (int c = 0; c < DG / 8; ++c)
-              dst[c] = make_uint4(pack2<T>(v[8 * c] * inv, v[8 * c + 1] * inv), pack2<T>(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
-                                  pack2<T>(v[8 * c + 4] * inv, v[8 * c + 5] * inv),
-                                  pack2<T>(v[8 * c + 6] * inv, v[8 * c + 7] * inv));
-          } else {
-            const size_t at_row = (size_t)slot * RT + r;
-            float4* dst = reinterpret_cast<float4*>(a.rows.o + at_row * D + g * DG);
-#pragma unroll
-            for (int c = 0; c < DG / 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
-          }
+      if (span.far_apart()) {
+        for (int r = 0; r < rows; ++r) {
+          const int rr = row0 + r, i = rr / G;
+          const size_t at_row = (size_t)slot * RT + r;
+          T* dst = static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride + (size_t)(pl.h * G + rr - i * G) * D;
+          exact_row<D, T>(a, pl.b, pl.s.s0, pl.s.n, pl.s.len, pl.h, rr, k0 * RK, k1 * RK, whole ? dst : nullptr,
+                          a.rows.o + at_row * D, a.rows.ml + at_row, 8.0f);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[e][f] += __shfl_xor_sync(0xFFFFFFFFu, l[e][f], off);
+            const int r = e * COLS + 2 * t4 + f;
+            float v[DG];
+#pragma unroll
+            for (int i = 0; i < NJ; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float x = o[i][e][2 * k + f];
+                if constexpr (SIDE) x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+                else if constexpr (SPLIT) x += o[i][NT - 1][2 * k + f];
+                v[2 * i + k] = x;
+              }
+            if (r >= rows || 2 * t4 + f >= COLS) continue;
+            if (whole) {
+              const int i = (row0 + r) / G;
+              const float inv = l[e][f] != 0.0f ? 1.0f / l[e][f] : 0.0f;
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (pl.s.s0 + i) * a.out_stride +
+                                                    (size_t)(pl.h * G + row0 + r - i * G) * D + g * DG);
+#pragma unroll
+              for (int c = 0; c < DG / 8; ++c)
+                dst[c] = make_uint4(pack2<T>(v[8 * c] * inv, v[8 * c + 1] * inv), pack2<T>(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
+                                    pack2<T>(v[8 * c + 4] * inv, v[8 * c + 5] * inv),
+                                    pack2<T>(v[8 * c + 6] * inv, v[8 * c + 7] * inv));
+            } else {
+              const size_t at_row = (size_t)slot * RT + r;
+              float4* dst = reinterpret_cast<float4*>(a.rows.o + at_row * D + g * DG);
+#pragma unroll
+              for (int c = 0; c < DG / 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+              if (g == 0) a.rows.ml[at_row] = make_float2(m[e][f], l[e][f]);
+            }
+          }
+      }
       if (u == pl.at && end < item_end) rec = {rows, (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, row0};
       u = min(end, item_end);
       if (u >= end || !next_place<RowsShare, RT, RK>(a, pl)) break;

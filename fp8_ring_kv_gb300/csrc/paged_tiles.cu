@@ -40,6 +40,7 @@
 // QK of the next tile overwrites the P that PV of this one reads, with another
 // accumulator: products of different accumulators have no documented order, so
 // it is issued once that PV has completed.
+#include "paged_exact.cuh"
 #include "paged_sched.cuh"
 #include "launch.h"
 
@@ -57,7 +58,9 @@ constexpr float kTop = 6.0f;                 // ... and starts its weights at 2^
 // What a block does of one item: its key tiles [k0, k1).  Some row sees keys
 // lo .. hi - 1, all rows see all_lo .. all_hi - 1.
 struct Stretch {
-  int b, h, tile, s0, n, len, lo, hi, all_lo, all_hi, k0, k1, flags, pad[3];
+  int b, h, tile, s0, n, len, lo, hi, all_lo, all_hi, k0, k1, flags;
+  int far_apart;                             // its pages' V scales (written with the last tile's)
+  int pad[2];
 };
 enum : int { STRETCH_SOME = 1, STRETCH_WHOLE = 2, STRETCH_HEAD = 4 };   // else: the end; the whole item; its beginning
 
@@ -457,7 +460,16 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       // Half of the channels per warp.  A thread has a row, memory wants rows side
       // by side in a warp: through half of the warp's rows of the query tile,
       // which every MMA is done with.
-      if (rows > 0) {
+      if (n > 0 && seg.far_apart) {
+        // half of the pair's rows each
+        for (int r = 32 * (warp & 3) + 16 * par; r < min(rows, 32 * (warp & 3) + 16 * par + 16); ++r) {
+          const int i2 = (r0 + r) / G;
+          const size_t at = (size_t)(2 * worker + (flags & STRETCH_HEAD ? 1 : 0)) * TTR + t * TM_ROWS + r;
+          T* dst = static_cast<T*>(a.out) + (s0 + i2) * a.out_stride + (size_t)(head0 + r0 + r - i2 * G) * D;
+          exact_row<D, T>(a, seg.b, s0, seg.n, seg.len, seg.h, r0 + r, k0 * KT, (k0 + n) * KT,
+                          flags & STRETCH_WHOLE ? dst : nullptr, a.tiles.o + at * D, a.tiles.ml + at, kTop);
+        }
+      } else if (rows > 0) {
         const bool whole = flags & STRETCH_WHOLE;
         const size_t at_row = (size_t)(2 * worker + (flags & STRETCH_HEAD ? 1 : 0)) * TTR + t * TM_ROWS + row;
         constexpr int HC = D / 16;                       // 16-byte chunks of half a row of the tile
@@ -639,6 +651,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
             const int i0 = pl.tile * TTR / G, i1 = min(pl.s.n - 1, (pl.tile * TTR + TTR - 1) / G);
             seg.all_hi = a.causal ? pl.s.len - pl.s.n + i0 + 1 : pl.s.len;
             seg.all_lo = a.window > 0 ? pl.s.len - pl.s.n + i1 - a.window + 1 : 0;
+            seg.far_apart = 0;
             seg.k0 = k0;
             seg.k1 = k1;
             seg.flags = STRETCH_SOME | (head ? STRETCH_HEAD : 0) | (head && end >= item_end ? STRETCH_WHOLE : 0);
@@ -653,6 +666,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         // which lie in one page.  Pages of zero values take a V scale near by.
         const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
         float near = 0.0f;
+        ScaleSpan span;
         // (Loads run a tile ahead: TMA of the next tile waits for nothing else than its stage.)
         auto page = [&](int k) -> int {
           const int key = k * KT + lane * 16;
@@ -684,6 +698,7 @@ __global__ void __launch_bounds__(TTHREADS, 1)
         for (int k = k0; k < k1; ++k) {
           const int g = done + k - k0;
           const int next = page(k + 1);
+          span.add(sv);
           float mx = top(sv);
           if (mx == 0.0f && near == 0.0f) {
             for (int s = k + 1; mx == 0.0f && s < k1; ++s) mx = top(scale(a.pv.v_scale, known(page(s))));
@@ -693,6 +708,10 @@ __global__ void __launch_bounds__(TTHREADS, 1)
           if (g >= TMETA && !warp_wait(&meta_free[g % TMETA], ((g - TMETA) / TMETA) & 1, abort_flag)) {
             ok = false;
             break;
+          }
+          if (k + 1 == k1) {
+            const bool far = span.far_apart();
+            if (lane == 0) segs[sg & 1].far_apart = far;
           }
           if (lane < NG) {
             const float v = sv > 0.0f ? sv : near;

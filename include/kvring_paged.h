@@ -47,7 +47,8 @@
  * Non-finite inputs spread to what is computed from them and no further: a
  * query or key with a NaN to the outputs of the query heads that it belongs to
  * or that see it, a value's NaN to the same channel or the whole of them.  An
- * infinity in k or v gives its page and head the scale 2^120.
+ * infinity in k or v gives its page and head the scale 2^120: the page's other
+ * values there become zeros, other pages and heads are as they were.
  * A handle must not be used by two host threads at once.  The caller orders
  * calls that touch the same pages, and the attention's scratch belongs to the
  * handle: two kvring_paged_attend calls on one handle must not run at the same
@@ -156,8 +157,10 @@ int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k
  *   scale    the softmax scale; 0: 1 / sqrt(D)
  * Queries are rotated by RoPE at q_pos (fp32) and then held in fp16 at a
  * power-of-two scale of their row; out = softmax(scale q.k) v with fp32 sums
- * and statistics and weights of V in fp16.  A query that sees nothing gives
- * zeros.  N * q_heads / kv_heads is at most 2^30.
+ * and statistics and weights of V in fp16.  (A weight is rounded by half a step
+ * of itself or 2^-17 of the row's largest one, whichever is more; where the V
+ * scales that a part of a row meets are more than 2^14 apart, that part is
+ * computed in fp32, slowly.)  A query that sees nothing gives zeros.  N * q_heads / kv_heads is at most 2^30.
  */
 int kvring_paged_attend(kvring_paged* p, int32_t layer, const void* q, int64_t q_stride, const int32_t* q_pos,
                         const int32_t* seq_start, const int32_t* kv_len, int32_t n_seqs, int32_t n_tokens,
