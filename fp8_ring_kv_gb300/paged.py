@@ -36,6 +36,12 @@ def kvring_paged_workspace_bytes(cfg: kvring_paged_config) -> int:
     return int(_k.load().kvring_paged_workspace_bytes(ctypes.byref(cfg)))
 
 
+def _as_stream(stream, device):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device)
+
+
 def _bad_ints(t, shape, index, what):
     """Why an int32 tensor is not as the kernels read it (None in ``shape``: any size)."""
     if t.dtype is not torch.int32:
@@ -65,7 +71,10 @@ class PagedKV:
     ``k_codes``, ``v_codes`` (uint8 [layers, n_pages, kv_heads, page_tokens,
     head_dim], e4m3) and ``k_scales``, ``v_scales`` (fp32 [layers, n_pages,
     kv_heads]) are views of the workspace; a cached value is code * scale.
-    For inference: nothing here has a gradient."""
+    For inference: nothing here has a gradient.
+
+    A workspace of its own is allocated on ``stream``.  Whoever uses the cache
+    on other streams keeps it until their work is done, as with any tensor."""
 
     def __init__(self, kv_heads, q_heads, head_dim, n_pages, page_tokens, axis_dims, pos_min, pos_count,
                  rope_base=10000.0, dtype=torch.bfloat16, layers=1, device="cuda", stream=None, workspace=None):
@@ -78,7 +87,12 @@ class PagedKV:
         self.layers, self.kv_heads, self.q_heads, self.head_dim = int(layers), int(kv_heads), int(q_heads), int(head_dim)
         self.n_pages, self.page_tokens, self.n_axes, self.dtype = int(n_pages), int(page_tokens), len(axis_dims), dtype
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if stream is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            else:
+                # memory that no other stream's queued work still uses
+                with torch.cuda.stream(_as_stream(stream, device)):
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         elif workspace.dtype != torch.uint8 or workspace.numel() < nbytes or workspace.data_ptr() % 256 \
                 or not workspace.is_contiguous() or not workspace.is_cuda:
             raise KVRingError("workspace: a uint8 CUDA tensor of kvring_paged_workspace_bytes, 256-byte aligned")
@@ -195,8 +209,7 @@ class PagedKV:
                 out = torch.empty_like(q, memory_format=torch.contiguous_format)
             else:
                 # memory that the allocator knows to be in use on that stream
-                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), self.device)
-                with torch.cuda.stream(s):
+                with torch.cuda.stream(_as_stream(stream, self.device)):
                     out = torch.empty_like(q, memory_format=torch.contiguous_format)
             os_ = self.q_heads * self.head_dim
         else:

@@ -101,3 +101,31 @@ def test_steps_without_a_pause(page, dim, new):
     for other in got[1:]:
         for i, (a, b) in enumerate(zip(got[0], other)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_cache_made_on_another_stream(raw):
+    """Its workspace is not a block that the current stream's queued work still
+    writes to."""
+    from fp8_ring_kv_gb300.paged import kvring_paged_workspace_bytes, make_paged_config
+    c = Case([(30, 100), (1, 50)], kv_heads=2, group=4)
+    shape = (2, 8, 128, c.n_pages, c.page, c.axis_dims, (0,), c.pos_count)
+    start, ln, pos = c.batch([(n, 0) for n in c.len])
+    k, v = c.draw(int(start[-1]), 2), c.draw(int(start[-1]), 2)
+    c.oracle.append(k.float().numpy(), v.float().numpy(), pos, start, ln, c.table)
+    side = torch.cuda.Stream()
+    args = [k.cuda(), v.cuda()] + [cu(x) for x in (pos, start, ln, c.table)]
+    block = torch.empty(kvring_paged_workspace_bytes(make_paged_config(*shape)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                            # some 0.1 s
+    block.fill_(0xFF)
+    del block
+    c.kv = paged(*shape, stream=side.cuda_stream if raw else side)
+    c.kv.append(*args, stream=side)
+    torch.cuda.synchronize()
+    c.check_cache()
+    q = c.draw(c.n, 8)
+    start, ln, pos = c.batch(c.seqs)
+    out = c.kv.attend(q.cuda(), cu(pos), cu(start), cu(ln), cu(c.table))
+    c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, ln, c.table))
+    assert c.kv.debug_state() == 0
