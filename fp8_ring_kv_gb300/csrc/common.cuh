@@ -189,10 +189,8 @@ __device__ __forceinline__ void rms_norm16(float* x, const uint4* g, float eps, 
 }
 
 // The axis and in-axis index of RoPE pair p, and its table entry for the
-// given positions.  Out-of-range positions are clamped and flagged.  View: a
-// RingView or a PagedView (the same table members).
-template <typename View>
-__device__ __forceinline__ float2 rope_cs(const View& rv, const int32_t* pos_row, int p, bool& bad) {
+// given positions.  Out-of-range positions are clamped and flagged.
+__device__ __forceinline__ float2 rope_cs(const RingView& rv, const int32_t* pos_row, int p, bool& bad) {
   int a = 0;
   if (rv.n_axes > 1 && p >= rv.pair_off[1]) a = 1;
   if (rv.n_axes > 2 && p >= rv.pair_off[2]) a = 2;

@@ -153,6 +153,25 @@ __device__ __forceinline__ void pow2_scale(float amax, float& scale, float& inv)
   inv = __uint_as_float((uint32_t)(127 - k) << 23);
 }
 
+// A position's table row before its bounds are applied; saturating, as positions
+// are any 32-bit numbers.
+__device__ __forceinline__ int table_row(int pos, int pos_min) {
+  int r;
+  asm("sub.sat.s32 %0, %1, %2;" : "=r"(r) : "r"(pos), "r"(pos_min));
+  return r;
+}
+
+// (cos, sin) of RoPE pair p at the positions pos_row[0 .. n_axes - 1]; out-of-range
+// positions are clamped and flagged.
+__device__ __forceinline__ float2 rope_cs(const PagedView& pv, const int32_t* pos_row, int p, bool& bad) {
+  int a = 0;
+  if (pv.n_axes > 1 && p >= pv.pair_off[1]) a = 1;
+  if (pv.n_axes > 2 && p >= pv.pair_off[2]) a = 2;
+  const int idx = table_row(pos_row[a], pv.pos_min[a]), at = max(0, min(idx, pv.pos_count[a] - 1));
+  bad = bad || at != idx;
+  return __ldg(pv.rope[a] + (size_t)at * pv.axis_pairs[a] + p - pv.pair_off[a]);
+}
+
 // The eight RoPE pairs p0 .. p0 + 7 that one thread rotates for many tokens.
 // Where they lie in one axis at an even place (axes of a multiple of 16
 // channels), a token's (cos, sin) are four 16-byte loads at one table row;
@@ -178,7 +197,7 @@ __device__ __forceinline__ RopeLane rope_lane(const PagedView& pv, int p0) {
 
 // The lane's table row (before its bounds are applied) at the positions
 // pr[0 .. n_axes - 1]
-__device__ __forceinline__ int rope_index(const RopeLane& r, const int32_t* pr) { return pr[r.axis] - r.pos_min; }
+__device__ __forceinline__ int rope_index(const RopeLane& r, const int32_t* pr) { return table_row(pr[r.axis], r.pos_min); }
 
 // (cos, sin) of the lane's pairs at the positions pr[0 .. n_axes - 1], idx = rope_index
 __device__ __forceinline__ void rope_load(const PagedView& pv, const RopeLane& r, const int32_t* pr, int idx,
