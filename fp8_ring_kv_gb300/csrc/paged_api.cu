@@ -232,6 +232,7 @@ int kvring_paged_attend(kvring_paged* p, int32_t layer, const void* q, int64_t q
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale_log2 = (float)((scale > 0.0f ? (double)scale : 1.0 / std::sqrt((double)a.pv.D)) * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return KVRING_ERR_INVALID_ARG;
   a.causal = causal;
   a.window = window < KVRING_PAGED_MAX_LEN ? window : 0;   // wider than any sequence: none
   a.max_new = max_new;

@@ -154,7 +154,7 @@ int kvring_paged_append(kvring_paged* p, int32_t layer, const void* k, int64_t k
  *            0: all kv_len of them (n may then exceed kv_len)
  *   window   0, or with causal the number of indices a query sees at most,
  *            its own included
- *   scale    the softmax scale; 0: 1 / sqrt(D)
+ *   scale    the softmax scale; 0: 1 / sqrt(D).  scale * log2(e) is an fp32 number
  * Queries are rotated by RoPE at q_pos (fp32) and then held in fp16 at a
  * power-of-two scale of their row; out = softmax(scale q.k) v with fp32 sums
  * and statistics and weights of V in fp16.  (A weight is rounded by half a step
