@@ -23,8 +23,8 @@ namespace kvring_dev {
 
 // Tokens per sequence, on average, up to which the kernel of few tokens is
 // taken.  128 sequences, 8 heads x 128, pages of 64, in us, against whole pages:
-// 1 token each 2.9 : 12.9, 4 tokens 5.3 : 13.2, 16 tokens 14.4 : 15.2, 64 tokens
-// 56 : 21; 16 sequences of 256 tokens 47 : 9.  Well below the crossing, because
+// 1 token each 3.2 : 10.7, 4 tokens 6.0 : 10.9, 16 tokens 16.2 : 11.7, 64 tokens
+// 41 : 21; 16 sequences of 256 tokens 52 : 9.  Well below the crossing, because
 // the average may hide one long sequence.
 constexpr int kAppendFew = 4;
 

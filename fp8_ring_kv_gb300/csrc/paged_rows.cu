@@ -16,8 +16,8 @@
 // stage, a ring of stages per warp) and from there, widened to fp16 (exact),
 // straight into the registers of mma.m16n8k16; a warp works by itself, with no
 // barrier between warps.  tcgen05 would want 128 rows.  Measured: a batch of 64
-// ragged contexts of 200 to 8,000 tokens (4 rows, 542 MB) 102 us with joining,
-// 5.3 TB/s; the stretch after the first codes runs at 6.3 TB/s (93% of a copy),
+// ragged contexts of 200 to 8,000 tokens (4 rows, 542 MB) 104 us with joining,
+// 5.2 TB/s; the stretch after the first codes runs at 6.3 TB/s (93% of a copy),
 // some 15 us go into the start (lengths, prefix sums, pages: 5 us) and the end.
 //
 // The products are S^T = K Q^T and O^T = V^T P^T: keys and channels are the

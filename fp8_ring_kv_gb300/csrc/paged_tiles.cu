@@ -10,7 +10,9 @@
 // cache's own; e4m3 operands would, Q and P having 3 bits of fraction there.
 // An fp16 query carries more bits than one fp16 number holds after the
 // rotation, and its output shows them: for that type Q = Q_hi + Q_lo, two
-// products into one S.
+// products into one S.  The weights are one fp16 number for either type (half a
+// step: 2^-11, as the fp16 output's own): a low part would be a second PV and
+// room for it in a tensor memory that is full.
 //
 // What bounds it: the tensor pipe (128 x 128 x 16 fp16 in about 64 cycles),
 // beside which the softmax and the widening have to run.  A block works on two
@@ -20,14 +22,16 @@
 // of both.  S is 128 keys wide in one product: with two buffers of 64 keys QK
 // could run ahead of the softmax, but a 128 x 64 x 16 product from shared memory
 // takes 58 cycles, hardly less than a 128 x 128 x 16 one.
-// Measured: 512 tokens over 65,000, 32 query heads on 8 key heads: 440 us by
-// itself (1.24 PFLOP/s, 66% of a library product), 490 us in a row of such
-// calls; three prompts of 1,731 to 3,644 tokens 283 us (0.72 PFLOP/s).  128 keys
-// of 256 rows take some 3,800 cycles: the products 2,200, the chain of one query
-// tile (softmax 2,000, its two products 1,100, hand-overs 500) the rest, beside
-// widening that is nearly as long; without any exponential, or any conversion,
-// the kernel is no more than 2% faster.  A piece of an item costs 12,000 cycles
-// beside its tiles (queries 6,500, the last product and the results 5,000).
+// Measured: 512 tokens over 65,000, 32 query heads on 8 key heads: 466 us
+// (1.17 PFLOP/s, 63% of a library product); three prompts of 1,731 to 3,644
+// tokens 313 us (0.65 PFLOP/s).  128 keys of 256 rows take some 4,000 cycles: the
+// products 2,200, the chain of one query tile (softmax 2,000, its two products
+// 1,100, hand-overs) the rest, beside widening that is nearly as long; without any
+// exponential, or any conversion, the kernel was no more than 2% faster.  A piece
+// of an item costs some 12,000 cycles beside its tiles (queries 6,500, the last
+// product and the results 5,000), and its phases' code does not stay in the
+// instruction caches (0.9 of 9 stalled warps per issue in the prompts, none worth
+// naming in the long chunk).
 //
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15       softmax: of query tile t and half p of its keys, warps
@@ -622,7 +626,8 @@ __global__ void __launch_bounds__(TTHREADS, 1)
       PieceRec rec = {};
       const int rows = a.pv.P < 32 ? a.pv.P : 32;
       // Codes leave the L2 first: a sequence longer than it pushes nothing else
-      // out (65,000 cached tokens: 490 us without the hint, 474 with it)
+      // out (65,000 cached tokens, two builds that differed in this alone: 490 us
+      // without the hint, 474 with it)
       const uint64_t once = l2_evict_first();
       int done = 0, sg = 0, issued = 0;                  // tiles, stretches; copies (K, V, K, ...)
       bool ok = true;
