@@ -39,7 +39,9 @@ def kvring_paged_workspace_bytes(cfg: kvring_paged_config) -> int:
 def _as_stream(stream, device):
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device)
+    handle = int(getattr(stream, "cuda_stream", stream))
+    # torch takes 0, the default stream's handle, for a request for a new stream
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
 
 
 def _bad_ints(t, shape, index, what):

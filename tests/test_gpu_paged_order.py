@@ -129,3 +129,23 @@ def test_a_cache_made_on_another_stream(raw):
     out = c.kv.attend(q.cuda(), cu(pos), cu(start), cu(ln), cu(c.table))
     c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, ln, c.table))
     assert c.kv.debug_state() == 0
+
+
+def test_the_default_streams_handle():
+    """A raw handle of 0 is the default stream, also for the memory of outputs."""
+    from fp8_ring_kv_gb300.paged import _as_stream
+    default, side = torch.cuda.default_stream(), torch.cuda.Stream()
+    assert default.cuda_stream == 0
+    for device in ("cuda", torch.device("cuda", torch.cuda.current_device())):
+        assert _as_stream(0, device) == default and _as_stream(default, device) == default
+        assert _as_stream(side.cuda_stream, device).cuda_stream == side.cuda_stream
+        assert _as_stream(side, device) is side
+    c = Case([(3, 40)], group=4)
+    c.fill(1)
+    start, ln, pos = c.batch(c.seqs)
+    q = c.draw(c.n, c.q_heads)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        out = c.kv.attend(q.cuda(), cu(pos), cu(start), cu(ln), cu(c.table), stream=0)
+    torch.cuda.synchronize()
+    c.check_out(out, *c.oracle.attend(q.float().numpy(), pos, start, ln, c.table))
