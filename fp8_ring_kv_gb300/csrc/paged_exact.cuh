@@ -64,6 +64,7 @@ __device__ __noinline__ void exact_row(const PagedAttn& a, int b, int s0, int n,
     if (pg < 0 || pg >= a.pv.n_pages) pg = 0;            // (flagged where the tiles were read)
     const size_t blk = (size_t)pg * a.pv.H + h;
     const size_t c0 = ((blk << a.pv.p_shift) + (k & (a.pv.P - 1))) * D + lane * V;
+    const float sk = a.pv.k_scale[blk], sv = a.pv.v_scale[blk];
     float kc[V], vc[V], s = 0.0f;
 #pragma unroll
     for (int p = 0; p < V / 2; ++p) {
@@ -71,8 +72,8 @@ __device__ __noinline__ void exact_row(const PagedAttn& a, int b, int s0, int n,
       const uint32_t vw = cvt_e4m3x2_to_f16x2(reinterpret_cast<const uint16_t*>(a.pv.v_codes + c0)[p]);
       const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw));
       const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vw));
-      kc[2 * p] = kf.x;
-      kc[2 * p + 1] = kf.y;
+      kc[2 * p] = kf.x * sk;                             // the key's own size: queries may be as large as it is small
+      kc[2 * p + 1] = kf.y * sk;
       vc[2 * p] = vf.x;
       vc[2 * p + 1] = vf.y;
     }
@@ -80,7 +81,7 @@ __device__ __noinline__ void exact_row(const PagedAttn& a, int b, int s0, int n,
     for (int c = 0; c < V; ++c) s = fmaf(x[c], kc[c], s);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    const float y = s * a.pv.k_scale[blk] * a.scale_log2, sv = a.pv.v_scale[blk];
+    const float y = s * a.scale_log2;
     const float mn = fmaxf(m, y);
     const float al = mn > m ? ex2f(m - mn) : 1.0f, w = y == -INFINITY ? 0.0f : ex2f(y - mn);
     m = mn;

@@ -129,3 +129,16 @@ def test_an_infinity_in_v(at, n, small):
     front = [i for i in range(n) if 3000 - n + i < at]
     assert np.isfinite(out[front]).all()
     check(c, small, skip=77, window=500)
+
+
+@pytest.mark.parametrize("n,small", CHUNKS, ids=[1, 4, 50])
+@pytest.mark.parametrize("spread", [0, 30])
+def test_queries_as_large_as_keys_are_small(spread, n, small):
+    """Scores of ordinary size from queries near 2^98 and keys near 2^-96."""
+    c = Case([(n, 900), (n, 40)], kv_heads=2, group=2)
+    k, v = c.draw(sum(c.len), 2).float() * 2.0 ** -96, c.draw(sum(c.len), 2).float()
+    v[17, :, 3] = 2.0 ** spread
+    fill(c, k, v)
+    draw = c.draw
+    c.draw = lambda rows, heads: (draw(rows, heads).float() * 2.0 ** 96).to(BF)
+    check(c, small)
