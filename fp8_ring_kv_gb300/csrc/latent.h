@@ -1,0 +1,51 @@
+// Internal definitions of the latent cache: the calls' arguments and the
+// kernels' host-side entry points.
+//
+// The paged cache's view, batch and sharing of work serve here as well: one
+// "key head" (the row that all heads share) with all query heads on it in the
+// absorbed form, and a key head per query head in the expanded form.
+#pragma once
+#include "paged.h"
+
+namespace kvring_dev {
+
+constexpr int kLatRope = 64;               // numbers of the rotated part
+constexpr int kLatHead = 128;              // of a head's key part and value in the expanded form
+constexpr int kLatMax = 512;               // of a latent, at most
+constexpr float kLatMinScale = 0x1p-40f;   // a row's scale, at least
+constexpr float kLatMaxScale = 0x1p40f;    // and at most (a row beyond is marked)
+constexpr int kLatRows = 64;               // query rows of an item of the absorbed form, at most
+
+struct Strides {
+  long long token, head;
+};
+
+// One absorbed call.  a.pv: k_codes, k_scale the cache's, D = C; a.q: q_latent.
+// a.tiles: pieces of [kLatRows][C].
+struct LatentAttn {
+  PagedAttn a;
+  const void* q_rope;
+  Strides q, qr, o;
+};
+
+// One expanded call.  a.pv.H heads with G = 1; a.pb.table = kv_start, a
+// "page" of 2^22 keys per sequence.  a.tiles: pieces of [kTilesRows][128].
+struct ExpandedAttn {
+  PagedAttn a;
+  Strides q, o;
+  int32_t n_keys;
+};
+
+size_t latent_scratch_bytes(int C);
+void latent_carve_scratch(uint8_t* base, int C, PagedAttn* a);
+
+cudaError_t launch_latent_append(const PagedView& pv, const PagedBatch& pb, const void* latent, long long latent_stride,
+                                 const void* rope, long long rope_stride, const int32_t* pos, bool f16, cudaStream_t st);
+cudaError_t launch_latent_read(const PagedView& pv, const PagedBatch& pb, void* out, long long out_stride, bool f16,
+                               cudaStream_t st);
+cudaError_t prepare_latent_attend();
+// tmC: the code rows as [rows][W] u8, box {128, P}, 128-byte swizzle; tmR: box {64, P}, 64-byte swizzle
+cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,
+                                 cudaStream_t st);
+
+}  // namespace kvring_dev

@@ -1,0 +1,860 @@
+// latent_attend: attention over the latent cache in the absorbed form, on the
+// tcgen05 tensor cores, straight from the e4m3 codes.
+//
+//   S^T = [C; R] Q^T      keys are the MMA's rows, query rows its columns
+//   P   = 2^(y - m) w     y = scale log2(e) s_t S + log2 s_t
+//   O^T += C^T P          the latent's channels are the rows
+// y carries the token's scale s_t as a weight on the codes that PV sums, so a
+// column's maximum m is that of what it adds, and l = sum P / s_t.
+//
+// A cached row is key and value: its codes lie in shared memory once, as TMA
+// left them (128 keys x 128 channels, 128-byte swizzle), and are read K-major by
+// QK and MN-major by PV.  Both products are e4m3 x e4m3, exact in fp32: a bf16
+// query has 8 bits and is the sum of two e4m3 numbers of 4, hi = e4m3(q) and
+// lo = e4m3(q - hi) (fp16: three), at a power-of-two scale of its row; a weight
+// is split the same way.  Two products at the 8-bit rate cost what one costs in
+// 16 bits, and nothing is widened: a 16-bit copy of a 128 x 576 tile would be 147
+// KB of shared memory and its conversion half of the tensor cores' time.
+// Numbers below 2^-6 of e4m3's scale lose bits: what is lost is below 2^-18 of
+// the row's largest query number, or of its largest weight.
+//
+// Warp roles (320 threads):
+//   warps 0-7   softmax: a key per thread, of columns half (warp / 4); they also
+//               rotate and split the queries and write the output
+//   warp 8      MMA issue; rows of a tile that no query sees become zeros here
+//   warp 9      the line of work, and TMA of the codes
+#include "latent.h"
+#include "launch.h"
+#include "paged_sched.cuh"
+
+namespace kvring_dev {
+
+constexpr int LKT = 128;                     // keys of a tile
+constexpr int LTHREADS = 320;
+constexpr int LFIX = 2;                      // what an item costs beside its tiles, in tiles
+constexpr float kLatTop = 7.807354922f;      // log2 224: weights start at 224 ...
+constexpr float kLatRaise = 1.0f;            // ... and may reach 448, e4m3's largest, before the maximum is raised
+constexpr float kNoMax = -1e30f;             // no key yet
+
+struct LatStretch {
+  int b, s0, n, len, lo, hi, all_lo, all_hi, k0, k1, tile, flags;
+};
+enum : int { LST_SOME = 1, LST_WHOLE = 2, LST_HEAD = 4 };
+
+template <typename T, int R>
+struct LatLayout {
+  static constexpr int NP = std::is_same_v<T, __half> ? 3 : 2;   // e4m3 parts of a query and of a weight
+  static constexpr int HC = R / 2;                               // columns of a softmax warp
+  static constexpr int CB = LKT * 128, RB = LKT * kLatRope;      // a chunk of 128 channels, the rotated part
+  static constexpr int STAGE = 4 * CB + RB;
+  static constexpr int QC = NP * R * 128;                        // a chunk of the queries, all parts
+  static constexpr int PB = LKT * R;                             // a part of the weights
+  static constexpr int PIN = RB / PB < NP ? RB / PB : NP;        // parts that lie where the rotated part was
+  static constexpr int K = 0;                                    // [2 stages]
+  static constexpr int Q = K + 2 * STAGE;
+  static constexpr int P = Q + 4 * QC + NP * R * kLatRope;       // the other parts
+  static constexpr int TOP = P + (NP - PIN) * PB;                // [2][4][HC] column maxima, sums
+  static constexpr int MINE = TOP + 8 * HC * 4;                  // [8 warps][HC] reference - kLatTop; 1 / l
+  static constexpr int FAC = MINE + 8 * HC * 4;                  // [R] logit factors
+  static constexpr int HI = FAC + R * 4;                         // [R] keys below are seen
+  static constexpr int FLAG = HI + R * 4;                        // [2][8]
+  static constexpr int SEG = FLAG + 64;                          // [2]
+  static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
+  static constexpr int NBAR = 10 + 10 + 2 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int MISC = BAR + NBAR * 8;
+  static constexpr int ALLOC = MISC + 16;
+  static_assert(ALLOC <= 232448, "shared memory of a block");
+  static_assert(2 * STAGE >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the stages at first");
+  static_assert(2 * NP * R + 4 * R <= 512, "tensor memory");
+  static_assert(8 * HC * 4 >= 8 * (LTHREADS / 32), "the prefix sums' warps lie in TOP and MINE at first");
+};
+
+// ---------------------------------------------------------------- small pieces
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t addr, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 |
+         (uint64_t)6u << 61;
+}
+
+// Two fp16 -> packed e4m3x2, round to nearest even, saturating.
+__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+
+// The next e4m3 part of two fp16 numbers, which keep the rest.
+__device__ __forceinline__ uint32_t split2(uint32_t& v) {
+  const uint32_t c = cvt_e4m3x2_f16x2(v);
+  const uint32_t back = cvt_e4m3x2_to_f16x2((uint16_t)c);
+  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&back));
+  v = *reinterpret_cast<const uint32_t*>(&rest);
+  return c;
+}
+
+__device__ __forceinline__ float warp_maxf(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_ld_32x32b_x32(at, r);
+  else tmem_ld_32x32b_x16(at, r);
+}
+
+// a warp waits with one answer; what it has to write for the others is written
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(LTHREADS, 1)
+    latent_attend_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
+                         const __grid_constant__ LatentAttn la) {
+  using LY = LatLayout<T, R>;
+  constexpr int NP = LY::NP, HC = LY::HC;
+  using SH = Share<R, LKT, LFIX, 0, 0x7FFFFFFF>;
+  constexpr uint32_t TM_O = 2 * NP * R;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const PagedAttn& a = la.a;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
+  uint64_t* full = bars;                   // [2][5] codes landed: four chunks, the rotated part
+  uint64_t* free_ = full + 10;             // [2][5] and every MMA is done with them
+  uint64_t* s_full = free_ + 10;           // [2] QK done
+  uint64_t* p_full = s_full + 2;           // P stored
+  uint64_t* o_done = p_full + 1;           // PV done
+  uint64_t* q_full = o_done + 1;           // queries written (once per stretch)
+  uint64_t* seg_full = q_full + 1;         // [2] stretch written
+  uint64_t* seg_free = seg_full + 2;       // [2]
+  uint64_t* flags_in = seg_free + 2;       // [2 halves] the warps' flags written
+  uint64_t* tops_in = flags_in + 2;        // [2 halves] their maxima, or sums
+  uint64_t* drain = tops_in + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
+  volatile LatStretch* segs = reinterpret_cast<volatile LatStretch*>(sm + LY::SEG);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long long* warp_sums = reinterpret_cast<long long*>(sm + LY::TOP);           // at first
+  unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::MINE);
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&free_[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_free[i], 9);
+      mbar_init(&flags_in[i], 4);
+      mbar_init(&tops_in[i], 4);
+      item_sums[i] = 0;
+    }
+    item_sums[2] = 0;
+    mbar_init(p_full, 8);
+    mbar_init(o_done, 1);
+    mbar_init(q_full, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&tmC);
+    tma_prefetch_desc(&tmR);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  long long* pre = reinterpret_cast<long long*>(sm + LY::K);
+  const Cut cut = SH::template prefix<LTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x);
+  const int G = a.pv.G, C = a.pv.D, NC = C >> 7;
+  const long long total = pre[a.pb.n_seqs];
+  long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
+  if (stretch < SH::kLeast) stretch = SH::kLeast;
+  if (cut.pad) stretch = cut.stretch;
+  const int worker = blockIdx.x;
+  long long u = min(total, stretch * worker);
+  const long long end = min(total, u + stretch);
+  Place pl;
+  if (warp == 9 && u < end) pl = find_place<SH, R, LKT>(a, pre, u, cut.pad);
+  __syncthreads();                         // the prefix sums' room is the stages' now
+
+  if (warp < 8) {
+    // ======================================================== softmax
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    float* tops = reinterpret_cast<float*>(sm + LY::TOP) + half * 4 * HC;   // [4][HC]
+    float* mine = reinterpret_cast<float*>(sm + LY::MINE) + warp * HC;
+    float* fac = reinterpret_cast<float*>(sm + LY::FAC);
+    int* his = reinterpret_cast<int*>(sm + LY::HI);
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + LY::FLAG);
+    const int key_row = 32 * quad + lane;
+    uint32_t n_tops = 0, n_q = 0;          // phases of tops_in and q_full so far
+    int done = 0;
+    bool ok = true;
+    // every warp of the half puts HC numbers (lane c the one of column c) into tops
+    auto share = [&](float v) -> bool {
+      if (lane < HC) tops[quad * HC + lane] = v;
+      warp_arrive(&tops_in[half]);
+      return warp_wait(&tops_in[half], n_tops++ & 1, abort_flag);
+    };
+    for (int sg = 0; ok; ++sg) {
+      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      const volatile LatStretch& seg = segs[sg & 1];
+      const int flags = seg.flags;
+      if (!(flags & LST_SOME)) break;
+      const int k0 = seg.k0, n = seg.k1 - k0, s0 = seg.s0, len_n = seg.len - seg.n, seq = seg.b;
+      const int lo = seg.lo, hi = seg.hi, all_lo = seg.all_lo, all_hi = seg.all_hi;
+      const int r0 = seg.tile * R, rows = min(R, seg.n * G - r0);
+      float l[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) l[c] = 0.0f;
+      if (lane < HC) mine[lane] = kNoMax;
+      if (n > 0) {
+        // ------------------------------------------------------ queries
+        constexpr int RW = R / 8;          // rows of a warp
+        const int w0 = warp * RW;
+        if (tid < R) {
+          // rows past the last: as the last one, with a factor of 0
+          const int i = (r0 + min(tid, rows - 1)) / G;
+          his[tid] = a.causal ? len_n + i + 1 : seg.len;
+        }
+        // the rotated parts of all of them: four lanes a row, 16 numbers each
+        float y[16];
+        uint32_t ytop = 0;
+        {
+          const int r = w0 + (lane >> 2), q = lane & 3;
+          const bool on = (lane >> 2) < RW && r < rows;
+          const int rr = r0 + (on ? r : 0), i = rr / G, h = rr - i * G;
+          uint4 a0 = {}, a1 = {};
+          if (on) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(la.q_rope) + (s0 + i) * la.qr.token +
+                                                              h * la.qr.head) + 2 * q;
+            a0 = src[0];
+            a1 = src[1];
+          }
+          bool bad = false;
+          float2 cs[8];
+          rope_load(a.pv, rope_lane(a.pv, 8 * q), a.q_pos + (size_t)(s0 + i) * a.pv.n_axes, cs, bad);
+          if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
+          load8_f32<T>(a0, y);
+          load8_f32<T>(a1, y + 8);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const float2 t = rope_query(y[2 * m], y[2 * m + 1], cs[m]);
+            y[2 * m] = t.x;
+            y[2 * m + 1] = t.y;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ytop = max(ytop, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+          ytop = max(ytop, __shfl_xor_sync(0xFFFFFFFFu, ytop, 1));
+          ytop = max(ytop, __shfl_xor_sync(0xFFFFFFFFu, ytop, 2));
+        }
+        // x * inv in parts: 16 codes of each to ``at`` + part * ``step``
+        auto put = [&](const float* x, float inv, uint8_t* at, int step) {
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = cvt_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t c0 = split2(v[2 * e]), c1 = split2(v[2 * e + 1]);
+              w[e] = c0 | c1 << 16;
+            }
+            *reinterpret_cast<uint4*>(at + p * step) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        };
+        float yinv = 0.0f;
+        constexpr int BATCH = 4;
+#pragma unroll 1
+        for (int b0 = 0; b0 < RW; b0 += BATCH) {
+          uint4 w[BATCH][2];
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int r = w0 + b0 + k;
+            w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+            if (r < rows && lane * 16 < C) {
+              const int i = (r0 + r) / G, h = r0 + r - i * G;
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + i) * la.q.token +
+                                                                h * la.q.head) + 2 * lane;
+              w[k][0] = src[0];
+              w[k][1] = src[1];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int r = w0 + b0 + k;
+            float x[16];
+            load8_f32<T>(w[k][0], x);
+            load8_f32<T>(w[k][1], x + 8);
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+            top = max(__reduce_max_sync(0xFFFFFFFFu, top), __shfl_sync(0xFFFFFFFFu, ytop, 4 * (b0 + k)));
+            float scale, inv;
+            pow2_scale(__uint_as_float(top), scale, inv);
+            const bool finite = top < 0x7F800000u;
+            if (!finite) {                 // the row's scores are NaN by its factor
+              scale = __int_as_float(0x7FC00000);
+              inv = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+            }
+            if ((lane >> 2) == b0 + k) {
+              yinv = inv;
+              if (!finite) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
+              }
+            }
+            if (lane == 0) fac[r] = r < rows ? a.scale_log2 * scale : 0.0f;
+            if (lane * 16 < C)
+              put(x, inv, sm + LY::Q + (lane >> 3) * LY::QC + r * 128 + (((lane & 7) ^ (r & 7)) << 4), R * 128);
+          }
+        }
+        if ((lane >> 2) < RW) {
+          const int r = w0 + (lane >> 2), q = lane & 3;
+          put(y, yinv, sm + LY::Q + 4 * LY::QC + r * 64 + ((q ^ ((r >> 1) & 3)) << 4), R * 64);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(q_full);
+        if (!warp_wait(q_full, n_q++ & 1, abort_flag)) break;
+        // ------------------------------------------------------ key tiles
+        const int32_t* tab = a.pb.table + seq * a.pb.table_stride;
+        auto page = [&](int j) -> int {    // of this thread's key of tile j; -1: not seen
+          const int t = (k0 + j) * LKT + key_row;
+          if (j >= n || t < lo || t >= hi) return -1;
+          const int pg = tab[t >> a.pv.p_shift];
+          return pg < 0 || pg >= a.pv.n_pages ? 0 : pg;
+        };
+        auto scale_of = [&](int j, int pg) -> float {
+          return pg < 0 ? 1.0f : a.pv.k_scale[((size_t)pg << a.pv.p_shift) + (((k0 + j) * LKT + key_row) & (a.pv.P - 1))];
+        };
+        int pg1 = page(1);
+        float s_next = scale_of(0, page(0));
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int g = done + j;
+          float st = s_next;
+          s_next = scale_of(j + 1, pg1);
+          pg1 = page(j + 2);
+          if (st == 0.0f) st = kLatMinScale;             // a row that was never written: zeros
+          const float est = __log2f(st), ist = 1.0f / st;
+          const int key = (k0 + j) * LKT + key_row;
+          const bool edge = (k0 + j) * LKT < all_lo || (k0 + j + 1) * LKT > all_hi;
+          if (!warp_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float x[HC];
+          auto scores = [&]() {            // S of the codes
+            uint32_t part[HC];
+            tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + half * HC, part);
+#pragma unroll
+            for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(part[c]);
+#pragma unroll
+            for (int p = 1; p < NP; ++p) {
+              tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + p * R + half * HC, part);
+#pragma unroll
+              for (int c = 0; c < HC; ++c) x[c] += __uint_as_float(part[c]);
+            }
+          };
+          // x becomes y minus what is in ``mine`` (raw: y itself)
+          auto logits = [&](bool raw) {
+            const float4* f4 = reinterpret_cast<const float4*>(fac + half * HC);
+            const float4* m4 = reinterpret_cast<const float4*>(mine);
+#pragma unroll
+            for (int c = 0; c < HC; c += 4) {
+              const float4 f = f4[c / 4], m = m4[c / 4];
+              const float2 s2 = make_float2(st, st);
+              const float2 g0 = mul2(make_float2(f.x, f.y), s2), g1 = mul2(make_float2(f.z, f.w), s2);
+              const float2 e0 = raw ? make_float2(est, est) : make_float2(est - m.x, est - m.y);
+              const float2 e1 = raw ? make_float2(est, est) : make_float2(est - m.z, est - m.w);
+              const float2 d0 = fma2(make_float2(x[c], x[c + 1]), g0, e0);
+              const float2 d1 = fma2(make_float2(x[c + 2], x[c + 3]), g1, e1);
+              x[c] = d0.x;
+              x[c + 1] = d0.y;
+              x[c + 2] = d1.x;
+              x[c + 3] = d1.y;
+            }
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < HC; ++c) {
+                const int h = his[half * HC + c];
+                if (key >= h || (a.window > 0 && key < h - a.window)) x[c] = -INFINITY;
+              }
+            }
+          };
+          scores();
+          logits(false);
+          float most = x[0];
+#pragma unroll
+          for (int c = 1; c < HC; ++c) most = fmaxf(most, x[c]);
+          const bool up = __any_sync(0xFFFFFFFFu, most > kLatTop + kLatRaise);
+          volatile int* fl = flag + (g & 1) * 8 + half * 4;
+          if (lane == 0) fl[quad] = up;
+          warp_arrive(&flags_in[half]);
+          if (!warp_wait(&flags_in[half], g & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (fl[0] | fl[1] | fl[2] | fl[3]) {
+            // a column's maximum is raised: what was summed is brought to the new one
+            scores();
+            logits(true);
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+              const float v = warp_maxf(x[c]);
+              if (lane == c) top = v;
+            }
+            if (!share(top)) {
+              ok = false;
+              break;
+            }
+            float al = 1.0f;
+            if (lane < HC) {
+              top = fmaxf(fmaxf(tops[lane], tops[HC + lane]), fmaxf(tops[2 * HC + lane], tops[3 * HC + lane])) - kLatTop;
+              const float was = mine[lane];
+              if (top > was + kLatRaise) {
+                mine[lane] = top;
+                al = ex2f(was - top);      // 0 for the column's first keys
+              }
+            }
+            __syncwarp();
+            if (j > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {
+              if (!warp_wait(o_done, (g - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < HC; ++c) l[c] *= __shfl_sync(0xFFFFFFFFu, al, c);
+#pragma unroll 1
+              for (int q = 0; q < NC; ++q) {
+#pragma unroll
+                for (int c0 = 0; c0 < HC; c0 += 16) {
+                  uint32_t o[16];
+                  const uint32_t at = tmem + lanes + TM_O + q * R + half * HC + c0;
+                  tmem_ld_32x32b_x16(at, o);
+#pragma unroll
+                  for (int c = 0; c < 16; ++c)
+                    o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xFFFFFFFFu, al, c0 + c));
+                  tmem_st_32x32b_x16(at, o);
+                }
+              }
+              tmem_st_wait();
+            }
+            scores();
+            logits(false);
+          }
+          // weights, their sums, and their parts
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) {
+            x[c] = ex2f(x[c]);
+            x[c + 1] = ex2f(x[c + 1]);
+            const float2 t = fma2(make_float2(x[c], x[c + 1]), make_float2(ist, ist), make_float2(l[c], l[c + 1]));
+            l[c] = t.x;
+            l[c + 1] = t.y;
+          }
+          uint32_t v[HC / 2];
+#pragma unroll
+          for (int c = 0; c < HC / 2; ++c) v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
+          // PV of the tile before is done with the weights' room
+          if (g > 0 && !warp_wait(o_done, (g - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            uint8_t* room = p < LY::PIN ? sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + p * LY::PB
+                                        : sm + LY::P + (p - LY::PIN) * LY::PB;
+            uint32_t w[HC / 4];
+#pragma unroll
+            for (int c = 0; c < HC / 4; ++c) {
+              const uint32_t c0 = split2(v[2 * c]), c1 = split2(v[2 * c + 1]);
+              w[c] = c0 | c1 << 16;
+            }
+#pragma unroll
+            for (int k = 0; k < HC / 16; ++k) {
+              const int unit = half * (HC / 16) + k;
+              const int at = R == 64 ? key_row * 64 + ((unit ^ ((key_row >> 1) & 3)) << 4)
+                                     : key_row * 32 + ((unit ^ ((key_row >> 2) & 1)) << 4);
+              *reinterpret_cast<uint4*>(room + at) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          warp_arrive(p_full);
+        }
+        if (!ok) break;
+      }
+      done += n;
+      // -------------------------------------------------------- results
+      if (n > 0) {
+        if (!warp_wait(o_done, (done - 1) & 1, abort_flag)) break;
+        tc_fence_after();
+      }
+      // the columns' sums: lane c that of column c
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) {
+        if (w >= HC) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], w);
+        } else {
+#pragma unroll
+          for (int c = 0; c < w; ++c) {
+            const bool up = lane & w;
+            const float give = up ? l[c] : l[c + w], keep = up ? l[c + w] : l[c];
+            l[c] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, w);
+          }
+        }
+      }
+      if (!share(l[0])) break;
+      const bool whole = flags & LST_WHOLE;
+      const size_t at_row = (size_t)(2 * worker + (flags & LST_HEAD ? 1 : 0)) * kLatRows + half * HC;
+      if (lane < HC) {
+        const float sum = (tops[lane] + tops[HC + lane]) + (tops[2 * HC + lane] + tops[3 * HC + lane]);
+        const float ref = mine[lane];
+        if (!whole && quad == 0) a.tiles.ml[at_row + lane] = make_float2(ref == kNoMax ? -INFINITY : ref, sum);
+        mine[lane] = sum != 0.0f ? 1.0f / sum : 0.0f;
+      }
+      __syncwarp();
+      if (whole || n > 0) {
+        const int live = min(HC, rows - half * HC);      // columns of this warp
+#pragma unroll 1
+        for (int q = 0; q < NC; ++q) {
+          uint32_t o[HC];
+          if (n > 0) {
+            tmem_ld_cols<HC>(tmem + lanes + TM_O + q * R + half * HC, o);
+          } else {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) o[c] = 0u;
+          }
+          const int ch = q * 128 + 32 * quad + lane;
+          if (whole) {
+            int i = (r0 + half * HC) / G, h = r0 + half * HC - i * G;
+            T* dst = static_cast<T*>(a.out) + ch;
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+              if (c < live) {
+                const float v = __uint_as_float(o[c]) * mine[c];
+                T r;
+                if constexpr (std::is_same_v<T, __half>) r = __float2half_rn(v);
+                else r = __float2bfloat16_rn(v);
+                dst[(s0 + i) * la.o.token + h * la.o.head] = r;
+              }
+              if (++h >= G) {
+                h = 0;
+                ++i;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < HC; ++c)
+              if (c < live) a.tiles.o[(at_row + c) * C + ch] = __uint_as_float(o[c]);
+          }
+        }
+      }
+      tc_fence_before();
+      warp_arrive(&seg_free[sg & 1]);
+    }
+  } else if (warp == 8) {
+    // ======================================================== MMA issue
+    constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
+    constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, R);
+    const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
+    int done = 0;
+    uint32_t n_q = 0;
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      const volatile LatStretch& seg = segs[sg & 1];
+      if (!(seg.flags & LST_SOME)) break;
+      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
+      if (n > 0 && !warp_wait(q_full, n_q++ & 1, abort_flag)) break;
+#pragma unroll 1
+      for (int j = 0; j <= n && n > 0; ++j) {
+        const int g = done + j, stage = g & 1;
+        if (j < n) {
+          uint64_t* f = full + stage * 5;
+          const uint32_t par = (g >> 1) & 1;
+          const uint32_t kt = k_at + stage * LY::STAGE;
+          const int t0 = (k0 + j) * LKT;
+          if (t0 < lo || t0 + LKT > hi) {
+            // rows that no query sees: their weights are zeros, which must meet numbers
+            for (int c = 0; c < NC && ok; ++c) ok = warp_wait(f + c, par, abort_flag);
+            ok = ok && warp_wait(f + 4, par, abort_flag);
+            if (!ok) break;
+            uint8_t* tile = sm + LY::K + stage * LY::STAGE;
+            for (int r = 0; r < LKT; ++r) {
+              if (t0 + r >= lo && t0 + r < hi) continue;
+              const uint4 zero = make_uint4(0, 0, 0, 0);
+              if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
+              if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const uint32_t d = tmem + stage * NP * R;
+          for (int c = 0; c < NC; ++c) {
+            ok = warp_wait(f + c, par, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+              const uint64_t bd = make_sdesc_sw128(q_at + c * LY::QC, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, c | k);
+            }
+            __syncwarp();
+          }
+          ok = ok && warp_wait(f + 4, par, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+            const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, 1);
+            mma_commit(&s_full[stage]);
+          }
+          __syncwarp();
+        }
+        if (j > 0) {
+          const int gp = g - 1, sp = gp & 1;
+          ok = warp_wait(p_full, gp & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kt = k_at + sp * LY::STAGE;
+            for (int c = 0; c < NC; ++c) {
+              const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+#pragma unroll
+              for (int p = 0; p < NP; ++p) {
+                const uint32_t room = p < LY::PIN ? kt + 4 * LY::CB + p * LY::PB : p_at + (p - LY::PIN) * LY::PB;
+                const uint64_t bd = R == 64 ? make_sdesc_sw64(room, 16, 512) : sdesc_sw32(room, 256);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_f8_ss(tmem + TM_O + c * R, ad + 256 * k, bd + k * (R * 32 / 16), idesc_pv, (j > 1) | p | k);
+              }
+              mma_commit(&free_[sp * 5 + c]);
+            }
+            mma_commit(&free_[sp * 5 + 4]);
+            mma_commit(o_done);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      done += n;
+      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+    }
+    // every MMA issued so far is done before the block releases its tensor memory
+    if (lane == 0) {
+      mma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ======================================================== the line of work
+    PieceRec rec = {};
+    const int P = a.pv.P, boxes = LKT / P;
+    const bool alone = (long long)a.max_new * G <= R;    // every key is read by one item only
+    const uint64_t once = l2_evict_first();
+    int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
+    bool ok = true;
+    for (bool more = u < end; ok; ++sg) {
+      if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+      int k0 = 0, k1 = 0;
+      long long item_end = 0;
+      if (more) {
+        item_end = pl.at + pl.units;
+        const int n = pl.t.t1 - pl.t.t0;
+        k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - LFIX));
+        k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - LFIX));
+      }
+      if (lane == 0) {
+        volatile LatStretch& seg = segs[sg & 1];
+        if (more) {
+          const bool head = u == pl.at;
+          const int i0 = pl.tile * R / G, i1 = min(pl.s.n - 1, (pl.tile * R + R - 1) / G);
+          seg.b = pl.b;
+          seg.s0 = pl.s.s0;
+          seg.n = pl.s.n;
+          seg.len = pl.s.len;
+          seg.lo = pl.t.lo;
+          seg.hi = pl.t.hi;
+          seg.all_hi = a.causal ? pl.s.len - pl.s.n + i0 + 1 : pl.s.len;
+          seg.all_lo = a.window > 0 ? pl.s.len - pl.s.n + i1 - a.window + 1 : 0;
+          seg.k0 = k0;
+          seg.k1 = k1;
+          seg.tile = pl.tile;
+          seg.flags = LST_SOME | (head ? LST_HEAD : 0) | (head && end >= item_end ? LST_WHOLE : 0);
+        } else {
+          seg.flags = 0;
+        }
+        mbar_arrive(&seg_full[sg & 1]);
+      }
+      __syncwarp();
+      if (!more) break;
+      const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
+      // lane i < boxes: the page of its keys of tile k; -1 where no query sees one
+      auto page = [&](int k) -> int {
+        const int key = k * LKT + lane * P;
+        if (lane >= boxes || k >= k1 || key >= pl.t.hi || key + P <= pl.t.lo) return -1;
+        const int pg = tab[key >> a.pv.p_shift];
+        if (pg < 0 || pg >= a.pv.n_pages) {
+          atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
+          return 0;
+        }
+        return pg;
+      };
+      int pg = page(k0);
+      for (int k = k0; k < k1; ++k) {
+        const int g = done + k - k0, stage = g & 1;
+        const int next = page(k + 1);
+        const bool on = pg >= 0;
+        const uint32_t n_on = __popc(__ballot_sync(0xFFFFFFFFu, on));
+        const int y = (int)a.pv.row0 + (pg << a.pv.p_shift);
+        uint8_t* tile = sm + LY::K + stage * LY::STAGE;
+#pragma unroll 1
+        for (int c = 0; c <= NC; ++c) {
+          const int slot = c < NC ? c : 4;
+          uint64_t* f = &full[stage * 5 + slot];
+          if (g >= 2 && !warp_wait(&free_[stage * 5 + slot], ((g - 2) >> 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int width = c < NC ? 128 : kLatRope;
+          if (lane == 0) mbar_arrive_expect_tx(f, n_on * P * width);
+          __syncwarp();
+          if (on) {
+            uint8_t* dst = tile + slot * LY::CB + lane * P * width;
+            const CUtensorMap* tm = c < NC ? &tmC : &tmR;
+            if (alone) tma_load_2d_hint(dst, tm, f, c * 128, y, once);
+            else tma_load_2d(dst, tm, f, c * 128, y);
+          }
+          armed = g * 5 + c + 1;
+        }
+        if (!ok) break;
+        pg = next;
+      }
+      done += k1 - k0;
+      if (u == pl.at && end < item_end)
+        rec = {min(pl.s.n * G - pl.tile * R, R), (int)quotient(item_end - 1, stretch), 0, pl.s.s0, pl.tile * R};
+      u = min(end, item_end);
+      more = u < end && next_place<SH, R, LKT>(a, pl, cut.pad);
+    }
+    if (lane == 0) a.tiles.rec[worker] = rec;
+    // after an abort: copies still in flight land in this block's shared memory
+    if (*abort_flag && armed > 0) {
+      const int g = (armed - 1) / 5;
+      for (int t = max(0, g - 1); t <= g; ++t)
+        for (int c = 0; c <= NC && t * 5 + c < armed; ++c)
+          mbar_wait(&full[(t & 1) * 5 + (c < NC ? c : 4)], (t >> 1) & 1, nullptr, 100000000ull);
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- joining
+// The items that several blocks share (see paged_join): a warp per row and 128
+// channels, the pieces in the workers' order.
+constexpr int kLatJoinWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const __grid_constant__ LatentAttn la) {
+  pdl_wait();
+  pdl_trigger();
+  const PagedAttn& a = la.a;
+  const int w = blockIdx.x, lane = threadIdx.x & 31, C = a.pv.D, NC = C >> 7;
+  const PieceRec it = a.tiles.rec[w];
+  for (int id = blockIdx.y * kLatJoinWarps + (threadIdx.x >> 5); id < it.rows * NC; id += gridDim.y * kLatJoinWarps) {
+    const int r = id / NC, c = (id - r * NC) * 128 + lane * 4;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = w; p <= it.last; ++p) {
+      const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * kLatRows + r;
+      const float2 ml = a.tiles.ml[row];
+      const float4 x = *reinterpret_cast<const float4*>(a.tiles.o + row * C + c);
+      const bool some = ml.x != -INFINITY;                 // else x was not written
+      const float mn = some ? fmaxf(m, ml.x) : m;
+      const float f0 = mn > m ? ex2f(m - mn) : 1.0f, f1 = some ? ex2f(ml.x - mn) : 0.0f;
+      m = mn;
+      l = l * f0 + (some ? ml.y * f1 : ml.y);              // no key: 0; scores all NaN: NaN
+      if (some) {
+        o.x = o.x * f0 + x.x * f1;
+        o.y = o.y * f0 + x.y * f1;
+        o.z = o.z * f0 + x.z * f1;
+        o.w = o.w * f0 + x.w * f1;
+      }
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    const int rr = it.row0 + r, i = rr / a.pv.G, h = rr - i * a.pv.G;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.s0 + i) * la.o.token + h * la.o.head + c) =
+        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+  }
+}
+
+// ---------------------------------------------------------------- host
+size_t latent_scratch_bytes(int C) {
+  const size_t slots = (size_t)2 * kPagedMaxSms * kLatRows, expanded = (size_t)2 * kPagedMaxSms * kTilesRows;
+  const size_t a = slots * C * 4 + slots * 8, b = expanded * kLatHead * 4 + expanded * 8;
+  return (a > b ? a : b) + kPagedMaxSms * sizeof(PieceRec);
+}
+
+void latent_carve_scratch(uint8_t* base, int C, PagedAttn* a) {
+  const size_t slots = (size_t)2 * kPagedMaxSms * (C == 0 ? kTilesRows : kLatRows);
+  const size_t width = C == 0 ? kLatHead : C;
+  a->tiles.o = reinterpret_cast<float*>(base);
+  a->tiles.ml = reinterpret_cast<float2*>(base + slots * width * 4);
+  a->tiles.rec = reinterpret_cast<PieceRec*>(base + slots * width * 4 + slots * 8);
+}
+
+template <typename T, int R>
+static cudaError_t prepare_t() {
+  return cudaFuncSetAttribute(latent_attend_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              LatLayout<T, R>::ALLOC);
+}
+
+cudaError_t prepare_latent_attend() {
+  cudaError_t e = prepare_t<__half, 32>();
+  if (e == cudaSuccess) e = prepare_t<__nv_bfloat16, 32>();
+  if (e == cudaSuccess) e = prepare_t<__nv_bfloat16, 64>();
+  return e;
+}
+
+template <typename T, int R>
+static cudaError_t attend_t(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, int blocks,
+                            cudaStream_t st) {
+  const cudaError_t e = launch_pdl(latent_attend_kernel<T, R>, dim3(blocks), dim3(LTHREADS), LatLayout<T, R>::ALLOC, st,
+                                   tmC, tmR, la);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(latent_join_kernel<T>, dim3(blocks, R * (la.a.pv.D >> 7) / kLatJoinWarps / 4), dim3(32 * kLatJoinWarps),
+                    0, st, la);
+}
+
+cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,
+                                 cudaStream_t st) {
+  const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
+  if (f16) return attend_t<__half, 32>(la, tmC, tmR, blocks, st);
+  if ((long long)la.a.max_new * la.a.pv.G <= 32) return attend_t<__nv_bfloat16, 32>(la, tmC, tmR, blocks, st);
+  return attend_t<__nv_bfloat16, 64>(la, tmC, tmR, blocks, st);
+}
+
+}  // namespace kvring_dev

@@ -42,6 +42,10 @@ KVRING_IN_F16 = 1
 KVRING_PAGED_MAX_SEQS = 2048
 KVRING_PAGED_MAX_LEN = 1 << 22
 
+# the latent cache (include/kvring_latent.h)
+KVRING_LATENT_ROPE = 64
+KVRING_LATENT_HEAD = 128
+
 EXPORTS = (
     "kvring_workspace_bytes", "kvring_create", "kvring_write", "kvring_write_global", "kvring_calibrate",
     "kvring_set_qk_norm",
@@ -51,6 +55,8 @@ EXPORTS = (
     "kvring_debug_wait_timeout",
     "kvring_paged_workspace_bytes", "kvring_paged_create", "kvring_paged_append", "kvring_paged_attend",
     "kvring_paged_destroy", "kvring_paged_layout", "kvring_paged_debug_state",
+    "kvring_latent_workspace_bytes", "kvring_latent_create", "kvring_latent_append", "kvring_latent_read",
+    "kvring_latent_attend", "kvring_latent_destroy", "kvring_latent_layout", "kvring_latent_debug_state",
 )
 
 
@@ -77,6 +83,22 @@ class kvring_paged_config(ctypes.Structure):
         ("kv_heads", ctypes.c_int32),
         ("q_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis_dims", ctypes.c_int32 * 3),
+        ("pos_min", ctypes.c_int32 * 3),
+        ("pos_count", ctypes.c_int32 * 3),
+        ("rope_base", ctypes.c_double),
+    ]
+
+
+class kvring_latent_config(ctypes.Structure):
+    _fields_ = [
+        ("layers", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32),
         ("page_tokens", ctypes.c_int32),
         ("n_pages", ctypes.c_int32),
         ("in_dtype", ctypes.c_int32),
@@ -132,6 +154,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvring_paged_destroy": (ctypes.c_int, [vp]),
         "kvring_paged_layout": (ctypes.c_int, [vp] + [ctypes.POINTER(vp)] * 5),
         "kvring_paged_debug_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i32)]),
+        "kvring_latent_workspace_bytes": (sz, [ctypes.POINTER(kvring_latent_config)]),
+        "kvring_latent_create": (ctypes.c_int, [ctypes.POINTER(kvring_latent_config), vp, sz, vp, ctypes.POINTER(vp)]),
+        "kvring_latent_append": (ctypes.c_int, [vp, i32, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i64, i32, vp]),
+        "kvring_latent_read": (ctypes.c_int, [vp, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, vp]),
+        "kvring_latent_attend": (ctypes.c_int, [vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, i64, i32,
+                                                i32, i32, ctypes.c_float, vp, i64, i64, vp]),
+        "kvring_latent_destroy": (ctypes.c_int, [vp]),
+        "kvring_latent_layout": (ctypes.c_int, [vp] + [ctypes.POINTER(vp)] * 3),
+        "kvring_latent_debug_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i32)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
