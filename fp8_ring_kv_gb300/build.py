@@ -16,7 +16,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvring.so")
 SOURCES = ["ring_kernels.cu", "attend.cu", "kvring_api.cu", "paged_append.cu", "paged_rows.cu", "paged_tiles.cu",
-           "paged_join.cu", "paged_api.cu", "latent_rows.cu", "latent_attend.cu", "latent_api.cu"]
+           "paged_join.cu", "paged_api.cu", "latent_rows.cu", "latent_attend.cu",
+           "latent_expanded.cu", "latent_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -33,11 +33,14 @@ struct LatentAttn {
 struct ExpandedAttn {
   PagedAttn a;
   Strides q, o;
+  const void* v;
+  long long v_token, v_head;
   int32_t n_keys;
 };
 
 size_t latent_scratch_bytes(int C);
-void latent_carve_scratch(uint8_t* base, int C, PagedAttn* a);
+// pieces of ``rows`` rows of ``width`` numbers
+void latent_carve_scratch(uint8_t* base, int rows, int width, PagedAttn* a);
 
 cudaError_t launch_latent_append(const PagedView& pv, const PagedBatch& pb, const void* latent, long long latent_stride,
                                  const void* rope, long long rope_stride, const int32_t* pos, bool f16, cudaStream_t st);
@@ -47,5 +50,12 @@ cudaError_t prepare_latent_attend();
 // tmC: the code rows as [rows][W] u8, box {128, P}, 128-byte swizzle; tmR: box {64, P}, 64-byte swizzle
 cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,
                                  cudaStream_t st);
+
+// the items that several blocks share; pieces of ``rows`` rows of a.pv.D numbers
+cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, bool f16, int blocks, cudaStream_t st);
+cudaError_t prepare_latent_expanded();
+// tmK, tmV: [heads][keys][128] in 16 bits, boxes {64, 128, 1} and {64, 64, 1}; tmR: [keys][64], box {64, 128}
+cudaError_t launch_latent_expanded(const ExpandedAttn& xa, const CUtensorMap& tmK, const CUtensorMap& tmR,
+                                   const CUtensorMap& tmV, bool f16, int sms, cudaStream_t st);
 
 }  // namespace kvring_dev

@@ -75,6 +75,22 @@ bool encode_rows(CUtensorMap* m, void* codes, const kvring_latent_config& c, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 16-bit rows [heads][n][width] (heads 0: [n][width]), boxes of 64 numbers of
+// ``rows`` rows.  A tensor of no rows has none to read: one, of which nothing is read.
+bool encode_heads(CUtensorMap* m, const void* base, bool f16, int width, int heads, int n, long long token,
+                  long long head, int rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  // a stride that is not used may be anything; the encoder wants a positive one
+  const cuuint64_t strides[2] = {(cuuint64_t)(token > 0 ? token : width) * 2, (cuuint64_t)(head > 0 ? head : width) * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)(n > 0 ? n : 1), (cuuint64_t)heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads > 0 ? 3 : 2,
+             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // the checks that all calls share
 int check_call(const kvring_latent* p, const int32_t* seq_start, const int32_t* kv_len, int32_t n_seqs,
                int32_t n_tokens) {
@@ -202,6 +218,7 @@ int kvring_latent_create(const kvring_latent_config* cfg, void* workspace, size_
       (!encode_rows(&p->c_map, pv.k_codes, *cfg, 128) || !encode_rows(&p->r_map, pv.k_codes, *cfg, kLatRope)))
     e = cudaErrorInvalidValue;
   if (e == cudaSuccess) e = prepare_latent_attend();
+  if (e == cudaSuccess) e = prepare_latent_expanded();
   if (e != cudaSuccess) {
     delete p;
     return cuda_fail(e);
@@ -271,9 +288,61 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
   a.q_pos = q_pos;
   a.out = out;
   la.q_rope = q_rope;
-  latent_carve_scratch(p->scratch, a.pv.D, &a);
+  latent_carve_scratch(p->scratch, kLatRows, a.pv.D, &a);
   const cudaError_t e = launch_latent_attend(la, p->c_map, p->r_map, p->cfg.in_dtype == KVRING_IN_F16, p->sms,
                                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVRING_OK : cuda_fail(e);
+}
+
+int kvring_latent_attend_expanded(kvring_latent* p, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                                  int64_t k_token, int64_t k_head, const void* k_rope, int64_t k_rope_token,
+                                  const void* v, int64_t v_token, int64_t v_head, int32_t n_keys, const int32_t* q_pos,
+                                  const int32_t* seq_start, const int32_t* kv_start, const int32_t* kv_len,
+                                  int32_t n_seqs, int32_t n_tokens, int32_t max_new, int32_t causal, int32_t window,
+                                  float scale, void* out, int64_t out_token, int64_t out_head, kvring_stream stream) {
+  if (!q || !q_pos || !kv_start || !out) return KVRING_ERR_INVALID_ARG;
+  if (n_keys == 0) k = v = k_rope = q;     // not read
+  if (!k || !k_rope || !v) return KVRING_ERR_INVALID_ARG;
+  ExpandedAttn xa{};
+  PagedAttn& a = xa.a;
+  int s = check_call(p, seq_start, kv_len, n_seqs, n_tokens);
+  if (scale == 0.0f) scale = (float)(1.0 / std::sqrt((double)(kLatHead + kLatRope)));
+  if (s == KVRING_OK) s = check_attend(p, n_tokens, max_new, causal, window, scale, &a);
+  if (s != KVRING_OK) return s;
+  const int heads = p->cfg.q_heads;
+  xa.q = {q_token, q_head};
+  xa.o = {out_token, out_head};
+  xa.v = v;
+  xa.v_token = v_token;
+  xa.v_head = v_head;
+  xa.n_keys = n_keys;
+  if (n_keys < 0 || n_keys > (1 << 30)) return KVRING_ERR_INVALID_ARG;
+  if (!strides_ok(xa.q, n_tokens, heads, kLatHead + kLatRope) || !strides_ok(xa.o, n_tokens, heads, kLatHead) ||
+      !strides_ok({k_token, k_head}, n_keys, heads, kLatHead) || !strides_ok({v_token, v_head}, n_keys, heads, kLatHead) ||
+      !stride_ok(k_rope_token, kLatRope))
+    return KVRING_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      !aligned(q_pos, 4) || !aligned(kv_start, 4))
+    return KVRING_ERR_MISALIGNED;
+  if (n_seqs == 0 || n_tokens == 0) return KVRING_OK;
+  a.pv = p->pv;
+  a.pv.H = heads;
+  a.pv.G = 1;
+  a.pv.D = kLatHead;
+  a.pv.p_shift = 22;                       // one "page" holds the longest sequence
+  static_assert(KVRING_PAGED_MAX_LEN == 1 << 22, "a sequence's keys");
+  a.pb = PagedBatch{seq_start, kv_len, kv_start, 1, n_seqs, n_tokens, 1};
+  a.q = q;
+  a.q_pos = q_pos;
+  a.out = out;
+  latent_carve_scratch(p->scratch, kTilesRows, kLatHead, &a);
+  CUtensorMap tmK, tmV, tmR;
+  const bool f16 = p->cfg.in_dtype == KVRING_IN_F16;
+  if (!encode_heads(&tmK, k, f16, kLatHead, heads, n_keys, k_token, k_head, 128) ||
+      !encode_heads(&tmV, v, f16, kLatHead, heads, n_keys, v_token, v_head, 64) ||
+      !encode_heads(&tmR, k_rope, f16, kLatRope, 0, n_keys, k_rope_token, 0, 128))
+    return cuda_fail(cudaErrorInvalidValue);
+  const cudaError_t e = launch_latent_expanded(xa, tmK, tmR, tmV, f16, p->sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVRING_OK : cuda_fail(e);
 }
 

@@ -773,14 +773,14 @@ __global__ void __launch_bounds__(LTHREADS, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// The items that several blocks share (see paged_join): a warp per row and 128
-// channels, the pieces in the workers' order.
+// The items that several blocks share (see paged_join), of either form: a warp
+// per row and 128 channels, the pieces in the workers' order.
 constexpr int kLatJoinWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const __grid_constant__ LatentAttn la) {
+__global__ void __launch_bounds__(32 * kLatJoinWarps)
+    latent_join_kernel(const __grid_constant__ PagedAttn a, Strides out, int slot_rows) {
   pdl_wait();
   pdl_trigger();
-  const PagedAttn& a = la.a;
   const int w = blockIdx.x, lane = threadIdx.x & 31, C = a.pv.D, NC = C >> 7;
   const PieceRec it = a.tiles.rec[w];
   for (int id = blockIdx.y * kLatJoinWarps + (threadIdx.x >> 5); id < it.rows * NC; id += gridDim.y * kLatJoinWarps) {
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const _
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int p = w; p <= it.last; ++p) {
-      const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * kLatRows + r;
+      const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * slot_rows + r;
       const float2 ml = a.tiles.ml[row];
       const float4 x = *reinterpret_cast<const float4*>(a.tiles.o + row * C + c);
       const bool some = ml.x != -INFINITY;                 // else x was not written
@@ -805,25 +805,34 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const _
       }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    const int rr = it.row0 + r, i = rr / a.pv.G, h = rr - i * a.pv.G;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.s0 + i) * la.o.token + h * la.o.head + c) =
+    const int rr = it.row0 + r, i = rr / a.pv.G, h = it.h * a.pv.G + rr - i * a.pv.G;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.s0 + i) * out.token + h * out.head + c) =
         make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
   }
 }
 
 // ---------------------------------------------------------------- host
-size_t latent_scratch_bytes(int C) {
-  const size_t slots = (size_t)2 * kPagedMaxSms * kLatRows, expanded = (size_t)2 * kPagedMaxSms * kTilesRows;
-  const size_t a = slots * C * 4 + slots * 8, b = expanded * kLatHead * 4 + expanded * 8;
-  return (a > b ? a : b) + kPagedMaxSms * sizeof(PieceRec);
+static size_t piece_bytes(int rows, int width) {
+  const size_t slots = (size_t)2 * kPagedMaxSms * rows;
+  return slots * width * 4 + slots * 8 + kPagedMaxSms * sizeof(PieceRec);
 }
 
-void latent_carve_scratch(uint8_t* base, int C, PagedAttn* a) {
-  const size_t slots = (size_t)2 * kPagedMaxSms * (C == 0 ? kTilesRows : kLatRows);
-  const size_t width = C == 0 ? kLatHead : C;
+size_t latent_scratch_bytes(int C) {
+  const size_t a = piece_bytes(kLatRows, C), b = piece_bytes(kTilesRows, kLatHead);
+  return a > b ? a : b;
+}
+
+void latent_carve_scratch(uint8_t* base, int rows, int width, PagedAttn* a) {
+  const size_t slots = (size_t)2 * kPagedMaxSms * rows;
   a->tiles.o = reinterpret_cast<float*>(base);
   a->tiles.ml = reinterpret_cast<float2*>(base + slots * width * 4);
   a->tiles.rec = reinterpret_cast<PieceRec*>(base + slots * width * 4 + slots * 8);
+}
+
+cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, bool f16, int blocks, cudaStream_t st) {
+  const dim3 grid(blocks, (rows * (a.pv.D >> 7) + 4 * kLatJoinWarps - 1) / (4 * kLatJoinWarps)), block(32 * kLatJoinWarps);
+  return f16 ? launch_pdl(latent_join_kernel<__half>, grid, block, 0, st, a, o, rows)
+             : launch_pdl(latent_join_kernel<__nv_bfloat16>, grid, block, 0, st, a, o, rows);
 }
 
 template <typename T, int R>
@@ -844,9 +853,7 @@ static cudaError_t attend_t(const LatentAttn& la, const CUtensorMap& tmC, const 
                             cudaStream_t st) {
   const cudaError_t e = launch_pdl(latent_attend_kernel<T, R>, dim3(blocks), dim3(LTHREADS), LatLayout<T, R>::ALLOC, st,
                                    tmC, tmR, la);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(latent_join_kernel<T>, dim3(blocks, R * (la.a.pv.D >> 7) / kLatJoinWarps / 4), dim3(32 * kLatJoinWarps),
-                    0, st, la);
+  return e == cudaSuccess ? launch_latent_join(la.a, la.o, kLatRows, std::is_same_v<T, __half>, blocks, st) : e;
 }
 
 cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,

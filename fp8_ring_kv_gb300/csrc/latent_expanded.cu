@@ -1,0 +1,598 @@
+// latent_expanded: attention with keys and values of every head, 128 numbers of
+// its own and a rotated key part of 64 that the heads share, on the tcgen05
+// tensor cores.
+//
+//   S = [Q, rope(Qr)] [K; Kr]^T    kind::f16, the inputs' own type
+//   P = 2^(y - m + 6), 16 bits, in tensor memory over the S it came from
+//   O += P V                       A = P from tensor memory
+//
+// A block works on two tiles of 128 query rows of one head over the same keys:
+// while the softmax of one runs, the tensor cores work on the other.  The shared
+// key part is a third block of K's tile, read where it lies, so no head's keys
+// are written out 192 wide.
+//
+// What bounds it: the tensor pipe (128 keys of 256 rows: 24 steps of 128 x 128 x
+// 16 for S and 16 for PV, 64 cycles each, 2,560), beside which 32,768
+// exponentials take 2,048 cycles.
+//
+// Warp roles (512 threads, registers moved from the last two groups to the softmax):
+//   warps 0-7    softmax, tile warp / 4, a row per thread; they also load and
+//                rotate the queries and write the output
+//   warp 8       MMA issue
+//   warp 9       the line of work, and TMA
+//   warps 12-15  values that not every row sees: those that no row sees become
+//                zeros, a NaN or infinity that some see is taken out (its weight in the
+//                others is 0, which must meet a number) and remembered
+// QK of the next tile overwrites the P that PV of this one reads, with another
+// accumulator: products of different accumulators have no documented order, so
+// it is issued once that PV has completed.
+#include "latent.h"
+#include "launch.h"
+#include "paged_sched.cuh"
+
+namespace kvring_dev {
+
+constexpr int XKT = 128, XROWS = 128, XTR = kTilesRows, XTHREADS = 512;
+static_assert(XTR == 2 * XROWS);
+constexpr int kXSoftmaxRegs = 192, kXOtherRegs = 64;   // per thread: 8 warps each
+constexpr int XRING = 8, XBLK = 16384;       // blocks of K (128 keys x 64 numbers) and V (64 keys x 128)
+constexpr float kXRaise = 8.0f;              // a row's maximum is raised when a tile exceeds it by 2^8 ...
+constexpr float kXTop = 6.0f;                // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
+
+struct XStretch {
+  int s0, n, len, lo, hi, all_lo, all_hi, k0, k1, tile, h, key0, flags;
+};
+enum : int { XST_SOME = 1, XST_WHOLE = 2, XST_HEAD = 4, XST_SKIP = 8 };
+
+struct XLayout {
+  static constexpr int QT = 3 * XROWS * 128;             // a query tile: three blocks of 64 numbers
+  static constexpr int Q = 0;
+  static constexpr int RING = Q + 2 * QT;
+  static constexpr int SEG = RING + XRING * XBLK;
+  static constexpr int BAR = SEG + 2 * 64;
+  static constexpr int NBAR = 2 * XRING + 5 * 2 + 4 + 1;
+  static constexpr int MISC = BAR + NBAR * 8;
+  static constexpr int ALLOC = MISC + 16;
+  static_assert(sizeof(XStretch) <= 64 && ALLOC <= 232448, "shared memory of a block");
+  static_assert(2 * QT >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the query tiles at first");
+};
+
+// The 16-bit numbers of w that are no numbers become zeros; true where there was one.
+template <typename T>
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  constexpr uint32_t E = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+  const bool lo = (w & E) == E, hi = (w & (E << 16)) == (E << 16);
+  if (lo) w &= 0xFFFF0000u;
+  if (hi) w &= 0x0000FFFFu;
+  return lo || hi;
+}
+
+// Whether one of the values of keys lo .. hi - 1 is no number, tiles that every
+// row sees left out.
+template <typename T>
+__device__ __noinline__ bool nonfinite_among(const T* v, long long v_token, int lo, int hi, int all_lo, int all_hi) {
+#pragma unroll 1
+  for (int key = lo; key < hi; ++key) {
+    const int k = key / XKT;
+    if (k * XKT >= all_lo && k * XKT + XKT <= all_hi) continue;
+    const uint4* p = reinterpret_cast<const uint4*>(v + key * v_token);
+#pragma unroll 1
+    for (int c = 0; c < kLatHead / 8; ++c) {
+      uint4 w = p[c];
+      if (drop_nonfinite<T>(w.x) | drop_nonfinite<T>(w.y) | drop_nonfinite<T>(w.z) | drop_nonfinite<T>(w.w)) return true;
+    }
+  }
+  return false;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(XTHREADS, 1)
+    latent_expanded_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmR,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ExpandedAttn xa) {
+  using LY = XLayout;
+  using SH = Share<XTR, XKT, 2, 0, 0x7FFFFFFF>;
+  constexpr uint32_t TM_S = 0, TM_O = 256;
+  constexpr uint32_t FMT = std::is_same_v<T, __half> ? 0 : 1;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const PagedAttn& a = xa.a;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
+  uint64_t* full = bars;                   // [XRING] block landed
+  uint64_t* free_ = full + XRING;          // [XRING] every MMA is done with it
+  uint64_t* q_full = free_ + XRING;        // [2 query tiles]
+  uint64_t* s_full = q_full + 2;           // [2] QK done
+  uint64_t* p_full = s_full + 2;           // [2] P stored
+  uint64_t* o_done = p_full + 2;           // [2] PV done
+  uint64_t* v_clean = o_done + 2;          // [2] (tiles in turn) values looked at
+  uint64_t* seg_full = v_clean + 2;        // [2]
+  uint64_t* seg_free = seg_full + 2;       // [2]
+  uint64_t* drain = seg_free + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
+  volatile int* odd_seen = reinterpret_cast<volatile int*>(sm + LY::MISC + 8);   // a value that is no number was taken out
+  auto seg_at = [&](int sg) { return reinterpret_cast<volatile XStretch*>(sm + LY::SEG + (sg & 1) * 64); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::RING);        // at first
+  long long* warp_sums = reinterpret_cast<long long*>(sm + LY::RING + 64);
+  if (tid == 0) {
+    for (int i = 0; i < XRING; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&free_[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&v_clean[i], 4);
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_free[i], 13);
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < 3; ++i) item_sums[i] = 0;
+    *abort_flag = 0;
+    *odd_seen = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmR);
+    tma_prefetch_desc(&tmV);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  long long* pre = reinterpret_cast<long long*>(sm + LY::Q);
+  const Cut cut = SH::template prefix<XTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x);
+  const long long total = pre[a.pb.n_seqs] * a.pv.H;
+  long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
+  if (stretch < SH::kLeast) stretch = SH::kLeast;
+  if (cut.pad) stretch = cut.stretch;
+  const int worker = blockIdx.x;
+  long long u = min(total, stretch * worker);
+  const long long end = min(total, u + stretch);
+  Place pl;
+  if (warp == 9 && u < end) pl = find_place<SH, XTR, XKT>(a, pre, u, cut.pad);
+  // the prefix sums' room is the query tiles' now, the others' the ring's
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  if (warp < 8) {
+    // ======================================================== softmax
+    reg_inc<kXSoftmaxRegs>();
+    const int t = warp >> 2, quad = warp & 3, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t s_at = tmem + lanes + TM_S + 128 * t, o_at = tmem + lanes + TM_O + 128 * t;
+    uint32_t tiles = 0;                    // of this query tile so far: the phases of its barriers
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      const volatile XStretch& seg = *seg_at(sg);
+      const int flags = seg.flags;
+      if (!(flags & XST_SOME)) break;
+      const int k0 = seg.k0, n = seg.k1 - k0, s0 = seg.s0, len_n = seg.len - seg.n, head = seg.h;
+      const int r0 = seg.tile * XTR + t * XROWS, rows = min(XROWS, seg.n - r0);   // of this query tile
+      const bool live = row < rows;
+      const int i = r0 + row;
+      const int hi = !live ? 0x7FFFFFFF : a.causal ? len_n + i + 1 : seg.len;
+      const int lo = live && a.window > 0 ? len_n + i - a.window + 1 : 0;
+      float m = -INFINITY, l = 0.0f;
+      if (n > 0 && rows > 0) {
+        // ------------------------------------------------------ queries
+        uint8_t* tile = sm + LY::Q + t * LY::QT;
+        const T* q = static_cast<const T*>(a.q) + (long long)(s0 + r0) * xa.q.token + (long long)head * xa.q.head;
+#pragma unroll 1
+        for (int b0 = 0; b0 < 32; b0 += 8) {             // 128 numbers of a row: 16 lanes
+          uint4 w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 32 * quad + b0 + 2 * k + (lane >> 4);
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows) w[k] = *(reinterpret_cast<const uint4*>(q + r * xa.q.token) + (lane & 15));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 32 * quad + b0 + 2 * k + (lane >> 4), c = lane & 15;
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * (XROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[k];
+          }
+        }
+        const int rq = lane & 3;                         // the rotated part: 4 lanes of 16 numbers
+        const RopeLane rl = rope_lane(a.pv, 8 * rq);
+        bool bad = false;
+#pragma unroll 1
+        for (int b0 = 0; b0 < 32; b0 += 8) {
+          const int r = 32 * quad + b0 + (lane >> 2);
+          const bool on = r < rows;
+          uint4 a0 = {}, a1 = {};
+          if (on) {
+            const uint4* src = reinterpret_cast<const uint4*>(q + r * xa.q.token + kLatHead) + 2 * rq;
+            a0 = src[0];
+            a1 = src[1];
+          }
+          float2 cs[8];
+          float x[16];
+          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + r0 + (on ? r : 0)) * a.pv.n_axes, cs, bad);
+          load8_f32<T>(a0, x);
+          load8_f32<T>(a1, x + 8);
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = rope_query(x[2 * e], x[2 * e + 1], cs[e]);
+            w[e] = pack2<T>(y.x, y.y);
+          }
+          uint8_t* at = tile + 2 * (XROWS * 128) + r * 128;
+          *reinterpret_cast<uint4*>(at + (((2 * rq) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(at + (((2 * rq + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[t]);
+        // ------------------------------------------------------ key tiles
+        const float rf = a.scale_log2;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++tiles) {
+          if (!warp_wait(&s_full[t], tiles & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t xr[128];
+          tmem_ld_32x32b_x64(s_at, *reinterpret_cast<uint32_t(*)[64]>(xr));
+          tmem_ld_32x32b_x64(s_at + 64, *reinterpret_cast<uint32_t(*)[64]>(xr + 64));
+          const int key0 = (k0 + j) * XKT;
+          if (__any_sync(0xFFFFFFFFu, key0 + XKT > hi || key0 < lo)) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (key0 + k >= hi || key0 + k < lo) xr[k] = 0xFF800000u;   // -inf
+          }
+          const float* s = reinterpret_cast<const float*>(xr);
+          float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k < 128; k += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = k + 4 < 128 ? max3f(m4[e], s[k + e], s[(k + 4 + e) & 127]) : fmaxf(m4[e], s[k + e]);
+          }
+          const float mm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rf;
+          if (__any_sync(0xFFFFFFFFu, mm > m + kXRaise)) {
+            // rare after a row's first keys: what was summed is brought to the new maximum
+            const float mn = mm > m + kXRaise ? mm : m;
+            const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
+            m = mn;
+            l *= al;
+            if (j > 0) {
+              // QK of this tile was issued after the PV before it had completed
+#pragma unroll 1
+              for (int k = 0; k < kLatHead; k += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_at + k, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st_32x32b_x16(o_at + k, o);
+              }
+            }
+          }
+          const float sub = m == -INFINITY ? 0.0f : kXTop - m;
+          float2 part[2] = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 y = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(rf, rf),
+                              make_float2(sub, sub));
+              y.x = ex2f(y.x);
+              y.y = ex2f(y.y);
+              part[e & 1] = add2(part[e & 1], y);
+              p[e] = pack2<T>(y.x, y.y);
+            }
+            tmem_st_32x32b_x16(s_at + 16 * c, p);
+          }
+          l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        if (ok && !warp_wait(&o_done[t], (tiles - 1) & 1, abort_flag)) ok = false;
+        if (!ok) break;
+        tc_fence_after();
+        if (*odd_seen && live &&
+            nonfinite_among<T>(static_cast<const T*>(xa.v) + (long long)seg.key0 * xa.v_token + (long long)head * xa.v_head,
+                               xa.v_token, max(max(lo, seg.lo), k0 * XKT), min(min(hi, seg.hi), (k0 + n) * XKT), seg.all_lo,
+                               seg.all_hi))
+          l = __int_as_float(0x7FFFFFFF);                // the row sees one of the values taken out
+      }
+      // -------------------------------------------------------- results
+      if (rows > 0 && !(flags & XST_SKIP)) {
+        const bool whole = flags & XST_WHOLE;
+        const size_t at_row = (size_t)(2 * worker + (flags & XST_HEAD ? 1 : 0)) * XTR + t * XROWS + row;
+        if (!whole && live) a.tiles.ml[at_row] = make_float2(m, l);
+        if (whole || n > 0) {
+          const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+          T* dst = static_cast<T*>(a.out) + (long long)(s0 + i) * xa.o.token + (long long)head * xa.o.head;
+#pragma unroll 1
+          for (int c = 0; c < kLatHead; c += 32) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld_32x32b_x32(o_at + c, o);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0u;
+            }
+            if (!live) continue;
+            if (whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack2<T>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                reinterpret_cast<uint4*>(dst + c)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                reinterpret_cast<uint4*>(a.tiles.o + at_row * kLatHead + c)[k] =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+    }
+  } else {
+    reg_dec<kXOtherRegs>();
+    if (warp == 8) {
+      // ====================================================== MMA issue
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = make_idesc(FMT, FMT, 0, 0, XROWS, XKT);
+        constexpr uint32_t idesc_pv = make_idesc(FMT, FMT, 0, 1, XROWS, kLatHead);
+        const uint32_t q0 = smem_u32(sm + LY::Q), ring = smem_u32(sm + LY::RING);
+        uint32_t nq[2] = {0, 0}, steps[2] = {0, 0};
+        int done = 0;
+        bool ok = true;
+        auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
+        auto wait_blocks = [&](int b, int n) -> bool {
+          for (int k = b; k < b + n; ++k)
+            if (!mbar_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
+          return true;
+        };
+        auto release = [&](int b, int n) {
+          for (int k = b; k < b + n; ++k) mma_commit(&free_[k & (XRING - 1)]);
+        };
+        auto qk = [&](int t, int g) {
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c)
+            mma4_f16_ss(tmem + TM_S + 128 * t, make_sdesc_sw128(q0 + t * LY::QT + c * (XROWS * 128), 16, 1024),
+                        make_sdesc_sw128(block(5 * g + c), 16, 1024), idesc_qk, c);
+        };
+        auto pv = [&](int t, int g, uint32_t accumulate) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half)
+            mma4_f16_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * half,
+                        make_sdesc_sw128(block(5 * g + 3 + half), XBLK / 2, 1024), idesc_pv, accumulate | half);
+        };
+        for (int sg = 0; ok; ++sg) {
+          if (!mbar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+          const volatile XStretch& seg = *seg_at(sg);
+          if (!(seg.flags & XST_SOME)) break;
+          const int n = seg.k1 - seg.k0;
+          const int last = seg.n - seg.tile * XTR > XROWS ? 1 : 0;   // the second query tile has rows
+          if (n > 0) {
+            ok = wait_blocks(5 * done, 3);
+            for (int t = 0; t <= last && ok; ++t) {
+              ok = mbar_wait(&q_full[t], nq[t]++ & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              qk(t, done);
+              mma_commit(&s_full[t]);
+            }
+            if (!ok) break;
+            release(5 * done, 3);
+          }
+#pragma unroll 1
+          for (int j = 0; j < n && ok; ++j) {
+            const int g = done + j;
+            ok = mbar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
+#pragma unroll 1
+            for (int t = 0; t <= last && ok; ++t) {
+              ok = mbar_wait(&p_full[t], steps[t] & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              pv(t, g, j > 0);
+              mma_commit(&o_done[t]);
+              if (t == last) release(5 * g + 3, 2);
+              if (j + 1 < n) {
+                ok = (t > 0 || wait_blocks(5 * (g + 1), 3)) && mbar_wait(&o_done[t], steps[t] & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                qk(t, g + 1);
+                mma_commit(&s_full[t]);
+                if (t == last) release(5 * (g + 1), 3);
+              }
+              ++steps[t];
+            }
+          }
+          if (!ok) break;
+          done += n;
+          mbar_arrive(&seg_free[sg & 1]);
+        }
+        // every MMA issued so far is done before the block releases its tensor memory
+        mma_commit(drain);
+        mbar_wait(drain, 0, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ====================================================== the line of work
+      PieceRec rec = {};
+      int done = 0, sg = 0, armed = 0;                   // tiles, stretches; blocks armed
+      bool ok = true;
+      for (bool more = u < end; ok; ++sg) {
+        if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+        int k0 = 0, k1 = 0, key0 = 0;
+        long long item_end = 0;
+        bool skip = false;
+        if (more) {
+          item_end = pl.at + pl.units;
+          const int n = pl.t.t1 - pl.t.t0;
+          k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - 2));
+          k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - 2));
+          key0 = a.pb.table[pl.b];
+          skip = key0 < 0 || (long long)key0 + pl.s.len > xa.n_keys;
+          if (skip) {
+            if (lane == 0) atomicOr(&a.pv.state[PST_ERR], DEVERR_SEQ);
+            k1 = k0;
+          }
+        }
+        if (lane == 0) {
+          volatile XStretch& seg = *seg_at(sg);
+          if (more) {
+            const bool head = u == pl.at;
+            const int i0 = pl.tile * XTR, i1 = min(pl.s.n - 1, pl.tile * XTR + XTR - 1);
+            seg.s0 = pl.s.s0;
+            seg.n = pl.s.n;
+            seg.len = pl.s.len;
+            seg.lo = pl.t.lo;
+            seg.hi = pl.t.hi;
+            seg.all_hi = a.causal ? pl.s.len - pl.s.n + i0 + 1 : pl.s.len;
+            seg.all_lo = a.window > 0 ? pl.s.len - pl.s.n + i1 - a.window + 1 : 0;
+            seg.k0 = k0;
+            seg.k1 = k1;
+            seg.tile = pl.tile;
+            seg.h = pl.h;
+            seg.key0 = key0;
+            seg.flags = XST_SOME | (skip ? XST_SKIP : 0) | (head ? XST_HEAD : 0) | (head && end >= item_end ? XST_WHOLE : 0);
+          } else {
+            seg.flags = 0;
+          }
+          mbar_arrive(&seg_full[sg & 1]);
+        }
+        __syncwarp();
+        if (!more) break;
+        for (int k = k0; k < k1 && ok; ++k) {
+          const int b0 = 5 * (done + k - k0), at = key0 + k * XKT;
+          for (int c = 0; c < 5; ++c) {
+            const int b = b0 + c, slot = b & (XRING - 1);
+            if (b >= XRING && !warp_wait(&free_[slot], ((b - XRING) / XRING) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              uint8_t* dst = sm + LY::RING + slot * XBLK;
+              mbar_arrive_expect_tx(&full[slot], XBLK);
+              if (c < 2) tma_load_3d(dst, &tmK, &full[slot], 64 * c, at, pl.h);
+              else if (c == 2) tma_load_2d(dst, &tmR, &full[slot], 0, at);
+              else
+                for (int d = 0; d < 2; ++d)
+                  tma_load_3d(dst + d * (XBLK / 2), &tmV, &full[slot], 64 * d, at + 64 * (c - 3), pl.h);
+            }
+            __syncwarp();
+            armed = b + 1;
+          }
+        }
+        if (!ok) break;
+        done += k1 - k0;
+        if (u == pl.at && end < item_end && !skip)
+          rec = {min(pl.s.n - pl.tile * XTR, XTR), (int)quotient(item_end - 1, stretch), pl.h, pl.s.s0, pl.tile * XTR};
+        u = min(end, item_end);
+        more = u < end && next_place<SH, XTR, XKT>(a, pl, cut.pad);
+      }
+      if (lane == 0) a.tiles.rec[worker] = rec;
+      // after an abort: copies still in flight land in this block's shared memory
+      if (*abort_flag)
+        for (int b = max(0, armed - XRING); b < armed; ++b)
+          mbar_wait(&full[b & (XRING - 1)], (b / XRING) & 1, nullptr, 100000000ull);
+    } else if (warp >= 12) {
+      // ====================================================== values
+      const int ct = tid - 12 * 32;
+      int done = 0;
+      bool ok = true;
+      for (int sg = 0; ok; ++sg) {
+        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile XStretch& seg = *seg_at(sg);
+        if (!(seg.flags & XST_SOME)) break;
+        const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi, all_lo = seg.all_lo, all_hi = seg.all_hi;
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int g = done + j, t0 = (k0 + j) * XKT;
+#pragma unroll 1
+          for (int half = 0; half < 2 && ok; ++half) {
+            const int b = 5 * g + 3 + half, slot = b & (XRING - 1);
+            ok = warp_wait(&full[slot], (b / XRING) & 1, abort_flag);
+            if (!ok) break;
+            if (t0 + XKT <= all_hi && t0 >= all_lo) continue;
+            uint8_t* blk = sm + LY::RING + slot * XBLK;
+            bool odd = false;
+#pragma unroll 4
+            for (int c = ct; c < XBLK / 16; c += 128) {   // 16-byte pieces: [2][64 keys][8]
+              const int key = t0 + 64 * half + (c >> 3 & 63);
+              uint4* at = reinterpret_cast<uint4*>(blk) + c;
+              uint4 w = *at;
+              if (key >= hi || key < lo) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (drop_nonfinite<T>(w.x) | drop_nonfinite<T>(w.y) | drop_nonfinite<T>(w.z) | drop_nonfinite<T>(w.w)) {
+                *at = w;
+                odd = true;
+              }
+            }
+            if (odd) *odd_seen = 1;
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_clean[g & 1]);
+        }
+        done += n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+template <typename T>
+static cudaError_t prepare_t() {
+  // reg_inc draws on the registers that the block was launched with: fewer
+  // would make it wait for ever
+  cudaFuncAttributes fa;
+  const cudaError_t e = cudaFuncGetAttributes(&fa, latent_expanded_kernel<T>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * XTHREADS < 32 * 8 * (kXSoftmaxRegs + kXOtherRegs)) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(latent_expanded_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, XLayout::ALLOC);
+}
+
+cudaError_t prepare_latent_expanded() {
+  const cudaError_t e = prepare_t<__half>();
+  return e == cudaSuccess ? prepare_t<__nv_bfloat16>() : e;
+}
+
+template <typename T>
+static cudaError_t expanded_t(const ExpandedAttn& xa, const CUtensorMap& tmK, const CUtensorMap& tmR,
+                              const CUtensorMap& tmV, int blocks, cudaStream_t st) {
+  return launch_pdl(latent_expanded_kernel<T>, dim3(blocks), dim3(XTHREADS), XLayout::ALLOC, st, tmK, tmR, tmV, xa);
+}
+
+cudaError_t launch_latent_expanded(const ExpandedAttn& xa, const CUtensorMap& tmK, const CUtensorMap& tmR,
+                                   const CUtensorMap& tmV, bool f16, int sms, cudaStream_t st) {
+  const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
+  const cudaError_t e = f16 ? expanded_t<__half>(xa, tmK, tmR, tmV, blocks, st)
+                            : expanded_t<__nv_bfloat16>(xa, tmK, tmR, tmV, blocks, st);
+  return e == cudaSuccess ? launch_latent_join(xa.a, xa.o, XTR, f16, blocks, st) : e;
+}
+
+}  // namespace kvring_dev

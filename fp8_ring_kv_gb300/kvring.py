@@ -56,7 +56,7 @@ EXPORTS = (
     "kvring_paged_workspace_bytes", "kvring_paged_create", "kvring_paged_append", "kvring_paged_attend",
     "kvring_paged_destroy", "kvring_paged_layout", "kvring_paged_debug_state",
     "kvring_latent_workspace_bytes", "kvring_latent_create", "kvring_latent_append", "kvring_latent_read",
-    "kvring_latent_attend", "kvring_latent_destroy", "kvring_latent_layout", "kvring_latent_debug_state",
+    "kvring_latent_attend", "kvring_latent_attend_expanded", "kvring_latent_destroy", "kvring_latent_layout", "kvring_latent_debug_state",
 )
 
 
@@ -160,6 +160,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvring_latent_read": (ctypes.c_int, [vp, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, vp]),
         "kvring_latent_attend": (ctypes.c_int, [vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, i64, i32,
                                                 i32, i32, ctypes.c_float, vp, i64, i64, vp]),
+        "kvring_latent_attend_expanded": (ctypes.c_int, [vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, vp,
+                                                         vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, i64, i64, vp]),
         "kvring_latent_destroy": (ctypes.c_int, [vp]),
         "kvring_latent_layout": (ctypes.c_int, [vp] + [ctypes.POINTER(vp)] * 3),
         "kvring_latent_debug_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i32)]),

@@ -91,7 +91,8 @@ class LatentKV:
             check(lib.kvring_latent_create(ctypes.byref(self.cfg), workspace.data_ptr(), workspace.numel(),
                                            self._stream(stream), ctypes.byref(h)), "kvring_latent_create")
         self.handle = h
-        self._append, self._read, self._attend = lib.kvring_latent_append, lib.kvring_latent_read, lib.kvring_latent_attend
+        self._append, self._read = lib.kvring_latent_append, lib.kvring_latent_read
+        self._attend, self._expanded = lib.kvring_latent_attend, lib.kvring_latent_attend_expanded
         ptrs = [ctypes.c_void_p() for _ in range(3)]
         check(lib.kvring_latent_layout(h, *[ctypes.byref(p) for p in ptrs]), "kvring_latent_layout")
         kc, ks, _ = [p.value - workspace.data_ptr() for p in ptrs]
@@ -165,7 +166,7 @@ class LatentKV:
 
     def _seqs(self, n_seqs, seq_start, kv_len):
         if n_seqs > _k.KVRING_PAGED_MAX_SEQS:
-            raise KVRingError(f"page_table: {n_seqs} sequences; a call takes at most {_k.KVRING_PAGED_MAX_SEQS}")
+            raise KVRingError(f"{n_seqs} sequences; a call takes at most {_k.KVRING_PAGED_MAX_SEQS}")
         return self._ints(seq_start, (n_seqs + 1,), "seq_start"), self._ints(kv_len, (n_seqs,), "kv_len"), n_seqs
 
     def _call(self, fn, *args):
@@ -254,6 +255,41 @@ class LatentKV:
             self._call(self._attend, layer, q_latent.data_ptr(), qt, qh, q_rope.data_ptr(), rt, rh, p, start, length,
                        n_seqs, n, n if max_new is None else max_new, *table, *mask, out.data_ptr(), ot, oh,
                        self._stream(stream))
+        return out
+
+    def attend_expanded(self, q, k, k_rope, v, q_pos, seq_start, kv_start, kv_len, out=None, causal=True, window=None,
+                        scale=None, max_new=None, stream=None):
+        """Attention of the new tokens' queries over keys and values that the
+        caller made from the rows (``read``); [N, q_heads, 128].
+
+        q: [N, q_heads, 192], its last 64 rotated here at q_pos.  k, v: [T,
+        q_heads, 128].  k_rope: [T, 64], rotated already, as ``read`` gives it.
+        Sequence b's keys are rows kv_start[b] .. kv_start[b] + kv_len[b] - 1, in
+        order; kv_len counts its new tokens' own.  scale: 1 / sqrt(192) unless
+        given; causal, window and max_new as in ``attend``.  q, k, v and out
+        have token and head strides of their own."""
+        if self.handle is None:
+            raise KVRingError("the cache is closed")
+        n, t = q.shape[0], k.shape[0]
+        if t > 1 << 30:
+            raise KVRingError(f"k: {t} rows; at most 2^30 are read")
+        qt, qh = self._heads(q, n, HEAD + ROPE, "q")
+        kt, kh = self._heads(k, t, HEAD, "k")
+        vt, vh = self._heads(v, t, HEAD, "v")
+        rt = self._rows(k_rope, t, ROPE, "k_rope")
+        if kv_len.dim() != 1:
+            raise KVRingError(_bad_ints(kv_len, (None,), self._index, "kv_len"))
+        start, length, n_seqs = self._seqs(kv_len.shape[0], seq_start, kv_len)
+        first = self._ints(kv_start, (n_seqs,), "kv_start")
+        p = self._ints(q_pos, (n, self.n_axes), "q_pos")
+        mask = self._mask(causal, window, 1.0 if scale is None else scale, max_new, n)
+        if out is None:
+            out = self._out((n, self.q_heads, HEAD), stream)
+        ot, oh = self._heads(out, n, HEAD, "out")
+        if n and n_seqs:
+            self._call(self._expanded, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, k_rope.data_ptr(), rt, v.data_ptr(), vt,
+                       vh, t, p, start, first, length, n_seqs, n, n if max_new is None else max_new, mask[0], mask[1],
+                       scale or 0.0, out.data_ptr(), ot, oh, self._stream(stream))
         return out
 
     def debug_state(self, stream=None):

@@ -123,6 +123,30 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
                          int32_t table_width, int32_t causal, int32_t window, float scale, void* out,
                          int64_t out_token, int64_t out_head, kvring_stream stream);
 
+/*
+ * Attention in the expanded form (latent_expanded): every head has a key part and
+ * a value of its own, made by the caller from the rows.
+ *   q        device [N][q_heads][128 + 64], the last 64 rotated here at q_pos
+ *   k, v     device [n_keys][q_heads][128]
+ *   k_rope   device [n_keys][64], rows k_rope_stride elements apart; rotated
+ *            already (as kvring_latent_read gives it)
+ *   kv_start device int32 [B]: sequence b's keys are rows kv_start[b] ..
+ *            kv_start[b] + kv_len[b] - 1; new token i of n has index kv_len - n + i
+ *   out      device [N][q_heads][128]
+ *   scale    0: 1 / sqrt(192)
+ *   causal, window, max_new   as kvring_paged_attend's
+ * Rotated queries and weights are rounded to the inputs' type once; sums and
+ * statistics are fp32.  A value that is no number spreads to the rows that see
+ * it, in its channel or in all of the head's, and to no other.
+ * A sequence whose keys do not lie in 0 .. n_keys - 1 is left out and flagged.
+ */
+int kvring_latent_attend_expanded(kvring_latent* p, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                                  int64_t k_token, int64_t k_head, const void* k_rope, int64_t k_rope_token,
+                                  const void* v, int64_t v_token, int64_t v_head, int32_t n_keys, const int32_t* q_pos,
+                                  const int32_t* seq_start, const int32_t* kv_start, const int32_t* kv_len,
+                                  int32_t n_seqs, int32_t n_tokens, int32_t max_new, int32_t causal, int32_t window,
+                                  float scale, void* out, int64_t out_token, int64_t out_head, kvring_stream stream);
+
 /* Free the host handle (the workspace stays the caller's). NULL is allowed. */
 int kvring_latent_destroy(kvring_latent* p);
 
