@@ -32,8 +32,8 @@ namespace kvring_dev {
 constexpr int LKT = 128;                     // keys of a tile
 constexpr int LTHREADS = 320;
 constexpr int LFIX = 2;                      // what an item costs beside its tiles, in tiles
-constexpr float kLatTop = 7.807354922f;      // log2 224: weights start at 224 ...
-constexpr float kLatRaise = 1.0f;            // ... and may reach 448, e4m3's largest, before the maximum is raised
+constexpr float kLatTop = 4.807354922f;      // log2 28: a column's weights start at 28 ...
+constexpr float kLatRaise = 4.0f;            // ... and may reach 448, e4m3's largest, before its maximum is raised
 constexpr float kNoMax = -1e30f;             // no key yet
 
 struct LatStretch {
@@ -48,25 +48,27 @@ struct LatLayout {
   static constexpr int CB = LKT * 128, RB = LKT * kLatRope;      // a chunk of 128 channels, the rotated part
   static constexpr int STAGE = 4 * CB + RB;
   static constexpr int QC = NP * R * 128;                        // a chunk of the queries, all parts
-  static constexpr int PB = LKT * R;                             // a part of the weights
-  static constexpr int PIN = RB / PB < NP ? RB / PB : NP;        // parts that lie where the rotated part was
   static constexpr int K = 0;                                    // [2 stages]
-  static constexpr int Q = K + 2 * STAGE;
-  static constexpr int P = Q + 4 * QC + NP * R * kLatRope;       // the other parts
-  static constexpr int TOP = P + (NP - PIN) * PB;                // [2][4][HC] column maxima, sums
+  static constexpr int Q = K + 2 * STAGE;                        // (then the outputs on their way)
+  // Weights: 64 bytes a key where the rotated part was (QK is done with it): 64
+  // columns' first part, or 32 columns' first and second.  The next part:
+  static constexpr int P = Q + 4 * QC + NP * R * kLatRope;
+  static constexpr int PB = R == 64 ? LKT * 64 : NP == 3 ? LKT * 32 : 0;
+  static constexpr int TOP = P + PB;                             // [2][4][HC] column maxima, sums
   static constexpr int MINE = TOP + 8 * HC * 4;                  // [8 warps][HC] reference - kLatTop; 1 / l
   static constexpr int FAC = MINE + 8 * HC * 4;                  // [R] logit factors
   static constexpr int HI = FAC + R * 4;                         // [R] keys below are seen
   static constexpr int FLAG = HI + R * 4;                        // [2][8]
   static constexpr int SEG = FLAG + 64;                          // [2]
   static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
-  static constexpr int NBAR = 10 + 10 + 2 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 4 + 4 + 2 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(ALLOC <= 232448, "shared memory of a block");
   static_assert(2 * STAGE >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the stages at first");
-  static_assert(2 * NP * R + 4 * R <= 512, "tensor memory");
+  static_assert(4 * NP * R <= 512, "tensor memory: two buffers of S below column 256, four accumulators of 64 columns");
   static_assert(8 * HC * 4 >= 8 * (LTHREADS / 32), "the prefix sums' warps lie in TOP and MINE at first");
+  static_assert(R == 64 ? NP == 2 : R == 32, "weights' room");
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -100,7 +102,21 @@ __device__ __forceinline__ float warp_maxf(float v) {
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
   if constexpr (N == 32) tmem_ld_32x32b_x32(at, r);
-  else tmem_ld_32x32b_x16(at, r);
+  else if constexpr (N == 16) tmem_ld_32x32b_x16(at, r);
+  else tmem_ld_32x32b_x8(at, r);
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Ask for a stretch of memory to be brought to the L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // a warp waits with one answer; what it has to write for the others is written
@@ -116,20 +132,20 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   using LY = LatLayout<T, R>;
   constexpr int NP = LY::NP, HC = LY::HC;
   using SH = Share<R, LKT, LFIX, 0, 0x7FFFFFFF>;
-  constexpr uint32_t TM_O = 2 * NP * R;
+  constexpr uint32_t TM_O = 256;           // four accumulators of 64 columns
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = la.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
-  uint64_t* full = bars;                   // [2][5] codes landed: four chunks, the rotated part
-  uint64_t* free_ = full + 10;             // [2][5] and every MMA is done with them
-  uint64_t* s_full = free_ + 10;           // [2] QK done
+  uint64_t* full = bars;                   // [2 stages][2 halves] codes landed: chunks 0 and 1; the others, the rotated part
+  uint64_t* free_ = full + 4;              // [2][2] and every MMA is done with them (the second: PV is done)
+  uint64_t* s_full = free_ + 4;            // [2] QK done
   uint64_t* p_full = s_full + 2;           // P stored
-  uint64_t* o_done = p_full + 1;           // PV done
-  uint64_t* q_full = o_done + 1;           // queries written (once per stretch)
-  uint64_t* seg_full = q_full + 1;         // [2] stretch written
+  uint64_t* q_full = p_full + 1;           // queries written (once per stretch)
+  uint64_t* q_free = q_full + 1;           // their room is free: the outputs before have left it
+  uint64_t* seg_full = q_free + 1;         // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2]
   uint64_t* flags_in = seg_free + 2;       // [2 halves] the warps' flags written
-  uint64_t* tops_in = flags_in + 2;        // [2 halves] their maxima, or sums
+  uint64_t* tops_in = flags_in + 2;        // [2 halves] their maxima, or sums, or outputs
   uint64_t* drain = tops_in + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
@@ -138,7 +154,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::TOP);           // at first
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::MINE);
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&free_[i], 1);
     }
@@ -152,8 +168,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     }
     item_sums[2] = 0;
     mbar_init(p_full, 8);
-    mbar_init(o_done, 1);
     mbar_init(q_full, 8);
+    mbar_init(q_free, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -193,17 +209,21 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     float* mine = reinterpret_cast<float*>(sm + LY::MINE) + warp * HC;
     float* fac = reinterpret_cast<float*>(sm + LY::FAC);
     int* his = reinterpret_cast<int*>(sm + LY::HI);
-    volatile int* flag = reinterpret_cast<volatile int*>(sm + LY::FLAG);
+    volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(sm + LY::FLAG);
     const int key_row = 32 * quad + lane;
     uint32_t n_tops = 0, n_q = 0;          // phases of tops_in and q_full so far
     int done = 0;
     bool ok = true;
     // every warp of the half puts HC numbers (lane c the one of column c) into tops
-    auto share = [&](float v) -> bool {
-      if (lane < HC) tops[quad * HC + lane] = v;
+    auto meet = [&]() -> bool {
       warp_arrive(&tops_in[half]);
       return warp_wait(&tops_in[half], n_tops++ & 1, abort_flag);
     };
+    auto share = [&](float v) -> bool {
+      if (lane < HC) tops[quad * HC + lane] = v;
+      return meet();
+    };
+    auto pv_done = [&](int g) -> bool { return warp_wait(&free_[(g & 1) * 2 + 1], (g >> 1) & 1, abort_flag); };
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile LatStretch& seg = segs[sg & 1];
@@ -220,10 +240,24 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         // ------------------------------------------------------ queries
         constexpr int RW = R / 8;          // rows of a warp
         const int w0 = warp * RW;
-        if (tid < R) {
-          // rows past the last: as the last one, with a factor of 0
-          const int i = (r0 + min(tid, rows - 1)) / G;
-          his[tid] = a.causal ? len_n + i + 1 : seg.len;
+        const bool mine16 = lane * 16 < C; // lane l: latent numbers 16 l .. 16 l + 15 of every row
+        uint4 w[RW][2];
+        {
+          int i = (r0 + w0) / G, h = r0 + w0 - i * G;
+#pragma unroll
+          for (int k = 0; k < RW; ++k) {
+            w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+            if (w0 + k < rows && mine16) {
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + i) * la.q.token +
+                                                                h * la.q.head) + 2 * lane;
+              w[k][0] = src[0];
+              w[k][1] = src[1];
+            }
+            if (++h >= G) {
+              h = 0;
+              ++i;
+            }
+          }
         }
         // the rotated parts of all of them: four lanes a row, 16 numbers each
         float y[16];
@@ -256,6 +290,15 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           ytop = max(ytop, __shfl_xor_sync(0xFFFFFFFFu, ytop, 1));
           ytop = max(ytop, __shfl_xor_sync(0xFFFFFFFFu, ytop, 2));
         }
+        // the outputs before have left the room
+        bulk_wait_read();
+        warp_arrive(q_free);
+        if (!warp_wait(q_free, n_q & 1, abort_flag)) break;
+        if (tid < R) {
+          // rows past the last: as the last one, with a factor of 0
+          const int i = (r0 + min(tid, rows - 1)) / G;
+          his[tid] = a.causal ? len_n + i + 1 : seg.len;
+        }
         // x * inv in parts: 16 codes of each to ``at`` + part * ``step``
         auto put = [&](const float* x, float inv, uint8_t* at, int step) {
           uint32_t v[8];
@@ -263,61 +306,43 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           for (int e = 0; e < 8; ++e) v[e] = cvt_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            uint32_t w[4];
+            uint32_t c[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t c0 = split2(v[2 * e]), c1 = split2(v[2 * e + 1]);
-              w[e] = c0 | c1 << 16;
+              c[e] = c0 | c1 << 16;
             }
-            *reinterpret_cast<uint4*>(at + p * step) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(at + p * step) = make_uint4(c[0], c[1], c[2], c[3]);
           }
         };
         float yinv = 0.0f;
-        constexpr int BATCH = 4;
-#pragma unroll 1
-        for (int b0 = 0; b0 < RW; b0 += BATCH) {
-          uint4 w[BATCH][2];
+        uint8_t* qat = sm + LY::Q + (lane >> 3) * LY::QC + w0 * 128;
 #pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = w0 + b0 + k;
+        for (int k = 0; k < RW; ++k) {
+          const int r = w0 + k;
+          const uint32_t mb = __vmaxu2(max8_bits(w[k][0]), max8_bits(w[k][1]));
+          uint32_t top = max(mb & 0xFFFFu, mb >> 16);
+          if constexpr (std::is_same_v<T, __half>) top = __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
+          else top <<= 16;
+          top = max(__reduce_max_sync(0xFFFFFFFFu, top), __shfl_sync(0xFFFFFFFFu, ytop, 4 * k));
+          float scale, inv;
+          pow2_scale(__uint_as_float(top), scale, inv);
+          if (top >= 0x7F800000u) {        // no numbers: the row's scores are NaN by its factor
+            scale = __int_as_float(0x7FC00000);
+            inv = 0.0f;
             w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
-            if (r < rows && lane * 16 < C) {
-              const int i = (r0 + r) / G, h = r0 + r - i * G;
-              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s0 + i) * la.q.token +
-                                                                h * la.q.head) + 2 * lane;
-              w[k][0] = src[0];
-              w[k][1] = src[1];
+            if ((lane >> 2) == k) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = 0.0f;
             }
           }
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = w0 + b0 + k;
+          if ((lane >> 2) == k) yinv = inv;
+          if (lane == k) fac[r] = r < rows ? a.scale_log2 * scale : 0.0f;
+          if (mine16) {
             float x[16];
             load8_f32<T>(w[k][0], x);
             load8_f32<T>(w[k][1], x + 8);
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-            top = max(__reduce_max_sync(0xFFFFFFFFu, top), __shfl_sync(0xFFFFFFFFu, ytop, 4 * (b0 + k)));
-            float scale, inv;
-            pow2_scale(__uint_as_float(top), scale, inv);
-            const bool finite = top < 0x7F800000u;
-            if (!finite) {                 // the row's scores are NaN by its factor
-              scale = __int_as_float(0x7FC00000);
-              inv = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-            }
-            if ((lane >> 2) == b0 + k) {
-              yinv = inv;
-              if (!finite) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-              }
-            }
-            if (lane == 0) fac[r] = r < rows ? a.scale_log2 * scale : 0.0f;
-            if (lane * 16 < C)
-              put(x, inv, sm + LY::Q + (lane >> 3) * LY::QC + r * 128 + (((lane & 7) ^ (r & 7)) << 4), R * 128);
+            put(x, inv, qat + k * 128 + (((lane & 7) ^ ((w0 + k) & 7)) << 4), R * 128);
           }
         }
         if ((lane >> 2) < RW) {
@@ -399,19 +424,29 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           float most = x[0];
 #pragma unroll
           for (int c = 1; c < HC; ++c) most = fmaxf(most, x[c]);
-          const bool up = __any_sync(0xFFFFFFFFu, most > kLatTop + kLatRaise);
-          volatile int* fl = flag + (g & 1) * 8 + half * 4;
-          if (lane == 0) fl[quad] = up;
+          uint32_t ups = 0;                // columns whose maximum this warp's keys raise
+          if (__any_sync(0xFFFFFFFFu, most > kLatTop + kLatRaise)) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatTop + kLatRaise ? 1u << c : 0u;
+            ups = __reduce_or_sync(0xFFFFFFFFu, ups);
+          }
+          volatile uint32_t* fl = flag + (g & 1) * 8 + half * 4;
+          if (lane == 0) fl[quad] = ups;
           warp_arrive(&flags_in[half]);
           if (!warp_wait(&flags_in[half], g & 1, abort_flag)) {
             ok = false;
             break;
           }
-          if (fl[0] | fl[1] | fl[2] | fl[3]) {
-            // a column's maximum is raised: what was summed is brought to the new one
-            scores();
-            logits(true);
+          ups = fl[0] | fl[1] | fl[2] | fl[3];
+          if (ups) {
+            // What was summed is brought to the new maximum.  Columns without a key
+            // so far (all of them in a stretch's first tile) take it as it is.
+            const bool fresh = __any_sync(0xFFFFFFFFu, lane < HC && (ups >> lane & 1) && mine[lane] == kNoMax);
             float top = -INFINITY;
+            if (fresh) {
+              scores();
+              logits(true);
+            }
 #pragma unroll
             for (int c = 0; c < HC; ++c) {
               const float v = warp_maxf(x[c]);
@@ -421,41 +456,46 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               ok = false;
               break;
             }
-            float al = 1.0f;
-            if (lane < HC) {
+            float al = 1.0f, shift = 0.0f;
+            if (lane < HC && (ups >> lane & 1)) {
               top = fmaxf(fmaxf(tops[lane], tops[HC + lane]), fmaxf(tops[2 * HC + lane], tops[3 * HC + lane])) - kLatTop;
               const float was = mine[lane];
-              if (top > was + kLatRaise) {
-                mine[lane] = top;
-                al = ex2f(was - top);      // 0 for the column's first keys
-              }
+              shift = fresh ? top - was : top;
+              mine[lane] = fresh ? top : was + top;
+              al = ex2f(-shift);           // 0 for the column's first keys
             }
             __syncwarp();
-            if (j > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) {
-              if (!warp_wait(o_done, (g - 1) & 1, abort_flag)) {
+            if (fresh) {
+              scores();
+              logits(false);
+            } else {
+#pragma unroll
+              for (int c = 0; c < HC; ++c) x[c] -= __shfl_sync(0xFFFFFFFFu, shift, c);
+            }
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < HC; ++c) l[c] *= __shfl_sync(0xFFFFFFFFu, al, c);
+              if (!pv_done(g - 1)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < HC; ++c) l[c] *= __shfl_sync(0xFFFFFFFFu, al, c);
 #pragma unroll 1
-              for (int q = 0; q < NC; ++q) {
+              for (uint32_t left = ups; left; left &= left - 1) {
+                const int c = __ffs(left) - 1;
+                const float f = __shfl_sync(0xFFFFFFFFu, al, c);
 #pragma unroll
-                for (int c0 = 0; c0 < HC; c0 += 16) {
-                  uint32_t o[16];
-                  const uint32_t at = tmem + lanes + TM_O + q * R + half * HC + c0;
-                  tmem_ld_32x32b_x16(at, o);
+                for (int part = 0; part < 64 / R; ++part) {
+                  const uint32_t at = tmem + lanes + TM_O + part * R + half * HC + c;
+                  uint32_t o[4];
+                  tmem_ld4_32x32b_x1(at, at + (NC > 1 ? 64 : 0), at + (NC > 2 ? 128 : 0), at + (NC > 3 ? 192 : 0), o);
 #pragma unroll
-                  for (int c = 0; c < 16; ++c)
-                    o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xFFFFFFFFu, al, c0 + c));
-                  tmem_st_32x32b_x16(at, o);
+                  for (int q = 0; q < 4; ++q)
+                    if (q < NC) tmem_st_32x32b_x1(at + q * 64, __float_as_uint(__uint_as_float(o[q]) * f));
                 }
               }
               tmem_st_wait();
             }
-            scores();
-            logits(false);
           }
           // weights, their sums, and their parts
 #pragma unroll
@@ -470,26 +510,29 @@ __global__ void __launch_bounds__(LTHREADS, 1)
 #pragma unroll
           for (int c = 0; c < HC / 2; ++c) v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
           // PV of the tile before is done with the weights' room
-          if (g > 0 && !warp_wait(o_done, (g - 1) & 1, abort_flag)) {
+          if (g > 0 && !pv_done(g - 1)) {
             ok = false;
             break;
           }
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            uint8_t* room = p < LY::PIN ? sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + p * LY::PB
-                                        : sm + LY::P + (p - LY::PIN) * LY::PB;
             uint32_t w[HC / 4];
 #pragma unroll
             for (int c = 0; c < HC / 4; ++c) {
               const uint32_t c0 = split2(v[2 * c]), c1 = split2(v[2 * c + 1]);
               w[c] = c0 | c1 << 16;
             }
+            uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
 #pragma unroll
             for (int k = 0; k < HC / 16; ++k) {
-              const int unit = half * (HC / 16) + k;
-              const int at = R == 64 ? key_row * 64 + ((unit ^ ((key_row >> 1) & 3)) << 4)
-                                     : key_row * 32 + ((unit ^ ((key_row >> 2) & 1)) << 4);
-              *reinterpret_cast<uint4*>(room + at) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              uint8_t* at;
+              if (R == 64) {
+                at = (p == 0 ? in_stage : sm + LY::P + key_row * 64) + (((2 * half + k) ^ ((key_row >> 1) & 3)) << 4);
+              } else {
+                at = p < 2 ? in_stage + (((2 * p + half) ^ ((key_row >> 1) & 3)) << 4)
+                           : sm + LY::P + key_row * 32 + ((half ^ ((key_row >> 2) & 1)) << 4);
+              }
+              *reinterpret_cast<uint4*>(at) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
           }
           fence_proxy_async_smem();
@@ -501,7 +544,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       done += n;
       // -------------------------------------------------------- results
       if (n > 0) {
-        if (!warp_wait(o_done, (done - 1) & 1, abort_flag)) break;
+        if (!pv_done(done - 1)) break;
         tc_fence_after();
       }
       // the columns' sums: lane c that of column c
@@ -529,49 +572,78 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         mine[lane] = sum != 0.0f ? 1.0f / sum : 0.0f;
       }
       __syncwarp();
-      if (whole || n > 0) {
-        const int live = min(HC, rows - half * HC);      // columns of this warp
+      const int live = max(0, min(HC, rows - half * HC));   // columns of this warp
+      auto out_row = [&](int c) -> T* {
+        const int r = r0 + half * HC + c, i = r / G;
+        return static_cast<T*>(a.out) + (s0 + i) * la.o.token + (r - i * G) * la.o.head;
+      };
+      if (n > 0) {
+        // A thread has a channel of every row: whole rows by way of the queries'
+        // room, 16-bit ones at once, fp32 pieces in two turns.
+        uint8_t* stage = sm + LY::Q + half * HC * C * 2;
+        constexpr int TC = HC / 2;
 #pragma unroll 1
-        for (int q = 0; q < NC; ++q) {
-          uint32_t o[HC];
-          if (n > 0) {
-            tmem_ld_cols<HC>(tmem + lanes + TM_O + q * R + half * HC, o);
-          } else {
-#pragma unroll
-            for (int c = 0; c < HC; ++c) o[c] = 0u;
+        for (int turn = 0; turn < 2; ++turn) {
+          if (turn > 0 && !whole) {
+            bulk_wait_read();
+            if (!(ok = meet())) break;
           }
-          const int ch = q * 128 + 32 * quad + lane;
-          if (whole) {
-            int i = (r0 + half * HC) / G, h = r0 + half * HC - i * G;
-            T* dst = static_cast<T*>(a.out) + ch;
+#pragma unroll 1
+          for (int q = 0; q < NC; ++q) {
+            const int ch = q * 128 + 32 * quad + lane;
+            const uint32_t at_o = tmem + lanes + TM_O + q * 64 + half * HC + turn * TC;
+            uint32_t o[TC];
+            tmem_ld_cols<TC>(at_o, o);
+            if constexpr (R == 32) {
+              uint32_t o1[TC];
+              tmem_ld_cols<TC>(at_o + R, o1);
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-              if (c < live) {
-                const float v = __uint_as_float(o[c]) * mine[c];
-                T r;
-                if constexpr (std::is_same_v<T, __half>) r = __float2half_rn(v);
-                else r = __float2bfloat16_rn(v);
-                dst[(s0 + i) * la.o.token + h * la.o.head] = r;
-              }
-              if (++h >= G) {
-                h = 0;
-                ++i;
-              }
+              for (int c = 0; c < TC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(o1[c]));
             }
-          } else {
+            if (whole) {
+              T* at = reinterpret_cast<T*>(stage) + turn * TC * C + ch;
+              const float* f = mine + turn * TC;
 #pragma unroll
-            for (int c = 0; c < HC; ++c)
-              if (c < live) a.tiles.o[(at_row + c) * C + ch] = __uint_as_float(o[c]);
+              for (int c = 0; c < TC; c += 2) {
+                const uint32_t two = pack2<T>(__uint_as_float(o[c]) * f[c], __uint_as_float(o[c + 1]) * f[c + 1]);
+                *reinterpret_cast<uint16_t*>(at + c * C) = (uint16_t)two;
+                *reinterpret_cast<uint16_t*>(at + (c + 1) * C) = (uint16_t)(two >> 16);
+              }
+            } else {
+              uint32_t* at = reinterpret_cast<uint32_t*>(stage) + ch;
+#pragma unroll
+              for (int c = 0; c < TC; ++c) at[c * C] = o[c];
+            }
           }
+          if (whole && turn == 0) continue;
+          fence_proxy_async_smem();
+          if (!(ok = meet())) break;       // the half's four warps have written
+          if (whole) {
+            const int c = quad * (HC / 4) + lane;
+            if (lane < HC / 4 && c < live) bulk_store(out_row(c), stage + c * C * 2, C * 2);
+          } else {
+            const int c = quad * (TC / 4), m = min(TC / 4, live - turn * TC - c);   // the warp's rows, side by side
+            if (lane == 0 && m > 0)
+              bulk_store(a.tiles.o + (at_row + turn * TC + c) * C, stage + c * C * 4, m * C * 4);
+          }
+          bulk_commit();
         }
+        if (!ok) break;
+      } else if (whole) {
+        for (int c = quad; c < live; c += 4)
+          if (lane * 16 < C) {
+            uint4* at = reinterpret_cast<uint4*>(out_row(c)) + 2 * lane;
+            at[0] = at[1] = make_uint4(0, 0, 0, 0);
+          }
       }
       tc_fence_before();
       warp_arrive(&seg_free[sg & 1]);
     }
+    bulk_wait();
   } else if (warp == 8) {
     // ======================================================== MMA issue
     constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
-    constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, R);
+    constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
     const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
     int done = 0;
     uint32_t n_q = 0;
@@ -582,18 +654,37 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       if (!(seg.flags & LST_SOME)) break;
       const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
       if (n > 0 && !warp_wait(q_full, n_q++ & 1, abort_flag)) break;
-#pragma unroll 1
-      for (int j = 0; j <= n && n > 0; ++j) {
-        const int g = done + j, stage = g & 1;
-        if (j < n) {
-          uint64_t* f = full + stage * 5;
+      // QK runs a tile ahead of PV where its codes are there in time; else PV goes first
+      int jq = 0, jp = 0;                  // the next of either
+      unsigned long long t0_ns = 0;
+      while (jp < n) {
+        int next = 0;                      // 1: PV, 2: QK, 0: given up
+        if (lane == 0) {
+          const int gp = done + jp, gq = done + jq;
+          for (uint32_t spins = 1; next == 0; ++spins) {
+            if (jp < jq && mbar_test_wait(p_full, gp & 1)) next = 1;
+            else if (jq < n && jq < jp + 2 && mbar_test_wait(full + (gq & 1) * 2, (gq >> 1) & 1) &&
+                     mbar_test_wait(full + (gq & 1) * 2 + 1, (gq >> 1) & 1)) next = 2;
+            else if ((spins & 63u) == 0) {
+              const unsigned long long now = globaltimer_ns();
+              if (spins == 64) t0_ns = now;
+              if (now - t0_ns > kWaitLimitNs) *abort_flag = 1;
+              if (*abort_flag) break;
+            }
+          }
+        }
+        next = __shfl_sync(0xFFFFFFFFu, next, 0);
+        ok = next != 0;
+        if (!ok) break;
+        if (next == 2) {
+          const int j = jq++, g = done + j, stage = g & 1;
+          uint64_t* f = full + stage * 2;
           const uint32_t par = (g >> 1) & 1;
           const uint32_t kt = k_at + stage * LY::STAGE;
           const int t0 = (k0 + j) * LKT;
           if (t0 < lo || t0 + LKT > hi) {
             // rows that no query sees: their weights are zeros, which must meet numbers
-            for (int c = 0; c < NC && ok; ++c) ok = warp_wait(f + c, par, abort_flag);
-            ok = ok && warp_wait(f + 4, par, abort_flag);
+            ok = warp_wait(f, par, abort_flag) && warp_wait(f + 1, par, abort_flag);
             if (!ok) break;
             uint8_t* tile = sm + LY::K + stage * LY::STAGE;
             for (int r = 0; r < LKT; ++r) {
@@ -606,51 +697,54 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             __syncwarp();
           }
           const uint32_t d = tmem + stage * NP * R;
-          for (int c = 0; c < NC; ++c) {
-            ok = warp_wait(f + c, par, abort_flag);
+          for (int h = 0; h < 2; ++h) {
+            ok = warp_wait(f + h, par, abort_flag);
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-              const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-              const uint64_t bd = make_sdesc_sw128(q_at + c * LY::QC, 16, 1024);
+              for (int c = 2 * h; c < min(NC, 2 * h + 2); ++c) {
+                const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+                const uint64_t bd = make_sdesc_sw128(q_at + c * LY::QC, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, c | k);
+                for (int k = 0; k < 4; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, c | k);
+              }
+              if (h == 1) {
+                const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+                const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, 1);
+                mma_commit(&s_full[stage]);
+              }
             }
             __syncwarp();
           }
-          ok = ok && warp_wait(f + 4, par, abort_flag);
           if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-            const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, 1);
-            mma_commit(&s_full[stage]);
-          }
-          __syncwarp();
-        }
-        if (j > 0) {
-          const int gp = g - 1, sp = gp & 1;
+        } else {
+          const int j = jp++, gp = done + j, sp = gp & 1;
           ok = warp_wait(p_full, gp & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
             const uint32_t kt = k_at + sp * LY::STAGE;
+            const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
             for (int c = 0; c < NC; ++c) {
               const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+              const uint32_t o = tmem + TM_O + 64 * c;
 #pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                const uint32_t room = p < LY::PIN ? kt + 4 * LY::CB + p * LY::PB : p_at + (p - LY::PIN) * LY::PB;
-                const uint64_t bd = R == 64 ? make_sdesc_sw64(room, 16, 512) : sdesc_sw32(room, 256);
+              for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b0 + 128 * k, idesc_pv, (j > 0) | k);
+              if constexpr (R == 64) {
+                const uint64_t b1 = make_sdesc_sw64(p_at, 16, 512);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_f8_ss(tmem + TM_O + c * R, ad + 256 * k, bd + k * (R * 32 / 16), idesc_pv, (j > 1) | p | k);
+                for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b1 + 128 * k, idesc_pv, 1);
+              } else if constexpr (NP == 3) {
+                const uint64_t b2 = sdesc_sw32(p_at, 256);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b2 + 64 * k, idesc_pv3, 1);
               }
-              mma_commit(&free_[sp * 5 + c]);
+              if (c == 1) mma_commit(&free_[sp * 2]);
             }
-            mma_commit(&free_[sp * 5 + 4]);
-            mma_commit(o_done);
+            if (NC == 1) mma_commit(&free_[sp * 2]);
+            mma_commit(&free_[sp * 2 + 1]);
           }
           __syncwarp();
         }
@@ -668,7 +762,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   } else {
     // ======================================================== the line of work
     PieceRec rec = {};
-    const int P = a.pv.P, boxes = LKT / P;
+    const int P = a.pv.P, boxes = LKT / P, W = C + kLatRope;
     const bool alone = (long long)a.max_new * G <= R;    // every key is read by one item only
     const uint64_t once = l2_evict_first();
     int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
@@ -707,6 +801,12 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       }
       __syncwarp();
       if (!more) break;
+      if (k0 < k1)                         // the queries, for when the softmax warps come to them
+        for (int r = lane; r < min(R, pl.s.n * G - pl.tile * R); r += 32) {
+          const int rr = pl.tile * R + r, i = rr / G, h = rr - i * G;
+          l2_prefetch(static_cast<const T*>(a.q) + (pl.s.s0 + i) * la.q.token + h * la.q.head, C * 2);
+          l2_prefetch(static_cast<const T*>(la.q_rope) + (pl.s.s0 + i) * la.qr.token + h * la.qr.head, kLatRope * 2);
+        }
       const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
       // lane i < boxes: the page of its keys of tile k; -1 where no query sees one
       auto page = [&](int k) -> int {
@@ -719,35 +819,48 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         }
         return pg;
       };
-      int pg = page(k0);
+      // the L2 is asked for a tile's codes well before its TMA, whose room is free late
+      auto ahead = [&](int k, int p) {
+        if (p < 0) return;
+        const int key = k * LKT + lane * P, first = max(0, pl.t.lo - key), last = min(P, pl.t.hi - key);
+        l2_prefetch(a.pv.k_codes + (((size_t)p << a.pv.p_shift) + first) * W, (uint32_t)((last - first) * W));
+      };
+      int pg = page(k0), pg1 = page(k0 + 1);
       for (int k = k0; k < k1; ++k) {
         const int g = done + k - k0, stage = g & 1;
-        const int next = page(k + 1);
+        const int pg2 = page(k + 2);
+        ahead(k + 2, pg2);
         const bool on = pg >= 0;
         const uint32_t n_on = __popc(__ballot_sync(0xFFFFFFFFu, on));
         const int y = (int)a.pv.row0 + (pg << a.pv.p_shift);
         uint8_t* tile = sm + LY::K + stage * LY::STAGE;
 #pragma unroll 1
-        for (int c = 0; c <= NC; ++c) {
-          const int slot = c < NC ? c : 4;
-          uint64_t* f = &full[stage * 5 + slot];
-          if (g >= 2 && !warp_wait(&free_[stage * 5 + slot], ((g - 2) >> 1) & 1, abort_flag)) {
+        for (int h = 0; h < 2; ++h) {
+          uint64_t* f = &full[stage * 2 + h];
+          if (g >= 2 && !warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          const int width = c < NC ? 128 : kLatRope;
-          if (lane == 0) mbar_arrive_expect_tx(f, n_on * P * width);
+          const int c1 = min(NC, 2 * h + 2), chunks = max(0, c1 - 2 * h);
+          if (lane == 0) mbar_arrive_expect_tx(f, n_on * P * (chunks * 128 + h * kLatRope));
           __syncwarp();
           if (on) {
-            uint8_t* dst = tile + slot * LY::CB + lane * P * width;
-            const CUtensorMap* tm = c < NC ? &tmC : &tmR;
-            if (alone) tma_load_2d_hint(dst, tm, f, c * 128, y, once);
-            else tma_load_2d(dst, tm, f, c * 128, y);
+            for (int c = 2 * h; c < c1; ++c) {
+              uint8_t* dst = tile + c * LY::CB + lane * P * 128;
+              if (alone) tma_load_2d_hint(dst, &tmC, f, c * 128, y, once);
+              else tma_load_2d(dst, &tmC, f, c * 128, y);
+            }
+            if (h == 1) {
+              uint8_t* dst = tile + 4 * LY::CB + lane * P * kLatRope;
+              if (alone) tma_load_2d_hint(dst, &tmR, f, C, y, once);
+              else tma_load_2d(dst, &tmR, f, C, y);
+            }
           }
-          armed = g * 5 + c + 1;
+          armed = g * 2 + h + 1;
         }
         if (!ok) break;
-        pg = next;
+        pg = pg1;
+        pg1 = pg2;
       }
       done += k1 - k0;
       if (u == pl.at && end < item_end)
@@ -757,12 +870,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     }
     if (lane == 0) a.tiles.rec[worker] = rec;
     // after an abort: copies still in flight land in this block's shared memory
-    if (*abort_flag && armed > 0) {
-      const int g = (armed - 1) / 5;
-      for (int t = max(0, g - 1); t <= g; ++t)
-        for (int c = 0; c <= NC && t * 5 + c < armed; ++c)
-          mbar_wait(&full[(t & 1) * 5 + (c < NC ? c : 4)], (t >> 1) & 1, nullptr, 100000000ull);
-    }
+    if (*abort_flag)
+      for (int b = max(0, armed - 4); b < armed; ++b) mbar_wait(&full[b & 3], (b >> 2) & 1, nullptr, 100000000ull);
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
