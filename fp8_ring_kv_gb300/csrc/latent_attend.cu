@@ -18,11 +18,11 @@
 // Numbers below 2^-6 of e4m3's scale lose bits: what is lost is below 2^-18 of
 // the row's largest query number, or of its largest weight.
 //
-// Warp roles (320 threads):
-//   warps 0-7   softmax: a key per thread, of columns half (warp / 4); they also
-//               rotate and split the queries and write the output
-//   warp 8      MMA issue; rows of a tile that no query sees become zeros here
-//   warp 9      the line of work, and TMA of the codes
+// Warp roles (640 threads, registers moved from the last group to the softmax):
+//   warps 0-15  softmax: a key per thread, of a quarter of the columns (warp / 4);
+//               they also rotate and split the queries and write the output
+//   warp 16     MMA issue; rows of a tile that no query sees become zeros here
+//   warp 17     the line of work, and TMA of the codes
 #include "latent.h"
 #include "launch.h"
 #include "paged_sched.cuh"
@@ -30,7 +30,9 @@
 namespace kvring_dev {
 
 constexpr int LKT = 128;                     // keys of a tile
-constexpr int LTHREADS = 320;
+constexpr int LSOFT = 16;                    // softmax warps
+constexpr int LTHREADS = 32 * (LSOFT + 4);  // (whole groups of four warps)
+constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
 constexpr int LFIX = 2;                      // what an item costs beside its tiles, in tiles
 constexpr float kLatTop = 4.807354922f;      // log2 28: a column's weights start at 28 ...
 constexpr float kLatRaise = 4.0f;            // ... and may reach 448, e4m3's largest, before its maximum is raised
@@ -44,7 +46,7 @@ enum : int { LST_SOME = 1, LST_WHOLE = 2, LST_HEAD = 4 };
 template <typename T, int R>
 struct LatLayout {
   static constexpr int NP = std::is_same_v<T, __half> ? 3 : 2;   // e4m3 parts of a query and of a weight
-  static constexpr int HC = R / 2;                               // columns of a softmax warp
+  static constexpr int HC = R / 4;                               // columns of a softmax warp
   static constexpr int CB = LKT * 128, RB = LKT * kLatRope;      // a chunk of 128 channels, the rotated part
   static constexpr int STAGE = 4 * CB + RB;
   static constexpr int QC = NP * R * 128;                        // a chunk of the queries, all parts
@@ -54,20 +56,20 @@ struct LatLayout {
   // columns' first part, or 32 columns' first and second.  The next part:
   static constexpr int P = Q + 4 * QC + NP * R * kLatRope;
   static constexpr int PB = R == 64 ? LKT * 64 : NP == 3 ? LKT * 32 : 0;
-  static constexpr int TOP = P + PB;                             // [2][4][HC] column maxima, sums
-  static constexpr int MINE = TOP + 8 * HC * 4;                  // [8 warps][HC] reference - kLatTop; 1 / l
-  static constexpr int FAC = MINE + 8 * HC * 4;                  // [R] logit factors
+  static constexpr int TOP = P + PB;                             // [4][4][HC] column maxima, sums
+  static constexpr int MINE = TOP + LSOFT * HC * 4;              // [warps][HC] reference - kLatTop; 1 / l
+  static constexpr int FAC = MINE + LSOFT * HC * 4;                  // [R] logit factors
   static constexpr int HI = FAC + R * 4;                         // [R] keys below are seen
-  static constexpr int FLAG = HI + R * 4;                        // [2][8]
-  static constexpr int SEG = FLAG + 64;                          // [2]
+  static constexpr int FLAG = HI + R * 4;                        // [2][16]
+  static constexpr int SEG = FLAG + 128;                         // [2]
   static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
-  static constexpr int NBAR = 4 + 4 + 2 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 4 + 4 + 2 + 1 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(ALLOC <= 232448, "shared memory of a block");
   static_assert(2 * STAGE >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the stages at first");
   static_assert(4 * NP * R <= 512, "tensor memory: two buffers of S below column 256, four accumulators of 64 columns");
-  static_assert(8 * HC * 4 >= 8 * (LTHREADS / 32), "the prefix sums' warps lie in TOP and MINE at first");
+  static_assert(LSOFT * HC * 4 >= 8 * (LTHREADS / 32), "the prefix sums' warps lie in TOP and MINE at first");
   static_assert(R == 64 ? NP == 2 : R == 32, "weights' room");
 };
 
@@ -103,7 +105,8 @@ template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
   if constexpr (N == 32) tmem_ld_32x32b_x32(at, r);
   else if constexpr (N == 16) tmem_ld_32x32b_x16(at, r);
-  else tmem_ld_32x32b_x8(at, r);
+  else if constexpr (N == 8) tmem_ld_32x32b_x8(at, r);
+  else tmem_ld_32x32b_x4(at, r);
 }
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -144,9 +147,9 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   uint64_t* q_free = q_full + 1;           // their room is free: the outputs before have left it
   uint64_t* seg_full = q_free + 1;         // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2]
-  uint64_t* flags_in = seg_free + 2;       // [2 halves] the warps' flags written
-  uint64_t* tops_in = flags_in + 2;        // [2 halves] their maxima, or sums, or outputs
-  uint64_t* drain = tops_in + 2;
+  uint64_t* flags_in = seg_free + 2;       // [4 quarters] the warps' flags written
+  uint64_t* tops_in = flags_in + 4;        // [4 quarters] their maxima, or sums, or outputs
+  uint64_t* drain = tops_in + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile LatStretch* segs = reinterpret_cast<volatile LatStretch*>(sm + LY::SEG);
@@ -161,24 +164,25 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], 9);
+      mbar_init(&seg_free[i], LSOFT + 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&flags_in[i], 4);
       mbar_init(&tops_in[i], 4);
-      item_sums[i] = 0;
     }
-    item_sums[2] = 0;
-    mbar_init(p_full, 8);
-    mbar_init(q_full, 8);
-    mbar_init(q_free, 8);
+    for (int i = 0; i < 3; ++i) item_sums[i] = 0;
+    mbar_init(p_full, LSOFT);
+    mbar_init(q_full, LSOFT);
+    mbar_init(q_free, LSOFT);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == LSOFT) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == LSOFT + 1 && lane == 0) {
     tma_prefetch_desc(&tmC);
     tma_prefetch_desc(&tmR);
   }
@@ -198,14 +202,15 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
   Place pl;
-  if (warp == 9 && u < end) pl = find_place<SH, R, LKT>(a, pre, u, cut.pad);
+  if (warp == LSOFT + 1 && u < end) pl = find_place<SH, R, LKT>(a, pre, u, cut.pad);
   __syncthreads();                         // the prefix sums' room is the stages' now
 
-  if (warp < 8) {
+  if (warp < LSOFT) {
     // ======================================================== softmax
-    const int quad = warp & 3, half = warp >> 2;
+    reg_inc<kLatSoftRegs>();
+    const int quad = warp & 3, quarter = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    float* tops = reinterpret_cast<float*>(sm + LY::TOP) + half * 4 * HC;   // [4][HC]
+    float* tops = reinterpret_cast<float*>(sm + LY::TOP) + quarter * 4 * HC;   // [4][HC]
     float* mine = reinterpret_cast<float*>(sm + LY::MINE) + warp * HC;
     float* fac = reinterpret_cast<float*>(sm + LY::FAC);
     int* his = reinterpret_cast<int*>(sm + LY::HI);
@@ -214,10 +219,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     uint32_t n_tops = 0, n_q = 0;          // phases of tops_in and q_full so far
     int done = 0;
     bool ok = true;
-    // every warp of the half puts HC numbers (lane c the one of column c) into tops
+    // every warp of the quarter puts HC numbers (lane c the one of column c) into tops
     auto meet = [&]() -> bool {
-      warp_arrive(&tops_in[half]);
-      return warp_wait(&tops_in[half], n_tops++ & 1, abort_flag);
+      warp_arrive(&tops_in[quarter]);
+      return warp_wait(&tops_in[quarter], n_tops++ & 1, abort_flag);
     };
     auto share = [&](float v) -> bool {
       if (lane < HC) tops[quad * HC + lane] = v;
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       if (lane < HC) mine[lane] = kNoMax;
       if (n > 0) {
         // ------------------------------------------------------ queries
-        constexpr int RW = R / 8;          // rows of a warp
+        constexpr int RW = R / LSOFT;      // rows of a warp
         const int w0 = warp * RW;
         const bool mine16 = lane * 16 < C; // lane l: latent numbers 16 l .. 16 l + 15 of every row
         uint4 w[RW][2];
@@ -383,19 +388,19 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           float x[HC];
           auto scores = [&]() {            // S of the codes
             uint32_t part[HC];
-            tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + half * HC, part);
+            tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + quarter * HC, part);
 #pragma unroll
             for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(part[c]);
 #pragma unroll
             for (int p = 1; p < NP; ++p) {
-              tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + p * R + half * HC, part);
+              tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + p * R + quarter * HC, part);
 #pragma unroll
               for (int c = 0; c < HC; ++c) x[c] += __uint_as_float(part[c]);
             }
           };
           // x becomes y minus what is in ``mine`` (raw: y itself)
           auto logits = [&](bool raw) {
-            const float4* f4 = reinterpret_cast<const float4*>(fac + half * HC);
+            const float4* f4 = reinterpret_cast<const float4*>(fac + quarter * HC);
             const float4* m4 = reinterpret_cast<const float4*>(mine);
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             if (edge) {
 #pragma unroll
               for (int c = 0; c < HC; ++c) {
-                const int h = his[half * HC + c];
+                const int h = his[quarter * HC + c];
                 if (key >= h || (a.window > 0 && key < h - a.window)) x[c] = -INFINITY;
               }
             }
@@ -430,10 +435,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             for (int c = 0; c < HC; ++c) ups |= x[c] > kLatTop + kLatRaise ? 1u << c : 0u;
             ups = __reduce_or_sync(0xFFFFFFFFu, ups);
           }
-          volatile uint32_t* fl = flag + (g & 1) * 8 + half * 4;
+          volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
           if (lane == 0) fl[quad] = ups;
-          warp_arrive(&flags_in[half]);
-          if (!warp_wait(&flags_in[half], g & 1, abort_flag)) {
+          warp_arrive(&flags_in[quarter]);
+          if (!warp_wait(&flags_in[quarter], g & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -486,7 +491,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
                 const float f = __shfl_sync(0xFFFFFFFFu, al, c);
 #pragma unroll
                 for (int part = 0; part < 64 / R; ++part) {
-                  const uint32_t at = tmem + lanes + TM_O + part * R + half * HC + c;
+                  const uint32_t at = tmem + lanes + TM_O + part * R + quarter * HC + c;
                   uint32_t o[4];
                   tmem_ld4_32x32b_x1(at, at + (NC > 1 ? 64 : 0), at + (NC > 2 ? 128 : 0), at + (NC > 3 ? 192 : 0), o);
 #pragma unroll
@@ -523,16 +528,15 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               w[c] = c0 | c1 << 16;
             }
             uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
-#pragma unroll
-            for (int k = 0; k < HC / 16; ++k) {
-              uint8_t* at;
-              if (R == 64) {
-                at = (p == 0 ? in_stage : sm + LY::P + key_row * 64) + (((2 * half + k) ^ ((key_row >> 1) & 3)) << 4);
-              } else {
-                at = p < 2 ? in_stage + (((2 * p + half) ^ ((key_row >> 1) & 3)) << 4)
-                           : sm + LY::P + key_row * 32 + ((half ^ ((key_row >> 2) & 1)) << 4);
-              }
-              *reinterpret_cast<uint4*>(at) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            uint8_t* extra = sm + LY::P;
+            if constexpr (R == 64) {
+              uint8_t* at = (p == 0 ? in_stage : extra + key_row * 64) + ((quarter ^ ((key_row >> 1) & 3)) << 4);
+              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              const int unit = quarter >> 1;
+              uint8_t* at = p < 2 ? in_stage + (((2 * p + unit) ^ ((key_row >> 1) & 3)) << 4)
+                                  : extra + key_row * 32 + ((unit ^ ((key_row >> 2) & 1)) << 4);
+              *reinterpret_cast<uint2*>(at + 8 * (quarter & 1)) = make_uint2(w[0], w[1]);
             }
           }
           fence_proxy_async_smem();
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       }
       if (!share(l[0])) break;
       const bool whole = flags & LST_WHOLE;
-      const size_t at_row = (size_t)(2 * worker + (flags & LST_HEAD ? 1 : 0)) * kLatRows + half * HC;
+      const size_t at_row = (size_t)(2 * worker + (flags & LST_HEAD ? 1 : 0)) * kLatRows + quarter * HC;
       if (lane < HC) {
         const float sum = (tops[lane] + tops[HC + lane]) + (tops[2 * HC + lane] + tops[3 * HC + lane]);
         const float ref = mine[lane];
@@ -572,15 +576,15 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         mine[lane] = sum != 0.0f ? 1.0f / sum : 0.0f;
       }
       __syncwarp();
-      const int live = max(0, min(HC, rows - half * HC));   // columns of this warp
+      const int live = max(0, min(HC, rows - quarter * HC));   // columns of this warp
       auto out_row = [&](int c) -> T* {
-        const int r = r0 + half * HC + c, i = r / G;
+        const int r = r0 + quarter * HC + c, i = r / G;
         return static_cast<T*>(a.out) + (s0 + i) * la.o.token + (r - i * G) * la.o.head;
       };
       if (n > 0) {
         // A thread has a channel of every row: whole rows by way of the queries'
         // room, 16-bit ones at once, fp32 pieces in two turns.
-        uint8_t* stage = sm + LY::Q + half * HC * C * 2;
+        uint8_t* stage = sm + LY::Q + quarter * HC * C * 2;
         constexpr int TC = HC / 2;
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
 #pragma unroll 1
           for (int q = 0; q < NC; ++q) {
             const int ch = q * 128 + 32 * quad + lane;
-            const uint32_t at_o = tmem + lanes + TM_O + q * 64 + half * HC + turn * TC;
+            const uint32_t at_o = tmem + lanes + TM_O + q * 64 + quarter * HC + turn * TC;
             uint32_t o[TC];
             tmem_ld_cols<TC>(at_o, o);
             if constexpr (R == 32) {
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           }
           if (whole && turn == 0) continue;
           fence_proxy_async_smem();
-          if (!(ok = meet())) break;       // the half's four warps have written
+          if (!(ok = meet())) break;       // the quarter's four warps have written
           if (whole) {
             const int c = quad * (HC / 4) + lane;
             if (lane < HC / 4 && c < live) bulk_store(out_row(c), stage + c * C * 2, C * 2);
@@ -640,7 +644,9 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       warp_arrive(&seg_free[sg & 1]);
     }
     bulk_wait();
-  } else if (warp == 8) {
+  } else {
+  reg_dec<kLatOtherRegs>();
+  if (warp == LSOFT) {
     // ======================================================== MMA issue
     constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
     constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
@@ -759,7 +765,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       mbar_wait(drain, 0, nullptr, 100000000ull);
     }
     __syncwarp();
-  } else {
+  } else if (warp == LSOFT + 1) {
     // ======================================================== the line of work
     PieceRec rec = {};
     const int P = a.pv.P, boxes = LKT / P, W = C + kLatRope;
@@ -873,9 +879,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     if (*abort_flag)
       for (int b = max(0, armed - 4); b < armed; ++b) mbar_wait(&full[b & 3], (b >> 2) & 1, nullptr, 100000000ull);
   }
+  }
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
-  if (warp == 8) {
+  if (warp == LSOFT) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -946,6 +953,12 @@ cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, b
 
 template <typename T, int R>
 static cudaError_t prepare_t() {
+  // reg_inc draws on the registers that the block was launched with: fewer
+  // would make it wait for ever
+  cudaFuncAttributes fa;
+  const cudaError_t e = cudaFuncGetAttributes(&fa, latent_attend_kernel<T, R>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * LTHREADS < 32 * (LSOFT * kLatSoftRegs + 4 * kLatOtherRegs)) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(latent_attend_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               LatLayout<T, R>::ALLOC);
 }
