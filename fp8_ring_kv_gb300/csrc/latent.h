@@ -26,6 +26,7 @@ struct LatentAttn {
   PagedAttn a;
   const void* q_rope;
   Strides q, qr, o;
+  int32_t code_rows;               // of all layers: the code arrays' height
 };
 
 // One expanded call.  a.pv.H heads with G = 1; a.pb.table = kv_start, a

@@ -288,6 +288,7 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
   a.q_pos = q_pos;
   a.out = out;
   la.q_rope = q_rope;
+  la.code_rows = p->cfg.layers * p->cfg.n_pages * p->cfg.page_tokens;
   latent_carve_scratch(p->scratch, kLatRows, a.pv.D, &a);
   const cudaError_t e = launch_latent_attend(la, p->c_map, p->r_map, p->cfg.in_dtype == KVRING_IN_F16, p->sms,
                                              reinterpret_cast<cudaStream_t>(stream));

@@ -63,7 +63,7 @@ struct LatLayout {
   static constexpr int FLAG = HI + R * 4;                        // [2][16]
   static constexpr int SEG = FLAG + 128;                         // [2]
   static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
-  static constexpr int NBAR = 4 + 4 + 2 + 1 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
+  static constexpr int NBAR = 4 + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(ALLOC <= 232448, "shared memory of a block");
@@ -122,6 +122,21 @@ __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Whether one of the 128 threads at named barrier ``id`` says so.  A warp that
+// gives up (the block's abort flag is set before) arrives once more: those that
+// wait go on, and look at the flag.
+__device__ __forceinline__ bool quarter_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void quarter_leave(int id) { asm volatile("barrier.cta.arrive %0, 128;" ::"r"(id) : "memory"); }
+
 // a warp waits with one answer; what it has to write for the others is written
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -142,8 +157,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   uint64_t* full = bars;                   // [2 stages][2 halves] codes landed: chunks 0 and 1; the others, the rotated part
   uint64_t* free_ = full + 4;              // [2][2] and every MMA is done with them (the second: PV is done)
   uint64_t* s_full = free_ + 4;            // [2] QK done
-  uint64_t* p_full = s_full + 2;           // P stored
-  uint64_t* q_full = p_full + 1;           // queries written (once per stretch)
+  uint64_t* p_full = s_full + 2;           // [2] P stored
+  uint64_t* q_full = p_full + 2;           // queries written (once per stretch)
   uint64_t* q_free = q_full + 1;           // their room is free: the outputs before have left it
   uint64_t* seg_full = q_free + 1;         // [2] stretch written
   uint64_t* seg_free = seg_full + 2;       // [2]
@@ -163,6 +178,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], LSOFT);
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_free[i], LSOFT + 1);
     }
@@ -171,7 +187,6 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       mbar_init(&tops_in[i], 4);
     }
     for (int i = 0; i < 3; ++i) item_sums[i] = 0;
-    mbar_init(p_full, LSOFT);
     mbar_init(q_full, LSOFT);
     mbar_init(q_free, LSOFT);
     mbar_init(drain, 1);
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     int* his = reinterpret_cast<int*>(sm + LY::HI);
     volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(sm + LY::FLAG);
     const int key_row = 32 * quad + lane;
-    uint32_t n_tops = 0, n_q = 0;          // phases of tops_in and q_full so far
+    uint32_t n_tops = 0, n_flags = 0, n_q = 0;   // phases of their barriers so far
     int done = 0;
     bool ok = true;
     // every warp of the quarter puts HC numbers (lane c the one of column c) into tops
@@ -429,21 +444,24 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           float most = x[0];
 #pragma unroll
           for (int c = 1; c < HC; ++c) most = fmaxf(most, x[c]);
-          uint32_t ups = 0;                // columns whose maximum this warp's keys raise
-          if (__any_sync(0xFFFFFFFFu, most > kLatTop + kLatRaise)) {
-#pragma unroll
-            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatTop + kLatRaise ? 1u << c : 0u;
-            ups = __reduce_or_sync(0xFFFFFFFFu, ups);
-          }
-          volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
-          if (lane == 0) fl[quad] = ups;
-          warp_arrive(&flags_in[quarter]);
-          if (!warp_wait(&flags_in[quarter], g & 1, abort_flag)) {
+          const bool raise = quarter_any(1 + quarter, most > kLatTop + kLatRaise);
+          if (*abort_flag) {
             ok = false;
             break;
           }
-          ups = fl[0] | fl[1] | fl[2] | fl[3];
-          if (ups) {
+          if (raise) {
+            uint32_t ups = 0;              // columns whose maximum is raised
+#pragma unroll
+            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatTop + kLatRaise ? 1u << c : 0u;
+            ups = __reduce_or_sync(0xFFFFFFFFu, ups);
+            volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
+            if (lane == 0) fl[quad] = ups;
+            warp_arrive(&flags_in[quarter]);
+            if (!warp_wait(&flags_in[quarter], n_flags++ & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ups = fl[0] | fl[1] | fl[2] | fl[3];
             // What was summed is brought to the new maximum.  Columns without a key
             // so far (all of them in a stretch's first tile) take it as it is.
             const bool fresh = __any_sync(0xFFFFFFFFu, lane < HC && (ups >> lane & 1) && mine[lane] == kNoMax);
@@ -514,11 +532,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           uint32_t v[HC / 2];
 #pragma unroll
           for (int c = 0; c < HC / 2; ++c) v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
-          // PV of the tile before is done with the weights' room
-          if (g > 0 && !pv_done(g - 1)) {
-            ok = false;
-            break;
-          }
+          uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
+          uint8_t* extra = sm + LY::P;
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t w[HC / 4];
@@ -527,8 +542,11 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               const uint32_t c0 = split2(v[2 * c]), c1 = split2(v[2 * c + 1]);
               w[c] = c0 | c1 << 16;
             }
-            uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
-            uint8_t* extra = sm + LY::P;
+            // PV of the tile before is done with the room that is there once
+            if (LY::PB > 0 && p == NP - 1 && g > 0 && !pv_done(g - 1)) {
+              ok = false;
+              break;
+            }
             if constexpr (R == 64) {
               uint8_t* at = (p == 0 ? in_stage : extra + key_row * 64) + ((quarter ^ ((key_row >> 1) & 3)) << 4);
               *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -539,9 +557,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               *reinterpret_cast<uint2*>(at + 8 * (quarter & 1)) = make_uint2(w[0], w[1]);
             }
           }
+          if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(p_full);
+          warp_arrive(&p_full[g & 1]);
         }
         if (!ok) break;
       }
@@ -644,6 +663,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       warp_arrive(&seg_free[sg & 1]);
     }
     bulk_wait();
+    if (*abort_flag) quarter_leave(1 + quarter);
   } else {
   reg_dec<kLatOtherRegs>();
   if (warp == LSOFT) {
@@ -660,100 +680,91 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       if (!(seg.flags & LST_SOME)) break;
       const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
       if (n > 0 && !warp_wait(q_full, n_q++ & 1, abort_flag)) break;
-      // QK runs a tile ahead of PV where its codes are there in time; else PV goes first
-      int jq = 0, jp = 0;                  // the next of either
-      unsigned long long t0_ns = 0;
-      while (jp < n) {
-        int next = 0;                      // 1: PV, 2: QK, 0: given up
+      // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
+      // can go goes first.  One lane issues; the warp is only called for
+      // rows that no query sees (in the first and last tile): their weights are
+      // zeros, which must meet numbers.
+      int jq = 0, jp = 0, cleared = -1;    // the next of either; the last tile cleared
+      for (;;) {
+        int ask = 0;                       // 1: rows to clear, -1: given up
         if (lane == 0) {
-          const int gp = done + jp, gq = done + jq;
-          for (uint32_t spins = 1; next == 0; ++spins) {
-            if (jp < jq && mbar_test_wait(p_full, gp & 1)) next = 1;
-            else if (jq < n && jq < jp + 2 && mbar_test_wait(full + (gq & 1) * 2, (gq >> 1) & 1) &&
-                     mbar_test_wait(full + (gq & 1) * 2 + 1, (gq >> 1) & 1)) next = 2;
-            else if ((spins & 63u) == 0) {
+          unsigned long long t0_ns = 0;
+          uint32_t spins = 0;
+          while (jp < n) {
+            const int gp = done + jp, gq = done + jq;
+            if (jp < jq && mbar_test_wait(&p_full[gp & 1], (gp >> 1) & 1)) {
+              tc_fence_after();
+              const int sp = gp & 1;
+              const uint32_t kt = k_at + sp * LY::STAGE;
+              const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+              const uint32_t go = jp > 0;
+#pragma unroll 1
+              for (int c = 0; c < NC; ++c) {
+                const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+                const uint32_t o = tmem + TM_O + 64 * c;
+                mma4_f8_ss(o, ad, b0, idesc_pv, go, 256, 128);
+                if constexpr (R == 64) mma4_f8_ss(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1, 256, 128);
+                else if constexpr (NP == 3) mma4_f8_ss(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1, 256, 64);
+                if (c == 1) mma_commit(&free_[sp * 2]);
+              }
+              if (NC == 1) mma_commit(&free_[sp * 2]);
+              mma_commit(&free_[sp * 2 + 1]);
+              ++jp;
+              spins = 0;
+            } else if (jq < n && jq < jp + 2 && mbar_test_wait(&full[(gq & 1) * 2], (gq >> 1) & 1) &&
+                       mbar_test_wait(&full[(gq & 1) * 2 + 1], (gq >> 1) & 1)) {
+              const int t0 = (k0 + jq) * LKT, stage = gq & 1;
+              if ((t0 < lo || t0 + LKT > hi) && cleared != jq) {
+                ask = 1;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t kt = k_at + stage * LY::STAGE, d = tmem + stage * NP * R;
+#pragma unroll 1
+              for (int c = 0; c < NC; ++c)
+                mma4_f8_ss(d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024), make_sdesc_sw128(q_at + c * LY::QC, 16, 1024),
+                           idesc_qk, c, 2, 2);
+              const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+              const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
+              mma_f8_ss(d, ad, bd, idesc_qk, 1);
+              mma_f8_ss(d, ad + 2, bd + 2, idesc_qk, 1);
+              mma_commit(&s_full[stage]);
+              ++jq;
+              spins = 0;
+            } else if ((++spins & 63u) == 0) {
               const unsigned long long now = globaltimer_ns();
               if (spins == 64) t0_ns = now;
               if (now - t0_ns > kWaitLimitNs) *abort_flag = 1;
-              if (*abort_flag) break;
+              if (*abort_flag) {
+                ask = -1;
+                break;
+              }
             }
           }
         }
-        next = __shfl_sync(0xFFFFFFFFu, next, 0);
-        ok = next != 0;
+        ask = __shfl_sync(0xFFFFFFFFu, ask, 0);
+        ok = ask >= 0;
+        if (ask <= 0) break;
+        const int j = __shfl_sync(0xFFFFFFFFu, jq, 0), g = done + j;
+        for (int h = 0; h < 2 && ok; ++h)  // (there already: every lane has seen it)
+          ok = warp_wait(&full[(g & 1) * 2 + h], (g >> 1) & 1, abort_flag);
         if (!ok) break;
-        if (next == 2) {
-          const int j = jq++, g = done + j, stage = g & 1;
-          uint64_t* f = full + stage * 2;
-          const uint32_t par = (g >> 1) & 1;
-          const uint32_t kt = k_at + stage * LY::STAGE;
-          const int t0 = (k0 + j) * LKT;
-          if (t0 < lo || t0 + LKT > hi) {
-            // rows that no query sees: their weights are zeros, which must meet numbers
-            ok = warp_wait(f, par, abort_flag) && warp_wait(f + 1, par, abort_flag);
-            if (!ok) break;
-            uint8_t* tile = sm + LY::K + stage * LY::STAGE;
-            for (int r = 0; r < LKT; ++r) {
-              if (t0 + r >= lo && t0 + r < hi) continue;
-              const uint4 zero = make_uint4(0, 0, 0, 0);
-              if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
-              if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+        // (pages that no query sees came as zeros)
+        uint8_t* tile = sm + LY::K + (g & 1) * LY::STAGE;
+        const int first = lo - (k0 + j) * LKT, end = hi - (k0 + j) * LKT, P = a.pv.P;
+        auto clear = [&](int r0, int r1) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+          for (int r = r0; r < r1; ++r) {
+            if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
+            if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
           }
-          const uint32_t d = tmem + stage * NP * R;
-          for (int h = 0; h < 2; ++h) {
-            ok = warp_wait(f + h, par, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              for (int c = 2 * h; c < min(NC, 2 * h + 2); ++c) {
-                const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-                const uint64_t bd = make_sdesc_sw128(q_at + c * LY::QC, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, c | k);
-              }
-              if (h == 1) {
-                const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-                const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, 1);
-                mma_commit(&s_full[stage]);
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-        } else {
-          const int j = jp++, gp = done + j, sp = gp & 1;
-          ok = warp_wait(p_full, gp & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t kt = k_at + sp * LY::STAGE;
-            const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-            for (int c = 0; c < NC; ++c) {
-              const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-              const uint32_t o = tmem + TM_O + 64 * c;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b0 + 128 * k, idesc_pv, (j > 0) | k);
-              if constexpr (R == 64) {
-                const uint64_t b1 = make_sdesc_sw64(p_at, 16, 512);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b1 + 128 * k, idesc_pv, 1);
-              } else if constexpr (NP == 3) {
-                const uint64_t b2 = sdesc_sw32(p_at, 256);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f8_ss(o, ad + 256 * k, b2 + 64 * k, idesc_pv3, 1);
-              }
-              if (c == 1) mma_commit(&free_[sp * 2]);
-            }
-            if (NC == 1) mma_commit(&free_[sp * 2]);
-            mma_commit(&free_[sp * 2 + 1]);
-          }
-          __syncwarp();
-        }
+        };
+        if (first > 0) clear(first & -P, first);
+        if (end < LKT) clear(end, min(LKT, (end + P - 1) & -P));
+        fence_proxy_async_smem();
+        __syncwarp();
+        cleared = j;
       }
       if (!ok) break;
       done += n;
@@ -836,9 +847,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         const int g = done + k - k0, stage = g & 1;
         const int pg2 = page(k + 2);
         ahead(k + 2, pg2);
-        const bool on = pg >= 0;
-        const uint32_t n_on = __popc(__ballot_sync(0xFFFFFFFFu, on));
-        const int y = (int)a.pv.row0 + (pg << a.pv.p_shift);
+        // (a page that no query sees: past the last row, where TMA finds zeros)
+        const int y = pg >= 0 ? (int)a.pv.row0 + (pg << a.pv.p_shift) : la.code_rows;
         uint8_t* tile = sm + LY::K + stage * LY::STAGE;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -848,9 +858,9 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             break;
           }
           const int c1 = min(NC, 2 * h + 2), chunks = max(0, c1 - 2 * h);
-          if (lane == 0) mbar_arrive_expect_tx(f, n_on * P * (chunks * 128 + h * kLatRope));
+          if (lane == 0) mbar_arrive_expect_tx(f, LKT * (chunks * 128 + h * kLatRope));
           __syncwarp();
-          if (on) {
+          if (lane < boxes) {
             for (int c = 2 * h; c < c1; ++c) {
               uint8_t* dst = tile + c * LY::CB + lane * P * 128;
               if (alone) tma_load_2d_hint(dst, &tmC, f, c * 128, y, once);
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps)
     const int r = id / NC, c = (id - r * NC) * 128 + lane * 4;
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
     for (int p = w; p <= it.last; ++p) {
       const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * slot_rows + r;
       const float2 ml = a.tiles.ml[row];
@@ -946,7 +956,7 @@ void latent_carve_scratch(uint8_t* base, int rows, int width, PagedAttn* a) {
 }
 
 cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, bool f16, int blocks, cudaStream_t st) {
-  const dim3 grid(blocks, (rows * (a.pv.D >> 7) + 4 * kLatJoinWarps - 1) / (4 * kLatJoinWarps)), block(32 * kLatJoinWarps);
+  const dim3 grid(blocks, (rows * (a.pv.D >> 7) + kLatJoinWarps - 1) / kLatJoinWarps), block(32 * kLatJoinWarps);
   return f16 ? launch_pdl(latent_join_kernel<__half>, grid, block, 0, st, a, o, rows)
              : launch_pdl(latent_join_kernel<__nv_bfloat16>, grid, block, 0, st, a, o, rows);
 }
