@@ -402,12 +402,14 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           tc_fence_after();
           float x[HC];
           auto scores = [&]() {            // S of the codes
-            uint32_t part[HC];
-            tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + quarter * HC, part);
+            uint32_t part[HC], part1[HC];
+            const uint32_t at = tmem + lanes + (g & 1) * NP * R + quarter * HC;
+            if constexpr (HC == 16) tmem_ld2_32x32b_x16(at, at + R, part, part1);
+            else tmem_ld2_32x32b_x8(at, at + R, part, part1);
 #pragma unroll
-            for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(part[c]);
+            for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(part[c]) + __uint_as_float(part1[c]);
 #pragma unroll
-            for (int p = 1; p < NP; ++p) {
+            for (int p = 2; p < NP; ++p) {
               tmem_ld_cols<HC>(tmem + lanes + (g & 1) * NP * R + p * R + quarter * HC, part);
 #pragma unroll
               for (int c = 0; c < HC; ++c) x[c] += __uint_as_float(part[c]);
@@ -441,9 +443,13 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           };
           scores();
           logits(false);
-          float most = x[0];
+          float most = fmaxf(x[0], x[1]), most1 = fmaxf(x[2], x[3]);
 #pragma unroll
-          for (int c = 1; c < HC; ++c) most = fmaxf(most, x[c]);
+          for (int c = 4; c < HC; c += 4) {
+            most = max3f(most, x[c], x[c + 1]);
+            most1 = max3f(most1, x[c + 2], x[c + 3]);
+          }
+          most = fmaxf(most, most1);
           const bool raise = quarter_any(1 + quarter, most > kLatTop + kLatRaise);
           if (*abort_flag) {
             ok = false;
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   } else if (warp == LSOFT + 1) {
     // ======================================================== the line of work
     PieceRec rec = {};
-    const int P = a.pv.P, boxes = LKT / P, W = C + kLatRope;
+    const int P = a.pv.P, boxes = LKT / P;
     const bool alone = (long long)a.max_new * G <= R;    // every key is read by one item only
     const uint64_t once = l2_evict_first();
     int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
@@ -836,17 +842,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         }
         return pg;
       };
-      // the L2 is asked for a tile's codes well before its TMA, whose room is free late
-      auto ahead = [&](int k, int p) {
-        if (p < 0) return;
-        const int key = k * LKT + lane * P, first = max(0, pl.t.lo - key), last = min(P, pl.t.hi - key);
-        l2_prefetch(a.pv.k_codes + (((size_t)p << a.pv.p_shift) + first) * W, (uint32_t)((last - first) * W));
-      };
-      int pg = page(k0), pg1 = page(k0 + 1);
+      int pg = page(k0);
       for (int k = k0; k < k1; ++k) {
         const int g = done + k - k0, stage = g & 1;
-        const int pg2 = page(k + 2);
-        ahead(k + 2, pg2);
+        const int next = page(k + 1);
         // (a page that no query sees: past the last row, where TMA finds zeros)
         const int y = pg >= 0 ? (int)a.pv.row0 + (pg << a.pv.p_shift) : la.code_rows;
         uint8_t* tile = sm + LY::K + stage * LY::STAGE;
@@ -875,8 +874,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           armed = g * 2 + h + 1;
         }
         if (!ok) break;
-        pg = pg1;
-        pg1 = pg2;
+        pg = next;
       }
       done += k1 - k0;
       if (u == pl.at && end < item_end)

@@ -11,16 +11,21 @@
 // key part is a third block of K's tile, read where it lies, so no head's keys
 // are written out 192 wide.
 //
-// What bounds it: the tensor pipe (128 keys of 256 rows: 24 steps of 128 x 128 x
-// 16 for S and 16 for PV, 64 cycles each, 2,560), beside which 32,768
-// exponentials take 2,048 cycles.
+// A bf16 weight would be off by as much as the bf16 output is rounded by, and
+// over many keys of like weight all of that shows: bf16 weights are the sum of two
+// bf16 numbers, two products into one O (S leaves room for both).
 //
-// Warp roles (512 threads, registers moved from the last two groups to the softmax):
-//   warps 0-7    softmax, tile warp / 4, a row per thread; they also load and
-//                rotate the queries and write the output
-//   warp 8       MMA issue
-//   warp 9       the line of work, and TMA
-//   warps 12-15  values that not every row sees: those that no row sees become
+// What bounds it: the tensor pipe (128 keys of 256 rows: 24 steps of 128 x 128 x
+// 16 for S and 16 (bf16: 32) for PV, 64 cycles each, 2,560 (3,584)), beside
+// which 32,768 exponentials take 2,048 cycles.
+//
+// Warp roles (640 threads, registers moved from the last group to the softmax):
+//   warps 0-15   softmax: of query tile t and half p of its keys, warps 8 p + 4 t
+//                .. + 3, one row per thread: two warps share a row.  They also load
+//                and rotate the queries and write the output
+//   warp 16      MMA issue
+//   warp 17      the line of work, and TMA
+//   warps 18, 19 values that not every row sees: those that no row sees become
 //                zeros, a NaN or infinity that some see is taken out (its weight in the
 //                others is 0, which must meet a number) and remembered
 // QK of the next tile overwrites the P that PV of this one reads, with another
@@ -32,9 +37,9 @@
 
 namespace kvring_dev {
 
-constexpr int XKT = 128, XROWS = 128, XTR = kTilesRows, XTHREADS = 512;
+constexpr int XKT = 128, XROWS = 128, XTR = kTilesRows, XTHREADS = 640;
 static_assert(XTR == 2 * XROWS);
-constexpr int kXSoftmaxRegs = 192, kXOtherRegs = 64;   // per thread: 8 warps each
+constexpr int kXSoftmaxRegs = 104, kXOtherRegs = 64;   // per thread: 16 warps and 4
 constexpr int XRING = 8, XBLK = 16384;       // blocks of K (128 keys x 64 numbers) and V (64 keys x 128)
 constexpr float kXRaise = 8.0f;              // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kXTop = 6.0f;                // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
@@ -49,8 +54,9 @@ struct XLayout {
   static constexpr int Q = 0;
   static constexpr int RING = Q + 2 * QT;
   static constexpr int SEG = RING + XRING * XBLK;
-  static constexpr int BAR = SEG + 2 * 64;
-  static constexpr int NBAR = 2 * XRING + 5 * 2 + 4 + 1;
+  static constexpr int SLOT = SEG + 2 * 64;              // [2 halves][256] a row's maxima; sums
+  static constexpr int BAR = SLOT + 2 * XTR * 4;
+  static constexpr int NBAR = 2 * XRING + 5 * 2 + 4 + 1 + 16 + 8;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(sizeof(XStretch) <= 64 && ALLOC <= 232448, "shared memory of a block");
@@ -67,12 +73,12 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// Whether one of the values of keys lo .. hi - 1 is no number, tiles that every
-// row sees left out.
+// Whether one of the values of keys lo, lo + 2, .. < hi is no number, tiles that
+// every row sees left out.
 template <typename T>
 __device__ __noinline__ bool nonfinite_among(const T* v, long long v_token, int lo, int hi, int all_lo, int all_hi) {
 #pragma unroll 1
-  for (int key = lo; key < hi; ++key) {
+  for (int key = lo; key < hi; key += 2) {
     const int k = key / XKT;
     if (k * XKT >= all_lo && k * XKT + XKT <= all_hi) continue;
     const uint4* p = reinterpret_cast<const uint4*>(v + key * v_token);
@@ -93,6 +99,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   using SH = Share<XTR, XKT, 2, 0, 0x7FFFFFFF>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr uint32_t FMT = std::is_same_v<T, __half> ? 0 : 1;
+  constexpr int PARTS = std::is_same_v<T, __half> ? 1 : 2;      // of a weight
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = xa.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
@@ -106,6 +113,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   uint64_t* seg_full = v_clean + 2;        // [2]
   uint64_t* seg_free = seg_full + 2;       // [2]
   uint64_t* drain = seg_free + 2;
+  uint64_t* m_ready = drain + 1;           // [2][4 warps][2 halves] a half's maxima written
+  uint64_t* both = m_ready + 16;           // [2][4] both warps of a row are here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile int* odd_seen = reinterpret_cast<volatile int*>(sm + LY::MISC + 8);   // a value that is no number was taken out
@@ -119,25 +128,27 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       mbar_init(&free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&o_done[i], 1);
-      mbar_init(&v_clean[i], 4);
+      mbar_init(&v_clean[i], 2);
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_free[i], 13);
+      mbar_init(&seg_free[i], 19);
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&m_ready[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&both[i], 2);
     mbar_init(drain, 1);
     for (int i = 0; i < 3; ++i) item_sums[i] = 0;
     *abort_flag = 0;
     *odd_seen = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 16) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == 17 && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmR);
     tma_prefetch_desc(&tmV);
@@ -157,18 +168,26 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   long long u = min(total, stretch * worker);
   const long long end = min(total, u + stretch);
   Place pl;
-  if (warp == 9 && u < end) pl = find_place<SH, XTR, XKT>(a, pre, u, cut.pad);
+  if (warp == 17 && u < end) pl = find_place<SH, XTR, XKT>(a, pre, u, cut.pad);
   // the prefix sums' room is the query tiles' now, the others' the ring's
   fence_proxy_async_smem();
   __syncthreads();
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ======================================================== softmax
     reg_inc<kXSoftmaxRegs>();
-    const int t = warp >> 2, quad = warp & 3, row = tid & 127;
+    const int t = (warp >> 2) & 1, par = warp >> 3, quad = warp & 3, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t s_at = tmem + lanes + TM_S + 128 * t, o_at = tmem + lanes + TM_O + 128 * t;
-    uint32_t tiles = 0;                    // of this query tile so far: the phases of its barriers
+    float* slots = reinterpret_cast<float*>(sm + LY::SLOT) + t * XROWS + row;
+    float *mine = slots + par * XTR, *other = slots + (par ^ 1) * XTR;
+    const int pair = 4 * t + quad;         // the two warps of these rows
+    uint32_t nb = 0, tiles = 0;            // phases of ``both``; of this query tile's barriers
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&both[pair]);
+      return warp_wait(&both[pair], nb++ & 1, abort_flag);
+    };
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -184,50 +203,49 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       float m = -INFINITY, l = 0.0f;
       if (n > 0 && rows > 0) {
         // ------------------------------------------------------ queries
+        // half of the pair's 32 rows each
         uint8_t* tile = sm + LY::Q + t * LY::QT;
         const T* q = static_cast<const T*>(a.q) + (long long)(s0 + r0) * xa.q.token + (long long)head * xa.q.head;
-#pragma unroll 1
-        for (int b0 = 0; b0 < 32; b0 += 8) {             // 128 numbers of a row: 16 lanes
-          uint4 w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 32 * quad + b0 + 2 * k + (lane >> 4);
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (r < rows) w[k] = *(reinterpret_cast<const uint4*>(q + r * xa.q.token) + (lane & 15));
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 32 * quad + b0 + 2 * k + (lane >> 4), c = lane & 15;
-            *reinterpret_cast<uint4*>(tile + (c >> 3) * (XROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[k];
-          }
-        }
+        const int w0 = 32 * quad + 16 * par;
         const int rq = lane & 3;                         // the rotated part: 4 lanes of 16 numbers
         const RopeLane rl = rope_lane(a.pv, 8 * rq);
         bool bad = false;
 #pragma unroll 1
-        for (int b0 = 0; b0 < 32; b0 += 8) {
-          const int r = 32 * quad + b0 + (lane >> 2);
-          const bool on = r < rows;
+        for (int b0 = 0; b0 < 16; b0 += 8) {
+          uint4 w[4];                                    // 128 numbers of a row: 16 lanes
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = w0 + b0 + 2 * k + (lane >> 4);
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows) w[k] = *(reinterpret_cast<const uint4*>(q + r * xa.q.token) + (lane & 15));
+          }
+          const int rr = w0 + b0 + (lane >> 2);
+          const bool on = rr < rows;
           uint4 a0 = {}, a1 = {};
           if (on) {
-            const uint4* src = reinterpret_cast<const uint4*>(q + r * xa.q.token + kLatHead) + 2 * rq;
+            const uint4* src = reinterpret_cast<const uint4*>(q + rr * xa.q.token + kLatHead) + 2 * rq;
             a0 = src[0];
             a1 = src[1];
           }
           float2 cs[8];
+          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + r0 + (on ? rr : 0)) * a.pv.n_axes, cs, bad);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = w0 + b0 + 2 * k + (lane >> 4), c = lane & 15;
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * (XROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[k];
+          }
           float x[16];
-          rope_load(a.pv, rl, a.q_pos + (size_t)(s0 + r0 + (on ? r : 0)) * a.pv.n_axes, cs, bad);
           load8_f32<T>(a0, x);
           load8_f32<T>(a1, x + 8);
-          uint32_t w[8];
+          uint32_t v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 y = rope_query(x[2 * e], x[2 * e + 1], cs[e]);
-            w[e] = pack2<T>(y.x, y.y);
+            v[e] = pack2<T>(y.x, y.y);
           }
-          uint8_t* at = tile + 2 * (XROWS * 128) + r * 128;
-          *reinterpret_cast<uint4*>(at + (((2 * rq) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(at + (((2 * rq + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          uint8_t* at = tile + 2 * (XROWS * 128) + rr * 128;
+          *reinterpret_cast<uint4*>(at + (((2 * rq) ^ (rr & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(at + (((2 * rq + 1) ^ (rr & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
         }
         if (bad) atomicOr(&a.pv.state[PST_ERR], DEVERR_POS_RANGE);
         fence_proxy_async_smem();
@@ -242,23 +260,32 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             break;
           }
           tc_fence_after();
-          uint32_t xr[128];
-          tmem_ld_32x32b_x64(s_at, *reinterpret_cast<uint32_t(*)[64]>(xr));
-          tmem_ld_32x32b_x64(s_at + 64, *reinterpret_cast<uint32_t(*)[64]>(xr + 64));
-          const int key0 = (k0 + j) * XKT;
-          if (__any_sync(0xFFFFFFFFu, key0 + XKT > hi || key0 < lo)) {
+          uint32_t xr[64];
+          tmem_ld_32x32b_x64(s_at + 64 * par, xr);
+          const int key0 = (k0 + j) * XKT + 64 * par;
+          if (__any_sync(0xFFFFFFFFu, key0 + 64 > hi || key0 < lo)) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
+            for (int k = 0; k < 64; ++k)
               if (key0 + k >= hi || key0 + k < lo) xr[k] = 0xFF800000u;   // -inf
           }
           const float* s = reinterpret_cast<const float*>(xr);
           float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int k = 4; k < 128; k += 8) {
+          for (int k = 4; k < 60; k += 8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = k + 4 < 128 ? max3f(m4[e], s[k + e], s[(k + 4 + e) & 127]) : fmaxf(m4[e], s[k + e]);
+            for (int e = 0; e < 4; ++e) m4[e] = max3f(m4[e], s[k + e], s[k + 4 + e]);
           }
-          const float mm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rf;
+          // the row's maximum: the other half's keys are the other warp's.  Both
+          // see the same numbers and do the same.
+          const float my = fmaxf(max3f(max3f(m4[0], s[60], s[61]), max3f(m4[1], s[62], s[63]), m4[2]), m4[3]) * rf;
+          *mine = my;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m_ready[2 * pair + par]);
+          if (!warp_wait(&m_ready[2 * pair + (par ^ 1)], tiles & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const float mm = fmaxf(my, *other);
           if (__any_sync(0xFFFFFFFFu, mm > m + kXRaise)) {
             // rare after a row's first keys: what was summed is brought to the new maximum
             const float mn = mm > m + kXRaise ? mm : m;
@@ -268,7 +295,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             if (j > 0) {
               // QK of this tile was issued after the PV before it had completed
 #pragma unroll 1
-              for (int k = 0; k < kLatHead; k += 16) {
+              for (int k = par * 64; k < par * 64 + 64; k += 16) {
                 uint32_t o[16];
                 tmem_ld_32x32b_x16(o_at + k, o);
 #pragma unroll
@@ -277,11 +304,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               }
             }
           }
+          // (both warps hold their scores in registers: P may go over all of S)
           const float sub = m == -INFINITY ? 0.0f : kXTop - m;
           float2 part[2] = {};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16], p1[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 y = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(rf, rf),
@@ -290,8 +318,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               y.y = ex2f(y.y);
               part[e & 1] = add2(part[e & 1], y);
               p[e] = pack2<T>(y.x, y.y);
+              if constexpr (PARTS == 2)
+                p1[e] = pack2<T>(y.x - __uint_as_float(p[e] << 16), y.y - __uint_as_float(p[e] & 0xFFFF0000u));
             }
-            tmem_st_32x32b_x16(s_at + 16 * c, p);
+            tmem_st_32x32b_x16(s_at + 32 * par + 16 * c, p);
+            if constexpr (PARTS == 2) tmem_st_32x32b_x16(s_at + 64 + 32 * par + 16 * c, p1);
           }
           l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
           tmem_st_wait();
@@ -304,20 +335,26 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         tc_fence_after();
         if (*odd_seen && live &&
             nonfinite_among<T>(static_cast<const T*>(xa.v) + (long long)seg.key0 * xa.v_token + (long long)head * xa.v_head,
-                               xa.v_token, max(max(lo, seg.lo), k0 * XKT), min(min(hi, seg.hi), (k0 + n) * XKT), seg.all_lo,
-                               seg.all_hi))
+                               xa.v_token, max(max(lo, seg.lo), k0 * XKT) + par, min(min(hi, seg.hi), (k0 + n) * XKT),
+                               seg.all_lo, seg.all_hi))
           l = __int_as_float(0x7FFFFFFF);                // the row sees one of the values taken out
+        // the row's sum: both halves
+        *mine = l;
+        if (!meet()) break;
+        l = slots[0] + slots[XTR];
+        if (!meet()) break;
       }
       // -------------------------------------------------------- results
       if (rows > 0 && !(flags & XST_SKIP)) {
+        // half of the channels each
         const bool whole = flags & XST_WHOLE;
         const size_t at_row = (size_t)(2 * worker + (flags & XST_HEAD ? 1 : 0)) * XTR + t * XROWS + row;
-        if (!whole && live) a.tiles.ml[at_row] = make_float2(m, l);
+        if (!whole && live && par == 0) a.tiles.ml[at_row] = make_float2(m, l);
         if (whole || n > 0) {
           const float inv = l != 0.0f ? 1.0f / l : 0.0f;
           T* dst = static_cast<T*>(a.out) + (long long)(s0 + i) * xa.o.token + (long long)head * xa.o.head;
 #pragma unroll 1
-          for (int c = 0; c < kLatHead; c += 32) {
+          for (int c = par * 64; c < par * 64 + 64; c += 32) {
             uint32_t o[32];
             if (n > 0) {
               tmem_ld_32x32b_x32(o_at + c, o);
@@ -350,7 +387,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     }
   } else {
     reg_dec<kXOtherRegs>();
-    if (warp == 8) {
+    if (warp == 16) {
       // ====================================================== MMA issue
       if (lane == 0) {
         constexpr uint32_t idesc_qk = make_idesc(FMT, FMT, 0, 0, XROWS, XKT);
@@ -376,9 +413,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         };
         auto pv = [&](int t, int g, uint32_t accumulate) {
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half)
-            mma4_f16_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * half,
-                        make_sdesc_sw128(block(5 * g + 3 + half), XBLK / 2, 1024), idesc_pv, accumulate | half);
+          for (int c = 0; c < 2 * PARTS; ++c)
+            mma4_f16_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * c,
+                        make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
         };
         for (int sg = 0; ok; ++sg) {
           if (!mbar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
@@ -430,7 +467,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         mbar_wait(drain, 0, nullptr, 100000000ull);
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // ====================================================== the line of work
       PieceRec rec = {};
       int done = 0, sg = 0, armed = 0;                   // tiles, stretches; blocks armed
@@ -510,9 +547,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (*abort_flag)
         for (int b = max(0, armed - XRING); b < armed; ++b)
           mbar_wait(&full[b & (XRING - 1)], (b / XRING) & 1, nullptr, 100000000ull);
-    } else if (warp >= 12) {
+    } else if (warp >= 18) {
       // ====================================================== values
-      const int ct = tid - 12 * 32;
+      const int ct = tid - 18 * 32;
       int done = 0;
       bool ok = true;
       for (int sg = 0; ok; ++sg) {
@@ -532,7 +569,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             uint8_t* blk = sm + LY::RING + slot * XBLK;
             bool odd = false;
 #pragma unroll 4
-            for (int c = ct; c < XBLK / 16; c += 128) {   // 16-byte pieces: [2][64 keys][8]
+            for (int c = ct; c < XBLK / 16; c += 64) {   // 16-byte pieces: [2][64 keys][8]
               const int key = t0 + 64 * half + (c >> 3 & 63);
               uint4* at = reinterpret_cast<uint4*>(blk) + c;
               uint4 w = *at;
@@ -558,7 +595,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -572,7 +609,7 @@ static cudaError_t prepare_t() {
   cudaFuncAttributes fa;
   const cudaError_t e = cudaFuncGetAttributes(&fa, latent_expanded_kernel<T>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * XTHREADS < 32 * 8 * (kXSoftmaxRegs + kXOtherRegs)) return cudaErrorInvalidConfiguration;
+  if (fa.numRegs * XTHREADS < 32 * (16 * kXSoftmaxRegs + 4 * kXOtherRegs)) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(latent_expanded_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, XLayout::ALLOC);
 }
 

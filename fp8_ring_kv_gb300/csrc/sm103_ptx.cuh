@@ -431,6 +431,17 @@ __device__ __forceinline__ void tmem_ld2_32x32b_x16(uint32_t a0, uint32_t a1, ui
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld2_32x32b_x8(uint32_t a0, uint32_t a1, uint32_t (&r)[8], uint32_t (&q)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7])
+      : "r"(a0), "r"(a1)
+      : "memory");
+}
+
 // 32x32b.x16: thread t <-> lane t, register i <-> column i, and the wait.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
