@@ -39,6 +39,22 @@ struct ExpandedAttn {
   int32_t n_keys;
 };
 
+// mbar_wait and warp_wait in fewer instructions: these kernels wait in many
+// places, and their roles' loops share the instruction caches.  The limit counts
+// tests, of some tens of cycles to a microsecond each (seconds in all).
+constexpr uint32_t kWaitTests = 1u << 24;
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t tests = 1; !mbar_try_wait(bar, parity); ++tests)
+    if ((tests & 255u) == 0) {
+      if (tests >= kWaitTests) *abort = 1;
+      if (*abort) return false;
+    }
+  return true;
+}
+__device__ __forceinline__ bool bar_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort));
+}
+
 size_t latent_scratch_bytes(int C);
 // pieces of ``rows`` rows of ``width`` numbers
 void latent_carve_scratch(uint8_t* base, int rows, int width, PagedAttn* a);

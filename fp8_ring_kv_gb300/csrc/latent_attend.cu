@@ -237,15 +237,15 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     // every warp of the quarter puts HC numbers (lane c the one of column c) into tops
     auto meet = [&]() -> bool {
       warp_arrive(&tops_in[quarter]);
-      return warp_wait(&tops_in[quarter], n_tops++ & 1, abort_flag);
+      return bar_warp_wait(&tops_in[quarter], n_tops++ & 1, abort_flag);
     };
     auto share = [&](float v) -> bool {
       if (lane < HC) tops[quad * HC + lane] = v;
       return meet();
     };
-    auto pv_done = [&](int g) -> bool { return warp_wait(&free_[(g & 1) * 2 + 1], (g >> 1) & 1, abort_flag); };
+    auto pv_done = [&](int g) -> bool { return bar_warp_wait(&free_[(g & 1) * 2 + 1], (g >> 1) & 1, abort_flag); };
     for (int sg = 0; ok; ++sg) {
-      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile LatStretch& seg = segs[sg & 1];
       const int flags = seg.flags;
       if (!(flags & LST_SOME)) break;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         // the outputs before have left the room
         bulk_wait_read();
         warp_arrive(q_free);
-        if (!warp_wait(q_free, n_q & 1, abort_flag)) break;
+        if (!bar_warp_wait(q_free, n_q & 1, abort_flag)) break;
         if (tid < R) {
           // rows past the last: as the last one, with a factor of 0
           const int i = (r0 + min(tid, rows - 1)) / G;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         }
         fence_proxy_async_smem();
         warp_arrive(q_full);
-        if (!warp_wait(q_full, n_q++ & 1, abort_flag)) break;
+        if (!bar_warp_wait(q_full, n_q++ & 1, abort_flag)) break;
         // ------------------------------------------------------ key tiles
         const int32_t* tab = a.pb.table + seq * a.pb.table_stride;
         auto page = [&](int j) -> int {    // of this thread's key of tile j; -1: not seen
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           const float est = __log2f(st), ist = 1.0f / st;
           const int key = (k0 + j) * LKT + key_row;
           const bool edge = (k0 + j) * LKT < all_lo || (k0 + j + 1) * LKT > all_hi;
-          if (!warp_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag)) {
+          if (!bar_warp_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
             if (lane == 0) fl[quad] = ups;
             warp_arrive(&flags_in[quarter]);
-            if (!warp_wait(&flags_in[quarter], n_flags++ & 1, abort_flag)) {
+            if (!bar_warp_wait(&flags_in[quarter], n_flags++ & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -681,11 +681,11 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     uint32_t n_q = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
-      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile LatStretch& seg = segs[sg & 1];
       if (!(seg.flags & LST_SOME)) break;
       const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
-      if (n > 0 && !warp_wait(q_full, n_q++ & 1, abort_flag)) break;
+      if (n > 0 && !bar_warp_wait(q_full, n_q++ & 1, abort_flag)) break;
       // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
       // can go goes first.  One lane issues; the warp is only called for
       // rows that no query sees (in the first and last tile): their weights are
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         if (ask <= 0) break;
         const int j = __shfl_sync(0xFFFFFFFFu, jq, 0), g = done + j;
         for (int h = 0; h < 2 && ok; ++h)  // (there already: every lane has seen it)
-          ok = warp_wait(&full[(g & 1) * 2 + h], (g >> 1) & 1, abort_flag);
+          ok = bar_warp_wait(&full[(g & 1) * 2 + h], (g >> 1) & 1, abort_flag);
         if (!ok) break;
         // (pages that no query sees came as zeros)
         uint8_t* tile = sm + LY::K + (g & 1) * LY::STAGE;
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
     bool ok = true;
     for (bool more = u < end; ok; ++sg) {
-      if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+      if (sg >= 2 && !bar_warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
       int k0 = 0, k1 = 0;
       long long item_end = 0;
       if (more) {
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint64_t* f = &full[stage * 2 + h];
-          if (g >= 2 && !warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
+          if (g >= 2 && !bar_warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
             ok = false;
             break;
           }

@@ -186,11 +186,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     auto meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(&both[pair]);
-      return warp_wait(&both[pair], nb++ & 1, abort_flag);
+      return bar_warp_wait(&both[pair], nb++ & 1, abort_flag);
     };
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
-      if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+      if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile XStretch& seg = *seg_at(sg);
       const int flags = seg.flags;
       if (!(flags & XST_SOME)) break;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         const float rf = a.scale_log2;
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++tiles) {
-          if (!warp_wait(&s_full[t], tiles & 1, abort_flag)) {
+          if (!bar_warp_wait(&s_full[t], tiles & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           *mine = my;
           __syncwarp();
           if (lane == 0) mbar_arrive(&m_ready[2 * pair + par]);
-          if (!warp_wait(&m_ready[2 * pair + (par ^ 1)], tiles & 1, abort_flag)) {
+          if (!bar_warp_wait(&m_ready[2 * pair + (par ^ 1)], tiles & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[t]);
         }
-        if (ok && !warp_wait(&o_done[t], (tiles - 1) & 1, abort_flag)) ok = false;
+        if (ok && !bar_warp_wait(&o_done[t], (tiles - 1) & 1, abort_flag)) ok = false;
         if (!ok) break;
         tc_fence_after();
         if (*odd_seen && live &&
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
         auto wait_blocks = [&](int b, int n) -> bool {
           for (int k = b; k < b + n; ++k)
-            if (!mbar_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
+            if (!bar_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
           return true;
         };
         auto release = [&](int b, int n) {
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
                         make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
         };
         for (int sg = 0; ok; ++sg) {
-          if (!mbar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+          if (!bar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
           const volatile XStretch& seg = *seg_at(sg);
           if (!(seg.flags & XST_SOME)) break;
           const int n = seg.k1 - seg.k0;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           if (n > 0) {
             ok = wait_blocks(5 * done, 3);
             for (int t = 0; t <= last && ok; ++t) {
-              ok = mbar_wait(&q_full[t], nq[t]++ & 1, abort_flag);
+              ok = bar_wait(&q_full[t], nq[t]++ & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
               qk(t, done);
@@ -438,17 +438,17 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 #pragma unroll 1
           for (int j = 0; j < n && ok; ++j) {
             const int g = done + j;
-            ok = mbar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
+            ok = bar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
 #pragma unroll 1
             for (int t = 0; t <= last && ok; ++t) {
-              ok = mbar_wait(&p_full[t], steps[t] & 1, abort_flag);
+              ok = bar_wait(&p_full[t], steps[t] & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
               pv(t, g, j > 0);
               mma_commit(&o_done[t]);
               if (t == last) release(5 * g + 3, 2);
               if (j + 1 < n) {
-                ok = (t > 0 || wait_blocks(5 * (g + 1), 3)) && mbar_wait(&o_done[t], steps[t] & 1, abort_flag);
+                ok = (t > 0 || wait_blocks(5 * (g + 1), 3)) && bar_wait(&o_done[t], steps[t] & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 qk(t, g + 1);
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       int done = 0, sg = 0, armed = 0;                   // tiles, stretches; blocks armed
       bool ok = true;
       for (bool more = u < end; ok; ++sg) {
-        if (sg >= 2 && !warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+        if (sg >= 2 && !bar_warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
         int k0 = 0, k1 = 0, key0 = 0;
         long long item_end = 0;
         bool skip = false;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           const int b0 = 5 * (done + k - k0), at = key0 + k * XKT;
           for (int c = 0; c < 5; ++c) {
             const int b = b0 + c, slot = b & (XRING - 1);
-            if (b >= XRING && !warp_wait(&free_[slot], ((b - XRING) / XRING) & 1, abort_flag)) {
+            if (b >= XRING && !bar_warp_wait(&free_[slot], ((b - XRING) / XRING) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       int done = 0;
       bool ok = true;
       for (int sg = 0; ok; ++sg) {
-        if (!warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
         const volatile XStretch& seg = *seg_at(sg);
         if (!(seg.flags & XST_SOME)) break;
         const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi, all_lo = seg.all_lo, all_hi = seg.all_hi;
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 #pragma unroll 1
           for (int half = 0; half < 2 && ok; ++half) {
             const int b = 5 * g + 3 + half, slot = b & (XRING - 1);
-            ok = warp_wait(&full[slot], (b / XRING) & 1, abort_flag);
+            ok = bar_warp_wait(&full[slot], (b / XRING) & 1, abort_flag);
             if (!ok) break;
             if (t0 + XKT <= all_hi && t0 >= all_lo) continue;
             uint8_t* blk = sm + LY::RING + slot * XBLK;
