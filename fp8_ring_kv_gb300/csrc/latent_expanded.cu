@@ -56,7 +56,7 @@ struct XLayout {
   static constexpr int SEG = RING + XRING * XBLK;
   static constexpr int SLOT = SEG + 2 * 64;              // [2 halves][256] a row's maxima; sums
   static constexpr int BAR = SLOT + 2 * XTR * 4;
-  static constexpr int NBAR = 2 * XRING + 5 * 2 + 4 + 1 + 16 + 8;
+  static constexpr int NBAR = XRING + 2 * 2 + 5 * 2 + 4 + 1 + 16 + 8;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(sizeof(XStretch) <= 64 && ALLOC <= 232448, "shared memory of a block");
@@ -104,8 +104,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   const PagedAttn& a = xa.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
   uint64_t* full = bars;                   // [XRING] block landed
-  uint64_t* free_ = full + XRING;          // [XRING] every MMA is done with it
-  uint64_t* q_full = free_ + XRING;        // [2 query tiles]
+  uint64_t* k_free = full + XRING;         // [2] (tiles in turn) every MMA is done with K's blocks
+  uint64_t* v_free = k_free + 2;           // [2] and with V's
+  uint64_t* q_full = v_free + 2;           // [2 query tiles]
   uint64_t* s_full = q_full + 2;           // [2] QK done
   uint64_t* p_full = s_full + 2;           // [2] P stored
   uint64_t* o_done = p_full + 2;           // [2] PV done
@@ -123,11 +124,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::RING);        // at first
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::RING + 64);
   if (tid == 0) {
-    for (int i = 0; i < XRING; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&free_[i], 1);
-    }
+    for (int i = 0; i < XRING; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_free[i], 1);
+      mbar_init(&v_free[i], 1);
       mbar_init(&q_full[i], 8);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
@@ -402,8 +402,13 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             if (!bar_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
           return true;
         };
-        auto release = [&](int b, int n) {
-          for (int k = b; k < b + n; ++k) mma_commit(&free_[k & (XRING - 1)]);
+        auto wait_v = [&](int g) -> bool {
+          return bar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
+        };
+        auto there = [&](uint64_t* bar, uint32_t phase) { return mbar_test_wait(bar, phase & 1); };
+        auto there_v = [&](int g) {
+          return there(&v_clean[g & 1], g >> 1) && there(&full[(5 * g + 3) & (XRING - 1)], (5 * g + 3) / XRING) &&
+                 there(&full[(5 * g + 4) & (XRING - 1)], (5 * g + 4) / XRING);
         };
         auto qk = [&](int t, int g) {
 #pragma unroll 1
@@ -433,31 +438,39 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               mma_commit(&s_full[t]);
             }
             if (!ok) break;
-            release(5 * done, 3);
+            mma_commit(&k_free[done & 1]);
           }
+          // What a product waits for is looked at while the one before it runs: a wait
+          // takes this thread hundreds of cycles even where it is over.
+          bool ready = false;
 #pragma unroll 1
           for (int j = 0; j < n && ok; ++j) {
             const int g = done + j;
-            ok = bar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
 #pragma unroll 1
             for (int t = 0; t <= last && ok; ++t) {
-              ok = bar_wait(&p_full[t], steps[t] & 1, abort_flag);
+              if (!ready) ok = (t > 0 || wait_v(g)) && bar_wait(&p_full[t], steps[t] & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
               pv(t, g, j > 0);
               mma_commit(&o_done[t]);
-              if (t == last) release(5 * g + 3, 2);
+              ready = false;
               if (j + 1 < n) {
-                ok = (t > 0 || wait_blocks(5 * (g + 1), 3)) && bar_wait(&o_done[t], steps[t] & 1, abort_flag);
+                if (t == 0) ok = wait_blocks(5 * (g + 1), 3);
+                if (t < last) ready = there(&p_full[1], steps[1]);
+                else if (last > 0) ready = there_v(g + 1) && there(&p_full[0], steps[0]);
+                ok = ok && bar_wait(&o_done[t], steps[t] & 1, abort_flag);
                 if (!ok) break;
+                if (t == last) mbar_arrive(&v_free[g & 1]);
                 tc_fence_after();
                 qk(t, g + 1);
                 mma_commit(&s_full[t]);
-                if (t == last) release(5 * (g + 1), 3);
+                if (t == last) mma_commit(&k_free[(g + 1) & 1]);
               }
               ++steps[t];
             }
           }
+          for (int t = 0; t <= last && n > 0 && ok; ++t) ok = bar_wait(&o_done[t], (steps[t] - 1) & 1, abort_flag);
+          if (ok && n > 0) mbar_arrive(&v_free[(done + n - 1) & 1]);
           if (!ok) break;
           done += n;
           mbar_arrive(&seg_free[sg & 1]);
@@ -518,9 +531,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           const int b0 = 5 * (done + k - k0), at = key0 + k * XKT;
           for (int c = 0; c < 5; ++c) {
             const int b = b0 + c, slot = b & (XRING - 1);
-            if (b >= XRING && !bar_warp_wait(&free_[slot], ((b - XRING) / XRING) & 1, abort_flag)) {
-              ok = false;
-              break;
+            if (b >= XRING) {              // the block that was there: K's or V's of tile o
+              const int o = (b - XRING) / 5;
+              if (!bar_warp_wait(((b - XRING) - 5 * o < 3 ? k_free : v_free) + (o & 1), (o >> 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
             }
             if (lane == 0) {
               uint8_t* dst = sm + LY::RING + slot * XBLK;
