@@ -676,101 +676,84 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     // ======================================================== MMA issue
     constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
     constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
+    // The warp goes together (what it counts by is the same in all lanes), one lane issues.
     const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
+    const uint32_t on = lane == 0, tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    auto there = [&](uint64_t* bar, int phase) -> bool { return same(mbar_test_wait(bar, phase & 1)); };
     int done = 0;
     uint32_t n_q = 0;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
       const volatile LatStretch& seg = segs[sg & 1];
-      if (!(seg.flags & LST_SOME)) break;
-      const int k0 = seg.k0, n = seg.k1 - k0, lo = seg.lo, hi = seg.hi;
+      if (!(same(seg.flags) & LST_SOME)) break;
+      const int k0 = same(seg.k0), n = same(seg.k1) - k0, lo = same(seg.lo), hi = same(seg.hi);
       if (n > 0 && !bar_warp_wait(q_full, n_q++ & 1, abort_flag)) break;
       // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
-      // can go goes first.  One lane issues; the warp is only called for
-      // rows that no query sees (in the first and last tile): their weights are
-      // zeros, which must meet numbers.
-      int jq = 0, jp = 0, cleared = -1;    // the next of either; the last tile cleared
-      for (;;) {
-        int ask = 0;                       // 1: rows to clear, -1: given up
-        if (lane == 0) {
-          unsigned long long t0_ns = 0;
-          uint32_t spins = 0;
-          while (jp < n) {
-            const int gp = done + jp, gq = done + jq;
-            if (jp < jq && mbar_test_wait(&p_full[gp & 1], (gp >> 1) & 1)) {
-              tc_fence_after();
-              const int sp = gp & 1;
-              const uint32_t kt = k_at + sp * LY::STAGE;
-              const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-              const uint32_t go = jp > 0;
+      // can go goes first.
+      int jq = 0, jp = 0;                  // the next of either
+      for (uint32_t tests = 1; jp < n; ++tests) {
+        const int gp = done + jp, gq = done + jq, sp = gp & 1, stage = gq & 1;
+        if (jp < jq && there(&p_full[sp], gp >> 1)) {
+          tc_fence_after();
+          const uint32_t kt = k_at + sp * LY::STAGE;
+          const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+          const uint32_t go = jp > 0;
 #pragma unroll 1
-              for (int c = 0; c < NC; ++c) {
-                const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-                const uint32_t o = tmem + TM_O + 64 * c;
-                mma4_f8_ss(o, ad, b0, idesc_pv, go, 256, 128);
-                if constexpr (R == 64) mma4_f8_ss(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1, 256, 128);
-                else if constexpr (NP == 3) mma4_f8_ss(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1, 256, 64);
-                if (c == 1) mma_commit(&free_[sp * 2]);
+          for (int c = 0; c < NC; ++c) {
+            const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+            const uint32_t o = tm + TM_O + 64 * c;
+            warp_mma4_f8_ss<256, 128>(on, o, ad, b0, idesc_pv, go);
+            if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(on, o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
+            else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(on, o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
+            if (c == 1) warp_mma_commit(on, &free_[sp * 2]);
+          }
+          if (NC == 1) warp_mma_commit(on, &free_[sp * 2]);
+          warp_mma_commit(on, &free_[sp * 2 + 1]);
+          ++jp;
+          tests = 0;
+        } else if (jq < n && jq < jp + 2 && there(&full[stage * 2], gq >> 1) && there(&full[stage * 2 + 1], gq >> 1)) {
+          const uint32_t kt = k_at + stage * LY::STAGE, d = tm + stage * NP * R;
+          const int first = lo - (k0 + jq) * LKT, end = hi - (k0 + jq) * LKT;
+          if (first > 0 || end < LKT) {
+            // Rows that no query sees (in the first and last tile): their weights are
+            // zeros, which must meet numbers.  (Pages of such rows came as zeros.)
+            for (int h = 0; h < 2 && ok; ++h)   // (there already: every lane has seen it)
+              ok = bar_warp_wait(&full[stage * 2 + h], (gq >> 1) & 1, abort_flag);
+            if (!ok) break;
+            uint8_t* tile = sm + LY::K + stage * LY::STAGE;
+            const int P = a.pv.P;
+            auto clear = [&](int r0, int r1) {
+              const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+              for (int r = r0; r < r1; ++r) {
+                if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
+                if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
               }
-              if (NC == 1) mma_commit(&free_[sp * 2]);
-              mma_commit(&free_[sp * 2 + 1]);
-              ++jp;
-              spins = 0;
-            } else if (jq < n && jq < jp + 2 && mbar_test_wait(&full[(gq & 1) * 2], (gq >> 1) & 1) &&
-                       mbar_test_wait(&full[(gq & 1) * 2 + 1], (gq >> 1) & 1)) {
-              const int t0 = (k0 + jq) * LKT, stage = gq & 1;
-              if ((t0 < lo || t0 + LKT > hi) && cleared != jq) {
-                ask = 1;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t kt = k_at + stage * LY::STAGE, d = tmem + stage * NP * R;
+            };
+            if (first > 0) clear(first & -P, first);
+            if (end < LKT) clear(end, min(LKT, (end + P - 1) & -P));
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < NC; ++c)
-                mma4_f8_ss(d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024), make_sdesc_sw128(q_at + c * LY::QC, 16, 1024),
-                           idesc_qk, c, 2, 2);
-              const uint64_t ad = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-              const uint64_t bd = make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512);
-              mma_f8_ss(d, ad, bd, idesc_qk, 1);
-              mma_f8_ss(d, ad + 2, bd + 2, idesc_qk, 1);
-              mma_commit(&s_full[stage]);
-              ++jq;
-              spins = 0;
-            } else if ((++spins & 63u) == 0) {
-              const unsigned long long now = globaltimer_ns();
-              if (spins == 64) t0_ns = now;
-              if (now - t0_ns > kWaitLimitNs) *abort_flag = 1;
-              if (*abort_flag) {
-                ask = -1;
-                break;
-              }
-            }
+          for (int c = 0; c < NC; ++c)
+            warp_mma4_f8_ss<2, 2>(on, d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024),
+                                  make_sdesc_sw128(q_at + c * LY::QC, 16, 1024), idesc_qk, c);
+          warp_mma2_f8_ss<2, 2>(on, d, make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512),
+                                idesc_qk, 1);
+          warp_mma_commit(on, &s_full[stage]);
+          ++jq;
+          tests = 0;
+        } else if ((tests & 255u) == 0) {
+          if (tests >= kWaitTests) *abort_flag = 1;
+          if (same(*abort_flag)) {
+            ok = false;
+            break;
           }
         }
-        ask = __shfl_sync(0xFFFFFFFFu, ask, 0);
-        ok = ask >= 0;
-        if (ask <= 0) break;
-        const int j = __shfl_sync(0xFFFFFFFFu, jq, 0), g = done + j;
-        for (int h = 0; h < 2 && ok; ++h)  // (there already: every lane has seen it)
-          ok = bar_warp_wait(&full[(g & 1) * 2 + h], (g >> 1) & 1, abort_flag);
-        if (!ok) break;
-        // (pages that no query sees came as zeros)
-        uint8_t* tile = sm + LY::K + (g & 1) * LY::STAGE;
-        const int first = lo - (k0 + j) * LKT, end = hi - (k0 + j) * LKT, P = a.pv.P;
-        auto clear = [&](int r0, int r1) {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-          for (int r = r0; r < r1; ++r) {
-            if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
-            if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
-          }
-        };
-        if (first > 0) clear(first & -P, first);
-        if (end < LKT) clear(end, min(LKT, (end + P - 1) & -P));
-        fence_proxy_async_smem();
-        __syncwarp();
-        cleared = j;
       }
       if (!ok) break;
       done += n;

@@ -389,93 +389,103 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     reg_dec<kXOtherRegs>();
     if (warp == 16) {
       // ====================================================== MMA issue
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = make_idesc(FMT, FMT, 0, 0, XROWS, XKT);
-        constexpr uint32_t idesc_pv = make_idesc(FMT, FMT, 0, 1, XROWS, kLatHead);
-        const uint32_t q0 = smem_u32(sm + LY::Q), ring = smem_u32(sm + LY::RING);
-        uint32_t nq[2] = {0, 0}, steps[2] = {0, 0};
-        int done = 0;
-        bool ok = true;
-        auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
-        auto wait_blocks = [&](int b, int n) -> bool {
-          for (int k = b; k < b + n; ++k)
-            if (!bar_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
-          return true;
-        };
-        auto wait_v = [&](int g) -> bool {
-          return bar_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
-        };
-        auto there = [&](uint64_t* bar, uint32_t phase) { return mbar_test_wait(bar, phase & 1); };
-        auto there_v = [&](int g) {
-          return there(&v_clean[g & 1], g >> 1) && there(&full[(5 * g + 3) & (XRING - 1)], (5 * g + 3) / XRING) &&
-                 there(&full[(5 * g + 4) & (XRING - 1)], (5 * g + 4) / XRING);
-        };
-        auto qk = [&](int t, int g) {
+      // The warp goes together (what it counts by is the same in all lanes), one lane issues.
+      constexpr uint32_t idesc_qk = make_idesc(FMT, FMT, 0, 0, XROWS, XKT);
+      constexpr uint32_t idesc_pv = make_idesc(FMT, FMT, 0, 1, XROWS, kLatHead);
+      const uint32_t q0 = smem_u32(sm + LY::Q), ring = smem_u32(sm + LY::RING);
+      const uint32_t on = lane == 0, tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+      uint32_t nq = 0, nq1 = 0, steps0 = 0, steps1 = 0;    // of either query tile
+      int done = 0;
+      bool ok = true;
+      auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
+      auto wait_blocks = [&](int b, int n) -> bool {
+        for (int k = b; k < b + n; ++k)
+          if (!bar_warp_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
+        return true;
+      };
+      auto wait_v = [&](int g) -> bool {
+        return bar_warp_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
+      };
+      auto there = [&](uint64_t* bar, uint32_t phase) -> bool { return same(mbar_test_wait(bar, phase & 1)); };
+      auto there_v = [&](int g) {
+        return there(&v_clean[g & 1], g >> 1) && there(&full[(5 * g + 3) & (XRING - 1)], (5 * g + 3) / XRING) &&
+               there(&full[(5 * g + 4) & (XRING - 1)], (5 * g + 4) / XRING);
+      };
+      auto qk = [&](int t, int g) {
 #pragma unroll 1
-          for (int c = 0; c < 3; ++c)
-            mma4_f16_ss(tmem + TM_S + 128 * t, make_sdesc_sw128(q0 + t * LY::QT + c * (XROWS * 128), 16, 1024),
-                        make_sdesc_sw128(block(5 * g + c), 16, 1024), idesc_qk, c);
-        };
-        auto pv = [&](int t, int g, uint32_t accumulate) {
+        for (int c = 0; c < 3; ++c)
+          warp_mma4_f16_ss(on, tm + TM_S + 128 * t, make_sdesc_sw128(q0 + t * LY::QT + c * (XROWS * 128), 16, 1024),
+                           make_sdesc_sw128(block(5 * g + c), 16, 1024), idesc_qk, c);
+      };
+      auto pv = [&](int t, int g, uint32_t accumulate) {
 #pragma unroll 1
-          for (int c = 0; c < 2 * PARTS; ++c)
-            mma4_f16_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * c,
-                        make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
-        };
-        for (int sg = 0; ok; ++sg) {
-          if (!bar_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
-          const volatile XStretch& seg = *seg_at(sg);
-          if (!(seg.flags & XST_SOME)) break;
-          const int n = seg.k1 - seg.k0;
-          const int last = seg.n - seg.tile * XTR > XROWS ? 1 : 0;   // the second query tile has rows
-          if (n > 0) {
-            ok = wait_blocks(5 * done, 3);
-            for (int t = 0; t <= last && ok; ++t) {
-              ok = bar_wait(&q_full[t], nq[t]++ & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              qk(t, done);
-              mma_commit(&s_full[t]);
-            }
-            if (!ok) break;
-            mma_commit(&k_free[done & 1]);
-          }
-          // What a product waits for is looked at while the one before it runs: a wait
-          // takes this thread hundreds of cycles even where it is over.
-          bool ready = false;
-#pragma unroll 1
-          for (int j = 0; j < n && ok; ++j) {
-            const int g = done + j;
-#pragma unroll 1
-            for (int t = 0; t <= last && ok; ++t) {
-              if (!ready) ok = (t > 0 || wait_v(g)) && bar_wait(&p_full[t], steps[t] & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              pv(t, g, j > 0);
-              mma_commit(&o_done[t]);
-              ready = false;
-              if (j + 1 < n) {
-                if (t == 0) ok = wait_blocks(5 * (g + 1), 3);
-                if (t < last) ready = there(&p_full[1], steps[1]);
-                else if (last > 0) ready = there_v(g + 1) && there(&p_full[0], steps[0]);
-                ok = ok && bar_wait(&o_done[t], steps[t] & 1, abort_flag);
-                if (!ok) break;
-                if (t == last) mbar_arrive(&v_free[g & 1]);
-                tc_fence_after();
-                qk(t, g + 1);
-                mma_commit(&s_full[t]);
-                if (t == last) mma_commit(&k_free[(g + 1) & 1]);
-              }
-              ++steps[t];
-            }
-          }
-          for (int t = 0; t <= last && n > 0 && ok; ++t) ok = bar_wait(&o_done[t], (steps[t] - 1) & 1, abort_flag);
-          if (ok && n > 0) mbar_arrive(&v_free[(done + n - 1) & 1]);
+        for (int c = 0; c < 2 * PARTS; ++c)
+          warp_mma4_f16_ts(on, tm + TM_O + 128 * t, tm + TM_S + 128 * t + 32 * c,
+                           make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
+      };
+      for (int sg = 0; ok; ++sg) {
+        if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile XStretch& seg = *seg_at(sg);
+        if (!(same(seg.flags) & XST_SOME)) break;
+        const int n = same(seg.k1) - same(seg.k0);
+        const int last = same(seg.n) - same(seg.tile) * XTR > XROWS ? 1 : 0;   // the second query tile has rows
+        if (n > 0) {
+          ok = wait_blocks(5 * done, 3) && bar_warp_wait(&q_full[0], nq++ & 1, abort_flag);
           if (!ok) break;
-          done += n;
-          mbar_arrive(&seg_free[sg & 1]);
+          tc_fence_after();
+          qk(0, done);
+          warp_mma_commit(on, &s_full[0]);
+          if (last) {
+            ok = bar_warp_wait(&q_full[1], nq1++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            qk(1, done);
+            warp_mma_commit(on, &s_full[1]);
+          }
+          warp_mma_commit(on, &k_free[done & 1]);
         }
-        // every MMA issued so far is done before the block releases its tensor memory
+        // What a product waits for is looked at while the one before it runs: a wait
+        // takes hundreds of cycles behind products even where it is over.
+        bool ready = false;
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int g = done + j;
+#pragma unroll 1
+          for (int t = 0; t <= last && ok; ++t) {
+            const uint32_t step = t ? steps1 : steps0;
+            if (!ready) ok = (t > 0 || wait_v(g)) && bar_warp_wait(&p_full[t], step & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            pv(t, g, j > 0);
+            warp_mma_commit(on, &o_done[t]);
+            ready = false;
+            if (j + 1 < n) {
+              if (t == 0) ok = wait_blocks(5 * (g + 1), 3);
+              if (t < last) ready = there(&p_full[1], steps1);
+              else if (last > 0) ready = there_v(g + 1) && there(&p_full[0], steps0);
+              ok = ok && bar_warp_wait(&o_done[t], step & 1, abort_flag);
+              if (!ok) break;
+              if (t == last && lane == 0) mbar_arrive(&v_free[g & 1]);
+              __syncwarp();
+              tc_fence_after();
+              qk(t, g + 1);
+              warp_mma_commit(on, &s_full[t]);
+              if (t == last) warp_mma_commit(on, &k_free[(g + 1) & 1]);
+            }
+            if (t) ++steps1;
+            else ++steps0;
+          }
+        }
+        if (ok && n > 0) ok = bar_warp_wait(&o_done[0], (steps0 - 1) & 1, abort_flag);
+        if (ok && n > 0 && last) ok = bar_warp_wait(&o_done[1], (steps1 - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (n > 0 && lane == 0) mbar_arrive(&v_free[(done + n - 1) & 1]);
+        done += n;
+        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
+      }
+      // every MMA issued so far is done before the block releases its tensor memory
+      if (lane == 0) {
         mma_commit(drain);
         mbar_wait(drain, 0, nullptr, 100000000ull);
       }
