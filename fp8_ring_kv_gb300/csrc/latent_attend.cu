@@ -63,7 +63,7 @@ struct LatLayout {
   static constexpr int FLAG = HI + R * 4;                        // [2][16]
   static constexpr int SEG = FLAG + 128;                         // [2]
   static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
-  static constexpr int NBAR = 4 + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
+  static constexpr int NBAR = 2 + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(ALLOC <= 232448, "shared memory of a block");
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = la.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
-  uint64_t* full = bars;                   // [2 stages][2 halves] codes landed: chunks 0 and 1; the others, the rotated part
-  uint64_t* free_ = full + 4;              // [2][2] and every MMA is done with them (the second: PV is done)
+  uint64_t* full = bars;                   // [2 stages] codes landed
+  uint64_t* free_ = full + 2;              // [2][2 halves] every MMA is done with chunks 0 and 1; with all (PV is done)
   uint64_t* s_full = free_ + 4;            // [2] QK done
   uint64_t* p_full = s_full + 2;           // [2] P stored
   uint64_t* q_full = p_full + 2;           // queries written (once per stretch)
@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::MINE);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&full[i], 1);
       mbar_init(&free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 2);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], LSOFT);
       mbar_init(&seg_full[i], 1);
@@ -713,14 +713,13 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           warp_mma_commit(on, &free_[sp * 2 + 1]);
           ++jp;
           tests = 0;
-        } else if (jq < n && jq < jp + 2 && there(&full[stage * 2], gq >> 1) && there(&full[stage * 2 + 1], gq >> 1)) {
+        } else if (jq < n && jq < jp + 2 && there(&full[stage], gq >> 1)) {
           const uint32_t kt = k_at + stage * LY::STAGE, d = tm + stage * NP * R;
           const int first = lo - (k0 + jq) * LKT, end = hi - (k0 + jq) * LKT;
           if (first > 0 || end < LKT) {
             // Rows that no query sees (in the first and last tile): their weights are
             // zeros, which must meet numbers.  (Pages of such rows came as zeros.)
-            for (int h = 0; h < 2 && ok; ++h)   // (there already: every lane has seen it)
-              ok = bar_warp_wait(&full[stage * 2 + h], (gq >> 1) & 1, abort_flag);
+            ok = bar_warp_wait(&full[stage], (gq >> 1) & 1, abort_flag);   // (there already: every lane has seen it)
             if (!ok) break;
             uint8_t* tile = sm + LY::K + stage * LY::STAGE;
             const int P = a.pv.P;
@@ -834,7 +833,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         uint8_t* tile = sm + LY::K + stage * LY::STAGE;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint64_t* f = &full[stage * 2 + h];
+          uint64_t* f = &full[stage];
           if (g >= 2 && !bar_warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
             ok = false;
             break;
@@ -866,9 +865,14 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       more = u < end && next_place<SH, R, LKT>(a, pl, cut.pad);
     }
     if (lane == 0) a.tiles.rec[worker] = rec;
-    // after an abort: copies still in flight land in this block's shared memory
-    if (*abort_flag)
-      for (int b = max(0, armed - 4); b < armed; ++b) mbar_wait(&full[b & 3], (b >> 2) & 1, nullptr, 100000000ull);
+    // After an abort: copies still in flight land in this block's shared memory.  A
+    // tile whose second half was not asked for is completed by an arrival.
+    if (*abort_flag && armed > 0) {
+      const int g = (armed - 1) >> 1;
+      if (lane == 0 && (armed & 1)) mbar_arrive(&full[g & 1]);
+      __syncwarp();
+      for (int t = max(0, g - 1); t <= g; ++t) mbar_wait(&full[t & 1], (t >> 1) & 1, nullptr, 100000000ull);
+    }
   }
   }
   __syncthreads();

@@ -56,7 +56,7 @@ struct XLayout {
   static constexpr int SEG = RING + XRING * XBLK;
   static constexpr int SLOT = SEG + 2 * 64;              // [2 halves][256] a row's maxima; sums
   static constexpr int BAR = SLOT + 2 * XTR * 4;
-  static constexpr int NBAR = XRING + 2 * 2 + 5 * 2 + 4 + 1 + 16 + 8;
+  static constexpr int NBAR = 4 * 2 + 5 * 2 + 4 + 1 + 16 + 8;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(sizeof(XStretch) <= 64 && ALLOC <= 232448, "shared memory of a block");
@@ -103,8 +103,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = xa.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
-  uint64_t* full = bars;                   // [XRING] block landed
-  uint64_t* k_free = full + XRING;         // [2] (tiles in turn) every MMA is done with K's blocks
+  uint64_t* k_full = bars;                 // [2] (tiles in turn) K's three blocks landed
+  uint64_t* v_full = k_full + 2;           // [2] V's two
+  uint64_t* k_free = v_full + 2;           // [2] every MMA is done with K's blocks
   uint64_t* v_free = k_free + 2;           // [2] and with V's
   uint64_t* q_full = v_free + 2;           // [2 query tiles]
   uint64_t* s_full = q_full + 2;           // [2] QK done
@@ -124,8 +125,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::RING);        // at first
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::RING + 64);
   if (tid == 0) {
-    for (int i = 0; i < XRING; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 3);
+      mbar_init(&v_full[i], 2);
       mbar_init(&k_free[i], 1);
       mbar_init(&v_free[i], 1);
       mbar_init(&q_full[i], 8);
@@ -399,19 +401,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       int done = 0;
       bool ok = true;
       auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
-      auto wait_blocks = [&](int b, int n) -> bool {
-        for (int k = b; k < b + n; ++k)
-          if (!bar_warp_wait(&full[k & (XRING - 1)], (k / XRING) & 1, abort_flag)) return false;
-        return true;
-      };
-      auto wait_v = [&](int g) -> bool {
-        return bar_warp_wait(&v_clean[g & 1], (g >> 1) & 1, abort_flag) && wait_blocks(5 * g + 3, 2);
-      };
+      auto wait = [&](uint64_t* bar, uint32_t phase) -> bool { return bar_warp_wait(bar, phase & 1, abort_flag); };
       auto there = [&](uint64_t* bar, uint32_t phase) -> bool { return same(mbar_test_wait(bar, phase & 1)); };
-      auto there_v = [&](int g) {
-        return there(&v_clean[g & 1], g >> 1) && there(&full[(5 * g + 3) & (XRING - 1)], (5 * g + 3) / XRING) &&
-               there(&full[(5 * g + 4) & (XRING - 1)], (5 * g + 4) / XRING);
-      };
       auto qk = [&](int t, int g) {
 #pragma unroll 1
         for (int c = 0; c < 3; ++c)
@@ -431,13 +422,13 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         const int n = same(seg.k1) - same(seg.k0);
         const int last = same(seg.n) - same(seg.tile) * XTR > XROWS ? 1 : 0;   // the second query tile has rows
         if (n > 0) {
-          ok = wait_blocks(5 * done, 3) && bar_warp_wait(&q_full[0], nq++ & 1, abort_flag);
+          ok = wait(&k_full[done & 1], done >> 1) && wait(&q_full[0], nq++);
           if (!ok) break;
           tc_fence_after();
           qk(0, done);
           warp_mma_commit(on, &s_full[0]);
           if (last) {
-            ok = bar_warp_wait(&q_full[1], nq1++ & 1, abort_flag);
+            ok = wait(&q_full[1], nq1++);
             if (!ok) break;
             tc_fence_after();
             qk(1, done);
@@ -454,17 +445,17 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 #pragma unroll 1
           for (int t = 0; t <= last && ok; ++t) {
             const uint32_t step = t ? steps1 : steps0;
-            if (!ready) ok = (t > 0 || wait_v(g)) && bar_warp_wait(&p_full[t], step & 1, abort_flag);
+            if (!ready) ok = (t > 0 || wait(&v_clean[g & 1], g >> 1)) && wait(&p_full[t], step);
             if (!ok) break;
             tc_fence_after();
             pv(t, g, j > 0);
             warp_mma_commit(on, &o_done[t]);
             ready = false;
             if (j + 1 < n) {
-              if (t == 0) ok = wait_blocks(5 * (g + 1), 3);
+              if (t == 0) ok = wait(&k_full[(g + 1) & 1], (g + 1) >> 1);
               if (t < last) ready = there(&p_full[1], steps1);
-              else if (last > 0) ready = there_v(g + 1) && there(&p_full[0], steps0);
-              ok = ok && bar_warp_wait(&o_done[t], step & 1, abort_flag);
+              else if (last > 0) ready = there(&v_clean[(g + 1) & 1], (g + 1) >> 1) && there(&p_full[0], steps0);
+              ok = ok && wait(&o_done[t], step);
               if (!ok) break;
               if (t == last && lane == 0) mbar_arrive(&v_free[g & 1]);
               __syncwarp();
@@ -477,8 +468,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             else ++steps0;
           }
         }
-        if (ok && n > 0) ok = bar_warp_wait(&o_done[0], (steps0 - 1) & 1, abort_flag);
-        if (ok && n > 0 && last) ok = bar_warp_wait(&o_done[1], (steps1 - 1) & 1, abort_flag);
+        if (ok && n > 0) ok = wait(&o_done[0], steps0 - 1);
+        if (ok && n > 0 && last) ok = wait(&o_done[1], steps1 - 1);
         if (!ok) break;
         if (n > 0 && lane == 0) mbar_arrive(&v_free[(done + n - 1) & 1]);
         done += n;
@@ -550,12 +541,13 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             }
             if (lane == 0) {
               uint8_t* dst = sm + LY::RING + slot * XBLK;
-              mbar_arrive_expect_tx(&full[slot], XBLK);
-              if (c < 2) tma_load_3d(dst, &tmK, &full[slot], 64 * c, at, pl.h);
-              else if (c == 2) tma_load_2d(dst, &tmR, &full[slot], 0, at);
+              uint64_t* bar = (c < 3 ? k_full : v_full) + ((done + k - k0) & 1);
+              mbar_arrive_expect_tx(bar, XBLK);
+              if (c < 2) tma_load_3d(dst, &tmK, bar, 64 * c, at, pl.h);
+              else if (c == 2) tma_load_2d(dst, &tmR, bar, 0, at);
               else
                 for (int d = 0; d < 2; ++d)
-                  tma_load_3d(dst + d * (XBLK / 2), &tmV, &full[slot], 64 * d, at + 64 * (c - 3), pl.h);
+                  tma_load_3d(dst + d * (XBLK / 2), &tmV, bar, 64 * d, at + 64 * (c - 3), pl.h);
             }
             __syncwarp();
             armed = b + 1;
@@ -569,10 +561,20 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         more = u < end && next_place<SH, XTR, XKT>(a, pl, cut.pad);
       }
       if (lane == 0) a.tiles.rec[worker] = rec;
-      // after an abort: copies still in flight land in this block's shared memory
-      if (*abort_flag)
-        for (int b = max(0, armed - XRING); b < armed; ++b)
-          mbar_wait(&full[b & (XRING - 1)], (b / XRING) & 1, nullptr, 100000000ull);
+      // After an abort: copies still in flight land in this block's shared memory.  A
+      // tile whose blocks were not all asked for is completed by arrivals.
+      if (*abort_flag && armed > 0) {
+        const int g = (armed - 1) / 5, c = armed - 5 * g;     // the last tile, and how many of its blocks
+        if (lane == 0) {
+          for (int k = c; k < 3; ++k) mbar_arrive(&k_full[g & 1]);
+          for (int k = max(c, 3); k < 5; ++k) mbar_arrive(&v_full[g & 1]);
+        }
+        __syncwarp();
+        for (int t = max(0, g - 1); t <= g; ++t) {
+          mbar_wait(&k_full[t & 1], (t >> 1) & 1, nullptr, 100000000ull);
+          mbar_wait(&v_full[t & 1], (t >> 1) & 1, nullptr, 100000000ull);
+        }
+      }
     } else if (warp >= 18) {
       // ====================================================== values
       const int ct = tid - 18 * 32;
@@ -588,8 +590,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           const int g = done + j, t0 = (k0 + j) * XKT;
 #pragma unroll 1
           for (int half = 0; half < 2 && ok; ++half) {
-            const int b = 5 * g + 3 + half, slot = b & (XRING - 1);
-            ok = bar_warp_wait(&full[slot], (b / XRING) & 1, abort_flag);
+            const int slot = (5 * g + 3 + half) & (XRING - 1);
+            if (half == 0) ok = bar_warp_wait(&v_full[g & 1], (g >> 1) & 1, abort_flag);
             if (!ok) break;
             if (t0 + XKT <= all_hi && t0 >= all_lo) continue;
             uint8_t* blk = sm + LY::RING + slot * XBLK;
