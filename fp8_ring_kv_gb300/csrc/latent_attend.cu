@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile LatStretch* segs = reinterpret_cast<volatile LatStretch*>(sm + LY::SEG);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // (the same in all lanes, for the compiler too)
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::TOP);           // at first
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::MINE);
   if (tid == 0) {
@@ -676,11 +677,11 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     // ======================================================== MMA issue
     constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
     constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
-    // The warp goes together (what it counts by is the same in all lanes), one lane issues.
+    // The warp goes together: what it counts by is the same in all lanes.
     const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
-    const uint32_t on = lane == 0, tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-    auto there = [&](uint64_t* bar, int phase) -> bool { return same(mbar_test_wait(bar, phase & 1)); };
+    auto there = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)); };
     int done = 0;
     uint32_t n_q = 0;
     bool ok = true;
@@ -700,17 +701,18 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           const uint32_t kt = k_at + sp * LY::STAGE;
           const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
           const uint32_t go = jp > 0;
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c >= NC) break;
             const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
             const uint32_t o = tm + TM_O + 64 * c;
-            warp_mma4_f8_ss<256, 128>(on, o, ad, b0, idesc_pv, go);
-            if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(on, o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
-            else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(on, o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
-            if (c == 1) warp_mma_commit(on, &free_[sp * 2]);
+            warp_mma4_f8_ss<256, 128>(o, ad, b0, idesc_pv, go);
+            if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
+            else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
+            if (c == 1) warp_mma_commit(&free_[sp * 2]);
           }
-          if (NC == 1) warp_mma_commit(on, &free_[sp * 2]);
-          warp_mma_commit(on, &free_[sp * 2 + 1]);
+          if (NC == 1) warp_mma_commit(&free_[sp * 2]);
+          warp_mma_commit(&free_[sp * 2 + 1]);
           ++jp;
           tests = 0;
         } else if (jq < n && jq < jp + 2 && there(&full[stage], gq >> 1)) {
@@ -737,13 +739,14 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             __syncwarp();
           }
           tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c)
-            warp_mma4_f8_ss<2, 2>(on, d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024),
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < NC)
+              warp_mma4_f8_ss<2, 2>(d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024),
                                   make_sdesc_sw128(q_at + c * LY::QC, 16, 1024), idesc_qk, c);
-          warp_mma2_f8_ss<2, 2>(on, d, make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512),
+          warp_mma2_f8_ss<2, 2>(d, make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512),
                                 idesc_qk, 1);
-          warp_mma_commit(on, &s_full[stage]);
+          warp_mma_commit(&s_full[stage]);
           ++jq;
           tests = 0;
         } else if ((tests & 255u) == 0) {
@@ -759,10 +762,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
     }
     // every MMA issued so far is done before the block releases its tensor memory
-    if (lane == 0) {
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr, 100000000ull);
-    }
+    warp_mma_commit(drain);
+    mbar_wait(drain, 0, nullptr, 100000000ull);
     __syncwarp();
   } else if (warp == LSOFT + 1) {
     // ======================================================== the line of work

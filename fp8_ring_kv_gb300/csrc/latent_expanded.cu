@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile int* odd_seen = reinterpret_cast<volatile int*>(sm + LY::MISC + 8);   // a value that is no number was taken out
   auto seg_at = [&](int sg) { return reinterpret_cast<volatile XStretch*>(sm + LY::SEG + (sg & 1) * 64); };
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // (the same in all lanes, for the compiler too)
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::RING);        // at first
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::RING + 64);
   if (tid == 0) {
@@ -391,28 +392,28 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     reg_dec<kXOtherRegs>();
     if (warp == 16) {
       // ====================================================== MMA issue
-      // The warp goes together (what it counts by is the same in all lanes), one lane issues.
+      // The warp goes together: what it counts by is the same in all lanes.
       constexpr uint32_t idesc_qk = make_idesc(FMT, FMT, 0, 0, XROWS, XKT);
       constexpr uint32_t idesc_pv = make_idesc(FMT, FMT, 0, 1, XROWS, kLatHead);
       const uint32_t q0 = smem_u32(sm + LY::Q), ring = smem_u32(sm + LY::RING);
-      const uint32_t on = lane == 0, tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
       uint32_t nq = 0, nq1 = 0, steps0 = 0, steps1 = 0;    // of either query tile
       int done = 0;
       bool ok = true;
       auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
       auto wait = [&](uint64_t* bar, uint32_t phase) -> bool { return bar_warp_wait(bar, phase & 1, abort_flag); };
-      auto there = [&](uint64_t* bar, uint32_t phase) -> bool { return same(mbar_test_wait(bar, phase & 1)); };
+      auto there = [&](uint64_t* bar, uint32_t phase) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)); };
       auto qk = [&](int t, int g) {
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 3; ++c)
-          warp_mma4_f16_ss(on, tm + TM_S + 128 * t, make_sdesc_sw128(q0 + t * LY::QT + c * (XROWS * 128), 16, 1024),
+          warp_mma4_f16_ss(tm + TM_S + 128 * t, make_sdesc_sw128(q0 + t * LY::QT + c * (XROWS * 128), 16, 1024),
                            make_sdesc_sw128(block(5 * g + c), 16, 1024), idesc_qk, c);
       };
       auto pv = [&](int t, int g, uint32_t accumulate) {
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 2 * PARTS; ++c)
-          warp_mma4_f16_ts(on, tm + TM_O + 128 * t, tm + TM_S + 128 * t + 32 * c,
+          warp_mma4_f16_ts(tm + TM_O + 128 * t, tm + TM_S + 128 * t + 32 * c,
                            make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
       };
       for (int sg = 0; ok; ++sg) {
@@ -426,15 +427,15 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           if (!ok) break;
           tc_fence_after();
           qk(0, done);
-          warp_mma_commit(on, &s_full[0]);
+          warp_mma_commit(&s_full[0]);
           if (last) {
             ok = wait(&q_full[1], nq1++);
             if (!ok) break;
             tc_fence_after();
             qk(1, done);
-            warp_mma_commit(on, &s_full[1]);
+            warp_mma_commit(&s_full[1]);
           }
-          warp_mma_commit(on, &k_free[done & 1]);
+          warp_mma_commit(&k_free[done & 1]);
         }
         // What a product waits for is looked at while the one before it runs: a wait
         // takes hundreds of cycles behind products even where it is over.
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             if (!ok) break;
             tc_fence_after();
             pv(t, g, j > 0);
-            warp_mma_commit(on, &o_done[t]);
+            warp_mma_commit(&o_done[t]);
             ready = false;
             if (j + 1 < n) {
               if (t == 0) ok = wait(&k_full[(g + 1) & 1], (g + 1) >> 1);
@@ -461,8 +462,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               __syncwarp();
               tc_fence_after();
               qk(t, g + 1);
-              warp_mma_commit(on, &s_full[t]);
-              if (t == last) warp_mma_commit(on, &k_free[(g + 1) & 1]);
+              warp_mma_commit(&s_full[t]);
+              if (t == last) warp_mma_commit(&k_free[(g + 1) & 1]);
             }
             if (t) ++steps1;
             else ++steps0;
@@ -476,10 +477,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
       }
       // every MMA issued so far is done before the block releases its tensor memory
-      if (lane == 0) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, nullptr, 100000000ull);
-      }
+      warp_mma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 100000000ull);
       __syncwarp();
     } else if (warp == 17) {
       // ====================================================== the line of work
