@@ -23,9 +23,8 @@
 //               they also rotate and split the queries and write the output
 //   warp 16     MMA issue; rows of a tile that no query sees become zeros here
 //   warp 17     the line of work, and TMA of the codes
-#include "latent.h"
+#include "latent_sched.cuh"
 #include "launch.h"
-#include "paged_sched.cuh"
 
 namespace kvring_dev {
 
@@ -33,7 +32,8 @@ constexpr int LKT = 128;                     // keys of a tile
 constexpr int LSOFT = 16;                    // softmax warps
 constexpr int LTHREADS = 32 * (LSOFT + 4);  // (whole groups of four warps)
 constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
-constexpr int LFIX = 2;                      // what an item costs beside its tiles, in tiles
+constexpr int LFIX = 4;                      // what an item costs beside its tiles, in tiles
+constexpr int LLEAST = 6, LCUT = 8;           // of the sharing of work (Share)
 constexpr float kLatTop = 4.807354922f;      // log2 28: a column's weights start at 28 ...
 constexpr float kLatRaise = 4.0f;            // ... and may reach 448, e4m3's largest, before its maximum is raised
 constexpr float kNoMax = -1e30f;             // no key yet
@@ -117,10 +117,8 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Ask for a stretch of memory to be brought to the L2.
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
+// Ask for a line of memory to be brought to the L2.
+__device__ __forceinline__ void l2_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
 // Whether one of the 128 threads at named barrier ``id`` says so.  A warp that
 // gives up (the block's abort flag is set before) arrives once more: those that
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
                          const __grid_constant__ LatentAttn la) {
   using LY = LatLayout<T, R>;
   constexpr int NP = LY::NP, HC = LY::HC;
-  using SH = Share<R, LKT, LFIX, 0, 0x7FFFFFFF>;
+  using SH = Share<R, LKT, LFIX, 0, 0x7FFFFFFF, LLEAST, LCUT>;
   constexpr uint32_t TM_O = 256;           // four accumulators of 64 columns
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = la.a;
@@ -172,6 +170,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // (the same in all lanes, for the compiler too)
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::TOP);           // at first
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::MINE);
+  LineOfWork* line = reinterpret_cast<LineOfWork*>(sm + LY::FAC);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&free_[i], 1);
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   long long* pre = reinterpret_cast<long long*>(sm + LY::K);
-  const Cut cut = SH::template prefix<LTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x);
+  const Cut cut = latent_prefix<SH, R, LKT, LFIX, LTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
   const int G = a.pv.G, C = a.pv.D, NC = C >> 7;
   const long long total = pre[a.pb.n_seqs];
   long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
@@ -807,11 +806,12 @@ __global__ void __launch_bounds__(LTHREADS, 1)
       }
       __syncwarp();
       if (!more) break;
-      if (k0 < k1)                         // the queries, for when the softmax warps come to them
+      if (sg > 0 && k0 < k1)               // the queries, for when the softmax warps come to them
         for (int r = lane; r < min(R, pl.s.n * G - pl.tile * R); r += 32) {
           const int rr = pl.tile * R + r, i = rr / G, h = rr - i * G;
-          l2_prefetch(static_cast<const T*>(a.q) + (pl.s.s0 + i) * la.q.token + h * la.q.head, C * 2);
-          l2_prefetch(static_cast<const T*>(la.q_rope) + (pl.s.s0 + i) * la.qr.token + h * la.qr.head, kLatRope * 2);
+          const T* q = static_cast<const T*>(a.q) + (pl.s.s0 + i) * la.q.token + h * la.q.head;
+          for (int c = 0; c < C; c += 64) l2_line(q + c);
+          l2_line(static_cast<const T*>(la.q_rope) + (pl.s.s0 + i) * la.qr.token + h * la.qr.head);
         }
       const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
       // lane i < boxes: the page of its keys of tile k; -1 where no query sees one

@@ -31,9 +31,8 @@
 // QK of the next tile overwrites the P that PV of this one reads, with another
 // accumulator: products of different accumulators have no documented order, so
 // it is issued once that PV has completed.
-#include "latent.h"
+#include "latent_sched.cuh"
 #include "launch.h"
-#include "paged_sched.cuh"
 
 namespace kvring_dev {
 
@@ -125,6 +124,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // (the same in all lanes, for the compiler too)
   unsigned long long* item_sums = reinterpret_cast<unsigned long long*>(sm + LY::RING);        // at first
   long long* warp_sums = reinterpret_cast<long long*>(sm + LY::RING + 64);
+  LineOfWork* line = reinterpret_cast<LineOfWork*>(sm + LY::RING + 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 3);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   long long* pre = reinterpret_cast<long long*>(sm + LY::Q);
-  const Cut cut = SH::template prefix<XTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x);
+  const Cut cut = latent_prefix<SH, XTR, XKT, 2, XTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
   const long long total = pre[a.pb.n_seqs] * a.pv.H;
   long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
   if (stretch < SH::kLeast) stretch = SH::kLeast;

@@ -51,7 +51,7 @@ struct Cut {
 
 // One kernel's share of the sequences: those with rows in (MIN, MAX].  FIX:
 // what an item costs beside its tiles, in tiles.
-template <int TR, int KT, int FIX, int MIN, int MAX>
+template <int TR, int KT, int FIX, int MIN, int MAX, int LEAST = 4, int CUT = 8>
 struct Share {
   // pad: 0, or what every item counts
   static __device__ __forceinline__ int units(const Tiles& t, int pad) {
@@ -134,14 +134,7 @@ struct Share {
     }
     Cut cut = {0, 0};
     if constexpr (FIX > 0) {
-      const long long total = (long long)sums[0] * a.pv.H, items = (long long)sums[1] * a.pv.H;
-      const int most = (int)sums[2];
-      if (items > 0 && items <= workers) {
-        const int per = workers / (int)items;            // workers of an item
-        const int part = max((most + per - 1) / per, kLeast);
-        if (part <= max(quotient(total + workers - 1, workers), (long long)kLeast) + kCut)
-          cut = {(most + part - 1) / part * part, part};
-      }
+      cut = choose((long long)sums[0] * a.pv.H, (long long)sums[1] * a.pv.H, (int)sums[2], workers);
       if (cut.pad) {
         for (int b = tid; b < B; b += NT) {
           bool ok;
@@ -174,6 +167,18 @@ struct Share {
     return cut;
   }
 
+  // How items of ``total`` units, the longest of ``most``, are cut.
+  static __device__ __forceinline__ Cut choose(long long total, long long items, int most, int workers) {
+    Cut cut = {0, 0};
+    if (items > 0 && items <= workers) {
+      const int per = workers / (int)items;              // workers of an item
+      const int part = max((most + per - 1) / per, kLeast);
+      if (part <= max(quotient(total + workers - 1, workers), (long long)kLeast) + kCut)
+        cut = {(most + part - 1) / part * part, part};
+    }
+    return cut;
+  }
+
   // units, items, and the longest item
   static __device__ __forceinline__ void add_items(unsigned long long* sums, long long u, int items, int most) {
     atomicAdd(&sums[0], (unsigned long long)u);
@@ -187,8 +192,8 @@ struct Share {
   // with 4, which cuts there: 107.8; with 12, which does not cut 512 tokens
   // over 16,000: 152.7 instead of 140.7).  Items to themselves take 22.9 us for
   // a prompt of 128 and 38 us for one of 1,024, cut ones 31.6 and 47.
-  static constexpr int kLeast = 4;
-  static constexpr int kCut = 8;
+  static constexpr int kLeast = LEAST;
+  static constexpr int kCut = CUT;
 };
 
 // A place on the line of items: (sequence, key head, row tile), the unit at
