@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           s_next = scale_of(j + 1, pg1);
           pg1 = page(j + 2);
           if (st == 0.0f) st = kLatMinScale;             // a row that was never written: zeros
-          const float est = __log2f(st), ist = 1.0f / st;
+          // a marked token has the scale NaN, and so y and weight, where it is seen
+          const float est = __log2f(st), ist = st == st ? 1.0f / st : 0.0f;
           const int key = (k0 + j) * LKT + key_row;
           const bool edge = (k0 + j) * LKT < all_lo || (k0 + j + 1) * LKT > all_hi;
           if (!bar_warp_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag)) {

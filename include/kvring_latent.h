@@ -131,14 +131,15 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
  *   k_rope   device [n_keys][64], rows k_rope_stride elements apart; rotated
  *            already (as kvring_latent_read gives it)
  *   kv_start device int32 [B]: sequence b's keys are rows kv_start[b] ..
- *            kv_start[b] + kv_len[b] - 1; new token i of n has index kv_len - n + i
+ *            kv_start[b] + kv_len[b] - 1; new token i of n has index kv_len - n + i.
+ *            A sequence whose rows are not all in 0 .. n_keys - 1 (kv_start beyond
+ *            n_keys too) is left out and flagged KVRING_DEVERR_SEQ
  *   out      device [N][q_heads][128]
  *   scale    0: 1 / sqrt(192)
  *   causal, window, max_new   as kvring_paged_attend's
- * Rotated queries and weights are rounded to the inputs' type once; sums and
- * statistics are fp32.  A value that is no number spreads to the rows that see
+ * Rotated queries are rounded to the inputs' type once; weights to fp16, or to a
+ * sum of two bf16 numbers; sums and statistics are fp32.  A value that is no number spreads to the rows that see
  * it, in its channel or in all of the head's, and to no other.
- * A sequence whose keys do not lie in 0 .. n_keys - 1 is left out and flagged.
  */
 int kvring_latent_attend_expanded(kvring_latent* p, const void* q, int64_t q_token, int64_t q_head, const void* k,
                                   int64_t k_token, int64_t k_head, const void* k_rope, int64_t k_rope_token,
