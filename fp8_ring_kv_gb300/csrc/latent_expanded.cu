@@ -402,8 +402,15 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       int done = 0;
       bool ok = true;
       auto block = [&](int b) { return ring + (b & (XRING - 1)) * XBLK; };
-      auto wait = [&](uint64_t* bar, uint32_t phase) -> bool { return bar_warp_wait(bar, phase & 1, abort_flag); };
       auto there = [&](uint64_t* bar, uint32_t phase) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)); };
+      auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+        for (uint32_t tests = 1; !there(bar, phase); ++tests)
+          if ((tests & 255u) == 0) {
+            if (tests >= kWaitTests) *abort_flag = 1;
+            if (same(*abort_flag)) return false;
+          }
+        return true;
+      };
       auto qk = [&](int t, int g) {
 #pragma unroll
         for (int c = 0; c < 3; ++c)
