@@ -68,8 +68,10 @@ cudaError_t prepare_latent_attend();
 cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,
                                  cudaStream_t st);
 
-// the items that several blocks share; pieces of ``rows`` rows of a.pv.D numbers
-cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, bool f16, int blocks, cudaStream_t st);
+// the items that several blocks share: pieces of up to ``rows`` rows of a.pv.D
+// numbers, ``slot_rows`` rows of room each
+cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int slot_rows, int rows, bool f16, int blocks,
+                               cudaStream_t st);
 cudaError_t prepare_latent_expanded();
 // tmK, tmV: [heads][keys][128] in 16 bits, boxes {64, 128, 1} and {64, 64, 1}; tmR: [keys][64], box {64, 128}
 cudaError_t launch_latent_expanded(const ExpandedAttn& xa, const CUtensorMap& tmK, const CUtensorMap& tmR,

@@ -888,7 +888,37 @@ __global__ void __launch_bounds__(LTHREADS, 1)
 // ---------------------------------------------------------------- joining
 // The items that several blocks share (see paged_join), of either form: a warp
 // per row and 128 channels, the pieces in the workers' order.
-constexpr int kLatJoinWarps = 8;
+constexpr int kLatJoinWarps = 8, kLatJoinBlocks = 4;      // blocks of an SM
+static_assert(32 * kLatJoinWarps >= kPagedMaxSms, "a thread per worker");
+struct JoinSum {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float2 ml, const float4& x) {
+    const bool some = ml.x != -INFINITY;                  // else x was not written
+    const float mn = some ? fmaxf(m, ml.x) : m;
+    const float f0 = mn > m ? ex2f(m - mn) : 1.0f, f1 = some ? ex2f(ml.x - mn) : 0.0f;
+    m = mn;
+    l = l * f0 + (some ? ml.y * f1 : ml.y);               // no key: 0; scores all NaN: NaN
+    if (some) {
+      o.x = o.x * f0 + x.x * f1;
+      o.y = o.y * f0 + x.y * f1;
+      o.z = o.z * f0 + x.z * f1;
+      o.w = o.w * f0 + x.w * f1;
+    }
+  }
+};
+
+// What a row's sum holds -> out
+template <typename T>
+__device__ __forceinline__ void join_store(const PagedAttn& a, const Strides& out, const PieceRec& it, int r, int c,
+                                           const JoinSum& s) {
+  const float inv = s.l != 0.0f ? 1.0f / s.l : 0.0f;
+  const int rr = it.row0 + r, i = rr / a.pv.G, h = it.h * a.pv.G + rr - i * a.pv.G;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.s0 + i) * out.token + h * out.head + c) =
+      make_uint2(pack2<T>(s.o.x * inv, s.o.y * inv), pack2<T>(s.o.z * inv, s.o.w * inv));
+}
+
+// Many items, of two or three pieces: blocks (worker, share of its item's rows).
 template <typename T>
 __global__ void __launch_bounds__(32 * kLatJoinWarps)
     latent_join_kernel(const __grid_constant__ PagedAttn a, Strides out, int slot_rows) {
@@ -898,29 +928,88 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps)
   const PieceRec it = a.tiles.rec[w];
   for (int id = blockIdx.y * kLatJoinWarps + (threadIdx.x >> 5); id < it.rows * NC; id += gridDim.y * kLatJoinWarps) {
     const int r = id / NC, c = (id - r * NC) * 128 + lane * 4;
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    JoinSum s = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
 #pragma unroll 8
     for (int p = w; p <= it.last; ++p) {
       const size_t row = (size_t)(2 * p + (p == w ? 1 : 0)) * slot_rows + r;
-      const float2 ml = a.tiles.ml[row];
-      const float4 x = *reinterpret_cast<const float4*>(a.tiles.o + row * C + c);
-      const bool some = ml.x != -INFINITY;                 // else x was not written
-      const float mn = some ? fmaxf(m, ml.x) : m;
-      const float f0 = mn > m ? ex2f(m - mn) : 1.0f, f1 = some ? ex2f(ml.x - mn) : 0.0f;
-      m = mn;
-      l = l * f0 + (some ? ml.y * f1 : ml.y);              // no key: 0; scores all NaN: NaN
-      if (some) {
-        o.x = o.x * f0 + x.x * f1;
-        o.y = o.y * f0 + x.y * f1;
-        o.z = o.z * f0 + x.z * f1;
-        o.w = o.w * f0 + x.w * f1;
+      s.add(a.tiles.ml[row], *reinterpret_cast<const float4*>(a.tiles.o + row * C + c));
+    }
+    join_store<T>(a, out, it, r, c, s);
+  }
+}
+
+// Few items, of many pieces: their rows are dealt out over one wave of blocks, and up
+// to 8 warps have a share of a row's pieces each.
+template <typename T>
+__global__ void __launch_bounds__(32 * kLatJoinWarps, kLatJoinBlocks)
+    latent_join_few_kernel(const __grid_constant__ PagedAttn a, Strides out, int slot_rows, int workers) {
+  __shared__ int upto[32 * kLatJoinWarps], sums[kLatJoinWarps];   // rows x chunks of the workers up to here
+  __shared__ float4 part_o[kLatJoinWarps][32];
+  __shared__ float2 part_ml[kLatJoinWarps];
+  __shared__ PieceRec recs[32 * kLatJoinWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = a.pv.D, NC = C >> 7;
+  int n = 0;
+  if (tid < workers) {
+    recs[tid] = a.tiles.rec[tid];
+    n = recs[tid].rows * NC;
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, n, d);
+    if (lane >= d) n += v;
+  }
+  if (lane == 31) sums[warp] = n;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < kLatJoinWarps; ++i) {
+    if (i < warp) n += sums[i];
+    total += sums[i];
+  }
+  upto[tid] = n;
+  __syncthreads();
+  int bits = 0;                            // 2^bits warps of a row
+  while ((1 << bits) < kLatJoinWarps && (total << (bits + 1)) <= (int)gridDim.x * kLatJoinWarps) ++bits;
+  const int split = 1 << bits, groups = kLatJoinWarps >> bits, part = warp & (split - 1);
+  for (int first = blockIdx.x * groups; first < total; first += gridDim.x * groups) {
+    const int id = first + (warp >> bits);
+    JoinSum s = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    PieceRec it = {};
+    int r = 0, c = 0;
+    if (id < total) {
+      int w = 0;
+#pragma unroll
+      for (int i = 0; i < kLatJoinWarps; ++i) w += __popc(__ballot_sync(0xFFFFFFFFu, upto[32 * i + lane] <= id));
+      const int at = id - (w > 0 ? upto[w - 1] : 0);
+      it = recs[w];
+      r = at / NC;
+      c = (at - r * NC) * 128 + lane * 4;
+      const int pieces = it.last - w + 1;
+      const int end = w + (pieces * (part + 1) >> bits);
+#pragma unroll 1
+      for (int p = w + (pieces * part >> bits); p < end; p += 4) {
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {      // (all loads on their way at once)
+          const size_t row = (size_t)(2 * (p + k) + (p + k == w ? 1 : 0)) * slot_rows + r;
+          ml[k] = p + k < end ? a.tiles.ml[row] : make_float2(-INFINITY, 0.0f);
+          x[k] = p + k < end ? *reinterpret_cast<const float4*>(a.tiles.o + row * C + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s.add(ml[k], x[k]);
       }
     }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    const int rr = it.row0 + r, i = rr / a.pv.G, h = it.h * a.pv.G + rr - i * a.pv.G;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (it.s0 + i) * out.token + h * out.head + c) =
-        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (split > 1) {                       // (one turn of the loop)
+      part_o[warp][lane] = s.o;
+      if (lane == 0) part_ml[warp] = make_float2(s.m, s.l);
+      __syncthreads();
+      if (part > 0 || id >= total) continue;
+      for (int i = 1; i < split; ++i) s.add(part_ml[warp + i], part_o[warp + i][lane]);
+    }
+    if (id < total) join_store<T>(a, out, it, r, c, s);
   }
 }
 
@@ -942,10 +1031,23 @@ void latent_carve_scratch(uint8_t* base, int rows, int width, PagedAttn* a) {
   a->tiles.rec = reinterpret_cast<PieceRec*>(base + slots * width * 4 + slots * 8);
 }
 
-cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int rows, bool f16, int blocks, cudaStream_t st) {
-  const dim3 grid(blocks, (rows * (a.pv.D >> 7) + kLatJoinWarps - 1) / kLatJoinWarps), block(32 * kLatJoinWarps);
-  return f16 ? launch_pdl(latent_join_kernel<__half>, grid, block, 0, st, a, o, rows)
-             : launch_pdl(latent_join_kernel<__nv_bfloat16>, grid, block, 0, st, a, o, rows);
+template <typename T>
+static cudaError_t join_t(const PagedAttn& a, const Strides& o, int slot_rows, int rows, int blocks, cudaStream_t st) {
+  const dim3 block(32 * kLatJoinWarps);
+  // No more items than this.  With four pieces each or more the rows of the few are
+  // dealt out (2 items of 128 heads: 8 us less); with fewer pieces the search for a row
+  // costs more than it gives (40 items, 9 chunks in 152: 3 to 5 us more).
+  const long long G = a.pv.G, by_seq = a.pb.n_seqs * ((a.max_new * G + rows - 1) / rows),
+                  by_row = a.pb.n_seqs + a.pb.n_tokens * G / rows;
+  if ((by_seq < by_row ? by_seq : by_row) * a.pv.H * 4 <= blocks)
+    return launch_pdl(latent_join_few_kernel<T>, dim3(blocks * kLatJoinBlocks), block, 0, st, a, o, slot_rows, blocks);
+  const int shares = (rows * (a.pv.D >> 7) + kLatJoinWarps - 1) / kLatJoinWarps;
+  return launch_pdl(latent_join_kernel<T>, dim3(blocks, shares), block, 0, st, a, o, slot_rows);
+}
+
+cudaError_t launch_latent_join(const PagedAttn& a, const Strides& o, int slot_rows, int rows, bool f16, int blocks,
+                               cudaStream_t st) {
+  return f16 ? join_t<__half>(a, o, slot_rows, rows, blocks, st) : join_t<__nv_bfloat16>(a, o, slot_rows, rows, blocks, st);
 }
 
 template <typename T, int R>
@@ -972,7 +1074,7 @@ static cudaError_t attend_t(const LatentAttn& la, const CUtensorMap& tmC, const 
                             cudaStream_t st) {
   const cudaError_t e = launch_pdl(latent_attend_kernel<T, R>, dim3(blocks), dim3(LTHREADS), LatLayout<T, R>::ALLOC, st,
                                    tmC, tmR, la);
-  return e == cudaSuccess ? launch_latent_join(la.a, la.o, kLatRows, std::is_same_v<T, __half>, blocks, st) : e;
+  return e == cudaSuccess ? launch_latent_join(la.a, la.o, kLatRows, R, std::is_same_v<T, __half>, blocks, st) : e;
 }
 
 cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, const CUtensorMap& tmR, bool f16, int sms,

@@ -663,7 +663,7 @@ cudaError_t launch_latent_expanded(const ExpandedAttn& xa, const CUtensorMap& tm
   const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
   const cudaError_t e = f16 ? expanded_t<__half>(xa, tmK, tmR, tmV, blocks, st)
                             : expanded_t<__nv_bfloat16>(xa, tmK, tmR, tmV, blocks, st);
-  return e == cudaSuccess ? launch_latent_join(xa.a, xa.o, XTR, f16, blocks, st) : e;
+  return e == cudaSuccess ? launch_latent_join(xa.a, xa.o, XTR, XTR, f16, blocks, st) : e;
 }
 
 }  // namespace kvring_dev
