@@ -9,7 +9,7 @@
 //
 // What bounds it: the chain of loads token -> sequence -> page for few tokens (2.4 to
 // 2.7 us warm, 9 cold); for many the bytes (3 (C + 64) a token, each way) behind such
-// chains: 17,600 tokens of 512 + 64 appended in 15 us cold (1.9 TB/s), 107,000 rows
+// chains: 16,662 tokens of 512 + 64 appended in 15 us cold (1.9 TB/s), 92,383 rows
 // read back in 34 (4.7 TB/s, 70% of a copy's rate).
 #include "latent.h"
 #include "launch.h"
@@ -20,7 +20,7 @@ constexpr int kRowWarps = 8;
 // Rows of a warp, their chains of loads side by side; one where there are few rows,
 // whose warps all run at once.  Append, one and four rows (us, warm): 777 tokens 2.4
 // and 3.2, 4,000 tokens 4.0 and 3.5, 9,600 tokens 6.7 and 4.6.  Read, one, two and four
-// (cold): 107,000 rows 38, 34 and 36.
+// (cold): 92,000 rows 38, 34 and 36.
 constexpr int kAppendRows = 4, kReadRows = 2, kFewRows = 2 * kRowWarps * 152;
 
 // Where a packed row belongs.  page < 0: nowhere.

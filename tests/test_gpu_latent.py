@@ -117,6 +117,9 @@ APPENDS = [
     dict(seqs=[(131, 130), (64, 64), (2, 31)], page=32, axes=3, latent=384),
     dict(seqs=[(300, 1), (128, 128), (127, 1), (1, 127)], page=128, latent=512, dtype=HF),
     dict(seqs=[(i % 3, i) for i in range(150)], page=16, latent=128),
+    # more rows than go one to a warp; sequences without tokens between them
+    dict(seqs=[(700, 0), (0, 5), (1, 3000), (2, 0)] + [(0, 0)] * 40 + [(1, i) for i in range(43)], page=16, latent=256),
+    dict(seqs=[(2999, 4), (1, 6), (0, 0), (3, 1)], page=128, latent=512, axes=3, dtype=HF),
 ]
 
 
@@ -138,6 +141,37 @@ def test_append_and_read_bit_for_bit(case, pieces):
         assert bool((out[:int(start[-1]), :c.C + ROPE].cpu() == want).all())
         assert bool((out[int(start[-1]):] == 7).all()) and bool((out[:, c.C + ROPE:] == 7).all())
     assert c.kv.debug_state() == 0
+
+
+def test_bad_pages_and_lengths_among_many_rows():
+    """Rows of several sequences in one warp, some of them nowhere."""
+    from fp8_ring_kv_gb300 import kvring as K
+    c = Case([(3, 0)] * 900 + [(0, 0)] * 5 + [(50, 0)] * 6, latent=128, page=16)
+    start, ln, pos = c.batch(c.seqs)
+    x, r = c.draw(c.n, 128), c.draw(c.n, ROPE)
+    x[2500, 3] = float("nan")
+    table, bad_len = c.table.copy(), ln.copy()
+    table[7, 0], table[300, 0], table[907, 1] = -1, c.n_pages, 2 ** 31 - 1
+    bad_len[5], bad_len[899] = 2, -1                       # fewer than the new tokens
+    lost = np.zeros(c.n, bool)
+    for b in (5, 7, 300, 899):
+        lost[start[b]:start[b + 1]] = True
+    lost[start[907] + 16:start[907] + 32] = True
+    keep = [b for b in range(len(ln)) if b not in (5, 7, 300, 899)]
+    c.kv.append(x.cuda(), r.cuda(), cu(pos), cu(start), cu(bad_len), cu(table))
+    assert c.kv.debug_state() == K.KVRING_DEVERR_SEQ | K.KVRING_DEVERR_PAGE
+    c.oracle.append(num(x), num(r), pos, start, ln, c.table)
+    want = torch.from_numpy(c.oracle.read(start, ln, c.table)).to(c.dtype)
+    for b in (5, 7, 300, 899):
+        c.oracle.codes[c.table[b, 0]], c.oracle.scales[c.table[b, 0]] = 0, 0
+    c.oracle.codes[c.table[907, 1]], c.oracle.scales[c.table[907, 1]] = 0, 0
+    c.check_cache()
+    out = torch.full((c.n + 2, c.C + ROPE), 7.0, dtype=c.dtype, device="cuda")
+    c.kv.read(cu(start), cu(bad_len), cu(table), out=out)
+    out = out.cpu()
+    assert bool((out[c.n:] == 7).all()) and bool((out[:c.n][lost] == 7).all()) and len(keep) == 907
+    good = out[:c.n][~lost]
+    assert bool(torch.isnan(out[2500]).all()) and bool(((good == want[~lost]) | torch.isnan(want[~lost])).all())
 
 
 def test_sizes_of_rows():
