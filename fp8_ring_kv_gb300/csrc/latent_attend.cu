@@ -18,6 +18,19 @@
 // Numbers below 2^-6 of e4m3's scale lose bits: what is lost is below 2^-18 of
 // the row's largest query number, or of its largest weight.
 //
+// 64 query rows of an item, or 32 (fp16's three parts; and calls of at most 32 rows a
+// sequence, where half of 64 would be empty: single tokens of 20 to 32 heads).  More
+// would take the tensor memory that S needs, O of 512 channels being 64 columns a
+// chunk of 128 channels.
+//
+// What bounds it: an instruction of 128 rows takes some 60 cycles whatever its
+// columns up to 128, 50 of them a tile (18 QK, 32 PV): 3,000 cycles; the tile takes
+// 4,300, since the next but one is loaded (2,900 cycles) only once PV has left its
+// stage, and the softmax (2,200) overlaps one tile's products.  64 contexts of 200 to
+// 8,000, 64 heads: 72 us; 2 of 100,000 to 131,000, 128 heads: 87 us (0.73 PFLOP/s of
+// attention, 1.5 in products of codes); 9 chunks of 2 to 131 tokens, 32 heads,
+// window 1,024: 103 us.
+//
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15  softmax: a key per thread, of a quarter of the columns (warp / 4);
 //               they also rotate and split the queries and write the output
@@ -32,8 +45,10 @@ constexpr int LKT = 128;                     // keys of a tile
 constexpr int LSOFT = 16;                    // softmax warps
 constexpr int LTHREADS = 32 * (LSOFT + 4);  // (whole groups of four warps)
 constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
-constexpr int LFIX = 4;                      // what an item costs beside its tiles, in tiles
-constexpr int LLEAST = 6, LCUT = 8;           // of the sharing of work (Share)
+// Of the sharing of work (Share): what an item costs beside its tiles (queries and
+// results, 16,000 cycles), in tiles; units of a stretch at least; from what a cut is
+// worth it (16 tokens over 2,000, 64 heads: 53 us; with 8: 60).
+constexpr int LFIX = 4, LLEAST = 6, LCUT = 4;
 constexpr float kLatTop = 4.807354922f;      // log2 28: a column's weights start at 28 ...
 constexpr float kLatRaise = 4.0f;            // ... and may reach 448, e4m3's largest, before its maximum is raised
 constexpr float kNoMax = -1e30f;             // no key yet
@@ -672,210 +687,210 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     bulk_wait();
     if (*abort_flag) quarter_leave(1 + quarter);
   } else {
-  reg_dec<kLatOtherRegs>();
-  if (warp == LSOFT) {
-    // ======================================================== MMA issue
-    constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
-    constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
-    // The warp goes together: what it counts by is the same in all lanes.
-    const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-    auto there = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)); };
-    int done = 0;
-    uint32_t n_q = 0;
-    bool ok = true;
-    for (int sg = 0; ok; ++sg) {
-      if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
-      const volatile LatStretch& seg = segs[sg & 1];
-      if (!(same(seg.flags) & LST_SOME)) break;
-      const int k0 = same(seg.k0), n = same(seg.k1) - k0, lo = same(seg.lo), hi = same(seg.hi);
-      if (n > 0 && !bar_warp_wait(q_full, n_q++ & 1, abort_flag)) break;
-      // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
-      // can go goes first.
-      int jq = 0, jp = 0;                  // the next of either
-      for (uint32_t tests = 1; jp < n; ++tests) {
-        const int gp = done + jp, gq = done + jq, sp = gp & 1, stage = gq & 1;
-        if (jp < jq && there(&p_full[sp], gp >> 1)) {
-          tc_fence_after();
-          const uint32_t kt = k_at + sp * LY::STAGE;
-          const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
-          const uint32_t go = jp > 0;
+    reg_dec<kLatOtherRegs>();
+    if (warp == LSOFT) {
+      // ======================================================== MMA issue
+      constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
+      constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
+      // The warp goes together: what it counts by is the same in all lanes.
+      const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+      auto there = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)); };
+      int done = 0;
+      uint32_t n_q = 0;
+      bool ok = true;
+      for (int sg = 0; ok; ++sg) {
+        if (!bar_warp_wait(&seg_full[sg & 1], (sg >> 1) & 1, abort_flag)) break;
+        const volatile LatStretch& seg = segs[sg & 1];
+        if (!(same(seg.flags) & LST_SOME)) break;
+        const int k0 = same(seg.k0), n = same(seg.k1) - k0, lo = same(seg.lo), hi = same(seg.hi);
+        if (n > 0 && !bar_warp_wait(q_full, n_q++ & 1, abort_flag)) break;
+        // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
+        // can go goes first.
+        int jq = 0, jp = 0;                  // the next of either
+        for (uint32_t tests = 1; jp < n; ++tests) {
+          const int gp = done + jp, gq = done + jq, sp = gp & 1, stage = gq & 1;
+          if (jp < jq && there(&p_full[sp], gp >> 1)) {
+            tc_fence_after();
+            const uint32_t kt = k_at + sp * LY::STAGE;
+            const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+            const uint32_t go = jp > 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c >= NC) break;
-            const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-            const uint32_t o = tm + TM_O + 64 * c;
-            warp_mma4_f8_ss<256, 128>(o, ad, b0, idesc_pv, go);
-            if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
-            else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
-            if (c == 1) warp_mma_commit(&free_[sp * 2]);
-          }
-          if (NC == 1) warp_mma_commit(&free_[sp * 2]);
-          warp_mma_commit(&free_[sp * 2 + 1]);
-          ++jp;
-          tests = 0;
-        } else if (jq < n && jq < jp + 2 && there(&full[stage], gq >> 1)) {
-          const uint32_t kt = k_at + stage * LY::STAGE, d = tm + stage * NP * R;
-          const int first = lo - (k0 + jq) * LKT, end = hi - (k0 + jq) * LKT;
-          if (first > 0 || end < LKT) {
-            // Rows that no query sees (in the first and last tile): their weights are
-            // zeros, which must meet numbers.  (Pages of such rows came as zeros.)
-            ok = bar_warp_wait(&full[stage], (gq >> 1) & 1, abort_flag);   // (there already: every lane has seen it)
-            if (!ok) break;
-            uint8_t* tile = sm + LY::K + stage * LY::STAGE;
-            const int P = a.pv.P;
-            auto clear = [&](int r0, int r1) {
-              const uint4 zero = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 4; ++c) {
+              if (c >= NC) break;
+              const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
+              const uint32_t o = tm + TM_O + 64 * c;
+              warp_mma4_f8_ss<256, 128>(o, ad, b0, idesc_pv, go);
+              if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
+              else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
+              if (c == 1) warp_mma_commit(&free_[sp * 2]);
+            }
+            if (NC == 1) warp_mma_commit(&free_[sp * 2]);
+            warp_mma_commit(&free_[sp * 2 + 1]);
+            ++jp;
+            tests = 0;
+          } else if (jq < n && jq < jp + 2 && there(&full[stage], gq >> 1)) {
+            const uint32_t kt = k_at + stage * LY::STAGE, d = tm + stage * NP * R;
+            const int first = lo - (k0 + jq) * LKT, end = hi - (k0 + jq) * LKT;
+            if (first > 0 || end < LKT) {
+              // Rows that no query sees (in the first and last tile): their weights are
+              // zeros, which must meet numbers.  (Pages of such rows came as zeros.)
+              ok = bar_warp_wait(&full[stage], (gq >> 1) & 1, abort_flag);   // (there already: every lane has seen it)
+              if (!ok) break;
+              uint8_t* tile = sm + LY::K + stage * LY::STAGE;
+              const int P = a.pv.P;
+              auto clear = [&](int r0, int r1) {
+                const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-              for (int r = r0; r < r1; ++r) {
-                if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
-                if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
-              }
-            };
-            if (first > 0) clear(first & -P, first);
-            if (end < LKT) clear(end, min(LKT, (end + P - 1) & -P));
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          tc_fence_after();
+                for (int r = r0; r < r1; ++r) {
+                  if (lane < 8 * NC) *reinterpret_cast<uint4*>(tile + (lane >> 3) * LY::CB + r * 128 + (lane & 7) * 16) = zero;
+                  if (lane < 4) *reinterpret_cast<uint4*>(tile + 4 * LY::CB + r * 64 + lane * 16) = zero;
+                }
+              };
+              if (first > 0) clear(first & -P, first);
+              if (end < LKT) clear(end, min(LKT, (end + P - 1) & -P));
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < NC)
-              warp_mma4_f8_ss<2, 2>(d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024),
-                                  make_sdesc_sw128(q_at + c * LY::QC, 16, 1024), idesc_qk, c);
-          warp_mma2_f8_ss<2, 2>(d, make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512),
-                                idesc_qk, 1);
-          warp_mma_commit(&s_full[stage]);
-          ++jq;
-          tests = 0;
-        } else if ((tests & 255u) == 0) {
-          if (tests >= kWaitTests) *abort_flag = 1;
-          if (same(*abort_flag)) {
-            ok = false;
-            break;
-          }
-        }
-      }
-      if (!ok) break;
-      done += n;
-      if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
-    }
-    // every MMA issued so far is done before the block releases its tensor memory
-    warp_mma_commit(drain);
-    mbar_wait(drain, 0, nullptr, 100000000ull);
-    __syncwarp();
-  } else if (warp == LSOFT + 1) {
-    // ======================================================== the line of work
-    PieceRec rec = {};
-    const int P = a.pv.P, boxes = LKT / P;
-    const bool alone = (long long)a.max_new * G <= R;    // every key is read by one item only
-    const uint64_t once = l2_evict_first();
-    int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
-    bool ok = true;
-    for (bool more = u < end; ok; ++sg) {
-      if (sg >= 2 && !bar_warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
-      int k0 = 0, k1 = 0;
-      long long item_end = 0;
-      if (more) {
-        item_end = pl.at + pl.units;
-        const int n = pl.t.t1 - pl.t.t0;
-        k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - LFIX));
-        k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - LFIX));
-      }
-      if (lane == 0) {
-        volatile LatStretch& seg = segs[sg & 1];
-        if (more) {
-          const bool head = u == pl.at;
-          const int i0 = pl.tile * R / G, i1 = min(pl.s.n - 1, (pl.tile * R + R - 1) / G);
-          seg.b = pl.b;
-          seg.s0 = pl.s.s0;
-          seg.n = pl.s.n;
-          seg.len = pl.s.len;
-          seg.lo = pl.t.lo;
-          seg.hi = pl.t.hi;
-          seg.all_hi = a.causal ? pl.s.len - pl.s.n + i0 + 1 : pl.s.len;
-          seg.all_lo = a.window > 0 ? pl.s.len - pl.s.n + i1 - a.window + 1 : 0;
-          seg.k0 = k0;
-          seg.k1 = k1;
-          seg.tile = pl.tile;
-          seg.flags = LST_SOME | (head ? LST_HEAD : 0) | (head && end >= item_end ? LST_WHOLE : 0);
-        } else {
-          seg.flags = 0;
-        }
-        mbar_arrive(&seg_full[sg & 1]);
-      }
-      __syncwarp();
-      if (!more) break;
-      if (sg > 0 && k0 < k1)               // the queries, for when the softmax warps come to them
-        for (int r = lane; r < min(R, pl.s.n * G - pl.tile * R); r += 32) {
-          const int rr = pl.tile * R + r, i = rr / G, h = rr - i * G;
-          const T* q = static_cast<const T*>(a.q) + (pl.s.s0 + i) * la.q.token + h * la.q.head;
-          for (int c = 0; c < C; c += 64) l2_line(q + c);
-          l2_line(static_cast<const T*>(la.q_rope) + (pl.s.s0 + i) * la.qr.token + h * la.qr.head);
-        }
-      const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
-      // lane i < boxes: the page of its keys of tile k; -1 where no query sees one
-      auto page = [&](int k) -> int {
-        const int key = k * LKT + lane * P;
-        if (lane >= boxes || k >= k1 || key >= pl.t.hi || key + P <= pl.t.lo) return -1;
-        const int pg = tab[key >> a.pv.p_shift];
-        if (pg < 0 || pg >= a.pv.n_pages) {
-          atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
-          return 0;
-        }
-        return pg;
-      };
-      int pg = page(k0);
-      for (int k = k0; k < k1; ++k) {
-        const int g = done + k - k0, stage = g & 1;
-        const int next = page(k + 1);
-        // (a page that no query sees: past the last row, where TMA finds zeros)
-        const int y = pg >= 0 ? (int)a.pv.row0 + (pg << a.pv.p_shift) : la.code_rows;
-        uint8_t* tile = sm + LY::K + stage * LY::STAGE;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint64_t* f = &full[stage];
-          if (g >= 2 && !bar_warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int c1 = min(NC, 2 * h + 2), chunks = max(0, c1 - 2 * h);
-          if (lane == 0) mbar_arrive_expect_tx(f, LKT * (chunks * 128 + h * kLatRope));
-          __syncwarp();
-          if (lane < boxes) {
-            for (int c = 2 * h; c < c1; ++c) {
-              uint8_t* dst = tile + c * LY::CB + lane * P * 128;
-              if (alone) tma_load_2d_hint(dst, &tmC, f, c * 128, y, once);
-              else tma_load_2d(dst, &tmC, f, c * 128, y);
-            }
-            if (h == 1) {
-              uint8_t* dst = tile + 4 * LY::CB + lane * P * kLatRope;
-              if (alone) tma_load_2d_hint(dst, &tmR, f, C, y, once);
-              else tma_load_2d(dst, &tmR, f, C, y);
+            for (int c = 0; c < 4; ++c)
+              if (c < NC)
+                warp_mma4_f8_ss<2, 2>(d, make_sdesc_sw128(kt + c * LY::CB, 16, 1024),
+                                    make_sdesc_sw128(q_at + c * LY::QC, 16, 1024), idesc_qk, c);
+            warp_mma2_f8_ss<2, 2>(d, make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), make_sdesc_sw64(q_at + 4 * LY::QC, 16, 512),
+                                  idesc_qk, 1);
+            warp_mma_commit(&s_full[stage]);
+            ++jq;
+            tests = 0;
+          } else if ((tests & 255u) == 0) {
+            if (tests >= kWaitTests) *abort_flag = 1;
+            if (same(*abort_flag)) {
+              ok = false;
+              break;
             }
           }
-          armed = g * 2 + h + 1;
         }
         if (!ok) break;
-        pg = next;
+        done += n;
+        if (lane == 0) mbar_arrive(&seg_free[sg & 1]);
       }
-      done += k1 - k0;
-      if (u == pl.at && end < item_end)
-        rec = {min(pl.s.n * G - pl.tile * R, R), (int)quotient(item_end - 1, stretch), 0, pl.s.s0, pl.tile * R};
-      u = min(end, item_end);
-      more = u < end && next_place<SH, R, LKT>(a, pl, cut.pad);
-    }
-    if (lane == 0) a.tiles.rec[worker] = rec;
-    // After an abort: copies still in flight land in this block's shared memory.  A
-    // tile whose second half was not asked for is completed by an arrival.
-    if (*abort_flag && armed > 0) {
-      const int g = (armed - 1) >> 1;
-      if (lane == 0 && (armed & 1)) mbar_arrive(&full[g & 1]);
+      // every MMA issued so far is done before the block releases its tensor memory
+      warp_mma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 100000000ull);
       __syncwarp();
-      for (int t = max(0, g - 1); t <= g; ++t) mbar_wait(&full[t & 1], (t >> 1) & 1, nullptr, 100000000ull);
+    } else if (warp == LSOFT + 1) {
+      // ======================================================== the line of work
+      PieceRec rec = {};
+      const int P = a.pv.P, boxes = LKT / P;
+      const bool alone = (long long)a.max_new * G <= R;    // every key is read by one item only
+      const uint64_t once = l2_evict_first();
+      int done = 0, sg = 0, armed = 0;                     // tiles, stretches; barriers armed
+      bool ok = true;
+      for (bool more = u < end; ok; ++sg) {
+        if (sg >= 2 && !bar_warp_wait(&seg_free[sg & 1], ((sg - 2) >> 1) & 1, abort_flag)) break;
+        int k0 = 0, k1 = 0;
+        long long item_end = 0;
+        if (more) {
+          item_end = pl.at + pl.units;
+          const int n = pl.t.t1 - pl.t.t0;
+          k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - LFIX));
+          k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - LFIX));
+        }
+        if (lane == 0) {
+          volatile LatStretch& seg = segs[sg & 1];
+          if (more) {
+            const bool head = u == pl.at;
+            const int i0 = pl.tile * R / G, i1 = min(pl.s.n - 1, (pl.tile * R + R - 1) / G);
+            seg.b = pl.b;
+            seg.s0 = pl.s.s0;
+            seg.n = pl.s.n;
+            seg.len = pl.s.len;
+            seg.lo = pl.t.lo;
+            seg.hi = pl.t.hi;
+            seg.all_hi = a.causal ? pl.s.len - pl.s.n + i0 + 1 : pl.s.len;
+            seg.all_lo = a.window > 0 ? pl.s.len - pl.s.n + i1 - a.window + 1 : 0;
+            seg.k0 = k0;
+            seg.k1 = k1;
+            seg.tile = pl.tile;
+            seg.flags = LST_SOME | (head ? LST_HEAD : 0) | (head && end >= item_end ? LST_WHOLE : 0);
+          } else {
+            seg.flags = 0;
+          }
+          mbar_arrive(&seg_full[sg & 1]);
+        }
+        __syncwarp();
+        if (!more) break;
+        if (sg > 0 && k0 < k1)               // the queries, for when the softmax warps come to them
+          for (int r = lane; r < min(R, pl.s.n * G - pl.tile * R); r += 32) {
+            const int rr = pl.tile * R + r, i = rr / G, h = rr - i * G;
+            const T* q = static_cast<const T*>(a.q) + (pl.s.s0 + i) * la.q.token + h * la.q.head;
+            for (int c = 0; c < C; c += 64) l2_line(q + c);
+            l2_line(static_cast<const T*>(la.q_rope) + (pl.s.s0 + i) * la.qr.token + h * la.qr.head);
+          }
+        const int32_t* tab = a.pb.table + pl.b * a.pb.table_stride;
+        // lane i < boxes: the page of its keys of tile k; -1 where no query sees one
+        auto page = [&](int k) -> int {
+          const int key = k * LKT + lane * P;
+          if (lane >= boxes || k >= k1 || key >= pl.t.hi || key + P <= pl.t.lo) return -1;
+          const int pg = tab[key >> a.pv.p_shift];
+          if (pg < 0 || pg >= a.pv.n_pages) {
+            atomicOr(&a.pv.state[PST_ERR], DEVERR_PAGE);
+            return 0;
+          }
+          return pg;
+        };
+        int pg = page(k0);
+        for (int k = k0; k < k1; ++k) {
+          const int g = done + k - k0, stage = g & 1;
+          const int next = page(k + 1);
+          // (a page that no query sees: past the last row, where TMA finds zeros)
+          const int y = pg >= 0 ? (int)a.pv.row0 + (pg << a.pv.p_shift) : la.code_rows;
+          uint8_t* tile = sm + LY::K + stage * LY::STAGE;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint64_t* f = &full[stage];
+            if (g >= 2 && !bar_warp_wait(&free_[stage * 2 + h], ((g - 2) >> 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const int c1 = min(NC, 2 * h + 2), chunks = max(0, c1 - 2 * h);
+            if (lane == 0) mbar_arrive_expect_tx(f, LKT * (chunks * 128 + h * kLatRope));
+            __syncwarp();
+            if (lane < boxes) {
+              for (int c = 2 * h; c < c1; ++c) {
+                uint8_t* dst = tile + c * LY::CB + lane * P * 128;
+                if (alone) tma_load_2d_hint(dst, &tmC, f, c * 128, y, once);
+                else tma_load_2d(dst, &tmC, f, c * 128, y);
+              }
+              if (h == 1) {
+                uint8_t* dst = tile + 4 * LY::CB + lane * P * kLatRope;
+                if (alone) tma_load_2d_hint(dst, &tmR, f, C, y, once);
+                else tma_load_2d(dst, &tmR, f, C, y);
+              }
+            }
+            armed = g * 2 + h + 1;
+          }
+          if (!ok) break;
+          pg = next;
+        }
+        done += k1 - k0;
+        if (u == pl.at && end < item_end)
+          rec = {min(pl.s.n * G - pl.tile * R, R), (int)quotient(item_end - 1, stretch), 0, pl.s.s0, pl.tile * R};
+        u = min(end, item_end);
+        more = u < end && next_place<SH, R, LKT>(a, pl, cut.pad);
+      }
+      if (lane == 0) a.tiles.rec[worker] = rec;
+      // After an abort: copies still in flight land in this block's shared memory.  A
+      // tile whose second half was not asked for is completed by an arrival.
+      if (*abort_flag && armed > 0) {
+        const int g = (armed - 1) >> 1;
+        if (lane == 0 && (armed & 1)) mbar_arrive(&full[g & 1]);
+        __syncwarp();
+        for (int t = max(0, g - 1); t <= g; ++t) mbar_wait(&full[t & 1], (t >> 1) & 1, nullptr, 100000000ull);
+      }
     }
-  }
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&a.pv.state[PST_ERR], DEVERR_TIMEOUT);
@@ -1081,6 +1096,8 @@ cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, c
                                  cudaStream_t st) {
   const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
   if (f16) return attend_t<__half, 32>(la, tmC, tmR, blocks, st);
+  // (items of 32 rows and of 64: one token of 32 heads over 900 30 and 38 us, 32 over
+  // 1,000 to 4,000 39 and 46)
   if ((long long)la.a.max_new * la.a.pv.G <= 32) return attend_t<__nv_bfloat16, 32>(la, tmC, tmR, blocks, st);
   return attend_t<__nv_bfloat16, 64>(la, tmC, tmR, blocks, st);
 }

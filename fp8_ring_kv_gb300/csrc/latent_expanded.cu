@@ -16,8 +16,11 @@
 // bf16 numbers, two products into one O (S leaves room for both).
 //
 // What bounds it: the tensor pipe (128 keys of 256 rows: 24 steps of 128 x 128 x
-// 16 for S and 16 (bf16: 32) for PV, 64 cycles each, 2,560 (3,584)), beside
-// which 32,768 exponentials take 2,048 cycles.
+// 16 for S and 16 (bf16: 32) for PV of each tile, 64 cycles each, 2,560 (3,584)); beside
+// it the tile takes some 5,000 cycles in bf16, mostly pauses between a PV and the
+// QK that overwrites its weights (below).  512 queries over 16,001 keys, 20
+// heads: 126 us (0.85 PFLOP/s of attention, 44% of what cuBLAS reaches in bf16, and
+// 1.6 times that in products); 3 prompts of 1,000 to 4,096, 32 heads, causal: 353.
 //
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15   softmax: of query tile t and half p of its keys, warps 8 p + 4 t
@@ -39,6 +42,11 @@ namespace kvring_dev {
 constexpr int XKT = 128, XROWS = 128, XTR = kTilesRows, XTHREADS = 640;
 static_assert(XTR == 2 * XROWS);
 constexpr int kXSoftmaxRegs = 104, kXOtherRegs = 64;   // per thread: 16 warps and 4
+// Of the sharing of work (Share): what an item costs beside its tiles (queries and
+// results, 15,000 cycles), in tiles (3 prompts of 1,000 to 4,096, 32 heads: 353 us;
+// with 2: 382, with 8: 368); units of a stretch at least; and from what a cut is worth
+// it (2 sequences of 100 to 2,000 over 3,000: 64 us, with 8: 73).
+constexpr int XFIX = 5, XLEAST = 6, XCUT = 3;
 constexpr int XRING = 8, XBLK = 16384;       // blocks of K (128 keys x 64 numbers) and V (64 keys x 128)
 constexpr float kXRaise = 8.0f;              // a row's maximum is raised when a tile exceeds it by 2^8 ...
 constexpr float kXTop = 6.0f;                // ... and starts its weights at 2^6, so they stay below 2^14 in fp16
@@ -95,7 +103,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     latent_expanded_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmR,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ExpandedAttn xa) {
   using LY = XLayout;
-  using SH = Share<XTR, XKT, 2, 0, 0x7FFFFFFF>;
+  using SH = Share<XTR, XKT, XFIX, 0, 0x7FFFFFFF, XLEAST, XCUT>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr uint32_t FMT = std::is_same_v<T, __half> ? 0 : 1;
   constexpr int PARTS = std::is_same_v<T, __half> ? 1 : 2;      // of a weight
@@ -500,8 +508,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (more) {
           item_end = pl.at + pl.units;
           const int n = pl.t.t1 - pl.t.t0;
-          k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - 2));
-          k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - 2));
+          k0 = pl.t.t0 + (int)max(0ll, min((long long)n, u - pl.at - XFIX));
+          k1 = pl.t.t0 + (int)max(0ll, min((long long)n, min(end, item_end) - pl.at - XFIX));
           key0 = a.pb.table[pl.b];
           skip = key0 < 0 || (long long)key0 + pl.s.len > xa.n_keys;
           if (skip) {
