@@ -41,7 +41,7 @@ struct ExpandedAttn {
 
 // mbar_wait and warp_wait in fewer instructions: these kernels wait in many
 // places, and their roles' loops share the instruction caches.  The limit counts
-// tests, of some tens of cycles to a microsecond each (seconds in all).
+// tests, of some tens of cycles to a microsecond each (a third of a second at least).
 constexpr uint32_t kWaitTests = 1u << 24;
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   for (uint32_t tests = 1; !mbar_try_wait(bar, parity); ++tests)

@@ -110,6 +110,18 @@ __device__ __forceinline__ uint32_t split2(uint32_t& v) {
   return c;
 }
 
+// What fp16 numbers v leave of x0 and x1, to be added to what the first part leaves of v:
+// three parts have a bit more than fp16 (its rounding alone was as much as that of an
+// fp16 output).  Two have less, and go by way of fp16 as it is.
+__device__ __forceinline__ uint32_t left_of(uint32_t v, float x0, float x1) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return cvt_f16x2(x0 - f.x, x1 - f.y);
+}
+__device__ __forceinline__ void add_left(uint32_t& v, uint32_t left) {
+  const __half2 sum = __hadd2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&left));
+  v = *reinterpret_cast<const uint32_t*>(&sum);
+}
+
 __device__ __forceinline__ float warp_maxf(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -336,9 +348,12 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         }
         // x * inv in parts: 16 codes of each to ``at`` + part * ``step``
         auto put = [&](const float* x, float inv, uint8_t* at, int step) {
-          uint32_t v[8];
+          uint32_t v[8], left[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = cvt_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+          for (int e = 0; e < 8; ++e) {
+            v[e] = cvt_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+            if (NP == 3) left[e] = left_of(v[e], x[2 * e] * inv, x[2 * e + 1] * inv);
+          }
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t c[4];
@@ -346,6 +361,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             for (int e = 0; e < 4; ++e) {
               const uint32_t c0 = split2(v[2 * e]), c1 = split2(v[2 * e + 1]);
               c[e] = c0 | c1 << 16;
+              if (NP == 3 && p == 0) {
+                add_left(v[2 * e], left[2 * e]);
+                add_left(v[2 * e + 1], left[2 * e + 1]);
+              }
             }
             *reinterpret_cast<uint4*>(at + p * step) = make_uint4(c[0], c[1], c[2], c[3]);
           }
@@ -551,9 +570,12 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             l[c] = t.x;
             l[c + 1] = t.y;
           }
-          uint32_t v[HC / 2];
+          uint32_t v[HC / 2], left[HC / 2];
 #pragma unroll
-          for (int c = 0; c < HC / 2; ++c) v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
+          for (int c = 0; c < HC / 2; ++c) {
+            v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
+            if (NP == 3) left[c] = left_of(v[c], x[2 * c], x[2 * c + 1]);
+          }
           uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
           uint8_t* extra = sm + LY::P;
 #pragma unroll
@@ -563,6 +585,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             for (int c = 0; c < HC / 4; ++c) {
               const uint32_t c0 = split2(v[2 * c]), c1 = split2(v[2 * c + 1]);
               w[c] = c0 | c1 << 16;
+              if (NP == 3 && p == 0) {
+                add_left(v[2 * c], left[2 * c]);
+                add_left(v[2 * c + 1], left[2 * c + 1]);
+              }
             }
             // PV of the tile before is done with the room that is there once
             if (LY::PB > 0 && p == NP - 1 && g > 0 && !pv_done(g - 1)) {

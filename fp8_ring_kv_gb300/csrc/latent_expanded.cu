@@ -11,13 +11,14 @@
 // key part is a third block of K's tile, read where it lies, so no head's keys
 // are written out 192 wide.
 //
-// A bf16 weight would be off by as much as the bf16 output is rounded by, and
-// over many keys of like weight all of that shows: bf16 weights are the sum of two
-// bf16 numbers, two products into one O (S leaves room for both).
+// A weight of the inputs' type would be off by as much as the output is rounded by,
+// and over many keys of like weight all of that shows (1.6 times the output's own
+// rounding, with the rotated queries'; 1.3 without it): weights are the sum of two such
+// numbers, two products into one O (S leaves room for both).
 //
 // What bounds it: the tensor pipe (128 keys of 256 rows: 24 steps of 128 x 128 x
-// 16 for S and 16 (bf16: 32) for PV of each tile, 64 cycles each, 2,560 (3,584)); beside
-// it the tile takes some 5,000 cycles in bf16, mostly pauses between a PV and the
+// 16 for S and 32 for PV of each tile, 64 cycles each, 3,584); the tile takes some 5,000
+// cycles, the difference mostly pauses between a PV and the
 // QK that overwrites its weights (below).  512 queries over 16,001 keys, 20
 // heads: 126 us (0.85 PFLOP/s of attention, 44% of what cuBLAS reaches in bf16, and
 // 1.6 times that in products); 3 prompts of 1,000 to 4,096, 32 heads, causal: 353.
@@ -70,6 +71,12 @@ struct XLayout {
   static_assert(2 * QT >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the query tiles at first");
 };
 
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // The 16-bit numbers of w that are no numbers become zeros; true where there was one.
 template <typename T>
 __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
@@ -106,7 +113,6 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   using SH = Share<XTR, XKT, XFIX, 0, 0x7FFFFFFF, XLEAST, XCUT>;
   constexpr uint32_t TM_S = 0, TM_O = 256;
   constexpr uint32_t FMT = std::is_same_v<T, __half> ? 0 : 1;
-  constexpr int PARTS = std::is_same_v<T, __half> ? 1 : 2;      // of a weight
   extern __shared__ __align__(1024) uint8_t sm[];
   const PagedAttn& a = xa.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR);
@@ -329,11 +335,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               y.y = ex2f(y.y);
               part[e & 1] = add2(part[e & 1], y);
               p[e] = pack2<T>(y.x, y.y);
-              if constexpr (PARTS == 2)
-                p1[e] = pack2<T>(y.x - __uint_as_float(p[e] << 16), y.y - __uint_as_float(p[e] & 0xFFFF0000u));
+              const float2 first = unpack2<T>(p[e]);
+              p1[e] = pack2<T>(y.x - first.x, y.y - first.y);
             }
             tmem_st_32x32b_x16(s_at + 32 * par + 16 * c, p);
-            if constexpr (PARTS == 2) tmem_st_32x32b_x16(s_at + 64 + 32 * par + 16 * c, p1);
+            tmem_st_32x32b_x16(s_at + 64 + 32 * par + 16 * c, p1);
           }
           l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
           tmem_st_wait();
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       };
       auto pv = [&](int t, int g, uint32_t accumulate) {
 #pragma unroll
-        for (int c = 0; c < 2 * PARTS; ++c)
+        for (int c = 0; c < 4; ++c)
           warp_mma4_f16_ts(tm + TM_O + 128 * t, tm + TM_S + 128 * t + 32 * c,
                            make_sdesc_sw128(block(5 * g + 3 + (c & 1)), XBLK / 2, 1024), idesc_pv, accumulate | c);
       };

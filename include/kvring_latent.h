@@ -137,8 +137,8 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
  *   out      device [N][q_heads][128]
  *   scale    0: 1 / sqrt(192)
  *   causal, window, max_new   as kvring_paged_attend's
- * Rotated queries are rounded to the inputs' type once; weights to fp16, or to a
- * sum of two bf16 numbers; sums and statistics are fp32.  A value that is no number spreads to the rows that see
+ * Rotated queries are rounded to the inputs' type once; weights are sums of two
+ * numbers of it; sums and statistics are fp32.  A value that is no number spreads to the rows that see
  * it, in its channel or in all of the head's, and to no other.
  */
 int kvring_latent_attend_expanded(kvring_latent* p, const void* q, int64_t q_token, int64_t q_head, const void* k,
