@@ -49,8 +49,12 @@ constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
 // results, 16,000 cycles), in tiles; units of a stretch at least; from what a cut is
 // worth it (16 tokens over 2,000, 64 heads: 53 us; with 8: 60).
 constexpr int LFIX = 4, LLEAST = 6, LCUT = 4;
-constexpr float kLatTop = 4.807354922f;      // log2 28: a column's weights start at 28 ...
-constexpr float kLatRaise = 4.0f;            // ... and may reach 448, e4m3's largest, before its maximum is raised
+// A column's weights start at 28 (fp16: 112) and may reach 448, e4m3's largest, before
+// its maximum is raised.  The step of the smallest numbers, 2^-9, is what fp16 loses most
+// by (from 28: errors up to 1.4 times the output's own rounding, from 112: 1.02); a higher
+// start is raised more often (24 contexts of 300 to 5,000, 20 heads: 36.5 us, from 28 35.5).
+template <typename T> constexpr float kTop = std::is_same_v<T, __half> ? 6.807354922f : 4.807354922f;
+constexpr float kLatMost = 8.807354922f;     // log2 448
 constexpr float kNoMax = -1e30f;             // no key yet
 
 struct LatStretch {
@@ -72,7 +76,7 @@ struct LatLayout {
   static constexpr int P = Q + 4 * QC + NP * R * kLatRope;
   static constexpr int PB = R == 64 ? LKT * 64 : NP == 3 ? LKT * 32 : 0;
   static constexpr int TOP = P + PB;                             // [4][4][HC] column maxima, sums
-  static constexpr int MINE = TOP + LSOFT * HC * 4;              // [warps][HC] reference - kLatTop; 1 / l
+  static constexpr int MINE = TOP + LSOFT * HC * 4;              // [warps][HC] reference - kTop; 1 / l
   static constexpr int FAC = MINE + LSOFT * HC * 4;                  // [R] logit factors
   static constexpr int HI = FAC + R * 4;                         // [R] keys below are seen
   static constexpr int FLAG = HI + R * 4;                        // [2][16]
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             most1 = max3f(most1, x[c + 2], x[c + 3]);
           }
           most = fmaxf(most, most1);
-          const bool raise = quarter_any(1 + quarter, most > kLatTop + kLatRaise);
+          const bool raise = quarter_any(1 + quarter, most > kLatMost);
           if (*abort_flag) {
             ok = false;
             break;
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           if (raise) {
             uint32_t ups = 0;              // columns whose maximum is raised
 #pragma unroll
-            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatTop + kLatRaise ? 1u << c : 0u;
+            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatMost ? 1u << c : 0u;
             ups = __reduce_or_sync(0xFFFFFFFFu, ups);
             volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
             if (lane == 0) fl[quad] = ups;
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             }
             float al = 1.0f, shift = 0.0f;
             if (lane < HC && (ups >> lane & 1)) {
-              top = fmaxf(fmaxf(tops[lane], tops[HC + lane]), fmaxf(tops[2 * HC + lane], tops[3 * HC + lane])) - kLatTop;
+              top = fmaxf(fmaxf(tops[lane], tops[HC + lane]), fmaxf(tops[2 * HC + lane], tops[3 * HC + lane])) - kTop<T>;
               const float was = mine[lane];
               shift = fresh ? top - was : top;
               mine[lane] = fresh ? top : was + top;

@@ -3,6 +3,7 @@ worst case of every term at once, and as a root mean square."""
 import numpy as np
 
 U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}                   # half a step of the type, relative
+START = {"bf16": 28, "f16": 112}                             # a row's largest weight, at least
 
 
 def absorbed(r, kind):
@@ -18,13 +19,13 @@ def absorbed(r, kind):
     those times the |k| they meet, a weight by twice that with its sum.
 
     Weights are split the same way, times their token's scale,
-    at a scale where the largest of a part of the row is at least 28: the floor is
-    2^-10 / 28 of the row's largest product.  fp32 sums of 576 products and some
+    at a scale where the largest of a part of the row is at least 28 (fp16: 112): the
+    floor is 2^-10 / 28 of the row's largest product.  fp32 sums of 576 products and some
     thousand keys: 2^-16 of the terms is generous.  Then the output's rounding."""
     step = 2.0 ** -8 + 2.0 ** -11 if kind == "bf16" else 2.0 ** -12 + 2.0 ** -14
     logit = step * r.turned + 2.0 ** -17.8 * r.ones + 2.0 ** -18 * r.all
     weight = step + 2.0 ** -16
-    bound = r.spread * (np.expm1(2 * logit)[..., None] + weight) + r.floor * 2.0 ** -10 / 28
+    bound = r.spread * (np.expm1(2 * logit)[..., None] + weight) + r.floor * 2.0 ** -10 / START[kind]
     return _rounded(bound, r, kind)
 
 
@@ -49,5 +50,5 @@ def absorbed_rms(r, kind):
     step = 2.0 ** -8 + 2.0 ** -11 if kind == "bf16" else 2.0 ** -12 + 2.0 ** -14
     logit = step * r.turned + 2.0 ** -17.8 * r.ones
     square = r.square * (step ** 2 / 3 + (4 * logit[..., None] ** 2) / 3) + r.out ** 2 * U[kind] ** 2 / 3 \
-        + (r.spread * 2.0 ** -16) ** 2 + (r.floor * 2.0 ** -10 / 28) ** 2 / 3 / 64
+        + (r.spread * 2.0 ** -16) ** 2 + (r.floor * 2.0 ** -10 / START[kind]) ** 2 / 3 / 64
     return float(np.sqrt(square.mean()))
