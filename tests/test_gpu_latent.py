@@ -378,17 +378,18 @@ def test_tokens_of_very_different_size(dtype, heads):
     assert c.kv.debug_state() == 0
 
 
-def test_maxima_that_rise_late():
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_maxima_that_rise_late(dtype):
     """Keys whose logits grow from tile to tile: the reference is raised again and
     again, by a little and by much."""
-    c = Case([(2, 1500)], heads=40, latent=128)
+    c = Case([(2, 1500)], heads=40, latent=128, dtype=dtype)
     total = c.len[0]
     x = (c.g.standard_normal((total, 128)) * 0.3).astype(np.float32)
     way = c.g.standard_normal(128).astype(np.float32)
     grow = np.repeat(np.cumsum(c.g.choice([0, 0.5, 3.0], total // 100 + 1)), 100)[:total]
     x += grow[:, None].astype(np.float32) * way / np.linalg.norm(way)
-    c.append([(total, 0)], torch.from_numpy(x).to(BF), c.draw(total, ROPE) * 0.1)
-    q = torch.from_numpy((c.g.uniform(0, 12, (2, 40, 1)) * way).astype(np.float32)).to(BF)
+    c.append([(total, 0)], torch.from_numpy(x).to(dtype), c.draw(total, ROPE) * 0.1)
+    q = torch.from_numpy((c.g.uniform(0, 12, (2, 40, 1)) * way).astype(np.float32)).to(dtype)
     c.attend(q=q, qr=c.draw(2, 40, ROPE) * 0.1)
     assert c.kv.debug_state() == 0
 
