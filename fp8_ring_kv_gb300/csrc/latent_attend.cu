@@ -9,14 +9,25 @@
 //
 // A cached row is key and value: its codes lie in shared memory once, as TMA
 // left them (128 keys x 128 channels, 128-byte swizzle), and are read K-major by
-// QK and MN-major by PV.  Both products are e4m3 x e4m3, exact in fp32: a bf16
-// query has 8 bits and is the sum of two e4m3 numbers of 4, hi = e4m3(q) and
-// lo = e4m3(q - hi) (fp16: three), at a power-of-two scale of its row; a weight
-// is split the same way.  Two products at the 8-bit rate cost what one costs in
-// 16 bits, and nothing is widened: a 16-bit copy of a 128 x 576 tile would be 147
-// KB of shared memory and its conversion half of the tensor cores' time.
-// Numbers below 2^-6 of e4m3's scale lose bits: what is lost is below 2^-18 of
-// the row's largest query number, or of its largest weight.
+// QK and MN-major by PV.  The products are of 8-bit numbers, exact in fp32, and
+// nothing is widened: a 16-bit copy of a 128 x 576 tile would be 147 KB of shared
+// memory and its conversion half of the tensor cores' time.
+//
+// A bf16 query has 8 bits and is the sum of two e4m3 numbers of 4, hi = e4m3(q) and
+// lo = e4m3(q - hi) (fp16: three), at a power-of-two scale of its row.  e4m3's
+// smallest step is 2^-9, so what is lost is below 2^-10 / 224 of the row's largest
+// number.
+//
+// A weight has no such neighbours: beside one key with most of a row's weight
+// thousands of others share the rest, each a millionth, and they are not to be lost
+// together (sums of e4m3 numbers at one scale lose what is below 2^-14.8 of the
+// largest: of 8,000 keys beside one of 0.9 most of the other 0.1).
+//   bf16: three e5m2 numbers of 3 bits, each of what the ones before leave.  From a
+//   column's largest weight, 3584 to 57344, down to 2^-16, e5m2's smallest step: off by
+//   2^-9 of a weight, or 2^-17, 2^-28.8 of the largest.
+//   fp16: e4m3 and e5m2 of what is left, and the same again of 256 times the rest, in
+//   an accumulator of its own: 4 + 3 + 4 + 3 bits; down to 2^-21 beside a largest weight of
+//   112 to 448, 2^-27.8 of it.
 //
 // 64 query rows of an item, or 32 (fp16's three parts; and calls of at most 32 rows a
 // sequence, where half of 64 would be empty: single tokens of 20 to 32 heads).  More
@@ -24,12 +35,14 @@
 // chunk of 128 channels.
 //
 // What bounds it: an instruction of 128 rows takes some 60 cycles whatever its
-// columns up to 128, 50 of them a tile (18 QK, 32 PV): 3,000 cycles; the tile takes
-// 4,300, since the next but one is loaded (2,900 cycles) only once PV has left its
-// stage, and the softmax (2,200) overlaps one tile's products.  64 contexts of 200 to
-// 8,000, 64 heads: 72 us; 2 of 100,000 to 131,000, 128 heads: 87 us (0.73 PFLOP/s of
-// attention, 1.5 in products of codes); 9 chunks of 2 to 131 tokens, 32 heads,
-// window 1,024: 103 us.
+// columns up to 128, 66 of them a tile of 64 query rows (18 QK, 48 PV): 4,000 cycles.
+// The tile takes 5,600: the next but one is loaded (2,900 cycles) only once PV has left
+// its stage, the softmax (2,200) overlaps one tile's products, and its warps wait for the
+// first part's (1,300) to put the third in its room: shared memory has no other.  64
+// contexts of 200 to 8,000, 64 heads: 84 us; 2 of 100,000 to 131,000, 128 heads: 105 us
+// (0.60 PFLOP/s of attention, 1.5 in products of codes); 9 chunks of 2 to 131 tokens, 32
+// heads, window 1,024: 119 us.  (With two e4m3 parts a weight, which lost small ones: 72,
+// 88 and 103.)
 //
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15  softmax: a key per thread, of a quarter of the columns (warp / 4);
@@ -49,12 +62,13 @@ constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
 // results, 16,000 cycles), in tiles; units of a stretch at least; from what a cut is
 // worth it (16 tokens over 2,000, 64 heads: 53 us; with 8: 60).
 constexpr int LFIX = 4, LLEAST = 6, LCUT = 4;
-// A column's weights start at 28 (fp16: 112) and may reach 448, e4m3's largest, before
-// its maximum is raised.  The step of the smallest numbers, 2^-9, is what fp16 loses most
-// by (from 28: errors up to 1.4 times the output's own rounding, from 112: 1.02); a higher
-// start is raised more often (24 contexts of 300 to 5,000, 20 heads: 36.5 us, from 28 35.5).
-template <typename T> constexpr float kTop = std::is_same_v<T, __half> ? 6.807354922f : 4.807354922f;
-constexpr float kLatMost = 8.807354922f;     // log2 448
+// A column's largest weight starts at 1/16 of its first part's largest number, 57344 of
+// e5m2 (fp16: 1/4 of 448, e4m3's), and may reach that before its maximum is raised.  A higher
+// start has less below the smallest steps and is raised more often (24 contexts of 300 to
+// 5,000, 20 heads, fp16: 36.5 us, from 1/16 35.5).
+template <typename T> constexpr float kTop = std::is_same_v<T, __half> ? 6.807354922f : 11.807354922f;
+template <typename T> constexpr float kLatMost = std::is_same_v<T, __half> ? 8.807354922f : 15.807354922f;
+constexpr float kRestScale = 256.0f;         // of an fp16 column's second accumulator
 constexpr float kNoMax = -1e30f;             // no key yet
 
 struct LatStretch {
@@ -64,7 +78,8 @@ enum : int { LST_SOME = 1, LST_WHOLE = 2, LST_HEAD = 4 };
 
 template <typename T, int R>
 struct LatLayout {
-  static constexpr int NP = std::is_same_v<T, __half> ? 3 : 2;   // e4m3 parts of a query and of a weight
+  static constexpr bool HALF = std::is_same_v<T, __half>;
+  static constexpr int NP = HALF ? 3 : 2;                        // e4m3 parts of a query
   static constexpr int HC = R / 4;                               // columns of a softmax warp
   static constexpr int CB = LKT * 128, RB = LKT * kLatRope;      // a chunk of 128 channels, the rotated part
   static constexpr int STAGE = 4 * CB + RB;
@@ -72,9 +87,10 @@ struct LatLayout {
   static constexpr int K = 0;                                    // [2 stages]
   static constexpr int Q = K + 2 * STAGE;                        // (then the outputs on their way)
   // Weights: 64 bytes a key where the rotated part was (QK is done with it): 64
-  // columns' first part, or 32 columns' first and second.  The next part:
+  // columns' first part, and their third once that is used; or 32 columns' two first
+  // parts (fp16: of either accumulator).  The others':
   static constexpr int P = Q + 4 * QC + NP * R * kLatRope;
-  static constexpr int PB = R == 64 ? LKT * 64 : NP == 3 ? LKT * 32 : 0;
+  static constexpr int PB = R == 64 || HALF ? LKT * 64 : LKT * 32;
   static constexpr int TOP = P + PB;                             // [4][4][HC] column maxima, sums
   static constexpr int MINE = TOP + LSOFT * HC * 4;              // [warps][HC] reference - kTop; 1 / l
   static constexpr int FAC = MINE + LSOFT * HC * 4;                  // [R] logit factors
@@ -82,14 +98,14 @@ struct LatLayout {
   static constexpr int FLAG = HI + R * 4;                        // [2][16]
   static constexpr int SEG = FLAG + 128;                         // [2]
   static constexpr int BAR = SEG + 2 * (int)sizeof(LatStretch);
-  static constexpr int NBAR = 2 + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 4 + 4 + 1;
+  static constexpr int NBAR = 2 + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 4 + 4 + 1 + 2;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int ALLOC = MISC + 16;
   static_assert(ALLOC <= 232448, "shared memory of a block");
   static_assert(2 * STAGE >= (kPagedMaxSeqs + 1) * 8, "the prefix sums lie in the stages at first");
   static_assert(4 * NP * R <= 512, "tensor memory: two buffers of S below column 256, four accumulators of 64 columns");
   static_assert(LSOFT * HC * 4 >= 8 * (LTHREADS / 32), "the prefix sums' warps lie in TOP and MINE at first");
-  static_assert(R == 64 ? NP == 2 : R == 32, "weights' room");
+  static_assert(R == 64 ? !HALF : R == 32, "weights' room");
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -114,9 +130,23 @@ __device__ __forceinline__ uint32_t split2(uint32_t& v) {
   return c;
 }
 
+// And the next e5m2 part: an e5m2 number is the upper byte of an fp16 number.
+__device__ __forceinline__ uint32_t cvt_e5m2x2_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t split2_wide(uint32_t& v) {
+  const uint32_t c = cvt_e5m2x2_f16x2(v);
+  const uint32_t back = __byte_perm(c, 0, 0x1404);
+  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&back));
+  v = *reinterpret_cast<const uint32_t*>(&rest);
+  return c;
+}
+
 // What fp16 numbers v leave of x0 and x1, to be added to what the first part leaves of v:
-// three parts have a bit more than fp16 (its rounding alone was as much as that of an
-// fp16 output).  Two have less, and go by way of fp16 as it is.
+// the parts of an fp16 query or weight have more bits than fp16 (its rounding alone was as
+// much as that of an fp16 output).  Those of bf16 have fewer, and go by way of fp16 as it is.
 __device__ __forceinline__ uint32_t left_of(uint32_t v, float x0, float x1) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
   return cvt_f16x2(x0 - f.x, x1 - f.y);
@@ -194,6 +224,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   uint64_t* flags_in = seg_free + 2;       // [4 quarters] the warps' flags written
   uint64_t* tops_in = flags_in + 4;        // [4 quarters] their maxima, or sums, or outputs
   uint64_t* drain = tops_in + 4;
+  uint64_t* first_done = drain + 1;        // (64 rows) PV is done with the weights' first part
+  uint64_t* third_full = first_done + 1;   // and their third stored in its room
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC + 4);
   volatile LatStretch* segs = reinterpret_cast<volatile LatStretch*>(sm + LY::SEG);
@@ -221,6 +253,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     mbar_init(q_full, LSOFT);
     mbar_init(q_free, LSOFT);
     mbar_init(drain, 1);
+    mbar_init(first_done, 1);
+    mbar_init(third_full, LSOFT);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -489,7 +523,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             most1 = max3f(most1, x[c + 2], x[c + 3]);
           }
           most = fmaxf(most, most1);
-          const bool raise = quarter_any(1 + quarter, most > kLatMost);
+          const bool raise = quarter_any(1 + quarter, most > kLatMost<T>);
           if (*abort_flag) {
             ok = false;
             break;
@@ -497,7 +531,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           if (raise) {
             uint32_t ups = 0;              // columns whose maximum is raised
 #pragma unroll
-            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatMost ? 1u << c : 0u;
+            for (int c = 0; c < HC; ++c) ups |= x[c] > kLatMost<T> ? 1u << c : 0u;
             ups = __reduce_or_sync(0xFFFFFFFFu, ups);
             volatile uint32_t* fl = flag + (g & 1) * 16 + quarter * 4;
             if (lane == 0) fl[quad] = ups;
@@ -574,45 +608,74 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             l[c] = t.x;
             l[c + 1] = t.y;
           }
-          uint32_t v[HC / 2], left[HC / 2];
+          uint32_t v[HC / 2];
 #pragma unroll
-          for (int c = 0; c < HC / 2; ++c) {
-            v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
-            if (NP == 3) left[c] = left_of(v[c], x[2 * c], x[2 * c + 1]);
-          }
+          for (int c = 0; c < HC / 2; ++c) v[c] = cvt_f16x2(x[2 * c], x[2 * c + 1]);
+          const int swz = key_row >> 1 & 3;              // of the 16-byte units of 64
           uint8_t* in_stage = sm + LY::K + (g & 1) * LY::STAGE + 4 * LY::CB + key_row * 64;
-          uint8_t* extra = sm + LY::P;
+          uint8_t* extra = sm + LY::P + key_row * (LY::PB / LKT);
+          uint32_t w[4][HC / 4];                         // the parts
+          if constexpr (LY::HALF) {
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            uint32_t w[HC / 4];
+            for (int c = 0; c < HC / 2; ++c) {
+              const uint32_t left = left_of(v[c], x[2 * c], x[2 * c + 1]);
+              uint32_t part[4];
+              part[0] = split2(v[c]);
+              add_left(v[c], left);
+              part[2] = split2_wide(v[c]);
+              const __half2 up = __hmul2(*reinterpret_cast<const __half2*>(&v[c]), __float2half2_rn(kRestScale));
+              v[c] = *reinterpret_cast<const uint32_t*>(&up);
+              part[1] = split2(v[c]);
+              part[3] = cvt_e5m2x2_f16x2(v[c]);
 #pragma unroll
-            for (int c = 0; c < HC / 4; ++c) {
-              const uint32_t c0 = split2(v[2 * c]), c1 = split2(v[2 * c + 1]);
-              w[c] = c0 | c1 << 16;
-              if (NP == 3 && p == 0) {
-                add_left(v[2 * c], left[2 * c]);
-                add_left(v[2 * c + 1], left[2 * c + 1]);
+              for (int p = 0; p < 4; ++p) w[p][c / 2] = c & 1 ? w[p][c / 2] | part[p] << 16 : part[p];
+            }
+          } else {
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int c = 0; c < HC / 4; ++c) {
+                const uint32_t c0 = split2_wide(v[2 * c]), c1 = split2_wide(v[2 * c + 1]);
+                w[p][c] = c0 | c1 << 16;
               }
-            }
-            // PV of the tile before is done with the room that is there once
-            if (LY::PB > 0 && p == NP - 1 && g > 0 && !pv_done(g - 1)) {
-              ok = false;
-              break;
-            }
-            if constexpr (R == 64) {
-              uint8_t* at = (p == 0 ? in_stage : extra + key_row * 64) + ((quarter ^ ((key_row >> 1) & 3)) << 4);
-              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if constexpr (R == 64) {
+            *reinterpret_cast<uint4*>(in_stage + ((quarter ^ swz) << 4)) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+          } else {
+            const int unit = quarter >> 1, half = 8 * (quarter & 1);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<uint2*>(in_stage + (((2 * p + unit) ^ swz) << 4) + half) = make_uint2(w[p][0], w[p][1]);
+          }
+          // PV of the tile before is done with the room that is there once
+          if (g > 0 && !pv_done(g - 1)) {
+            ok = false;
+            break;
+          }
+          if constexpr (R == 64) {
+            *reinterpret_cast<uint4*>(extra + ((quarter ^ swz) << 4)) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+          } else {
+            const int unit = quarter >> 1, half = 8 * (quarter & 1);
+            if constexpr (LY::HALF) {
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<uint2*>(extra + (((2 * p + unit) ^ swz) << 4) + half) = make_uint2(w[2 + p][0], w[2 + p][1]);
             } else {
-              const int unit = quarter >> 1;
-              uint8_t* at = p < 2 ? in_stage + (((2 * p + unit) ^ ((key_row >> 1) & 3)) << 4)
-                                  : extra + key_row * 32 + ((unit ^ ((key_row >> 2) & 1)) << 4);
-              *reinterpret_cast<uint2*>(at + 8 * (quarter & 1)) = make_uint2(w[0], w[1]);
+              *reinterpret_cast<uint2*>(extra + ((unit ^ (key_row >> 2 & 1)) << 4) + half) = make_uint2(w[2][0], w[2][1]);
             }
           }
-          if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_before();
           warp_arrive(&p_full[g & 1]);
+          if constexpr (R == 64) {                       // the third part where the first was
+            if (!bar_warp_wait(first_done, g & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            *reinterpret_cast<uint4*>(in_stage + ((quarter ^ swz) << 4)) = make_uint4(w[2][0], w[2][1], w[2][2], w[2][3]);
+            fence_proxy_async_smem();
+            warp_arrive(third_full);
+          }
         }
         if (!ok) break;
       }
@@ -673,7 +736,8 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               uint32_t o1[TC];
               tmem_ld_cols<TC>(at_o + R, o1);
 #pragma unroll
-              for (int c = 0; c < TC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(o1[c]));
+              for (int c = 0; c < TC; ++c)
+                o[c] = __float_as_uint(fmaf(__uint_as_float(o1[c]), LY::HALF ? 1.0f / kRestScale : 1.0f, __uint_as_float(o[c])));
             }
             if (whole) {
               T* at = reinterpret_cast<T*>(stage) + turn * TC * C + ch;
@@ -721,7 +785,9 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     if (warp == LSOFT) {
       // ======================================================== MMA issue
       constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, LKT, NP * R);
-      constexpr uint32_t idesc_pv = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv3 = make_idesc(0, 0, 1, 1, 128, 32);
+      // (B e4m3, or e5m2 of 64 and of 32 columns)
+      constexpr uint32_t idesc_pv4 = make_idesc(0, 0, 1, 1, 128, 64), idesc_pv5 = make_idesc(0, 1, 1, 1, 128, 64),
+                         idesc_pv5_32 = make_idesc(0, 1, 1, 1, 128, 32);
       // The warp goes together: what it counts by is the same in all lanes.
       const uint32_t k_at = smem_u32(sm + LY::K), q_at = smem_u32(sm + LY::Q), p_at = smem_u32(sm + LY::P);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -739,25 +805,44 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         // QK runs up to a tile ahead of PV where its codes are there in time; a PV that
         // can go goes first.
         int jq = 0, jp = 0;                  // the next of either
+        bool begun = false;                  // of PV jp two parts are issued
         for (uint32_t tests = 1; jp < n; ++tests) {
           const int gp = done + jp, gq = done + jq, sp = gp & 1, stage = gq & 1;
-          if (jp < jq && there(&p_full[sp], gp >> 1)) {
+          if (begun ? there(third_full, gp) : jp < jq && there(&p_full[sp], gp >> 1)) {
             tc_fence_after();
-            const uint32_t kt = k_at + sp * LY::STAGE;
-            const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512);
+            const uint32_t kt = k_at + sp * LY::STAGE, o = tm + TM_O;
+            const uint64_t b0 = make_sdesc_sw64(kt + 4 * LY::CB, 16, 512), b1 = make_sdesc_sw64(p_at, 16, 512);
             const uint32_t go = jp > 0;
+            if (R == 64 && !begun) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < NC) warp_mma4_f8_ss<256, 128>(o + 64 * c, make_sdesc_sw128(kt + c * LY::CB, 16, 1024), b0, idesc_pv5, go);
+              warp_mma_commit(first_done);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < NC) warp_mma4_f8_ss<256, 128>(o + 64 * c, make_sdesc_sw128(kt + c * LY::CB, 16, 1024), b1, idesc_pv5, 1);
+              begun = true;
+              tests = 0;
+              continue;
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (c >= NC) break;
               const uint64_t ad = make_sdesc_sw128(kt + c * LY::CB, 16, 1024);
-              const uint32_t o = tm + TM_O + 64 * c;
-              warp_mma4_f8_ss<256, 128>(o, ad, b0, idesc_pv, go);
-              if constexpr (R == 64) warp_mma4_f8_ss<256, 128>(o, ad, make_sdesc_sw64(p_at, 16, 512), idesc_pv, 1);
-              else if constexpr (NP == 3) warp_mma4_f8_ss<256, 64>(o, ad, sdesc_sw32(p_at, 256), idesc_pv3, 1);
+              if constexpr (R == 64) {
+                warp_mma4_f8_ss<256, 128>(o + 64 * c, ad, b0, idesc_pv5, 1);
+              } else if constexpr (LY::HALF) {
+                warp_mma4_f8_ss<256, 128>(o + 64 * c, ad, b0, idesc_pv4, go);
+                warp_mma4_f8_ss<256, 128>(o + 64 * c, ad, b1, idesc_pv5, 1);
+              } else {
+                warp_mma4_f8_ss<256, 128>(o + 64 * c, ad, b0, idesc_pv5, go);
+                warp_mma4_f8_ss<256, 64>(o + 64 * c, ad, sdesc_sw32(p_at, 256), idesc_pv5_32, 1);
+              }
               if (c == 1) warp_mma_commit(&free_[sp * 2]);
             }
             if (NC == 1) warp_mma_commit(&free_[sp * 2]);
             warp_mma_commit(&free_[sp * 2 + 1]);
+            begun = false;
             ++jp;
             tests = 0;
           } else if (jq < n && jq < jp + 2 && there(&full[stage], gq >> 1)) {
