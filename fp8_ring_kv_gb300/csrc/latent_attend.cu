@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   const long long end = min(total, u + stretch);
   Place pl;
   if (warp == LSOFT + 1 && u < end) pl = find_place<SH, R, LKT>(a, pre, u, cut.pad);
-  __syncthreads();                         // the prefix sums' room is the stages' now
+  // the prefix sums' room is the stages' now: TMA writes there
+  fence_proxy_async_smem();
+  __syncthreads();
 
   if (warp < LSOFT) {
     // ======================================================== softmax
