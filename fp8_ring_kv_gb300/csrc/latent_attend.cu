@@ -69,7 +69,7 @@ constexpr int LFIX = 4, LLEAST = 6, LCUT = 4;
 template <typename T> constexpr float kTop = std::is_same_v<T, __half> ? 6.807354922f : 11.807354922f;
 template <typename T> constexpr float kLatMost = std::is_same_v<T, __half> ? 8.807354922f : 15.807354922f;
 constexpr float kRestScale = 256.0f;         // of an fp16 column's second accumulator
-constexpr float kNoMax = -1e30f;             // no key yet
+constexpr float kNoMax = -3.402823466e38f;   // no key yet: below every logit
 
 struct LatStretch {
   int b, s0, n, len, lo, hi, all_lo, all_hi, k0, k1, tile, flags;

@@ -1,0 +1,54 @@
+"""Latent attention at the ends of its ranges."""
+import numpy as np
+import pytest
+import torch
+
+from latent_bounds import U
+from test_gpu_latent import BF, HF, KIND, ROPE, Case, cu, num
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(c, q, scale, qr=None):
+    start, ln, pos = c.batch(c.seqs)
+    qr = torch.zeros(c.n, c.heads, ROPE, dtype=c.dtype) if qr is None else qr
+    out = c.kv.attend(q.cuda(), qr.cuda(), cu(pos), cu(start), cu(ln), cu(c.table), scale)
+    assert c.kv.debug_state() == 0
+    return out, c.oracle.attend(num(q), num(qr), pos, start, ln, c.table, scale)
+
+
+def known(c, first):
+    """Rows whose first channel is ``first`` [keys]; the rest drawn, nothing to rotate."""
+    x = c.draw(len(first), c.C)
+    x[:, 0] = torch.tensor(first).to(c.dtype)
+    c.append([(len(first), 0)], x, torch.zeros(len(first), ROPE, dtype=c.dtype))
+
+
+def near(out, want, dtype):
+    """Single weights: 2^-9 + 2^-11 (fp16 2^-13) and fp32 sums, then the output's rounding."""
+    u = U[KIND[dtype]]
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= np.abs(want) * (u + (2.0 ** -13 if dtype is HF else 2.0 ** -9 + 2.0 ** -11) * (1 + u) + 2.0 ** -16))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads", [3, 64])
+@pytest.mark.parametrize("keys", [1])
+def test_logits_far_below_zero(keys, heads, dtype):
+    """Scale 2^100 and products of one sign: the key with the largest logit has all of
+    the weight, however negative its logit is."""
+    c = Case([(1, keys - 1)], heads=heads, latent=128, page=16, dtype=dtype)
+    first = 2.0 + np.arange(keys) % 5
+    first[keys * 2 // 3] = 1.0
+    if keys > 3:
+        first[keys // 3] = 7.0
+    known(c, first)
+    for size in (1.0, 2.0 ** 14, 2.0 ** -20 if dtype is BF else 2.0 ** -10):
+        for sign, at in ((-1, keys * 2 // 3), (1, keys // 3)):
+            q = torch.zeros(1, heads, 128, dtype=dtype)
+            q[..., 0] = sign * size
+            out, r = attend(c, q, 2.0 ** 100)
+            value = c.oracle.rows(c.table[0], keys)[at, :128]
+            if sign < 0 or keys > 3:
+                assert np.allclose(r.out, value)
+            near(out, r.out, dtype)
