@@ -490,19 +490,23 @@ __global__ void __launch_bounds__(LTHREADS, 1)
               for (int c = 0; c < HC; ++c) x[c] += __uint_as_float(part[c]);
             }
           };
-          // x becomes y minus what is in ``mine`` (raw: y itself)
+          // x becomes y minus what is in ``mine`` (raw: y itself).  y is rounded before the
+          // difference, as where the maximum was taken: of large logits a fused one would
+          // leave that rounding.
           auto logits = [&](bool raw) {
             const float4* f4 = reinterpret_cast<const float4*>(fac + quarter * HC);
             const float4* m4 = reinterpret_cast<const float4*>(mine);
+            const float2 s2 = make_float2(st, st), e2 = make_float2(est, est);
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
-              const float4 f = f4[c / 4], m = m4[c / 4];
-              const float2 s2 = make_float2(st, st);
-              const float2 g0 = mul2(make_float2(f.x, f.y), s2), g1 = mul2(make_float2(f.z, f.w), s2);
-              const float2 e0 = raw ? make_float2(est, est) : make_float2(est - m.x, est - m.y);
-              const float2 e1 = raw ? make_float2(est, est) : make_float2(est - m.z, est - m.w);
-              const float2 d0 = fma2(make_float2(x[c], x[c + 1]), g0, e0);
-              const float2 d1 = fma2(make_float2(x[c + 2], x[c + 3]), g1, e1);
+              const float4 f = f4[c / 4];
+              float2 d0 = fma2(make_float2(x[c], x[c + 1]), mul2(make_float2(f.x, f.y), s2), e2);
+              float2 d1 = fma2(make_float2(x[c + 2], x[c + 3]), mul2(make_float2(f.z, f.w), s2), e2);
+              if (!raw) {
+                const float4 m = m4[c / 4];
+                d0 = add2(d0, make_float2(-m.x, -m.y));
+                d1 = add2(d1, make_float2(-m.z, -m.w));
+              }
               x[c] = d0.x;
               x[c + 1] = d0.y;
               x[c + 2] = d1.x;

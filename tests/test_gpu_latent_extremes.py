@@ -33,7 +33,7 @@ def near(out, want, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("heads", [3, 64])
-@pytest.mark.parametrize("keys", [1])
+@pytest.mark.parametrize("keys", [1, 40, 3000])
 def test_logits_far_below_zero(keys, heads, dtype):
     """Scale 2^100 and products of one sign: the key with the largest logit has all of
     the weight, however negative its logit is."""
