@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       const int i = r0 + row;
       const int hi = !live ? 0x7FFFFFFF : a.causal ? len_n + i + 1 : seg.len;
       const int lo = live && a.window > 0 ? len_n + i - a.window + 1 : 0;
-      float m = -INFINITY, l = 0.0f;
+      float ms = -INFINITY, m = -INFINITY, l = 0.0f;    // the reference as a score and as a logit; the sum
       if (n > 0 && rows > 0) {
         // ------------------------------------------------------ queries
         // half of the pair's 32 rows each
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           }
           // the row's maximum: the other half's keys are the other warp's.  Both
           // see the same numbers and do the same.
-          const float my = fmaxf(max3f(max3f(m4[0], s[60], s[61]), max3f(m4[1], s[62], s[63]), m4[2]), m4[3]) * rf;
+          const float my = fmaxf(max3f(max3f(m4[0], s[60], s[61]), max3f(m4[1], s[62], s[63]), m4[2]), m4[3]);
           *mine = my;
           __syncwarp();
           if (lane == 0) mbar_arrive(&m_ready[2 * pair + par]);
@@ -302,11 +302,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             ok = false;
             break;
           }
-          const float mm = fmaxf(my, *other);
+          const float mms = fmaxf(my, *other), mm = mms * rf;
           if (__any_sync(0xFFFFFFFFu, mm > m + kXRaise)) {
             // rare after a row's first keys: what was summed is brought to the new maximum
             const float mn = mm > m + kXRaise ? mm : m;
             const float al = mn > m ? ex2f(m - mn) : 1.0f;     // 0 for the row's first keys
+            if (mn > m) ms = mms;
             m = mn;
             l *= al;
             if (j > 0) {
@@ -322,15 +323,17 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             }
           }
           // (both warps hold their scores in registers: P may go over all of S)
-          const float sub = m == -INFINITY ? 0.0f : kXTop - m;
+          // Differences of scores, then their logits: of large logits the maximum's rounding
+          // would show in a difference of those.
+          const float from = m == -INFINITY ? 0.0f : -ms;
           float2 part[2] = {};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t p[16], p1[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float2 y = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(rf, rf),
-                              make_float2(sub, sub));
+              float2 y = fma2(add2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(from, from)),
+                              make_float2(rf, rf), make_float2(kXTop, kXTop));
               y.x = ex2f(y.x);
               y.y = ex2f(y.y);
               part[e & 1] = add2(part[e & 1], y);

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from latent_bounds import U
+from oracle.latent import attend_expanded
 from test_gpu_latent import BF, HF, KIND, ROPE, Case, cu, num
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,27 @@ def test_logits_far_below_zero(keys, heads, dtype):
             if sign < 0 or keys > 3:
                 assert np.allclose(r.out, value)
             near(out, r.out, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("seqs", [[(1, 0)], [(1, 2999), (3, 40)], [(300, 7)]])
+def test_large_logits_of_the_expanded_form(seqs, dtype):
+    """Products of one channel and a large scale: the keys with the largest logit that a
+    row sees share its weight."""
+    c = Case(seqs, heads=2, latent=128, page=16, dtype=dtype)
+    start, ln, pos = c.batch(seqs)
+    total = sum(c.len)
+    k, v, kr = c.draw(total, 2, 128), c.draw(total, 2, 128), c.draw(total, ROPE)
+    k[..., 0] = torch.from_numpy(2.0 + (np.arange(total) % 7 + np.arange(total) % 5)[:, None] / 4 + [0, 0.5]).to(dtype)
+    first = np.concatenate([[0], np.cumsum(ln)]).astype(np.int32)[:len(seqs)]
+    for scale in (2.0 ** 20, 2.0 ** 29, 2.0 ** 40, 2.0 ** 100):
+        for sign in (1.0, -1.0):
+            q = torch.zeros(c.n, 2, 192, dtype=dtype)
+            q[..., 0] = sign * 1.375
+            out = c.kv.attend_expanded(q.cuda(), k.cuda(), kr.cuda(), v.cuda(), cu(pos), cu(start), cu(first), cu(ln), scale=scale)
+            want = attend_expanded(num(q), num(k), num(kr), num(v), pos, start, first, ln, scale=scale)
+            u = U[KIND[dtype]]
+            err = np.abs(out.double().cpu().numpy() - want.out)
+            # weights 2^-16, sums 2^-16; then the output's rounding
+            assert np.all(err <= want.spread * 2.0 ** -15 * (1 + u) + np.abs(want.out) * u + 2.0 ** -24), (scale, sign)
+    assert c.kv.debug_state() == 0
