@@ -156,6 +156,20 @@ __device__ __forceinline__ void add_left(uint32_t& v, uint32_t left) {
   v = *reinterpret_cast<const uint32_t*>(&sum);
 }
 
+// A query row's scale and 1 / scale: pow2_scale's as far down as both are normal numbers
+// (smaller queries are no zeros yet: a large softmax scale may follow).
+__device__ __forceinline__ void query_scale(float amax, float& scale, float& inv) {
+  if (amax < 0x1p-118f) {
+    scale = 0x1p-126f;
+    inv = 0x1p126f;
+    return;
+  }
+  const uint32_t u = __float_as_uint(amax);
+  const uint32_t e = (u >> 23) - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7);   // 448 = 1.75 x 2^8
+  scale = __uint_as_float(e << 23);
+  inv = __uint_as_float((254 - e) << 23);
+}
+
 __device__ __forceinline__ float warp_maxf(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
           else top <<= 16;
           top = max(__reduce_max_sync(0xFFFFFFFFu, top), __shfl_sync(0xFFFFFFFFu, ytop, 4 * k));
           float scale, inv;
-          pow2_scale(__uint_as_float(top), scale, inv);
+          query_scale(__uint_as_float(top), scale, inv);
           if (top >= 0x7F800000u) {        // no numbers: the row's scores are NaN by its factor
             scale = __int_as_float(0x7FC00000);
             inv = 0.0f;

@@ -3,9 +3,10 @@ import numpy as np
 import pytest
 import torch
 
+import latent_bounds
 from latent_bounds import U
 from oracle.latent import attend_expanded
-from test_gpu_latent import BF, HF, KIND, ROPE, Case, cu, num
+from test_gpu_latent import BF, HF, KIND, ROPE, Case, check, cu, num
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,21 @@ def test_large_logits_of_the_expanded_form(seqs, dtype):
             # weights 2^-16, sums 2^-16; then the output's rounding
             assert np.all(err <= want.spread * 2.0 ** -15 * (1 + u) + np.abs(want.out) * u + 2.0 ** -24), (scale, sign)
     assert c.kv.debug_state() == 0
+
+
+@pytest.mark.parametrize("exponent", [-99, -105, -119, -128])
+@pytest.mark.parametrize("heads", [3, 64])
+def test_queries_near_the_smallest_numbers(exponent, heads):
+    """Tiny queries, large keys and scale 2^100: logits of ordinary size."""
+    c = Case([(1, 500), (2, 30)], heads=heads, latent=128, page=16)
+    total = sum(c.len)
+    size = np.float32(2.0 ** (-100 - exponent) / 16)
+    x, r = c.draw(total, 128).float() * size, c.draw(total, ROPE).float() * size
+    c.append([(n, 0) for n in c.len], x.bfloat16(), r.bfloat16())
+    q = (c.draw(c.n, heads, 128).double() * 2.0 ** exponent).bfloat16()
+    # rotated numbers of the last size are below what two parts hold of a row: none
+    qr = (c.draw(c.n, heads, ROPE).double() * (2.0 ** exponent if exponent > -128 else 0.0)).bfloat16()
+    assert float(num(q).__abs__().max()) > 0
+    out, want = attend(c, q, 2.0 ** 100, qr)
+    check(out, want, latent_bounds.absorbed(want, "bf16"))
+    assert float(np.abs(want.out - want.out[:1]).max()) > 0
