@@ -445,7 +445,10 @@ __global__ void __launch_bounds__(LTHREADS, 1)
             }
           }
           if ((lane >> 2) == k) yinv = inv;
-          if (lane == k) fac[r] = r < rows ? a.scale_log2 * scale : 0.0f;
+          // (a factor beyond fp32 would make NaN of products that are 0; at 2^87 a product that
+          // is not leaves the others no weight either.  A NaN stays.)
+          const float f = a.scale_log2 * scale;
+          if (lane == k) fac[r] = r < rows ? (f > 0x1p87f ? 0x1p87f : f) : 0.0f;
           if (mine16) {
             float x[16];
             load8_f32<T>(w[k][0], x);

@@ -96,3 +96,20 @@ def test_queries_near_the_smallest_numbers(exponent, heads):
     out, want = attend(c, q, 2.0 ** 100, qr)
     check(out, want, latent_bounds.absorbed(want, "bf16"))
     assert float(np.abs(want.out - want.out[:1]).max()) > 0
+
+
+@pytest.mark.parametrize("heads", [3, 64])
+def test_queries_near_the_largest_numbers(heads):
+    """A query number times the scale is beyond fp32: keys without that channel have the
+    logit 0, others are far away from it."""
+    c = Case([(1, 299)], heads=heads, latent=128, page=16)
+    first = np.where(np.arange(300) % 3 == 0, 0.0, -1.0 - np.arange(300) % 2)
+    known(c, first)
+    for size in (2.0 ** 30, 2.0 ** 60, 2.0 ** 120):
+        q = torch.zeros(1, heads, 128, dtype=BF)
+        q[..., 0] = size
+        out, want = attend(c, q, 2.0 ** 80)
+        # logits of one product are exact: 0, or too far away to matter.  A weight is off by
+        # 2^-9 + 2^-11, sums by 2^-16, the output by its rounding.
+        assert np.all(np.abs(out.double().cpu().numpy() - want.out) <=
+                      want.spread * (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -16) * (1 + U["bf16"]) + np.abs(want.out) * U["bf16"])
