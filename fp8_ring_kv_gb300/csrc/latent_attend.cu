@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   long long* pre = reinterpret_cast<long long*>(sm + LY::K);
-  const Cut cut = latent_prefix<SH, R, LKT, LFIX, LTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
+  const Cut cut = latent_prefix<SH, R, LKT, LTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
   const int G = a.pv.G, C = a.pv.D, NC = C >> 7;
   const long long total = pre[a.pb.n_seqs];
   long long stretch = quotient(total + gridDim.x - 1, gridDim.x);

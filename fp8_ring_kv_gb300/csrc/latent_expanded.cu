@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   long long* pre = reinterpret_cast<long long*>(sm + LY::Q);
-  const Cut cut = latent_prefix<SH, XTR, XKT, 2, XTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
+  const Cut cut = latent_prefix<SH, XTR, XKT, XTHREADS>(a, pre, warp_sums, blockIdx.x == 0, item_sums, gridDim.x, line);
   const long long total = pre[a.pb.n_seqs] * a.pv.H;
   long long stretch = quotient(total + gridDim.x - 1, gridDim.x);
   if (stretch < SH::kLeast) stretch = SH::kLeast;

@@ -18,7 +18,7 @@ struct LineOfWork {
 
 // Share::prefix, by all threads; ``line`` in shared memory (warp_sums, sums as
 // there).  The same numbers, whichever way they come.
-template <class SH, int TR, int KT, int FIX, int NT>
+template <class SH, int TR, int KT, int NT>
 __device__ __forceinline__ Cut latent_prefix(const PagedAttn& a, long long* pre, long long* warp_sums, bool report,
                                              unsigned long long* sums, int workers, LineOfWork* line) {
   const int lane = threadIdx.x & 31, B = a.pb.n_seqs;
