@@ -59,13 +59,13 @@ constexpr int LSOFT = 16;                    // softmax warps
 constexpr int LTHREADS = 32 * (LSOFT + 4);  // (whole groups of four warps)
 constexpr int kLatSoftRegs = 104, kLatOtherRegs = 64;   // per thread
 // Of the sharing of work (Share): what an item costs beside its tiles (queries and
-// results, 16,000 cycles), in tiles; units of a stretch at least; from what a cut is
-// worth it (16 tokens over 2,000, 64 heads: 53 us; with 8: 60).
+// results, 16,000 cycles), in tiles (with 3: even); units of a stretch at least; from what
+// a cut is worth it (chunks over windows 120 us; with 8: 120 to 122).
 constexpr int LFIX = 4, LLEAST = 6, LCUT = 4;
 // A column's largest weight starts at 1/16 of its first part's largest number, 57344 of
 // e5m2 (fp16: 1/4 of 448, e4m3's), and may reach that before its maximum is raised.  A higher
 // start has less below the smallest steps and is raised more often (24 contexts of 300 to
-// 5,000, 20 heads, fp16: 36.5 us, from 1/16 35.5).
+// 5,000, 20 heads, fp16: 38 us, from 1/16 36).
 template <typename T> constexpr float kTop = std::is_same_v<T, __half> ? 6.807354922f : 11.807354922f;
 template <typename T> constexpr float kLatMost = std::is_same_v<T, __half> ? 8.807354922f : 15.807354922f;
 constexpr float kRestScale = 256.0f;         // of an fp16 column's second accumulator
@@ -1234,8 +1234,8 @@ cudaError_t launch_latent_attend(const LatentAttn& la, const CUtensorMap& tmC, c
                                  cudaStream_t st) {
   const int blocks = sms < kPagedMaxSms ? sms : kPagedMaxSms;
   if (f16) return attend_t<__half, 32>(la, tmC, tmR, blocks, st);
-  // (items of 32 rows and of 64: one token of 32 heads over 900 30 and 38 us, 32 over
-  // 1,000 to 4,000 39 and 46)
+  // (items of 32 rows and of 64: one token of 32 heads over 900 34 and 47 us, 32 over
+  // 1,000 to 4,000 42 and 54)
   if ((long long)la.a.max_new * la.a.pv.G <= 32) return attend_t<__nv_bfloat16, 32>(la, tmC, tmR, blocks, st);
   return attend_t<__nv_bfloat16, 64>(la, tmC, tmR, blocks, st);
 }

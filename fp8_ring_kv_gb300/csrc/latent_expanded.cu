@@ -21,7 +21,7 @@
 // cycles, the difference mostly pauses between a PV and the
 // QK that overwrites its weights (below).  512 queries over 16,001 keys, 20
 // heads: 126 us (0.85 PFLOP/s of attention, 44% of what cuBLAS reaches in bf16, and
-// 1.6 times that in products); 3 prompts of 1,000 to 4,096, 32 heads, causal: 353.
+// 1.6 times that in products); 3 prompts of 1,000 to 4,096, 32 heads, causal: 357.
 //
 // Warp roles (640 threads, registers moved from the last group to the softmax):
 //   warps 0-15   softmax: of query tile t and half p of its keys, warps 8 p + 4 t

@@ -110,11 +110,11 @@ int kvring_latent_read(kvring_latent* p, int32_t layer, const int32_t* seq_start
  *   causal, window, max_new   as kvring_paged_attend's
  * The products run on e4m3 codes.  A query is a sum of two (bf16) or three
  * (fp16) e4m3 numbers at a power-of-two scale of its row: off by at most 2^-8
- * (2^-12) of itself or 2^-17.8 of the row's largest number, whichever is more (a
- * number of q_latent is exact but for the latter).  A weight is a sum of three
- * (bf16) or four (fp16) 8-bit numbers: off by at most 2^-9 + 2^-11 (2^-13) of itself,
- * or, where that is more, 2^-28.8 (2^-27.8) of the largest product of a weight and
- * its token's scale in the row, divided by its own token's scale.  Sums and
+ * (2^-12) of itself or 2^-17.8 of the row's largest number or 2^-136, whichever is
+ * most (a number of q_latent is exact but for the last two).  A weight is a sum of
+ * three (bf16) or four (fp16) 8-bit numbers: off by at most 2^-9 + 2^-11 (2^-13) of
+ * itself, or, where that is more, 2^-28.8 (2^-27.8) of the largest product of a weight
+ * and its token's scale in the row, divided by its own token's scale.  Sums and
  * statistics are fp32.
  * A query that sees nothing gives zeros.  N * q_heads is at most 2^30.
  */
@@ -139,9 +139,10 @@ int kvring_latent_attend(kvring_latent* p, int32_t layer, const void* q_latent, 
  *   out      device [N][q_heads][128]
  *   scale    0: 1 / sqrt(192)
  *   causal, window, max_new   as kvring_paged_attend's
- * Rotated queries are rounded to the inputs' type once; weights are sums of two
- * numbers of it; sums and statistics are fp32.  A value that is no number spreads to the rows that see
- * it, in its channel or in all of the head's, and to no other.
+ * Rotated queries are rounded to the inputs' type once (fp16: what is beyond 65504
+ * after the rotation is an infinity); weights are sums of two numbers of it; sums and
+ * statistics are fp32.  A value that is no number spreads to the rows that see it, in
+ * its channel or in all of the head's, and to no other.
  */
 int kvring_latent_attend_expanded(kvring_latent* p, const void* q, int64_t q_token, int64_t q_head, const void* k,
                                   int64_t k_token, int64_t k_head, const void* k_rope, int64_t k_rope_token,
